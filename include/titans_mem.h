@@ -78,6 +78,7 @@ extern "C" {
 #define TM_IO_BF16 1
 
 #define TM_ACT_SILU 0
+#define TM_ACT_NONE 1   /* titans_mem_group_norm only */
 
 /* which state retrieval reads (section 3.1 "Retrieving a Memory" has no
  * time index; the write-then-read memory view of section 2.1 reads M_t) */
@@ -334,6 +335,124 @@ int titans_mem_input(const titans_input_desc* desc,
                      void* k_out, void* v_out, void* q_out,
                      float* alpha_out, float* eta_out, float* theta_out,
                      void* stream);
+
+/*
+ * titans_mem_delta_forward -- the gated delta memory: the linear memory
+ * M(k) = W k updated after every token, without momentum, its residual taken
+ * at the decayed memory of the token before.  Per stream and token:
+ *
+ *   f_t = v_t - (1 - alpha_t) W_{t-1} k_t      section 3.1, "Objective"
+ *   W_t = (1 - alpha_t) W_{t-1} + theta_t f_t k_t^T   "Forgetting Mechanism"
+ *   y_t = W_t q_t                              "Retrieving a Memory"
+ *
+ * Unlike titans_mem_forward's linear memory (gradients at the chunk's start)
+ * this is the token-by-token rule at every length; the chunks of the chunked
+ * kernel are an implementation detail that no result depends on.
+ *
+ *   k, q       [B,Hk,N,d]  io dtype, device, read-only; value head h reads
+ *              key head h / (H / Hk)
+ *   v          [B,H,N,d]   io dtype, device, read-only
+ *   alpha, theta  [B,H,N]  fp32, device, read-only: forgetting gate
+ *              (alpha <= 1; 1 forgets everything; NaN comes out of more)
+ *              and step size
+ *   lengths    [B] int32, device, read-only, or NULL (all N): tokens of each
+ *              sequence, clamped to 0..N.  Later tokens are not read, their
+ *              rows of y_out are left as they were, and W_out is the state
+ *              after the last token of its sequence (W_in for length 0).
+ *   W_in, W_out  [B,H,d,d] fp32, device, row-major [n_out x n_in]; W_out ==
+ *              W_in (exact in-place) is allowed, any other overlap of a
+ *              written buffer is TM_ERR_ALIAS
+ *   y_out      [B,H,N,d]   io dtype, device, written
+ *   workspace  titans_mem_delta_workspace_bytes(desc) bytes of device
+ *              scratch (may be NULL when that is 0)
+ *
+ * State, sums and gates are fp32; products of bf16 inputs are exact.  y is
+ * rounded once.  d <= 128 (TM_ERR_UNSUPPORTED otherwise); N == 0 copies the
+ * state.  TM_FLAG_FORCE_GENERIC runs the token-by-token kernel at any N.
+ * titans_mem_delta_select_path reports the kernel that a call runs.
+ */
+#define TM_PATH_DELTA_RECURRENT 0   /* token by token */
+#define TM_PATH_DELTA_CHUNKED   1   /* by chunks, on the matrix cores */
+
+typedef struct {
+    int32_t abi_version;  /* must equal TITANS_MEM_ABI_VERSION */
+    int32_t B, H, Hk;     /* batch, value heads, key heads (Hk divides H) */
+    int32_t N, d;         /* tokens per sequence (N >= 0), width of k, v, q */
+    int32_t io_dtype;     /* TM_IO_F32 or TM_IO_BF16 */
+    uint32_t flags;       /* 0 or TM_FLAG_FORCE_GENERIC */
+} titans_delta_desc;
+
+int32_t titans_mem_delta_select_path(const titans_delta_desc* desc);
+int64_t titans_mem_delta_workspace_bytes(const titans_delta_desc* desc);
+
+int titans_mem_delta_forward(const titans_delta_desc* desc,
+                             const void* k, const void* v, const void* q,
+                             const float* alpha, const float* theta,
+                             const int32_t* lengths, const float* W_in,
+                             void* y_out, float* W_out,
+                             void* workspace, int64_t workspace_bytes,
+                             void* stream);
+
+/*
+ * titans_mem_group_norm -- group norm with an activation, from the memory's
+ * y to the channels-last rows that a block's output projection reads
+ * (section 4.4, "Architectural Details": normalization and gating before the
+ * output projection).  A group is one head's d channels of one token:
+ *
+ *   n = (x - mean) / sqrt(var + eps) * weight + bias
+ *   out = act(gate) * n  with a gate,  act(n)  without one
+ *
+ * act is SiLU (TM_ACT_SILU) or the identity (TM_ACT_NONE); var is the mean
+ * of the squared deviations.
+ *
+ *   x          [B,H,N,d] io dtype, device, read-only (the layout of y); with
+ *              TM_FLAG_CHANNELS_LAST [B,N,H*d]
+ *   gate       [B,N,H*d] io dtype, device, read-only, or NULL
+ *   weight, bias  [H*d] fp32, device, read-only, or NULL (ones, zeros)
+ *   lengths    [B] int32, device, read-only, or NULL (all N): later tokens
+ *              are neither read nor written
+ *   out        [B,N,H*d] io dtype, device, written
+ * Sums and the normalised values are fp32; out is rounded once.
+ * Supported: d <= 1024, H <= 65535 (TM_ERR_UNSUPPORTED otherwise), eps >= 0.
+ * Any overlap of out with an input is TM_ERR_ALIAS.
+ */
+#define TM_FLAG_CHANNELS_LAST 8u   /* titans_mem_group_norm: x is [B,N,H*d] */
+
+typedef struct {
+    int32_t abi_version;  /* must equal TITANS_MEM_ABI_VERSION */
+    int32_t B, H, N, d;   /* batch, groups, tokens (N >= 0), channels per group */
+    int32_t io_dtype;     /* TM_IO_F32 or TM_IO_BF16 */
+    int32_t activation;   /* TM_ACT_SILU or TM_ACT_NONE */
+    float eps;
+    uint32_t flags;       /* 0 or TM_FLAG_CHANNELS_LAST */
+} titans_norm_desc;
+
+int titans_mem_group_norm(const titans_norm_desc* desc, const void* x,
+                          const void* gate, const float* weight,
+                          const float* bias, const int32_t* lengths,
+                          void* out, void* stream);
+
+/*
+ * titans_mem_group_norm_backward -- its vector-Jacobian products with
+ *   dout       [B,N,H*d] io dtype, device, read-only: dL/dout
+ * into
+ *   dx         x's layout, io dtype, device, written
+ *   dgate      [B,N,H*d] io dtype, device, written (NULL iff gate is NULL)
+ *   dweight, dbias  [H*d] fp32, device, written (also where weight and bias
+ *              are NULL)
+ * Rows past a sequence's length get zero gradients and add nothing to
+ * dweight and dbias, which are summed in a fixed order.  Any overlap of a
+ * written buffer is TM_ERR_ALIAS.
+ */
+int64_t titans_mem_group_norm_backward_workspace_bytes(const titans_norm_desc* desc);
+
+int titans_mem_group_norm_backward(const titans_norm_desc* desc, const void* x,
+                                   const void* gate, const float* weight,
+                                   const float* bias, const int32_t* lengths,
+                                   const void* dout, void* dx, void* dgate,
+                                   float* dweight, float* dbias,
+                                   void* workspace, int64_t workspace_bytes,
+                                   void* stream);
 
 /* Static text for a status code. */
 const char* titans_mem_status_string(int status);

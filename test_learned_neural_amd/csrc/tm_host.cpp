@@ -351,6 +351,150 @@ int titans_mem_input(const titans_input_desc* desc, const void* x, const void* w
   return err == hipSuccess ? TM_OK : TM_ERR_HIP;
 }
 
+}  // extern "C"
+
+namespace {
+
+using titans::DeltaShape;
+using titans::NormShape;
+
+constexpr double kMostElements = 1e15;   // of one tensor: byte counts stay far inside 64 bits
+
+int build_delta(const titans_delta_desc* desc, DeltaShape* s) {
+  if (!desc || desc->abi_version != TITANS_MEM_ABI_VERSION) return TM_ERR_INVALID;
+  if (desc->B <= 0 || desc->H <= 0 || desc->Hk <= 0 || desc->H % desc->Hk || desc->N < 0 || desc->d <= 0)
+    return TM_ERR_INVALID;
+  if (desc->io_dtype != TM_IO_F32 && desc->io_dtype != TM_IO_BF16) return TM_ERR_INVALID;
+  if (desc->flags & ~TM_FLAG_FORCE_GENERIC) return TM_ERR_INVALID;
+  if (desc->d > titans::kMaxWidthDelta || (int64_t)desc->B * desc->H > (int64_t)1 << 24) return TM_ERR_UNSUPPORTED;
+  if ((double)desc->B * desc->H * desc->N * desc->d > kMostElements) return TM_ERR_UNSUPPORTED;
+  *s = {desc->B, desc->H, desc->Hk, desc->N, desc->d, desc->io_dtype, desc->flags};
+  return TM_OK;
+}
+
+int build_norm(const titans_norm_desc* desc, NormShape* s) {
+  if (!desc || desc->abi_version != TITANS_MEM_ABI_VERSION) return TM_ERR_INVALID;
+  if (desc->B <= 0 || desc->H <= 0 || desc->N < 0 || desc->d <= 0) return TM_ERR_INVALID;
+  if (desc->io_dtype != TM_IO_F32 && desc->io_dtype != TM_IO_BF16) return TM_ERR_INVALID;
+  if (desc->activation != TM_ACT_SILU && desc->activation != TM_ACT_NONE) return TM_ERR_INVALID;
+  if (!(desc->eps >= 0.f) || desc->eps > 3.0e38f) return TM_ERR_INVALID;
+  if (desc->flags & ~TM_FLAG_CHANNELS_LAST) return TM_ERR_INVALID;
+  if (desc->d > titans::kMaxWidthNorm || desc->H > titans::kMaxHeadsNorm) return TM_ERR_UNSUPPORTED;
+  if ((double)desc->B * desc->H * desc->N * desc->d > kMostElements) return TM_ERR_UNSUPPORTED;
+  *s = {desc->B, desc->H, desc->N, desc->d, desc->io_dtype, desc->activation == TM_ACT_SILU,
+        !(desc->flags & TM_FLAG_CHANNELS_LAST), desc->eps};
+  return TM_OK;
+}
+
+int delta_path(const DeltaShape&) { return TM_PATH_DELTA_RECURRENT; }
+
+// a pointer that must be there (unless its buffer is empty) / may be NULL
+bool needed(const void* p, int64_t bytes) { return aligned16(p) && (p || bytes == 0); }
+
+// no written range meets another; `same`: the one pair that may be equal
+bool disjoint(const Range* r, int n, int same_a = -1, int same_b = -1) {
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j) {
+      if (!(r[i].writes || r[j].writes) || !overlap(r[i], r[j])) continue;
+      if (i == same_a && j == same_b && r[i].lo == r[j].lo) continue;
+      return false;
+    }
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t titans_mem_delta_select_path(const titans_delta_desc* desc) {
+  DeltaShape s;
+  int rc = build_delta(desc, &s);
+  return rc ? rc : delta_path(s);
+}
+
+int64_t titans_mem_delta_workspace_bytes(const titans_delta_desc* desc) {
+  DeltaShape s;
+  int rc = build_delta(desc, &s);
+  return rc ? rc : 0;
+}
+
+int titans_mem_delta_forward(const titans_delta_desc* desc, const void* k, const void* v, const void* q,
+                             const float* alpha, const float* theta, const int32_t* lengths, const float* W_in,
+                             void* y_out, float* W_out, void* workspace, int64_t workspace_bytes, void* stream) {
+  DeltaShape s;
+  int rc = build_delta(desc, &s);
+  if (rc) return rc;
+  const int64_t esz = s.io == TM_IO_BF16 ? 2 : 4, need = titans_mem_delta_workspace_bytes(desc);
+  const int64_t keys = (int64_t)s.B * s.Hk * s.N * s.d * esz, vals = (int64_t)s.B * s.H * s.N * s.d * esz;
+  const int64_t gates = (int64_t)s.B * s.H * s.N * 4, state = (int64_t)s.B * s.H * s.d * s.d * 4;
+  if (!needed(k, keys) || !needed(q, keys) || !needed(v, vals) || !needed(y_out, vals) || !needed(alpha, gates) ||
+      !needed(theta, gates) || !needed(W_in, state) || !needed(W_out, state) || !aligned16(lengths) ||
+      !aligned16(workspace))
+    return TM_ERR_INVALID;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return TM_ERR_WORKSPACE;
+  const Range r[] = {{(const char*)k, keys, false},          {(const char*)v, vals, false},
+                     {(const char*)q, keys, false},          {(const char*)alpha, gates, false},
+                     {(const char*)theta, gates, false},     {(const char*)lengths, (int64_t)s.B * 4, false},
+                     {(const char*)W_in, state, false},      {(const char*)W_out, state, true},
+                     {(const char*)y_out, vals, true},       {(const char*)workspace, need, true}};
+  if (!disjoint(r, 10, 6, 7)) return TM_ERR_ALIAS;
+  hipError_t err = titans::launch_delta_recurrent(s, k, v, q, alpha, theta, lengths, W_in, y_out, W_out,
+                                                  (hipStream_t)stream);
+  return err == hipSuccess ? TM_OK : TM_ERR_HIP;
+}
+
+int titans_mem_group_norm(const titans_norm_desc* desc, const void* x, const void* gate, const float* weight,
+                          const float* bias, const int32_t* lengths, void* out, void* stream) {
+  NormShape s;
+  int rc = build_norm(desc, &s);
+  if (rc) return rc;
+  const int64_t C = (int64_t)s.H * s.d, all = (int64_t)s.B * s.N * C * (s.io == TM_IO_BF16 ? 2 : 4);
+  if (!needed(x, all) || !needed(out, all) || !aligned16(gate) || !aligned16(weight) || !aligned16(bias) ||
+      !aligned16(lengths))
+    return TM_ERR_INVALID;
+  const Range r[] = {{(const char*)x, all, false},        {(const char*)gate, all, false},
+                     {(const char*)weight, C * 4, false}, {(const char*)bias, C * 4, false},
+                     {(const char*)lengths, (int64_t)s.B * 4, false}, {(const char*)out, all, true}};
+  if (!disjoint(r, 6)) return TM_ERR_ALIAS;
+  if (s.N == 0) return TM_OK;
+  return titans::launch_group_norm(s, x, gate, weight, bias, lengths, out, (hipStream_t)stream) == hipSuccess
+             ? TM_OK
+             : TM_ERR_HIP;
+}
+
+int64_t titans_mem_group_norm_backward_workspace_bytes(const titans_norm_desc* desc) {
+  NormShape s;
+  int rc = build_norm(desc, &s);
+  return rc ? rc : titans::norm_backward_ws_bytes(s);
+}
+
+int titans_mem_group_norm_backward(const titans_norm_desc* desc, const void* x, const void* gate,
+                                   const float* weight, const float* bias, const int32_t* lengths, const void* dout,
+                                   void* dx, void* dgate, float* dweight, float* dbias, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+  NormShape s;
+  int rc = build_norm(desc, &s);
+  if (rc) return rc;
+  const int64_t C = (int64_t)s.H * s.d, all = (int64_t)s.B * s.N * C * (s.io == TM_IO_BF16 ? 2 : 4);
+  if (!needed(x, all) || !needed(dout, all) || !needed(dx, all) || !needed(dweight, C) || !needed(dbias, C) ||
+      !aligned16(gate) || !aligned16(dgate) || !aligned16(weight) || !aligned16(bias) || !aligned16(lengths) ||
+      !aligned16(workspace) || (all > 0 && !gate != !dgate))
+    return TM_ERR_INVALID;
+  const int64_t need = titans::norm_backward_ws_bytes(s);
+  if (!workspace || workspace_bytes < need) return TM_ERR_WORKSPACE;
+  const Range r[] = {{(const char*)x, all, false},           {(const char*)gate, all, false},
+                     {(const char*)weight, C * 4, false},    {(const char*)bias, C * 4, false},
+                     {(const char*)lengths, (int64_t)s.B * 4, false}, {(const char*)dout, all, false},
+                     {(const char*)dx, all, true},           {(const char*)dgate, all, true},
+                     {(const char*)dweight, C * 4, true},    {(const char*)dbias, C * 4, true},
+                     {(const char*)workspace, need, true}};
+  if (!disjoint(r, 11)) return TM_ERR_ALIAS;
+  return titans::launch_group_norm_backward(s, x, gate, weight, bias, lengths, dout, dx, dgate, dweight, dbias,
+                                            (float*)workspace, (hipStream_t)stream) == hipSuccess
+             ? TM_OK
+             : TM_ERR_HIP;
+}
+
 const char* titans_mem_status_string(int status) {
   switch (status) {
     case TM_OK: return "ok";

@@ -119,4 +119,31 @@ hipError_t launch_input(int B, int N, int D, int H, int d, int w, const void* x,
                         const float* conv_w, const void* w_gate, const float* b_gate, const float scale[3],
                         void* const kvq[3], float* const gates[3], hipStream_t stream);
 
+// The gated delta memory (token-exact linear memory).  W [B,H,d,d] fp32;
+// lengths may be null.  W_out == W_in is allowed.
+constexpr int kMaxWidthDelta = 128;
+struct DeltaShape {
+  int B, H, Hk, N, d, io;
+  unsigned flags;
+};
+hipError_t launch_delta_recurrent(const DeltaShape& s, const void* k, const void* v, const void* q,
+                                  const float* alpha, const float* theta, const int32_t* lengths, const float* W_in,
+                                  void* y, float* W_out, hipStream_t stream);
+
+// Group norm with an activation (one head's d channels of a token a group)
+// and its gradient.  gate, weight, bias and lengths may be null; first: x is
+// [B,H,N,d], else [B,N,H d].
+constexpr int kMaxWidthNorm = 1024;
+constexpr int kMaxHeadsNorm = 65535;   // a grid's second dimension
+struct NormShape {
+  int B, H, N, d, io, silu, first;
+  float eps;
+};
+int64_t norm_backward_ws_bytes(const NormShape& s);
+hipError_t launch_group_norm(const NormShape& s, const void* x, const void* gate, const float* weight,
+                             const float* bias, const int32_t* lengths, void* out, hipStream_t stream);
+hipError_t launch_group_norm_backward(const NormShape& s, const void* x, const void* gate, const float* weight,
+                                      const float* bias, const int32_t* lengths, const void* dout, void* dx,
+                                      void* dgate, float* dweight, float* dbias, float* ws, hipStream_t stream);
+
 }  // namespace titans

@@ -15,12 +15,14 @@ from typing import Optional, Tuple
 ABI_VERSION = 1
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_ALIAS, ERR_HIP, ERR_GAVE_UP = 0, -1, -2, -3, -4, -5, -6
 IO_F32, IO_BF16 = 0, 1
-ACT_SILU = 0
+ACT_SILU, ACT_NONE = 0, 1
 READ_AFTER_WRITE, READ_CHUNK_START = 0, 1
 FLAG_FORCE_GENERIC = 1
 FLAG_CHUNK_GATES = 2
 FLAG_NO_WAIT = 4
+FLAG_CHANNELS_LAST = 8
 PATH_GENERIC_F32, PATH_MLP2_D64_H256, PATH_DEEP_BF16 = 0, 1, 2
+PATH_DELTA_RECURRENT, PATH_DELTA_CHUNKED = 0, 1
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtitans_mem.so")
 
@@ -28,7 +30,9 @@ EXPORTS = ("titans_mem_abi_version", "titans_mem_param_count", "titans_mem_selec
            "titans_mem_workspace_bytes", "titans_mem_forward", "titans_mem_forward_noalloc",
            "titans_mem_workspace_status", "titans_mem_retrieve",
            "titans_mem_input", "titans_mem_backward", "titans_mem_backward_workspace_bytes",
-           "titans_mem_status_string")
+           "titans_mem_delta_select_path", "titans_mem_delta_workspace_bytes", "titans_mem_delta_forward",
+           "titans_mem_group_norm", "titans_mem_group_norm_backward",
+           "titans_mem_group_norm_backward_workspace_bytes", "titans_mem_status_string")
 
 
 class Desc(ctypes.Structure):
@@ -43,6 +47,27 @@ class InputDesc(ctypes.Structure):
     _fields_ = [("abi_version", ctypes.c_int32), ("B", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("D", ctypes.c_int32), ("H", ctypes.c_int32), ("d", ctypes.c_int32),
                 ("conv_width", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class DeltaDesc(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("B", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("B", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("d", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("eps", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+def make_delta_desc(B: int, H: int, Hk: int, N: int, d: int, io: str = "bf16", flags: int = 0) -> DeltaDesc:
+    return DeltaDesc(ABI_VERSION, B, H, Hk, N, d, IO_BF16 if io == "bf16" else IO_F32, flags)
+
+
+def make_norm_desc(B: int, H: int, N: int, d: int, io: str = "bf16", activation: int = ACT_SILU, eps: float = 1e-5,
+                   flags: int = 0) -> NormDesc:
+    return NormDesc(ABI_VERSION, B, H, N, d, IO_BF16 if io == "bf16" else IO_F32, activation, eps, flags)
 
 
 def make_input_desc(B: int, N: int, D: int, H: int, d: int, conv_width: int = 4, flags: int = 0) -> InputDesc:
@@ -99,6 +124,19 @@ def load():
     lib.titans_mem_input.restype = ctypes.c_int
     lib.titans_mem_input.argtypes = [ctypes.POINTER(InputDesc), vp, vp, fp, vp, fp, ctypes.c_float, ctypes.c_float,
                                      ctypes.c_float, vp, vp, vp, fp, fp, fp, vp]
+    ep, nq = ctypes.POINTER(DeltaDesc), ctypes.POINTER(NormDesc)
+    lib.titans_mem_delta_select_path.restype = i32
+    lib.titans_mem_delta_select_path.argtypes = [ep]
+    lib.titans_mem_delta_workspace_bytes.restype = i64
+    lib.titans_mem_delta_workspace_bytes.argtypes = [ep]
+    lib.titans_mem_delta_forward.restype = ctypes.c_int
+    lib.titans_mem_delta_forward.argtypes = [ep, vp, vp, vp, fp, fp, vp, fp, vp, fp, vp, i64, vp]
+    lib.titans_mem_group_norm.restype = ctypes.c_int
+    lib.titans_mem_group_norm.argtypes = [nq, vp, vp, fp, fp, vp, vp, vp]
+    lib.titans_mem_group_norm_backward_workspace_bytes.restype = i64
+    lib.titans_mem_group_norm_backward_workspace_bytes.argtypes = [nq]
+    lib.titans_mem_group_norm_backward.restype = ctypes.c_int
+    lib.titans_mem_group_norm_backward.argtypes = [nq, vp, vp, fp, fp, vp, vp, vp, vp, fp, fp, vp, i64, vp]
     lib.titans_mem_status_string.restype = ctypes.c_char_p
     lib.titans_mem_status_string.argtypes = [ctypes.c_int]
     if lib.titans_mem_abi_version() != ABI_VERSION:
@@ -162,6 +200,37 @@ def raw_input(desc: InputDesc, x, w_proj, conv_w, w_gate, b_gate, scales, k_out,
     return int(load().titans_mem_input(ctypes.byref(desc), x, w_proj, conv_w, w_gate, b_gate, float(scales[0]),
                                        float(scales[1]), float(scales[2]), k_out, v_out, q_out, alpha_out,
                                        eta_out, theta_out, stream))
+
+
+def delta_select_path(desc: DeltaDesc) -> int:
+    return int(load().titans_mem_delta_select_path(ctypes.byref(desc)))
+
+
+def delta_workspace_bytes(desc: DeltaDesc) -> int:
+    return int(load().titans_mem_delta_workspace_bytes(ctypes.byref(desc)))
+
+
+def raw_delta_forward(desc: DeltaDesc, k, v, q, alpha, theta, lengths, W_in, y_out, W_out, workspace,
+                      workspace_bytes_, stream) -> int:
+    """Direct call of titans_mem_delta_forward with integer device addresses; returns the status."""
+    return load().titans_mem_delta_forward(ctypes.byref(desc), k, v, q, alpha, theta, lengths, W_in, y_out, W_out,
+                                           workspace, workspace_bytes_, stream)
+
+
+def raw_group_norm(desc: NormDesc, x, gate, weight, bias, lengths, out, stream) -> int:
+    """Direct call of titans_mem_group_norm with integer device addresses; returns the status."""
+    return load().titans_mem_group_norm(ctypes.byref(desc), x, gate, weight, bias, lengths, out, stream)
+
+
+def group_norm_backward_workspace_bytes(desc: NormDesc) -> int:
+    return int(load().titans_mem_group_norm_backward_workspace_bytes(ctypes.byref(desc)))
+
+
+def raw_group_norm_backward(desc: NormDesc, x, gate, weight, bias, lengths, dout, dx, dgate, dweight, dbias, workspace,
+                            workspace_bytes_, stream) -> int:
+    """Direct call of titans_mem_group_norm_backward with integer device addresses; returns the status."""
+    return load().titans_mem_group_norm_backward(ctypes.byref(desc), x, gate, weight, bias, lengths, dout, dx, dgate,
+                                                 dweight, dbias, workspace, workspace_bytes_, stream)
 
 
 # ----------------------------------------------------------------------------
@@ -350,4 +419,151 @@ def backward(k, v, q, alpha, eta, theta, W_in, S_in, chunk: int, *, hidden: int,
                       _ptr(ws), need, stream)
     if rc != OK:
         raise TitansMemError(rc, "titans_mem_backward")
+    return g
+
+
+def _io_of(t) -> str:
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return "bf16"
+    if t.dtype == torch.float32:
+        return "f32"
+    raise ValueError(f"float32 or bfloat16 expected, got {t.dtype}")
+
+
+def _on_device(dev, what, fn, *args):
+    """fn(*args, stream) on torch's current stream of ``dev``, with ``dev`` current; raises on a bad status."""
+    torch = _torch()
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: tensors must be on a GPU, got {dev}")
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != OK:
+        raise TitansMemError(rc, what)
+
+
+def _workspace(workspace, need, dev, what):
+    """(tensor or None, bytes): the caller's workspace, or a new one of ``need`` bytes."""
+    if need < 0:
+        raise TitansMemError(need, what)
+    if workspace is None:
+        return (_torch().empty(need, dtype=_torch().uint8, device=dev), need) if need > 0 else (None, 0)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _check_delta(k, v, q, alpha, theta, W_in, lengths):
+    torch = _torch()
+    if k.dim() != 4 or v.dim() != 4:
+        raise ValueError("k and v must be [B, heads, N, d]")
+    B, Hk, N, d = k.shape
+    H, dev, f32 = v.shape[1], k.device, torch.float32
+    _check(v, "v", (B, H, N, d), k.dtype, dev)
+    _check(k, "k", (B, Hk, N, d), k.dtype, dev)
+    _check(q, "q", (B, Hk, N, d), k.dtype, dev)
+    _check(alpha, "alpha", (B, H, N), f32, dev)
+    _check(theta, "theta", (B, H, N), f32, dev)
+    _check(W_in, "W_in", (B, H, d, d), f32, dev)
+    if lengths is not None:
+        _check(lengths, "lengths", (B,), torch.int32, dev)
+    return B, H, Hk, N, d, dev
+
+
+def delta_forward(k, v, q, alpha, theta, W_in, *, lengths=None, force_recurrent: bool = False, y_out=None, W_out=None,
+                  workspace=None) -> Tuple:
+    """The gated delta memory over sequences or single tokens (titans_mem_delta_forward).
+
+    k, q: [B, Hk, N, d]; v: [B, H, N, d] (float32 or bfloat16, Hk divides H:
+    value head h reads key head h // (H // Hk)); alpha, theta: [B, H, N]
+    float32; W_in: [B, H, d, d] float32; lengths: [B] int32 or None.  Returns
+    (y, W_out).  A new y_out holds zeros past a sequence's length; rows of a
+    y_out that is passed in are left as they were there.
+    """
+    torch = _torch()
+    B, H, Hk, N, d, dev = _check_delta(k, v, q, alpha, theta, W_in, lengths)
+    desc = make_delta_desc(B, H, Hk, N, d, _io_of(k), FLAG_FORCE_GENERIC if force_recurrent else 0)
+    if y_out is None:
+        y_out = (torch.empty if lengths is None else torch.zeros)((B, H, N, d), dtype=k.dtype, device=dev)
+    else:
+        _check(y_out, "y_out", (B, H, N, d), k.dtype, dev)
+    if W_out is None:
+        W_out = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
+    else:
+        _check(W_out, "W_out", (B, H, d, d), torch.float32, dev)
+    ws, ws_bytes = _workspace(workspace, delta_workspace_bytes(desc), dev, "titans_mem_delta_workspace_bytes")
+    _on_device(dev, "titans_mem_delta_forward", raw_delta_forward, desc, k.data_ptr(), v.data_ptr(), q.data_ptr(),
+               alpha.data_ptr(), theta.data_ptr(), _ptr(lengths), W_in.data_ptr(), y_out.data_ptr(), W_out.data_ptr(),
+               _ptr(ws), ws_bytes)
+    return y_out, W_out
+
+
+def _check_norm(x, weight, bias, H, gate, lengths, activation, eps):
+    torch = _torch()
+    io, dev = _io_of(x), x.device
+    if x.dim() == 4:
+        B, heads, N, d = x.shape
+        if H is not None and H != heads:
+            raise ValueError(f"x has {heads} heads, H is {H}")
+        H, flags = heads, 0
+    elif x.dim() == 3 and H is not None and H > 0 and x.shape[2] % H == 0:
+        B, N, C = x.shape
+        d, flags = C // H, FLAG_CHANNELS_LAST
+    else:
+        raise ValueError("x must be [B, H, N, d], or [B, N, H*d] with H given")
+    _check(x, "x", tuple(x.shape), x.dtype, dev)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check(t, name, (H * d,), torch.float32, dev)
+    if gate is not None:
+        _check(gate, "gate", (B, N, H * d), x.dtype, dev)
+    if lengths is not None:
+        _check(lengths, "lengths", (B,), torch.int32, dev)
+    return make_norm_desc(B, H, N, d, io, activation, eps, flags), (B, N, H * d), dev
+
+
+def group_norm(x, weight=None, bias=None, *, H: Optional[int] = None, gate=None, activation: int = ACT_SILU,
+               eps: float = 1e-5, lengths=None, out=None):
+    """Group norm of each head's channels with an activation, channels-last out (titans_mem_group_norm).
+
+    x: [B, H, N, d] as the memory writes y, or [B, N, H*d] with H given
+    (float32 or bfloat16); weight, bias: [H*d] float32 or None; gate:
+    [B, N, H*d] or None.  Returns act(gate) * norm(x), or act(norm(x)) without
+    a gate, as [B, N, H*d].  A new out holds zeros past a sequence's length.
+    """
+    torch = _torch()
+    desc, shape, dev = _check_norm(x, weight, bias, H, gate, lengths, activation, eps)
+    if out is None:
+        out = (torch.empty if lengths is None else torch.zeros)(shape, dtype=x.dtype, device=dev)
+    else:
+        _check(out, "out", shape, x.dtype, dev)
+    _on_device(dev, "titans_mem_group_norm", raw_group_norm, desc, x.data_ptr(), _ptr(gate), _ptr(weight), _ptr(bias),
+               _ptr(lengths), out.data_ptr())
+    return out
+
+
+def group_norm_backward(x, weight, bias, dout, *, H: Optional[int] = None, gate=None, activation: int = ACT_SILU,
+                        eps: float = 1e-5, lengths=None, workspace=None):
+    """Gradients through group_norm() (titans_mem_group_norm_backward).
+
+    Same inputs as group_norm(); dout: [B, N, H*d] in x's type.  Returns a
+    dict: x (x's layout and type), gate (with a gate), weight, bias [H*d]
+    float32.
+    """
+    torch = _torch()
+    desc, shape, dev = _check_norm(x, weight, bias, H, gate, lengths, activation, eps)
+    _check(dout, "dout", shape, x.dtype, dev)
+    g = {"x": torch.empty_like(x)}
+    if gate is not None:
+        g["gate"] = torch.empty_like(gate)
+    g["weight"] = torch.empty(shape[2], dtype=torch.float32, device=dev)
+    g["bias"] = torch.empty(shape[2], dtype=torch.float32, device=dev)
+    ws, ws_bytes = _workspace(workspace, group_norm_backward_workspace_bytes(desc), dev,
+                              "titans_mem_group_norm_backward_workspace_bytes")
+    _on_device(dev, "titans_mem_group_norm_backward", raw_group_norm_backward, desc, x.data_ptr(), _ptr(gate),
+               _ptr(weight), _ptr(bias), _ptr(lengths), dout.data_ptr(), g["x"].data_ptr(), _ptr(g.get("gate")),
+               g["weight"].data_ptr(), g["bias"].data_ptr(), _ptr(ws), ws_bytes)
     return g

@@ -1,0 +1,178 @@
+"""The gated delta memory on the GPU against its fp64 token-by-token oracle."""
+import numpy as np
+import pytest
+
+from delta_util import check, cuda, make, tol32
+from oracle import delta_oracle as do
+
+pytestmark = pytest.mark.gpu
+
+NAMES = ("k", "v", "q", "alpha", "theta", "W_in")
+
+#         B  H  Hk N    d    io      ragged resets edge
+SHAPES = [(1, 1, 1, 1, 64, "bf16", False, False, None),
+          (2, 4, 2, 1, 128, "bf16", True, False, None),
+          (3, 2, 2, 1, 33, "f32", False, False, None),
+          (2, 2, 1, 2, 1, "f32", False, False, None),
+          (1, 3, 3, 7, 16, "bf16", False, False, None),
+          (4, 6, 2, 31, 72, "bf16", True, True, None),
+          (2, 2, 2, 32, 64, "bf16", False, False, None),
+          (2, 2, 2, 33, 64, "f32", False, False, None),
+          (1, 4, 1, 64, 128, "bf16", False, False, None),
+          (3, 4, 2, 65, 100, "f32", True, True, None),
+          (2, 3, 3, 129, 63, "bf16", True, False, None),
+          (2, 2, 1, 200, 128, "f32", True, True, None),
+          (5, 2, 2, 300, 64, "bf16", True, True, None),
+          (1, 2, 2, 1000, 64, "bf16", False, False, None),
+          (1, 1, 1, 999, 48, "f32", False, False, None),
+          (1, 2, 2, 100, 64, "bf16", False, False, "keep"),
+          (1, 2, 2, 100, 64, "bf16", False, False, "forget"),
+          (1, 2, 2, 100, 64, "f32", False, False, "still"),
+          (1, 2, 2, 100, 80, "f32", False, False, "full"),
+          (2, 2, 2, 100, 64, "f32", False, False, "strong")]
+
+
+def _oracle(f):
+    return do.delta_forward(*(f[n] for n in NAMES), f["lengths"])
+
+
+def _run(t, **kw):
+    from test_learned_neural_amd import titans_mem as tmm
+    return tmm.delta_forward(*(t[n] for n in NAMES), lengths=t["lengths"], **kw)
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward(shape, recurrent):
+    B, H, Hk, N, d, io, ragged, resets, edge = shape
+    t, f = make(11, B, H, Hk, N, d, io, ragged, resets, edge)
+    y, W = _run(cuda(t), force_recurrent=recurrent)
+    yr, Wr = _oracle(f)
+    tol = tol32(N, d)
+    print(shape, "y", check("y", y, yr, io, tol), "W", check("W", W, Wr, "f32", tol), flush=True)
+
+
+def test_rows_past_a_length_are_left_as_they_were():
+    import torch
+    t, f = make(12, 4, 2, 2, 70, 64, "bf16", lengths=[0, 70, 1, 33])
+    g = cuda(t)
+    for recurrent in (False, True):
+        y0 = torch.full((4, 2, 70, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        for name in ("k", "v", "q", "alpha", "theta"):      # what is not read may be anything
+            x = t[name].clone()
+            for b, n in enumerate(f["lengths"]):
+                x[b, :, n:] = float("nan")
+            g[name] = x.cuda()
+        y, W = _run(g, y_out=y0, force_recurrent=recurrent)
+        assert y is y0
+        yr, Wr = _oracle(f)
+        for b, n in enumerate(f["lengths"]):
+            assert (y[b, :, n:] == 7.0).all()
+            check("y", y[b:b + 1, :, :n], yr[b:b + 1, :, :n], "bf16", tol32(70, 64))
+        check("W", W, Wr, "f32", tol32(70, 64))
+        assert torch.equal(W[0], g["W_in"][0])
+
+
+def test_lengths_outside_the_range_are_clamped():
+    t, f = make(13, 3, 1, 1, 40, 64, "bf16", lengths=[-5, 1000, 40])
+    for recurrent in (False, True):
+        y, W = _run(cuda(t), force_recurrent=recurrent)
+        yr, Wr = _oracle(f)
+        check("y", y, yr, "bf16", tol32(40, 64))
+        check("W", W, Wr, "f32", tol32(40, 64))
+
+
+def test_no_tokens_copy_the_state():
+    import torch
+    t, _ = make(14, 2, 3, 3, 0, 64, "bf16")
+    g = cuda(t)
+    y, W = _run(g)
+    assert y.shape == (2, 3, 0, 64) and torch.equal(W, g["W_in"])
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_in_place_state_and_resuming(io):
+    """A sequence cut anywhere and continued in place gives the whole's result; so does token by token."""
+    import torch
+    t, f = make(15, 2, 4, 2, 150, 64, io, resets=True)
+    g = cuda(t)
+    yr, Wr = _oracle(f)
+    for cuts in ([0, 70, 71, 150], [0, 1, 33, 97, 150], list(range(140, 151))):
+        if cuts[0]:
+            cuts = [0] + cuts
+        W, ys = g["W_in"].clone(), []
+        for a, b in zip(cuts, cuts[1:]):
+            part = {n: g[n][:, :, a:b].contiguous() for n in ("k", "v", "q", "alpha", "theta")}
+            y, W1 = _run({**part, "W_in": W, "lengths": None}, W_out=W)
+            assert W1 is W
+            ys.append(y)
+        check("y", torch.cat(ys, 2), yr, io, tol32(150, 64))
+        check("W", W, Wr, "f32", tol32(150, 64))
+
+
+def test_a_nan_stays_in_its_stream():
+    import torch
+    t, f = make(16, 2, 2, 2, 90, 64, "bf16")
+    g = cuda(t)
+    g["k"][0, 1, 50, 3] = float("nan")
+    g["alpha"][1, 0, 20] = 1.5           # past its range
+    for recurrent in (False, True):
+        y, W = _run(g, force_recurrent=recurrent)
+        assert torch.isnan(W[0, 1]).any() and torch.isnan(W[1, 0]).any()
+        assert torch.isnan(y[0, 1, 60]).any() and torch.isfinite(y[0, 1, :32]).all()
+        yr, Wr = _oracle(f)
+        for b, h in ((0, 0), (1, 1)):
+            check("y", y[b:b + 1, h:h + 1], yr[b:b + 1, h:h + 1], "bf16", tol32(90, 64))
+            check("W", W[b:b + 1, h:h + 1], Wr[b:b + 1, h:h + 1], "f32", tol32(90, 64))
+
+
+@pytest.mark.parametrize("scale", [1e-12, 1e12])
+def test_scales_far_from_one(scale):
+    """k, v and W of other magnitudes: the products keep fp32's range (theta makes the step of order one)."""
+    import torch
+    t, f = make(17, 1, 2, 2, 100, 64, "f32")
+    for name, by in (("k", scale), ("v", 1 / scale), ("W_in", scale ** -2), ("theta", scale ** -2)):
+        t[name] = (t[name].double() * by).float()
+        f[name] = t[name].double().numpy()
+    y, W = _run(cuda(t))
+    yr, Wr = _oracle(f)
+    check("W", W, Wr, "f32", tol32(100, 64))
+    check("y", y, yr, "f32", tol32(100, 64))
+
+
+def test_another_stream_and_replayed_graphs():
+    """On a side stream; and captured twice with a workspace each, replayed in turn between eager work."""
+    import torch
+    t, _ = make(18, 2, 4, 4, 200, 64, "bf16", ragged=True)
+    g = cuda(t)
+    y0, W0 = _run(g)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y1, W1 = _run(g)
+    s.synchronize()
+    assert torch.equal(y0, y1) and torch.equal(W0, W1)
+    graphs = []
+    for i in range(2):
+        x = {n: None if v is None else v.clone() for n, v in g.items()}
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = _run(x)
+        graphs.append((graph, x, out))
+    for rep in range(4):
+        for i, (graph, x, out) in enumerate(graphs):
+            x["v"].copy_(g["v"] * (rep + 1 + i))
+            want = _run({**g, "v": g["v"] * (rep + 1 + i)})
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_same_bits_every_time():
+    import torch
+    t, _ = make(19, 2, 4, 2, 500, 64, "bf16")
+    g = cuda(t)
+    first = _run(g)
+    for _ in range(3):
+        again = _run(g)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
