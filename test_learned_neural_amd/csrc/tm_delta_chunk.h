@@ -1,0 +1,343 @@
+// What the chunked delta kernels share (device code only): fp32 values as
+// sums of bf16 planes, matrix-core tiles over them, and the matrices of one
+// chunk of 32 tokens.
+//
+// Chunk form.  With a_t = 1 - alpha_t, G_t = a_1..a_t within the chunk and
+// D[t,j] = G_t / G_j, the token recurrence
+//   f_t = v_t - a_t W_{t-1} k_t,  W_t = a_t W_{t-1} + theta_t f_t k_t^T
+// over a chunk that starts at W is
+//   (I + B) F = V - diag(G) K W^T,   B[t,j] = D[t,j] (k_t.k_j) theta_j,  j < t
+//   Y = diag(G) Q W^T + P F,         P[t,j] = D[t,j] (q_t.k_j) theta_j,  j <= t
+//   W' = G_C W + (diag(E theta) F)^T K,  E_j = G_C / G_j.
+// F holds the residuals themselves, so theta = 0 divides nothing.
+//
+// Decays.  D is exp2 of a difference of prefix sums of log2 a, taken in fp64
+// and kept as a pair of floats, so a difference carries no more error than
+// its own rounding however far the sums have run.  a = 0 (alpha = 1) counts
+// as log2 a = -2000: every product over it is exactly 0.
+//
+// Precision.  A float is the exact sum of three bf16 numbers (8 bits each,
+// by truncation).  A product of two floats keeps the six partial products
+// down to 2^-16 (the three dropped ones are below 2^-24 of it), a product
+// with a bf16 input, which is its own first plane, the three that exist: so
+// the bf16 matrix cores (16 times the fp32 ones' rate) give fp32 results.
+#pragma once
+
+#include "tm_internal.h"
+
+namespace titans {
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
+constexpr int kC = 32;          // tokens per chunk
+constexpr int kCS = kC + 8;     // row stride of a [32][32] plane, in bf16
+constexpr int kBS = kC + 4;     // row stride of the fp32 scratch
+
+__device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+__device__ __forceinline__ float flt(uint32_t x) { return __builtin_bit_cast(float, x); }
+__device__ __forceinline__ float top(float x) { return flt(bits(x) & 0xffff0000u); }
+// the bf16 halves of two floats side by side
+__device__ __forceinline__ uint32_t tops(float a, float b) { return __builtin_amdgcn_perm(bits(b), bits(a), 0x07060302u); }
+
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// A 16x16 accumulator tile has column l % 16 and rows 4 (l / 16) + 0..3 in
+// lane l; an operand has 8 contraction indices a lane.  Two stacked tiles are
+// therefore an operand over 32 rows without a move, if both operands run
+// through those rows in the order 4g..4g+3, 16+4g..16+4g+3 for lane group g.
+// Every 32-long contraction axis in LDS is stored in that order, so that an
+// operand is one 16-byte read: element e of the axis lies at perm32(e).
+__device__ __forceinline__ constexpr int perm32(int e) { return ((e & 15) >> 2) * 8 + (e >> 4) * 4 + (e & 3); }
+
+// Two stacked tiles as NP planes of one operand.
+template <int NP>
+__device__ __forceinline__ void split8(const f32x4& a, const f32x4& b, bf16x8 (&out)[NP]) {
+  float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const u32x4 u = {tops(x[0], x[1]), tops(x[2], x[3]), tops(x[4], x[5]), tops(x[6], x[7])};
+    out[p] = __builtin_bit_cast(bf16x8, u);
+    if (p + 1 < NP) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] -= top(x[i]);
+    }
+  }
+}
+
+// Four consecutive values of one row to NP planes in LDS.
+template <int NP>
+__device__ __forceinline__ void put4(uint16_t* at, int plane, float x0, float x1, float x2, float x3) {
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    *(uint2*)(at + p * plane) = make_uint2(tops(x0, x1), tops(x2, x3));
+    x0 -= top(x0), x1 -= top(x1), x2 -= top(x2), x3 -= top(x3);
+  }
+}
+
+// c += A B over one 32-long step, A in NA planes (from LDS, `plane` apart), B in NB; the products kept are those of
+// planes i + j < max(NA, NB), smallest first.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mul(const uint16_t* a, int plane, const bf16x8 (&b)[NB], f32x4 c) {
+  constexpr int kMost = NA > NB ? NA : NB;
+  bf16x8 av[NA];
+#pragma unroll
+  for (int i = 0; i < NA; ++i) av[i] = *(const bf16x8*)(a + i * plane);
+#pragma unroll
+  for (int o = kMost - 1; o >= 0; --o)
+#pragma unroll
+    for (int i = NA - 1; i >= 0; --i)
+      if (o - i >= 0 && o - i < NB) c = mfma(av[i], b[o - i], c);
+  return c;
+}
+
+// The operand A[m][k] of a [k][m] array (row stride rs in bf16, k = 32 tokens in their natural row order, m0 the tile's
+// first column): the hardware's transposing read gives a group of 16 lanes 4 rows by 16 columns, a column per lane.
+__device__ __forceinline__ bf16x8 read_transposed(const uint16_t* base, int rs, int m0, int lane) {
+  typedef __attribute__((address_space(3))) bf16x4 lds4;
+  const int g = lane >> 4, i = lane & 15;
+  // columns 4c..4c+3 of a permuted row are contiguous, at perm32
+  const int col = m0 + 4 * (i & 3), at = (col & ~31) + perm32(col & 31);
+  const uint16_t* p0 = base + (4 * g + (i >> 2)) * rs + at;
+  const bf16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)p0);
+  const bf16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(p0 + 16 * rs));
+  return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Orders a wave's own LDS traffic between lanes.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// log2(1 - alpha); alpha = 1: -2000; above 1: NaN
+__device__ __forceinline__ float log2_keep(float alpha) {
+  const float x = log1pf(-alpha) * 1.44269504088896f;
+  return x < -2000.f ? -2000.f : x;
+}
+
+// LDS of one chunk: NP planes of K and Q, three of T = (I + B)^-1, NPP of P,
+// and per-token factors.  T's upper right block is zeroed once.
+template <int DP, int NP, int NPP>
+struct ChunkLds {
+  static constexpr int RS = DP + 8;                 // row stride of K and Q in bf16
+  static constexpr int KP = kC * RS, CP = kC * kCS; // plane sizes
+  static constexpr int OFF_K = 0, OFF_Q = OFF_K + NP * KP * 2, OFF_T = OFF_Q + NP * KP * 2, OFF_P = OFF_T + 3 * CP * 2,
+                       OFF_G = OFF_P + NPP * CP * 2, BYTES = OFF_G + (2 * kC + 4) * 4;
+  static_assert(NPP * CP * 2 >= kC * kBS * 4, "the fp32 scratch lies where P comes to lie");
+  static_assert(16 * kCS * 2 >= 3 * kC * 4, "the gates' scratch lies in T's lower half");
+  unsigned char* base;
+  __device__ uint16_t* k() const { return (uint16_t*)(base + OFF_K); }
+  __device__ uint16_t* q() const { return (uint16_t*)(base + OFF_Q); }
+  __device__ uint16_t* t() const { return (uint16_t*)(base + OFF_T); }
+  __device__ uint16_t* p() const { return (uint16_t*)(base + OFF_P); }
+  __device__ float* g() const { return (float*)(base + OFF_G); }          // G_t
+  __device__ float* eth() const { return (float*)(base + OFF_G) + kC; }   // E_j theta_j over theta's scale
+  __device__ float* gc() const { return (float*)(base + OFF_G) + 2 * kC; }   // G_C, and theta's scale (a power of two)
+  __device__ float* scratch() const { return (float*)(base + OFF_P); }    // [32][kBS]
+  __device__ float* gates() const { return (float*)(base + OFF_T + 16 * kCS * 2); }   // log2 G (hi, lo), theta
+};
+
+// Raw rows of a chunk's K or Q on their way from global memory to LDS: the
+// loads of a later chunk are in flight while this one is computed.
+// F32: fp32 input.  VB: bytes of the pieces that rows consist of and are
+// aligned for (16 or 8); 0: any row, element by element and not ahead of
+// time (such rows are rare, and their registers would be many).
+template <int DP, bool F32, int VB>
+struct RowLoad {
+  static constexpr int PER = VB ? VB / (F32 ? 4 : 2) : 4;    // elements per piece
+  static constexpr int PIECES = kC * DP / PER / 64;          // per lane
+  static constexpr int RS = DP + 8, KP = kC * RS;
+  uint32_t raw[VB ? PIECES : 1][VB ? VB / 4 : 1];
+  const void* src;
+  int64_t row0;
+  int n, d;
+  // rows r0 .. r0 + rows - 1 of [.., width]; the others, and columns past the width, are zero
+  __device__ __forceinline__ void load(const void* from, int64_t r0, int rows, int width, int lane) {
+    src = from, row0 = r0, n = rows, d = width;
+    if constexpr (VB > 0) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
+#pragma unroll
+        for (int j = 0; j < VB / 4; ++j) raw[i][j] = 0;
+        if (r >= n || c >= d) continue;
+        const char* at = (const char*)src + ((row0 + r) * d + c) * (F32 ? 4 : 2);
+        if constexpr (VB == 16) {
+          const u32x4 x = *(const u32x4*)at;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) raw[i][j] = x[j];
+        } else {
+          const uint2 x = *(const uint2*)at;
+          raw[i][0] = x.x, raw[i][1] = x.y;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* dst, int lane) const {
+    if constexpr (VB > 0) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
+        uint16_t* at = dst + r * RS + (c & ~31);
+        if constexpr (F32) {
+          put4<3>(at + perm32(c & 31), KP, flt(raw[i][0]), flt(raw[i][1]), flt(raw[i][2]), flt(raw[i][3]));
+        } else {
+          *(uint2*)(at + perm32(c & 31)) = make_uint2(raw[i][0], raw[i][1]);
+          if constexpr (VB == 16) *(uint2*)(at + perm32((c + 4) & 31)) = make_uint2(raw[i][2], raw[i][3]);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < PIECES; ++i) {
+        const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (r < n && c + j < d) {
+            const int64_t at = (row0 + r) * d + c + j;
+            x[j] = F32 ? ((const float*)src)[at] : flt((uint32_t)((const uint16_t*)src)[at] << 16);
+          }
+        put4<F32 ? 3 : 1>(dst + r * RS + (c & ~31) + perm32(c & 31), KP, x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+};
+
+// One wave builds a chunk's matrices in LDS from its K and Q (already stored)
+// and its gates (lane t < 32: token t's log2 a and theta; 0 past the end).
+template <int DP, int NP, int NPP>
+__device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP>& L, float la, float th, int lane) {
+  using Lds = ChunkLds<DP, NP, NPP>;
+  const int g = lane >> 4, li = lane & 15;
+  // prefix sums of log2 a in fp64, over lanes 0..31 (32..63 run along)
+  double sum = lane < kC ? (double)la : 0.0;
+#pragma unroll
+  for (int m = 1; m < kC; m *= 2) {
+    const double up = __shfl_up(sum, m, 32);
+    if ((lane & 31) >= m) sum += up;
+  }
+  const double all = __shfl(sum, kC - 1, 64);
+  const float hi = (float)sum;
+  // E theta f is split into planes, whose last bits lie 2^-24 below it: where theta alone would bring them near the
+  // least fp32 exponent (or theta f near the largest), a power of two is taken out of theta
+  float most = fabsf(th);
+#pragma unroll
+  for (int m = 1; m < kC; m *= 2) most = fmaxf(most, __shfl_xor(most, m, 32));
+  int e = most > 0.f && most < 3.0e38f ? ilogbf(most) : 0;
+  e = abs(e) <= 40 ? 0 : min(max(e, -100), 100);
+  const float scale = __shfl(ldexpf(1.f, e), 0, 64);
+  float* gs = L.gates();
+  if (lane < kC) {
+    gs[lane] = hi;
+    gs[kC + lane] = (float)(sum - (double)hi);
+    gs[2 * kC + lane] = th;
+    L.g()[lane] = exp2f(hi);
+    L.eth()[lane] = exp2f((float)(all - sum)) * (th / scale);
+    if (lane == 0) L.gc()[0] = exp2f((float)all), L.gc()[1] = scale;
+  }
+  wave_fence();
+  // K K^T and K Q^T by 16x16 tiles (j rows, t columns), j tile <= t tile:
+  // 0: j 0 t 0, 1: j 0 t 1, 2: j 1 t 1
+  f32x4 kk[3], qk[3];
+#pragma unroll
+  for (int x = 0; x < 3; ++x) kk[x] = qk[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < DP / 32; ++s) {
+    const int at = li * Lds::RS + 32 * s + 8 * g;
+    bf16x8 k1[NP], q0[NP], q1[NP], k0[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      k0[i] = *(const bf16x8*)(L.k() + i * Lds::KP + at);
+      k1[i] = *(const bf16x8*)(L.k() + i * Lds::KP + 16 * Lds::RS + at);
+      q0[i] = *(const bf16x8*)(L.q() + i * Lds::KP + at);
+      q1[i] = *(const bf16x8*)(L.q() + i * Lds::KP + 16 * Lds::RS + at);
+    }
+#pragma unroll
+    for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+      for (int i = o; i >= 0; --i) {
+        kk[0] = mfma(k0[i], k0[o - i], kk[0]);
+        kk[1] = mfma(k0[i], k1[o - i], kk[1]);
+        kk[2] = mfma(k1[i], k1[o - i], kk[2]);
+        qk[0] = mfma(k0[i], q0[o - i], qk[0]);
+        qk[1] = mfma(k0[i], q1[o - i], qk[1]);
+        qk[2] = mfma(k1[i], q1[o - i], qk[2]);
+      }
+  }
+  // lane: token t = 16 tt + li, tokens j = 16 jt + 4 g + 0..3
+  float* sc = L.scratch();
+#pragma unroll
+  for (int x = 0; x < 3; ++x) {
+    const int tt = x > 0, jt = x > 1, t = 16 * tt + li, j0 = 16 * jt + 4 * g;
+    const float th_ = gs[t], tl = gs[kC + t];
+    const f32x4 jh = *(const f32x4*)(gs + j0), jl = *(const f32x4*)(gs + kC + j0), tj = *(const f32x4*)(gs + 2 * kC + j0);
+    f32x4 b;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float D = exp2f((th_ - jh[r]) + (tl - jl[r])) * tj[r];
+      b[r] = t > j0 + r ? D * kk[x][r] : 0.f;
+      qk[x][r] = t >= j0 + r ? D * qk[x][r] : 0.f;
+    }
+    *(f32x4*)(sc + t * kBS + j0) = b;
+  }
+  wave_fence();
+  // the two diagonal blocks' inverses: lane (block, column) by forward
+  // substitution down the rows (stable for any B)
+  {
+    const int o = 16 * (g & 1);
+    float T[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float s0 = r == li ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < r; j += 4) {
+        const f32x4 b = *(const f32x4*)(sc + (o + r) * kBS + o + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < r) {
+            if (e & 1)
+              s1 = fmaf(-b[e], T[j + e], s1);
+            else
+              s0 = fmaf(-b[e], T[j + e], s0);
+          }
+      }
+      T[r] = s0 + s1;
+    }
+    wave_fence();
+    if (lane < 32) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sc[(o + r) * kBS + o + li] = T[r];
+    }
+  }
+  wave_fence();
+  // T10^T = -T00^T (B10^T T11^T) in fp32 matrix instructions; the inner
+  // product's tile is the second one's operand over rows 4 g + r
+  f32x4 x = {0.f, 0.f, 0.f, 0.f}, t10 = x;
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    x = __builtin_amdgcn_mfma_f32_16x16x4f32(sc[(16 + 4 * s + g) * kBS + li], sc[(16 + li) * kBS + 16 + 4 * s + g], x, 0, 0, 0);
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    t10 = __builtin_amdgcn_mfma_f32_16x16x4f32(sc[(4 * g + r) * kBS + li], x[r], t10, 0, 0, 0);
+  const f32x4 t00 = *(const f32x4*)(sc + li * kBS + 4 * g), t11 = *(const f32x4*)(sc + (16 + li) * kBS + 16 + 4 * g);
+  wave_fence();
+  uint16_t* T = L.t() + li * kCS + 8 * g;
+  put4<3>(T, Lds::CP, t00[0], t00[1], t00[2], t00[3]);
+  put4<3>(T + 16 * kCS, Lds::CP, -t10[0], -t10[1], -t10[2], -t10[3]);
+  put4<3>(T + 16 * kCS + 4, Lds::CP, t11[0], t11[1], t11[2], t11[3]);
+  uint16_t* P = L.p() + li * kCS + 8 * g;
+  put4<NPP>(P, Lds::CP, qk[0][0], qk[0][1], qk[0][2], qk[0][3]);
+  put4<NPP>(P + 4, Lds::CP, 0.f, 0.f, 0.f, 0.f);
+  put4<NPP>(P + 16 * kCS, Lds::CP, qk[1][0], qk[1][1], qk[1][2], qk[1][3]);
+  put4<NPP>(P + 16 * kCS + 4, Lds::CP, qk[2][0], qk[2][1], qk[2][2], qk[2][3]);
+}
+
+}  // namespace
+}  // namespace titans

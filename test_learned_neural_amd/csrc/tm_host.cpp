@@ -386,7 +386,10 @@ int build_norm(const titans_norm_desc* desc, NormShape* s) {
   return TM_OK;
 }
 
-int delta_path(const DeltaShape&) { return TM_PATH_DELTA_RECURRENT; }
+int delta_path(const DeltaShape& s) {
+  if ((s.flags & TM_FLAG_FORCE_GENERIC) || s.N < titans::kMinTokensDeltaChunked) return TM_PATH_DELTA_RECURRENT;
+  return TM_PATH_DELTA_CHUNKED;
+}
 
 // a pointer that must be there (unless its buffer is empty) / may be NULL
 bool needed(const void* p, int64_t bytes) { return aligned16(p) && (p || bytes == 0); }
@@ -438,8 +441,8 @@ int titans_mem_delta_forward(const titans_delta_desc* desc, const void* k, const
                      {(const char*)W_in, state, false},      {(const char*)W_out, state, true},
                      {(const char*)y_out, vals, true},       {(const char*)workspace, need, true}};
   if (!disjoint(r, 10, 6, 7)) return TM_ERR_ALIAS;
-  hipError_t err = titans::launch_delta_recurrent(s, k, v, q, alpha, theta, lengths, W_in, y_out, W_out,
-                                                  (hipStream_t)stream);
+  const auto launch = delta_path(s) == TM_PATH_DELTA_CHUNKED ? titans::launch_delta_chunked : titans::launch_delta_recurrent;
+  hipError_t err = launch(s, k, v, q, alpha, theta, lengths, W_in, y_out, W_out, (hipStream_t)stream);
   return err == hipSuccess ? TM_OK : TM_ERR_HIP;
 }
 

@@ -129,6 +129,11 @@ struct DeltaShape {
 hipError_t launch_delta_recurrent(const DeltaShape& s, const void* k, const void* v, const void* q,
                                   const float* alpha, const float* theta, const int32_t* lengths, const float* W_in,
                                   void* y, float* W_out, hipStream_t stream);
+// Chunks of 32 tokens on the matrix cores, for sequences.
+constexpr int kMinTokensDeltaChunked = 24;
+hipError_t launch_delta_chunked(const DeltaShape& s, const void* k, const void* v, const void* q, const float* alpha,
+                                const float* theta, const int32_t* lengths, const float* W_in, void* y, float* W_out,
+                                hipStream_t stream);
 
 // Group norm with an activation (one head's d channels of a token a group)
 // and its gradient.  gate, weight, bias and lengths may be null; first: x is
