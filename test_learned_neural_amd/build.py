@@ -31,7 +31,7 @@ DEVICE = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang", "-p
 
 # MFMA results in VGPRs: the MFMA kernel post-processes every accumulator on
 # the VALU and keeps the memory state in VGPRs
-PER_FILE = {"tm_mlp2_group.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+PER_FILE = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for f in ("tm_mlp2_group.hip", "tm_delta_chunk.hip")}
 
 
 def hipcc() -> str:

@@ -116,6 +116,24 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// 2^x in one instruction, 0 below 2^-126
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// a double moved by a DPP control (0 where no lane supplies it), and one lane's
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_f64(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // log2(1 - alpha); alpha = 1: -2000; above 1: NaN
 __device__ __forceinline__ float log2_keep(float alpha) {
   const float x = log1pf(-alpha) * 1.44269504088896f;
@@ -165,10 +183,8 @@ struct RowLoad {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
         const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
-#pragma unroll
-        for (int j = 0; j < VB / 4; ++j) raw[i][j] = 0;
-        if (r >= n || c >= d) continue;
-        const char* at = (const char*)src + ((row0 + r) * d + c) * (F32 ? 4 : 2);
+        // a clamped address, and zeros by selection when stored: no branch between the loads
+        const char* at = (const char*)src + (row0 * d + (int64_t)(min(r, n - 1) * d + min(c, d - PER))) * (F32 ? 4 : 2);
         if constexpr (VB == 16) {
           const u32x4 x = *(const u32x4*)at;
 #pragma unroll
@@ -186,11 +202,15 @@ struct RowLoad {
       for (int i = 0; i < PIECES; ++i) {
         const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
         uint16_t* at = dst + r * RS + (c & ~31);
+        const bool in = r < n && c < d;
+        uint32_t x[VB / 4];
+#pragma unroll
+        for (int j = 0; j < VB / 4; ++j) x[j] = in ? raw[i][j] : 0u;
         if constexpr (F32) {
-          put4<3>(at + perm32(c & 31), KP, flt(raw[i][0]), flt(raw[i][1]), flt(raw[i][2]), flt(raw[i][3]));
+          put4<3>(at + perm32(c & 31), KP, flt(x[0]), flt(x[1]), flt(x[2]), flt(x[3]));
         } else {
-          *(uint2*)(at + perm32(c & 31)) = make_uint2(raw[i][0], raw[i][1]);
-          if constexpr (VB == 16) *(uint2*)(at + perm32((c + 4) & 31)) = make_uint2(raw[i][2], raw[i][3]);
+          *(uint2*)(at + perm32(c & 31)) = make_uint2(x[0], x[1]);
+          if constexpr (VB == 16) *(uint2*)(at + perm32((c + 4) & 31)) = make_uint2(x[2], x[3]);
         }
       }
     } else {
@@ -216,31 +236,34 @@ template <int DP, int NP, int NPP>
 __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP>& L, float la, float th, int lane) {
   using Lds = ChunkLds<DP, NP, NPP>;
   const int g = lane >> 4, li = lane & 15;
-  // prefix sums of log2 a in fp64, over lanes 0..31 (32..63 run along)
-  double sum = lane < kC ? (double)la : 0.0;
-#pragma unroll
-  for (int m = 1; m < kC; m *= 2) {
-    const double up = __shfl_up(sum, m, 32);
-    if ((lane & 31) >= m) sum += up;
-  }
-  const double all = __shfl(sum, kC - 1, 64);
+  // prefix sums of log2 a in fp64 over lanes 0..31, by DPP (16 lanes a row)
+  double sum = la;
+  sum += dpp_f64<0x111>(sum);
+  sum += dpp_f64<0x112>(sum);
+  sum += dpp_f64<0x114>(sum);
+  sum += dpp_f64<0x118>(sum);
+  const double half = lane_f64(sum, 15);
+  if (lane >= 16) sum += half;
+  const double all = lane_f64(sum, kC - 1);
   const float hi = (float)sum;
   // E theta f is split into planes, whose last bits lie 2^-24 below it: where theta alone would bring them near the
   // least fp32 exponent (or theta f near the largest), a power of two is taken out of theta
-  float most = fabsf(th);
+  float scale = 1.f;
+  const float size = lane < kC ? fabsf(th) : 0.f;
+  if (__ballot(size > 0x1p40f) || (!__ballot(size >= 0x1p-40f) && __ballot(size > 0.f))) {
+    float most = size;
 #pragma unroll
-  for (int m = 1; m < kC; m *= 2) most = fmaxf(most, __shfl_xor(most, m, 32));
-  int e = most > 0.f && most < 3.0e38f ? ilogbf(most) : 0;
-  e = abs(e) <= 40 ? 0 : min(max(e, -100), 100);
-  const float scale = __shfl(ldexpf(1.f, e), 0, 64);
+    for (int m = 1; m < 64; m *= 2) most = fmaxf(most, __shfl_xor(most, m, 64));
+    scale = most < 3.0e38f ? ldexpf(1.f, min(max(ilogbf(most), -100), 100)) : 1.f;
+  }
   float* gs = L.gates();
   if (lane < kC) {
     gs[lane] = hi;
     gs[kC + lane] = (float)(sum - (double)hi);
     gs[2 * kC + lane] = th;
-    L.g()[lane] = exp2f(hi);
-    L.eth()[lane] = exp2f((float)(all - sum)) * (th / scale);
-    if (lane == 0) L.gc()[0] = exp2f((float)all), L.gc()[1] = scale;
+    L.g()[lane] = exp2_of(hi);
+    L.eth()[lane] = exp2_of((float)(all - sum)) * (th * (1.f / scale));
+    if (lane == 0) L.gc()[0] = exp2_of((float)all), L.gc()[1] = scale;
   }
   wave_fence();
   // K K^T and K Q^T by 16x16 tiles (j rows, t columns), j tile <= t tile:
@@ -281,7 +304,7 @@ __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP>& L, floa
     f32x4 b;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float D = exp2f((th_ - jh[r]) + (tl - jl[r])) * tj[r];
+      const float D = exp2_of((th_ - jh[r]) + (tl - jl[r])) * tj[r];
       b[r] = t > j0 + r ? D * kk[x][r] : 0.f;
       qk[x][r] = t >= j0 + r ? D * qk[x][r] : 0.f;
     }
@@ -292,21 +315,21 @@ __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP>& L, floa
   // substitution down the rows (stable for any B)
   {
     const int o = 16 * (g & 1);
+    f32x4 B[16][4];   // row r's first r entries, all read before the first is used
+#pragma unroll
+    for (int r = 1; r < 16; ++r)
+#pragma unroll
+      for (int j = 0; j < r; j += 4) B[r][j / 4] = *(const f32x4*)(sc + (o + r) * kBS + o + j);
     float T[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       float s0 = r == li ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-      for (int j = 0; j < r; j += 4) {
-        const f32x4 b = *(const f32x4*)(sc + (o + r) * kBS + o + j);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + e < r) {
-            if (e & 1)
-              s1 = fmaf(-b[e], T[j + e], s1);
-            else
-              s0 = fmaf(-b[e], T[j + e], s0);
-          }
+      for (int j = 0; j < r; ++j) {
+        if (j & 1)
+          s1 = fmaf(-B[r][j / 4][j % 4], T[j], s1);
+        else
+          s0 = fmaf(-B[r][j / 4][j % 4], T[j], s0);
       }
       T[r] = s0 + s1;
     }

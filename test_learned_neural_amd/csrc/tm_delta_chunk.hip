@@ -97,30 +97,33 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
       }
     }
   }
-  const int64_t vbase = (int64_t)s * p.N * d + col;
-  float vr[PW][8];
+  const int64_t vbase = (int64_t)s * p.N * d + min(col, d - 1);
+  uint32_t vr[PW][8];
   auto fetch_v = [&](int step) {
 #pragma unroll
     for (int x = 0; x < PW; ++x)
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         const int t = (step * PW + x) * kC + (r >> 2) * 16 + 4 * g + (r & 3);
-        float v = 0.f;
-        if (live && t < n) {
-          const int64_t at = vbase + (int64_t)t * d;
-          v = F32 ? ((const float*)p.v)[at] : flt((uint32_t)((const uint16_t*)p.v)[at] << 16);
-        }
-        vr[x][r] = v;
+        // a clamped address (no branch between the loads); what lies past the end is zeroed when used
+        const int64_t at = vbase + (int64_t)min(t, n - 1) * d;
+        if constexpr (F32)
+          vr[x][r] = ((const uint32_t*)p.v)[at];
+        else
+          vr[x][r] = ((const uint16_t*)p.v)[at];
       }
   };
-  fetch_v(0);
+  if (n > 0) fetch_v(0);
   __syncthreads();
   for (int i = 0; i < steps; ++i) {
     float v[PW][8];
 #pragma unroll
     for (int x = 0; x < PW; ++x)
 #pragma unroll
-      for (int r = 0; r < 8; ++r) v[x][r] = vr[x][r];
+      for (int r = 0; r < 8; ++r) {
+        const int t = (i * PW + x) * kC + (r >> 2) * 16 + 4 * g + (r & 3);
+        v[x][r] = live && t < n ? flt(F32 ? vr[x][r] : vr[x][r] << 16) : 0.f;
+      }
     fetch_v(i + 1);
 #pragma unroll
     for (int x = 0; x < PW; ++x) {
@@ -183,6 +186,7 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
         }
       }
       // Y = diag(G) Q W^T + P F
+      f32x4 out[2];
       bf16x8 fp[NS];
       split8<NS>(F[0], F[1], fp);
 #pragma unroll
@@ -192,16 +196,24 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
         for (int r = 0; r < 4; ++r) y[r] = G[rt][r] * qs[rt][r];
         y = mul<NPP, NS>(pa + rt * 16 * kCS, Lds::CP, fp, y);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = t0 + 16 * rt + 4 * g + r;
-          if (live && t < n) {
-            const int64_t at = vbase + (int64_t)t * d;
-            if (F32)
-              ((float*)p.y)[at] = y[r];
-            else
-              ((uint16_t*)p.y)[at] = __builtin_bit_cast(uint16_t, (__bf16)y[r]);
-          }
+        for (int r = 0; r < 4; ++r) out[rt][r] = y[r];
+      }
+      auto store = [&](int rt, int r) {
+        const int64_t at = vbase + (int64_t)(t0 + 16 * rt + 4 * g + r) * d;
+        if (F32)
+          ((float*)p.y)[at] = out[rt][r];
+        else
+          ((uint16_t*)p.y)[at] = __builtin_bit_cast(uint16_t, (__bf16)out[rt][r]);
+      };
+      if (t0 + kC <= n) {   // a whole chunk: one branch
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) store(e >> 2, e & 3);
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (live && t0 + 16 * (e >> 2) + 4 * g + (e & 3) < n) store(e >> 2, e & 3);
       }
     }
     __syncthreads();
