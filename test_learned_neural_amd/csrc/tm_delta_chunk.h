@@ -80,20 +80,26 @@ __device__ __forceinline__ void put4(uint16_t* at, int plane, float x0, float x1
   }
 }
 
-// c += A B over one 32-long step, A in NA planes (from LDS, `plane` apart), B in NB; the products kept are those of
-// planes i + j < max(NA, NB), smallest first.
+// c += A B over one 32-long step for two row tiles of A (the second `step`
+// further on), A in NA planes (from LDS, `plane` apart), B in NB; the products
+// kept are those of planes i + j < max(NA, NB), smallest first, the two tiles'
+// accumulation chains in turn.
 template <int NA, int NB>
-__device__ __forceinline__ f32x4 mul(const uint16_t* a, int plane, const bf16x8 (&b)[NB], f32x4 c) {
+__device__ __forceinline__ void mul2(const uint16_t* a, int plane, int step, const bf16x8 (&b)[NB], f32x4 (&c)[2]) {
   constexpr int kMost = NA > NB ? NA : NB;
-  bf16x8 av[NA];
+  bf16x8 av[2][NA];
 #pragma unroll
-  for (int i = 0; i < NA; ++i) av[i] = *(const bf16x8*)(a + i * plane);
+  for (int i = 0; i < NA; ++i)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) av[t][i] = *(const bf16x8*)(a + i * plane + t * step);
 #pragma unroll
   for (int o = kMost - 1; o >= 0; --o)
 #pragma unroll
     for (int i = NA - 1; i >= 0; --i)
-      if (o - i >= 0 && o - i < NB) c = mfma(av[i], b[o - i], c);
-  return c;
+      if (o - i >= 0 && o - i < NB) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) c[t] = mfma(av[t][i], b[o - i], c[t]);
+      }
 }
 
 // The operand A[m][k] of a [k][m] array (row stride rs in bf16, k = 32 tokens in their natural row order, m0 the tile's
@@ -173,39 +179,49 @@ struct RowLoad {
   static constexpr int PIECES = kC * DP / PER / 64;          // per lane
   static constexpr int RS = DP + 8, KP = kC * RS;
   uint32_t raw[VB ? PIECES : 1][VB ? VB / 4 : 1];
-  const void* src;
-  int64_t row0;
+  const char* src;
   int n, d;
-  // rows r0 .. r0 + rows - 1 of [.., width]; the others, and columns past the width, are zero
-  __device__ __forceinline__ void load(const void* from, int64_t r0, int rows, int width, int lane) {
-    src = from, row0 = r0, n = rows, d = width;
+  // rows 0 .. rows - 1 at `from`, of `width` elements; the other rows and columns are zero
+  __device__ __forceinline__ void load(const char* from, int rows, int width, int lane) {
+    src = from, n = rows, d = width;
     if constexpr (VB > 0) {
+      if (n == kC && d == DP) {   // offsets that no chunk changes
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
-        // a clamped address, and zeros by selection when stored: no branch between the loads
-        const char* at = (const char*)src + (row0 * d + (int64_t)(min(r, n - 1) * d + min(c, d - PER))) * (F32 ? 4 : 2);
-        if constexpr (VB == 16) {
-          const u32x4 x = *(const u32x4*)at;
+        for (int i = 0; i < PIECES; ++i) take(i, (i * 64 + lane) * VB);
+      } else {   // clamped addresses: no branch between the loads
 #pragma unroll
-          for (int j = 0; j < 4; ++j) raw[i][j] = x[j];
-        } else {
-          const uint2 x = *(const uint2*)at;
-          raw[i][0] = x.x, raw[i][1] = x.y;
+        for (int i = 0; i < PIECES; ++i) {
+          const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
+          take(i, (min(r, n - 1) * d + min(c, d - PER)) * (F32 ? 4 : 2));
         }
       }
     }
   }
-  __device__ __forceinline__ void store(uint16_t* dst, int lane) const {
+  __device__ __forceinline__ void take(int i, int at) {
+    if constexpr (VB == 16) {
+      const u32x4 x = *(const u32x4*)(src + (uint32_t)at);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) raw[i][j] = x[j];
+    } else {
+      const uint2 x = *(const uint2*)(src + (uint32_t)at);
+      raw[i][0] = x.x, raw[i][1] = x.y;
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* dst, int lane) {
     if constexpr (VB > 0) {
+      if (n != kC || d != DP) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+          const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
+#pragma unroll
+          for (int j = 0; j < VB / 4; ++j) raw[i][j] = r < n && c < d ? raw[i][j] : 0u;
+        }
+      }
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
         const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
         uint16_t* at = dst + r * RS + (c & ~31);
-        const bool in = r < n && c < d;
-        uint32_t x[VB / 4];
-#pragma unroll
-        for (int j = 0; j < VB / 4; ++j) x[j] = in ? raw[i][j] : 0u;
+        const auto& x = raw[i];
         if constexpr (F32) {
           put4<3>(at + perm32(c & 31), KP, flt(x[0]), flt(x[1]), flt(x[2]), flt(x[3]));
         } else {
@@ -221,7 +237,7 @@ struct RowLoad {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (r < n && c + j < d) {
-            const int64_t at = (row0 + r) * d + c + j;
+            const int at = r * d + c + j;
             x[j] = F32 ? ((const float*)src)[at] : flt((uint32_t)((const uint16_t*)src)[at] << 16);
           }
         put4<F32 ? 3 : 1>(dst + r * RS + (c & ~31) + perm32(c & 31), KP, x[0], x[1], x[2], x[3]);

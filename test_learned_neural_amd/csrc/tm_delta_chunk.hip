@@ -28,7 +28,7 @@ struct ChainParams {
 template <int DP, bool F32, int CW, int PW, int VB>
 __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams p) {
   constexpr int NP = F32 ? 3 : 1, NPP = F32 ? 3 : 2, NS = F32 ? 3 : 2;   // planes: inputs, P, and W and F for y
-  constexpr int NT = DP / 16, NK = DP / 32;
+  constexpr int NT = DP / 16, NK = DP / 32, kE = F32 ? 4 : 2;
   using Lds = ChunkLds<DP, NP, NPP>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
@@ -55,8 +55,8 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
     auto fetch = [&](int c) {
       const int t0 = c * kC, m = min(kC, n - t0);
       if (m <= 0) return;
-      kr.load(p.k, krow + t0, m, d, lane);
-      qr.load(p.q, krow + t0, m, d, lane);
+      kr.load((const char*)p.k + (krow + t0) * d * kE, m, d, lane);
+      qr.load((const char*)p.q + (krow + t0) * d * kE, m, d, lane);
       al = lane < m ? alpha[t0 + lane] : 0.f;
       th = lane < m ? theta[t0 + lane] : 0.f;
     };
@@ -97,21 +97,31 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
       }
     }
   }
-  const int64_t vbase = (int64_t)s * p.N * d + min(col, d - 1);
+  // v and y: a uniform address per chunk and this lane's offsets within it
+  const char* vsrc = (const char*)p.v + (int64_t)s * p.N * d * kE;
+  char* ydst = (char*)p.y + (int64_t)s * p.N * d * kE;
+  uint32_t off[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) off[r] = ((16 * (r >> 2) + 4 * g + (r & 3)) * d + min(col, d - 1)) * kE;
   uint32_t vr[PW][8];
+  // Rows past the end read the last token's v: their K, theta and so their
+  // effect is zero.
   auto fetch_v = [&](int step) {
 #pragma unroll
-    for (int x = 0; x < PW; ++x)
+    for (int x = 0; x < PW; ++x) {
+      const int t0 = (step * PW + x) * kC;
+      if (t0 >= n) return;
+      const char* at = vsrc + (int64_t)t0 * d * kE;
+      auto take = [&](uint32_t o) { return F32 ? *(const uint32_t*)(at + o) : *(const uint16_t*)(at + o); };
+      if (t0 + kC <= n) {
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int t = (step * PW + x) * kC + (r >> 2) * 16 + 4 * g + (r & 3);
-        // a clamped address (no branch between the loads); what lies past the end is zeroed when used
-        const int64_t at = vbase + (int64_t)min(t, n - 1) * d;
-        if constexpr (F32)
-          vr[x][r] = ((const uint32_t*)p.v)[at];
-        else
-          vr[x][r] = ((const uint16_t*)p.v)[at];
+        for (int r = 0; r < 8; ++r) vr[x][r] = take(off[r]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          vr[x][r] = take((uint32_t)(min(16 * (r >> 2) + 4 * g + (r & 3), n - 1 - t0) * d + min(col, d - 1)) * kE);
       }
+    }
   };
   if (n > 0) fetch_v(0);
   __syncthreads();
@@ -120,10 +130,7 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
 #pragma unroll
     for (int x = 0; x < PW; ++x)
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int t = (i * PW + x) * kC + (r >> 2) * 16 + 4 * g + (r & 3);
-        v[x][r] = live && t < n ? flt(F32 ? vr[x][r] : vr[x][r] << 16) : 0.f;
-      }
+      for (int r = 0; r < 8; ++r) v[x][r] = flt(F32 ? vr[x][r] : vr[x][r] << 16);
     fetch_v(i + 1);
 #pragma unroll
     for (int x = 0; x < PW; ++x) {
@@ -139,13 +146,11 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
       for (int kx = 0; kx < NK; ++kx) {
         bf16x8 sp[3];
         split8<3>(S[2 * kx], S[2 * kx + 1], sp);
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) ks[rt] = mul<NP, 3>(ka + rt * 16 * Lds::RS + 32 * kx, Lds::KP, sp, ks[rt]);
+        mul2<NP, 3>(ka + 32 * kx, Lds::KP, 16 * Lds::RS, sp, ks);
         bf16x8 sq[NS];
 #pragma unroll
         for (int e = 0; e < NS; ++e) sq[e] = sp[e];
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) qs[rt] = mul<NP, NS>(qa + rt * 16 * Lds::RS + 32 * kx, Lds::KP, sq, qs[rt]);
+        mul2<NP, NS>(qa + 32 * kx, Lds::KP, 16 * Lds::RS, sq, qs);
       }
       f32x4 G[2], E[2], R[2], F[2];
 #pragma unroll
@@ -158,8 +163,7 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
       }
       bf16x8 rp[3];
       split8<3>(R[0], R[1], rp);
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) F[rt] = mul<3, 3>(ta + rt * 16 * kCS, Lds::CP, rp, F[rt]);
+      mul2<3, 3>(ta, Lds::CP, 16 * kCS, rp, F);
       // W' = G_C W + K^T (E theta F)
       {
         f32x4 U[2];
@@ -168,21 +172,33 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
         bf16x8 up[3];
         split8<3>(U[0], U[1], up);
         const float gc = L.gc()[0], scale = L.gc()[1];
-        const bool scaled = scale != 1.f;   // seldom: theta far from 1 all over the chunk
+        const bool scaled = __builtin_amdgcn_readfirstlane(bits(scale)) != 0x3f800000u;
+        f32x4 acc[NT];
 #pragma unroll
-        for (int ti = 0; ti < NT; ++ti) {
-          bf16x8 kt[NP];
+        for (int ti = 0; ti < NT; ++ti) acc[ti] = S[ti] * gc;
+        if (scaled) {   // seldom: theta far from 1 all over the chunk
 #pragma unroll
-          for (int e = 0; e < NP; ++e) kt[e] = read_transposed(L.k() + e * Lds::KP, Lds::RS, 16 * ti, lane);
-          f32x4 acc = S[ti] * gc;
-          const f32x4 kept = acc;
-          if (scaled) acc = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int ti = 0; ti < NT; ++ti) S[ti] = acc[ti], acc[ti] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        bf16x8 kt[NT][NP];
 #pragma unroll
-          for (int o = 2; o >= 0; --o)
+        for (int ti = 0; ti < NT; ++ti)
 #pragma unroll
-            for (int e = NP - 1; e >= 0; --e)
-              if (o - e >= 0) acc = mfma(kt[e], up[o - e], acc);
-          S[ti] = scaled ? acc * scale + kept : acc;
+          for (int e = 0; e < NP; ++e) kt[ti][e] = read_transposed(L.k() + e * Lds::KP, Lds::RS, 16 * ti, lane);
+#pragma unroll
+        for (int o = 2; o >= 0; --o)
+#pragma unroll
+          for (int e = NP - 1; e >= 0; --e)
+            if (o - e >= 0) {
+#pragma unroll
+              for (int ti = 0; ti < NT; ++ti) acc[ti] = mfma(kt[ti][e], up[o - e], acc[ti]);
+            }
+        if (scaled) {
+#pragma unroll
+          for (int ti = 0; ti < NT; ++ti) S[ti] += acc[ti] * scale;
+        } else {
+#pragma unroll
+          for (int ti = 0; ti < NT; ++ti) S[ti] = acc[ti];
         }
       }
       // Y = diag(G) Q W^T + P F
@@ -190,30 +206,24 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
       bf16x8 fp[NS];
       split8<NS>(F[0], F[1], fp);
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt) {
-        f32x4 y;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) y[r] = G[rt][r] * qs[rt][r];
-        y = mul<NPP, NS>(pa + rt * 16 * kCS, Lds::CP, fp, y);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) out[rt][r] = y[r];
-      }
-      auto store = [&](int rt, int r) {
-        const int64_t at = vbase + (int64_t)(t0 + 16 * rt + 4 * g + r) * d;
+      for (int rt = 0; rt < 2; ++rt) out[rt] = G[rt] * qs[rt];
+      mul2<NPP, NS>(pa, Lds::CP, 16 * kCS, fp, out);
+      char* at = ydst + (int64_t)t0 * d * kE;
+      auto store = [&](int e) {
         if (F32)
-          ((float*)p.y)[at] = out[rt][r];
+          *(float*)(at + off[e]) = out[e >> 2][e & 3];
         else
-          ((uint16_t*)p.y)[at] = __builtin_bit_cast(uint16_t, (__bf16)out[rt][r]);
+          *(uint16_t*)(at + off[e]) = __builtin_bit_cast(uint16_t, (__bf16)out[e >> 2][e & 3]);
       };
       if (t0 + kC <= n) {   // a whole chunk: one branch
         if (live) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) store(e >> 2, e & 3);
+          for (int e = 0; e < 8; ++e) store(e);
         }
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (live && t0 + 16 * (e >> 2) + 4 * g + (e & 3) < n) store(e >> 2, e & 3);
+          if (live && t0 + 16 * (e >> 2) + 4 * g + (e & 3) < n) store(e);
       }
     }
     __syncthreads();
