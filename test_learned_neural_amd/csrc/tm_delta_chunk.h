@@ -80,36 +80,46 @@ __device__ __forceinline__ void put4(uint16_t* at, int plane, float x0, float x1
   }
 }
 
-// c += A B over one 32-long step for two row tiles of A (the second `step`
-// further on), A in NA planes (from LDS, `plane` apart), B in NB; the products
-// kept are those of planes i + j < max(NA, NB), smallest first, the two tiles'
-// accumulation chains in turn.
-template <int NA, int NB>
-__device__ __forceinline__ void mul2(const uint16_t* a, int plane, int step, const bf16x8 (&b)[NB], f32x4 (&c)[2]) {
-  constexpr int kMost = NA > NB ? NA : NB;
-  bf16x8 av[2][NA];
+// Both row tiles (the second `step` further on) of one 32-long step of A from
+// LDS, in NA planes `plane` apart.
+template <int NA>
+__device__ __forceinline__ void read2(const uint16_t* a, int plane, int step, bf16x8 (&av)[2][NA]) {
 #pragma unroll
-  for (int i = 0; i < NA; ++i)
+  for (int i = NA - 1; i >= 0; --i)
 #pragma unroll
     for (int t = 0; t < 2; ++t) av[t][i] = *(const bf16x8*)(a + i * plane + t * step);
+}
+
+// c += A B for the two tiles; the products kept are those of planes
+// i + j < max(NA, NB), smallest first, the two tiles' accumulation chains in
+// turn.  B may have more planes than NB.  SWAP: the product's transpose (an
+// operand's lanes hold the same values on either side).
+template <bool SWAP, int NB, int NA, int MB>
+__device__ __forceinline__ void mul2(const bf16x8 (&av)[2][NA], const bf16x8 (&b)[MB], f32x4 (&c)[2]) {
+  static_assert(NB <= MB, "planes of B");
+  constexpr int kMost = NA > NB ? NA : NB;
 #pragma unroll
   for (int o = kMost - 1; o >= 0; --o)
 #pragma unroll
     for (int i = NA - 1; i >= 0; --i)
       if (o - i >= 0 && o - i < NB) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) c[t] = mfma(av[t][i], b[o - i], c[t]);
+        for (int t = 0; t < 2; ++t) c[t] = SWAP ? mfma(b[o - i], av[t][i], c[t]) : mfma(av[t][i], b[o - i], c[t]);
       }
 }
 
+// Keeps what is written before it ahead of what is written after it.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 // The operand A[m][k] of a [k][m] array (row stride rs in bf16, k = 32 tokens in their natural row order, m0 the tile's
-// first column): the hardware's transposing read gives a group of 16 lanes 4 rows by 16 columns, a column per lane.
+// first column; PERM: its rows
+// are permuted): the hardware's transposing read gives a group of 16 lanes 4 rows by 16 columns, a column per lane.
+template <bool PERM>
 __device__ __forceinline__ bf16x8 read_transposed(const uint16_t* base, int rs, int m0, int lane) {
   typedef __attribute__((address_space(3))) bf16x4 lds4;
-  const int g = lane >> 4, i = lane & 15;
   // columns 4c..4c+3 of a permuted row are contiguous, at perm32
-  const int col = m0 + 4 * (i & 3), at = (col & ~31) + perm32(col & 31);
-  const uint16_t* p0 = base + (4 * g + (i >> 2)) * rs + at;
+  const int col = m0 + 4 * (lane & 3), at = PERM ? (col & ~31) + perm32(col & 31) : col;
+  const uint16_t* p0 = base + (4 * (lane >> 4) + ((lane & 15) >> 2)) * rs + at;
   const bf16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)p0);
   const bf16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(p0 + 16 * rs));
   return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -140,20 +150,25 @@ __device__ __forceinline__ double lane_f64(double x, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// log2(1 - alpha); alpha = 1: -2000; above 1: NaN
+// log2(1 - alpha); alpha = 1: -2000; above 1: NaN.  1 - alpha is rounded, by
+// u; log2 u (-alpha) / (u - 1) is log2(1 - alpha) to a few units in the last
+// place, as log x / (x - 1) hardly changes over one rounding of x.
 __device__ __forceinline__ float log2_keep(float alpha) {
-  const float x = log1pf(-alpha) * 1.44269504088896f;
-  return x < -2000.f ? -2000.f : x;
+  const float u = 1.f - alpha, x = u - 1.f;
+  const float l = x == 0.f ? -alpha * 1.44269504088896f : __builtin_amdgcn_logf(u) * (-alpha * __builtin_amdgcn_rcpf(x));
+  return l < -2000.f ? -2000.f : l;
 }
 
 // LDS of one chunk: NP planes of K and Q, three of T = (I + B)^-1, NPP of P,
-// and per-token factors.  T's upper right block is zeroed once.
-template <int DP, int NP, int NPP>
+// per-token factors, and VC columns of V.  T's upper right block is zeroed once.
+template <int DP, int NP, int NPP, int VC>
 struct ChunkLds {
   static constexpr int RS = DP + 8;                 // row stride of K and Q in bf16
   static constexpr int KP = kC * RS, CP = kC * kCS; // plane sizes
   static constexpr int OFF_K = 0, OFF_Q = OFF_K + NP * KP * 2, OFF_T = OFF_Q + NP * KP * 2, OFF_P = OFF_T + 3 * CP * 2,
-                       OFF_G = OFF_P + NPP * CP * 2, BYTES = OFF_G + (2 * kC + 4) * 4;
+                       OFF_G = OFF_P + NPP * CP * 2, OFF_V = OFF_G + (2 * kC + 4) * 4,
+                       VS = VC + (NP == 1 ? 8 : 4),   // row stride of V: bf16, or fp32 where NP is 3
+                       BYTES = OFF_V + kC * VS * (NP == 1 ? 2 : 4);
   static_assert(NPP * CP * 2 >= kC * kBS * 4, "the fp32 scratch lies where P comes to lie");
   static_assert(16 * kCS * 2 >= 3 * kC * 4, "the gates' scratch lies in T's lower half");
   unsigned char* base;
@@ -164,6 +179,7 @@ struct ChunkLds {
   __device__ float* g() const { return (float*)(base + OFF_G); }          // G_t
   __device__ float* eth() const { return (float*)(base + OFF_G) + kC; }   // E_j theta_j over theta's scale
   __device__ float* gc() const { return (float*)(base + OFF_G) + 2 * kC; }   // G_C, and theta's scale (a power of two)
+  __device__ unsigned char* v() const { return base + OFF_V; }
   __device__ float* scratch() const { return (float*)(base + OFF_P); }    // [32][kBS]
   __device__ float* gates() const { return (float*)(base + OFF_T + 16 * kCS * 2); }   // log2 G (hi, lo), theta
 };
@@ -173,26 +189,28 @@ struct ChunkLds {
 // F32: fp32 input.  VB: bytes of the pieces that rows consist of and are
 // aligned for (16 or 8); 0: any row, element by element and not ahead of
 // time (such rows are rare, and their registers would be many).
-template <int DP, bool F32, int VB>
+template <int DP, int COLS, bool F32, int VB>
 struct RowLoad {
   static constexpr int PER = VB ? VB / (F32 ? 4 : 2) : 4;    // elements per piece
-  static constexpr int PIECES = kC * DP / PER / 64;          // per lane
-  static constexpr int RS = DP + 8, KP = kC * RS;
+  static constexpr int PIECES = kC * COLS / PER / 64;        // per lane
   uint32_t raw[VB ? PIECES : 1][VB ? VB / 4 : 1];
   const char* src;
-  int n, d;
-  // rows 0 .. rows - 1 at `from`, of `width` elements; the other rows and columns are zero
-  __device__ __forceinline__ void load(const char* from, int rows, int width, int lane) {
-    src = from, n = rows, d = width;
+  int n, d, cols;
+  // `rows` rows of `real` columns at `from`, d elements apart; the other rows and columns are zero
+  __device__ __forceinline__ void load(const char* from, int rows, int width, int real, int lane) {
+    src = from, n = rows, d = width, cols = real;
     if constexpr (VB > 0) {
       if (n == kC && d == DP) {   // offsets that no chunk changes
 #pragma unroll
-        for (int i = 0; i < PIECES; ++i) take(i, (i * 64 + lane) * VB);
+        for (int i = 0; i < PIECES; ++i) {
+          const int e = (i * 64 + lane) * PER;
+          take(i, (e / COLS * DP + e % COLS) * (F32 ? 4 : 2));
+        }
       } else {   // clamped addresses: no branch between the loads
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-          const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
-          take(i, (min(r, n - 1) * d + min(c, d - PER)) * (F32 ? 4 : 2));
+          const int e = (i * 64 + lane) * PER, r = e / COLS, c = e % COLS;
+          take(i, (min(r, n - 1) * d + max(min(c, cols - PER), 0)) * (F32 ? 4 : 2));
         }
       }
     }
@@ -207,50 +225,61 @@ struct RowLoad {
       raw[i][0] = x.x, raw[i][1] = x.y;
     }
   }
-  __device__ __forceinline__ void store(uint16_t* dst, int lane) {
+  // put(row, column, 4 values in order, as stored bits) for every 4 columns
+  template <class Put>
+  __device__ __forceinline__ void store(int lane, Put put) {
     if constexpr (VB > 0) {
-      if (n != kC || d != DP) {
+      if (n != kC || cols < COLS) {
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-          const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
+          const int e = (i * 64 + lane) * PER, r = e / COLS, c = e % COLS;
 #pragma unroll
-          for (int j = 0; j < VB / 4; ++j) raw[i][j] = r < n && c < d ? raw[i][j] : 0u;
+          for (int j = 0; j < VB / 4; ++j) raw[i][j] = r < n && c < cols ? raw[i][j] : 0u;
         }
       }
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
-        uint16_t* at = dst + r * RS + (c & ~31);
-        const auto& x = raw[i];
-        if constexpr (F32) {
-          put4<3>(at + perm32(c & 31), KP, flt(x[0]), flt(x[1]), flt(x[2]), flt(x[3]));
-        } else {
-          *(uint2*)(at + perm32(c & 31)) = make_uint2(x[0], x[1]);
-          if constexpr (VB == 16) *(uint2*)(at + perm32((c + 4) & 31)) = make_uint2(x[2], x[3]);
-        }
+        const int e = (i * 64 + lane) * PER, r = e / COLS, c = e % COLS;
+#pragma unroll
+        for (int j = 0; j < PER; j += 4) put(r, c + j, raw[i] + (F32 ? j : j / 2));
       }
     } else {
 #pragma unroll 1
       for (int i = 0; i < PIECES; ++i) {
-        const int e = (i * 64 + lane) * PER, r = e / DP, c = e % DP;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        const int e = (i * 64 + lane) * PER, r = e / COLS, c = e % COLS;
+        uint32_t x[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (r < n && c + j < d) {
-            const int at = r * d + c + j;
-            x[j] = F32 ? ((const float*)src)[at] : flt((uint32_t)((const uint16_t*)src)[at] << 16);
+          if (r < n && c + j < cols) {
+            if (F32)
+              x[j] = ((const uint32_t*)src)[r * d + c + j];
+            else
+              x[j / 2] |= (uint32_t)((const uint16_t*)src)[r * d + c + j] << (j % 2 * 16);
           }
-        put4<F32 ? 3 : 1>(dst + r * RS + (c & ~31) + perm32(c & 31), KP, x[0], x[1], x[2], x[3]);
+        put(r, c, x);
       }
     }
   }
 };
 
+// Rows of K or Q into their permuted planes.
+template <int DP, bool F32, class Load>
+__device__ __forceinline__ void store_planes(Load& rows, uint16_t* dst, int lane) {
+  constexpr int RS = DP + 8, KP = kC * RS;
+  rows.store(lane, [&](int r, int c, const uint32_t* x) {
+    uint16_t* at = dst + r * RS + (c & ~31) + perm32(c & 31);
+    if constexpr (F32)
+      put4<3>(at, KP, flt(x[0]), flt(x[1]), flt(x[2]), flt(x[3]));
+    else
+      *(uint2*)at = make_uint2(x[0], x[1]);
+  });
+}
+
 // One wave builds a chunk's matrices in LDS from its K and Q (already stored)
 // and its gates (lane t < 32: token t's log2 a and theta; 0 past the end).
-template <int DP, int NP, int NPP>
-__device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP>& L, float la, float th, int lane) {
-  using Lds = ChunkLds<DP, NP, NPP>;
+template <int DP, int NP, int NPP, int VC>
+__device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP, VC>& L, float la, float th, int lane) {
+  using Lds = ChunkLds<DP, NP, NPP, VC>;
   const int g = lane >> 4, li = lane & 15;
   // prefix sums of log2 a in fp64 over lanes 0..31, by DPP (16 lanes a row)
   double sum = la;
@@ -321,8 +350,8 @@ __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP>& L, floa
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const float D = exp2_of((th_ - jh[r]) + (tl - jl[r])) * tj[r];
-      b[r] = t > j0 + r ? D * kk[x][r] : 0.f;
-      qk[x][r] = t >= j0 + r ? D * qk[x][r] : 0.f;
+      b[r] = x == 1 || t > j0 + r ? D * kk[x][r] : 0.f;
+      qk[x][r] = x == 1 || t >= j0 + r ? D * qk[x][r] : 0.f;
     }
     *(f32x4*)(sc + t * kBS + j0) = b;
   }
@@ -331,14 +360,21 @@ __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP>& L, floa
   // substitution down the rows (stable for any B)
   {
     const int o = 16 * (g & 1);
-    f32x4 B[16][4];   // row r's first r entries, all read before the first is used
+    f32x4 B[16][4];   // row r's first r entries, four rows read ahead
+    auto rows = [&](int r0) {
 #pragma unroll
-    for (int r = 1; r < 16; ++r)
+      for (int r = r0; r < r0 + 4; ++r)
 #pragma unroll
-      for (int j = 0; j < r; j += 4) B[r][j / 4] = *(const f32x4*)(sc + (o + r) * kBS + o + j);
+        for (int j = 0; j < r; j += 4) B[r][j / 4] = *(const f32x4*)(sc + (o + r) * kBS + o + j);
+    };
     float T[16];
+    rows(0);
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
+      if (r % 4 == 0) {
+        in_order();
+        if (r < 12) rows(r + 4);
+      }
       float s0 = r == li ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
       for (int j = 0; j < r; ++j) {

@@ -5,12 +5,16 @@
 // other.  So a "chain" wave owns 16 value channels of a stream for the whole
 // sequence: W^T's [d x 16] slice stays in its accumulators, and every product
 // of a chunk (K W^T, T R, P F, K^T U) has those accumulators' tiles as the
-// operand in place, so the chain needs no exchange, no transposition and no
-// barrier of its own.  What is not serial (K K^T, Q K^T, the decays, the
+// operand in place, so the chain needs no exchange and no transposition.
+// What is not serial (the loads of K, Q and V, K K^T, Q K^T, the decays, the
 // triangular inverse, the bf16 planes) "builder" waves of the same workgroup
-// prepare in LDS, PW chunks ahead of the chain, with the loads of the chunks
-// after those in flight in their registers; one barrier every PW chunks.
-// Nothing but the inputs and outputs touches memory.
+// prepare in a ring of NB chunk buffers in LDS, PB chunks at once, with the
+// loads of the chunks after those in flight in their registers.  The waves
+// meet through two kinds of counters in LDS: a builder's last finished chunk,
+// and a chain wave's.  All waves of a workgroup are resident, a builder waits
+// only for chunks built before its own to be consumed and a chain wave only
+// for the next chunk, so every wait ends.  Nothing but the inputs and outputs
+// touches memory.
 #include "tm_delta_chunk.h"
 
 namespace titans {
@@ -25,12 +29,26 @@ struct ChainParams {
   int streams, H, Hk, N, d, parts;
 };
 
-template <int DP, bool F32, int CW, int PW, int VB>
-__global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams p) {
+// A counter in LDS that one wave raises and others wait for.
+__device__ __forceinline__ int seen(const int* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP); }
+__device__ __forceinline__ void wait_for(const int* p, int value) {
+  while (seen(p) < value) __builtin_amdgcn_s_sleep(1);
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+__device__ __forceinline__ void raise_to(int* p, int value, int lane) {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  if (lane == 0) __hip_atomic_store(p, value, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+template <int DP, bool F32, int CW, int PB, int NB, int VB>
+__global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams p) {
+  static_assert(NB > PB, "a chunk is consumed while PB are built");
   constexpr int NP = F32 ? 3 : 1, NPP = F32 ? 3 : 2, NS = F32 ? 3 : 2;   // planes: inputs, P, and W and F for y
   constexpr int NT = DP / 16, NK = DP / 32, kE = F32 ? 4 : 2;
-  using Lds = ChunkLds<DP, NP, NPP>;
+  using Lds = ChunkLds<DP, NP, NPP, CW * 16>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  int* built = (int*)(smem + NB * Lds::BYTES);   // [PB]: chunks a builder has finished, counted from the sequence's start
+  int* used = built + PB;                        // [CW]: chunks a chain wave has finished
   const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // the parts of a stream read the same K and Q: workgroups 8 apart share an XCD's L2
@@ -39,40 +57,51 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
   if (s >= p.streams) return;
   const int b = s / p.H, h = s % p.H, d = p.d;
   const int n = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
-  const int chunks = (n + kC - 1) / kC, steps = (chunks + PW - 1) / PW;
+  const int chunks = (n + kC - 1) / kC;
+  if (threadIdx.x < PB + CW) built[threadIdx.x] = 0;
+  // T's block that stays zero
+  for (int x = wave; x < 3 * NB; x += CW + PB) {
+    Lds L{smem + x / 3 * Lds::BYTES};
+    *(uint2*)(L.t() + x % 3 * Lds::CP + li * kCS + 8 * g + 4) = make_uint2(0, 0);
+  }
+  __syncthreads();
 
   if (wave >= CW) {
     // ---- builder ----
-    const int pw = wave - CW;
+    const int pw = wave - CW, col0 = part * CW * 16;
     const int64_t krow = ((int64_t)b * p.Hk + h / (p.H / p.Hk)) * p.N;
     const float *alpha = p.alpha + (int64_t)s * p.N, *theta = p.theta + (int64_t)s * p.N;
-    for (int i = 0; i < 2; ++i) {   // T's block that stays zero
-      Lds L{smem + (i * PW + pw) * Lds::BYTES};
-      for (int x = 0; x < 3; ++x) *(uint2*)(L.t() + x * Lds::CP + li * kCS + 8 * g + 4) = make_uint2(0, 0);
-    }
-    RowLoad<DP, F32, VB> kr, qr;
+    RowLoad<DP, DP, F32, VB> kr, qr;
+    RowLoad<DP, CW * 16, F32, VB> vr;
     float al = 0.f, th = 0.f;
     auto fetch = [&](int c) {
       const int t0 = c * kC, m = min(kC, n - t0);
       if (m <= 0) return;
-      kr.load((const char*)p.k + (krow + t0) * d * kE, m, d, lane);
-      qr.load((const char*)p.q + (krow + t0) * d * kE, m, d, lane);
-      al = lane < m ? alpha[t0 + lane] : 0.f;
-      th = lane < m ? theta[t0 + lane] : 0.f;
+      kr.load((const char*)p.k + (krow + t0) * d * kE, m, d, d, lane);
+      qr.load((const char*)p.q + (krow + t0) * d * kE, m, d, d, lane);
+      vr.load((const char*)p.v + (((int64_t)s * p.N + t0) * d + col0) * kE, m, d, d - col0, lane);
+      al = alpha[t0 + min(lane, m - 1)];   // (zeroed when used: nothing here waits)
+      th = theta[t0 + min(lane, m - 1)];
     };
     fetch(pw);
-    for (int i = 0; i <= steps; ++i) {
-      const int c = i * PW + pw;
-      if (c < chunks) {
-        Lds L{smem + ((i & 1) * PW + pw) * Lds::BYTES};
-        kr.store(L.k(), lane);
-        qr.store(L.q(), lane);
-        const float la = log2_keep(al), th0 = th;
-        fetch(c + PW);
-        wave_fence();
-        build_chunk<DP, NP, NPP>(L, la, th0, lane);
-      }
-      __syncthreads();
+    for (int c = pw; c < chunks; c += PB) {
+      Lds L{smem + c % NB * Lds::BYTES};
+      const bool in = c * kC + lane < n;
+      const float la = in ? log2_keep(al) : 0.f, th0 = in ? th : 0.f;
+#pragma unroll
+      for (int w = 0; w < CW; ++w) wait_for(used + w, c - NB + 1);
+      store_planes<DP, F32>(kr, L.k(), lane);
+      store_planes<DP, F32>(qr, L.q(), lane);
+      vr.store(lane, [&](int r, int cc, const uint32_t* x) {
+        if constexpr (F32)
+          *(uint4*)((float*)L.v() + r * Lds::VS + cc) = make_uint4(x[0], x[1], x[2], x[3]);
+        else
+          *(uint2*)((uint16_t*)L.v() + r * Lds::VS + cc) = make_uint2(x[0], x[1]);
+      });
+      fetch(c + PB);
+      wave_fence();
+      build_chunk(L, la, th0, lane);
+      raise_to(built + pw, c + 1, lane);
     }
     return;
   }
@@ -97,136 +126,131 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
       }
     }
   }
-  // v and y: a uniform address per chunk and this lane's offsets within it
-  const char* vsrc = (const char*)p.v + (int64_t)s * p.N * d * kE;
-  char* ydst = (char*)p.y + (int64_t)s * p.N * d * kE;
-  uint32_t off[8];
+  // y's tiles are computed transposed: a lane has 4 consecutive channels of
+  // a token, stored in one piece at a uniform address per chunk plus this
+  const int ych = (part * CW + wave) * 16 + 4 * g;
+  char* ydst = (char*)p.y + ((int64_t)s * p.N * d + ych) * kE;
+  const uint32_t yoff = (uint32_t)li * d * kE;
+  for (int c = 0; c < chunks; ++c) {
+    wait_for(built + c % PB, c + 1);
+    const Lds L{smem + c % NB * Lds::BYTES};
+    const uint16_t *ka = L.k() + li * Lds::RS + 8 * g, *qa = L.q() + li * Lds::RS + 8 * g;
+    const uint16_t *ta = L.t() + li * kCS + 8 * g, *pa = L.p() + li * kCS + 8 * g;
+    // The order below keeps LDS reads a product ahead of their use, and
+    // products off the serial path (Q W^T, P F) in its gaps.
+    f32x4 ks[2], qs[2], V[2], G[2], E[2], R[2], F[2];
 #pragma unroll
-  for (int r = 0; r < 8; ++r) off[r] = ((16 * (r >> 2) + 4 * g + (r & 3)) * d + min(col, d - 1)) * kE;
-  uint32_t vr[PW][8];
-  // Rows past the end read the last token's v: their K, theta and so their
-  // effect is zero.
-  auto fetch_v = [&](int step) {
+    for (int rt = 0; rt < 2; ++rt) ks[rt] = qs[rt] = F[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    bf16x8 ra[NK][2][NP];
 #pragma unroll
-    for (int x = 0; x < PW; ++x) {
-      const int t0 = (step * PW + x) * kC;
-      if (t0 >= n) return;
-      const char* at = vsrc + (int64_t)t0 * d * kE;
-      auto take = [&](uint32_t o) { return F32 ? *(const uint32_t*)(at + o) : *(const uint16_t*)(at + o); };
-      if (t0 + kC <= n) {
+    for (int kx = 0; kx < NK; ++kx) read2<NP>(ka + 32 * kx, Lds::KP, 16 * Lds::RS, ra[kx]);
+    if constexpr (F32) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) vr[x][r] = take(off[r]);
+      for (int e = 0; e < 8; ++e)
+        V[e >> 2][e & 3] = ((const float*)L.v())[(16 * (e >> 2) + 4 * g + (e & 3)) * Lds::VS + 16 * wave + li];
+    } else {
+      const u32x4 x = __builtin_bit_cast(u32x4, read_transposed<false>((const uint16_t*)L.v(), Lds::VS, 16 * wave, lane));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) V[e >> 2][e & 3] = e & 1 ? top(flt(x[e >> 1])) : flt(x[e >> 1] << 16);
+    }
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) G[rt] = *(const f32x4*)(L.g() + 16 * rt + 4 * g);
+    if (!F32) in_order();
+    bf16x8 sp[NK][3];
+#pragma unroll
+    for (int kx = 0; kx < NK; ++kx) {
+      split8<3>(S[2 * kx], S[2 * kx + 1], sp[kx]);
+      mul2<false, 3>(ra[kx], sp[kx], ks);
+    }
+    bf16x8 rt3[2][3];
+    read2<3>(ta, Lds::CP, 16 * kCS, rt3);
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) E[rt] = *(const f32x4*)(L.eth() + 16 * rt + 4 * g);
+    if (!F32) in_order();
+    bf16x8 rq[NK][2][NP];
+#pragma unroll
+    for (int kx = 0; kx < NK; ++kx) read2<NP>(qa + 32 * kx, Lds::KP, 16 * Lds::RS, rq[kx]);
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) R[rt][r] = fmaf(-G[rt][r], ks[rt][r], V[rt][r]);
+    bf16x8 rp[3];
+    split8<3>(R[0], R[1], rp);
+    mul2<false, 3>(rt3, rp, F);
+    if (!F32) in_order();
+    bf16x8 kt[NT][NP];
+#pragma unroll
+    for (int ti = 0; ti < NT; ++ti)
+#pragma unroll
+      for (int e = 0; e < NP; ++e) kt[ti][e] = read_transposed<true>(L.k() + e * Lds::KP, Lds::RS, 16 * ti, lane);
+#pragma unroll
+    for (int kx = 0; kx < NK; ++kx) mul2<true, NS>(rq[kx], sp[kx], qs);
+    const float gc = L.gc()[0], scale = L.gc()[1];
+    if (!F32) in_order();
+    // W' = G_C W + K^T (E theta F)
+    {
+      f32x4 U[2];
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) U[rt] = F[rt] * E[rt];
+      bf16x8 up[3];
+      split8<3>(U[0], U[1], up);
+      const bool scaled = __builtin_amdgcn_readfirstlane(bits(scale)) != 0x3f800000u;
+      f32x4 acc[NT];
+#pragma unroll
+      for (int ti = 0; ti < NT; ++ti) acc[ti] = S[ti] * gc;
+      if (scaled) {   // seldom: theta far from 1 all over the chunk
+#pragma unroll
+        for (int ti = 0; ti < NT; ++ti) S[ti] = acc[ti], acc[ti] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int o = 2; o >= 0; --o)
+#pragma unroll
+        for (int e = NP - 1; e >= 0; --e)
+          if (o - e >= 0) {
+#pragma unroll
+            for (int ti = 0; ti < NT; ++ti) acc[ti] = mfma(kt[ti][e], up[o - e], acc[ti]);
+          }
+      if (scaled) {
+#pragma unroll
+        for (int ti = 0; ti < NT; ++ti) S[ti] += acc[ti] * scale;
       } else {
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          vr[x][r] = take((uint32_t)(min(16 * (r >> 2) + 4 * g + (r & 3), n - 1 - t0) * d + min(col, d - 1)) * kE);
+        for (int ti = 0; ti < NT; ++ti) S[ti] = acc[ti];
       }
     }
-  };
-  if (n > 0) fetch_v(0);
-  __syncthreads();
-  for (int i = 0; i < steps; ++i) {
-    float v[PW][8];
+    // Y^T = W Q^T diag(G) + F^T P^T
+    f32x4 out[2];
+    bf16x8 fp[NS], rp2[2][NPP];
+    read2<NPP>(pa, Lds::CP, 16 * kCS, rp2);
+    split8<NS>(F[0], F[1], fp);
 #pragma unroll
-    for (int x = 0; x < PW; ++x)
+    for (int rt = 0; rt < 2; ++rt) out[rt] = qs[rt] * L.g()[16 * rt + li];
+    mul2<true, NS>(rp2, fp, out);
+    raise_to(used + wave, c + 1, lane);
+    const int t0 = c * kC;
+    char* at = ydst + (int64_t)t0 * d * kE;
 #pragma unroll
-      for (int r = 0; r < 8; ++r) v[x][r] = flt(F32 ? vr[x][r] : vr[x][r] << 16);
-    fetch_v(i + 1);
-#pragma unroll
-    for (int x = 0; x < PW; ++x) {
-      const int t0 = (i * PW + x) * kC;
-      if (t0 >= n) break;
-      const Lds L{smem + ((i & 1) * PW + x) * Lds::BYTES};
-      const uint16_t *ka = L.k() + li * Lds::RS + 8 * g, *qa = L.q() + li * Lds::RS + 8 * g;
-      const uint16_t *ta = L.t() + li * kCS + 8 * g, *pa = L.p() + li * kCS + 8 * g;
-      f32x4 ks[2], qs[2];
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) ks[rt] = qs[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int kx = 0; kx < NK; ++kx) {
-        bf16x8 sp[3];
-        split8<3>(S[2 * kx], S[2 * kx + 1], sp);
-        mul2<NP, 3>(ka + 32 * kx, Lds::KP, 16 * Lds::RS, sp, ks);
-        bf16x8 sq[NS];
-#pragma unroll
-        for (int e = 0; e < NS; ++e) sq[e] = sp[e];
-        mul2<NP, NS>(qa + 32 * kx, Lds::KP, 16 * Lds::RS, sq, qs);
-      }
-      f32x4 G[2], E[2], R[2], F[2];
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) {
-        G[rt] = *(const f32x4*)(L.g() + 16 * rt + 4 * g);
-        E[rt] = *(const f32x4*)(L.eth() + 16 * rt + 4 * g);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) R[rt][r] = fmaf(-G[rt][r], ks[rt][r], v[x][4 * rt + r]);
-        F[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
-      bf16x8 rp[3];
-      split8<3>(R[0], R[1], rp);
-      mul2<3, 3>(ta, Lds::CP, 16 * kCS, rp, F);
-      // W' = G_C W + K^T (E theta F)
-      {
-        f32x4 U[2];
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) U[rt] = F[rt] * E[rt];
-        bf16x8 up[3];
-        split8<3>(U[0], U[1], up);
-        const float gc = L.gc()[0], scale = L.gc()[1];
-        const bool scaled = __builtin_amdgcn_readfirstlane(bits(scale)) != 0x3f800000u;
-        f32x4 acc[NT];
-#pragma unroll
-        for (int ti = 0; ti < NT; ++ti) acc[ti] = S[ti] * gc;
-        if (scaled) {   // seldom: theta far from 1 all over the chunk
-#pragma unroll
-          for (int ti = 0; ti < NT; ++ti) S[ti] = acc[ti], acc[ti] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-        bf16x8 kt[NT][NP];
-#pragma unroll
-        for (int ti = 0; ti < NT; ++ti)
-#pragma unroll
-          for (int e = 0; e < NP; ++e) kt[ti][e] = read_transposed(L.k() + e * Lds::KP, Lds::RS, 16 * ti, lane);
-#pragma unroll
-        for (int o = 2; o >= 0; --o)
-#pragma unroll
-          for (int e = NP - 1; e >= 0; --e)
-            if (o - e >= 0) {
-#pragma unroll
-              for (int ti = 0; ti < NT; ++ti) acc[ti] = mfma(kt[ti][e], up[o - e], acc[ti]);
-            }
-        if (scaled) {
-#pragma unroll
-          for (int ti = 0; ti < NT; ++ti) S[ti] += acc[ti] * scale;
-        } else {
-#pragma unroll
-          for (int ti = 0; ti < NT; ++ti) S[ti] = acc[ti];
-        }
-      }
-      // Y = diag(G) Q W^T + P F
-      f32x4 out[2];
-      bf16x8 fp[NS];
-      split8<NS>(F[0], F[1], fp);
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) out[rt] = G[rt] * qs[rt];
-      mul2<NPP, NS>(pa, Lds::CP, 16 * kCS, fp, out);
-      char* at = ydst + (int64_t)t0 * d * kE;
-      auto store = [&](int e) {
-        if (F32)
-          *(float*)(at + off[e]) = out[e >> 2][e & 3];
-        else
-          *(uint16_t*)(at + off[e]) = __builtin_bit_cast(uint16_t, (__bf16)out[e >> 2][e & 3]);
-      };
-      if (t0 + kC <= n) {   // a whole chunk: one branch
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) store(e);
+    for (int rt = 0; rt < 2; ++rt) {
+      if (t0 + 16 * rt + li >= n) continue;
+      char* to = at + (yoff + 16u * rt * d * kE);
+      if constexpr (VB > 0) {
+        if (ych < d) {
+          if constexpr (F32)
+            *(f32x4*)to = out[rt];
+          else
+            *(bf16x4*)to = __builtin_convertvector(out[rt], bf16x4);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (live && t0 + 16 * (e >> 2) + 4 * g + (e & 3) < n) store(e);
+        for (int r = 0; r < 4; ++r)
+          if (ych + r < d) {
+            if constexpr (F32)
+              ((float*)to)[r] = out[rt][r];
+            else
+              ((__bf16*)to)[r] = (__bf16)out[rt][r];
+          }
       }
     }
-    __syncthreads();
   }
   if (!live) return;
   float* W_out = p.W_out + (int64_t)s * d * d + (int64_t)col * d;
@@ -243,24 +267,25 @@ __global__ void __launch_bounds__((CW + PW) * 64) delta_chain_kernel(ChainParams
   }
 }
 
-template <int DP, bool F32, int CW, int PW, int VB>
+template <int DP, bool F32, int CW, int PB, int NB, int VB>
 hipError_t launch_as(ChainParams p, hipStream_t stream) {
-  constexpr int lds = 2 * PW * ChunkLds<DP, F32 ? 3 : 1, F32 ? 3 : 2>::BYTES;
+  constexpr int lds = NB * ChunkLds<DP, F32 ? 3 : 1, F32 ? 3 : 2, CW * 16>::BYTES + (PB + CW) * 4;
   static_assert(lds <= 160 * 1024, "LDS of one workgroup");
   p.parts = ((p.d + 15) / 16 + CW - 1) / CW;
-  auto kernel = delta_chain_kernel<DP, F32, CW, PW, VB>;
+  auto kernel = delta_chain_kernel<DP, F32, CW, PB, NB, VB>;
   hipError_t err = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (err != hipSuccess) return err;
   const unsigned grid = (unsigned)((p.streams + 7) / 8 * 8 * p.parts);
-  kernel<<<grid, (CW + PW) * 64, lds, stream>>>(p);
+  kernel<<<grid, (CW + PB) * 64, lds, stream>>>(p);
   return hipGetLastError();
 }
 
 template <int DP, bool F32, int VB>
 hipError_t launch_chain(const ChainParams& p, hipStream_t stream) {
-  constexpr int PW = F32 ? 1 : 2;
-  if (p.streams >= 256) return launch_as<DP, F32, 4, PW, VB>(p, stream);
-  return launch_as<DP, F32, 2, PW, VB>(p, stream);
+  // as many buffers as LDS holds, a builder less
+  constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : 4, PB = F32 && DP == 128 ? 1 : 2;
+  if (p.streams >= 256) return launch_as<DP, F32, 4, PB, NB, VB>(p, stream);
+  return launch_as<DP, F32, 2, PB, NB, VB>(p, stream);
 }
 
 template <bool F32, int VB>
