@@ -368,7 +368,8 @@ int titans_mem_input(const titans_input_desc* desc,
  *
  * State, sums and gates are fp32; products of bf16 inputs are exact.  y is
  * rounded once.  d <= 128 (TM_ERR_UNSUPPORTED otherwise); N == 0 copies the
- * state.  TM_FLAG_FORCE_GENERIC runs the token-by-token kernel at any N.
+ * state.  Where chunks are used, a NaN or infinity of a token may reach the
+ * 31 tokens before it (of its stream) too.  TM_FLAG_FORCE_GENERIC runs the token-by-token kernel at any N.
  * titans_mem_delta_select_path reports the kernel that a call runs.
  */
 #define TM_PATH_DELTA_RECURRENT 0   /* token by token */
@@ -392,6 +393,35 @@ int titans_mem_delta_forward(const titans_delta_desc* desc,
                              void* y_out, float* W_out,
                              void* workspace, int64_t workspace_bytes,
                              void* stream);
+
+/*
+ * titans_mem_delta_backward -- gradients through titans_mem_delta_forward:
+ * the vector-Jacobian products with the output adjoints
+ *   dy         [B,H,N,d]   io dtype, device, read-only: dL/dy
+ *   dW_out     [B,H,d,d]   fp32, device, read-only, or NULL (zero)
+ * into
+ *   dk, dq     [B,Hk,N,d]  io dtype, device, written: sums over the value
+ *              heads of a key head, in their order
+ *   dv         [B,H,N,d]   io dtype, device, written
+ *   dalpha, dtheta  [B,H,N] fp32, device, written
+ *   dW_in      [B,H,d,d]   fp32, device, written
+ * Same inputs as the forward call.  Tokens past a sequence's length get zero
+ * gradients, whatever dy holds there.  At alpha = 1 dalpha is the derivative
+ * there.  Arithmetic is fp32; dk, dv and dq are rounded once.  Any overlap of
+ * a written buffer is TM_ERR_ALIAS.  The workspace holds W and its adjoint at
+ * every 32nd token: titans_mem_delta_backward_workspace_bytes(desc) bytes.
+ */
+int64_t titans_mem_delta_backward_workspace_bytes(const titans_delta_desc* desc);
+
+int titans_mem_delta_backward(const titans_delta_desc* desc,
+                              const void* k, const void* v, const void* q,
+                              const float* alpha, const float* theta,
+                              const int32_t* lengths, const float* W_in,
+                              const void* dy, const float* dW_out,
+                              void* dk, void* dv, void* dq,
+                              float* dalpha, float* dtheta, float* dW_in,
+                              void* workspace, int64_t workspace_bytes,
+                              void* stream);
 
 /*
  * titans_mem_group_norm -- group norm with an activation, from the memory's

@@ -3,5 +3,5 @@ retrieval behind the C ABI of include/titans_mem.h (libtitans_mem.so)."""
 from . import workloads  # noqa: F401
 from .titans_mem import (  # noqa: F401
     forward, retrieve, load, make_desc, param_count, select_path, workspace_bytes,
-    TitansMemError, delta_forward, group_norm, group_norm_backward,
+    TitansMemError, delta_forward, delta_backward, group_norm, group_norm_backward,
 )

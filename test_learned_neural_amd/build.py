@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
 SOURCES = ["tm_host.cpp", "tm_generic.hip", "tm_linear.hip", "tm_mlp2_group.hip", "tm_input.hip", "tm_backward.hip",
-           "tm_retrieve.hip", "tm_deep.hip", "tm_delta.hip", "tm_delta_chunk.hip",
+           "tm_retrieve.hip", "tm_deep.hip", "tm_delta.hip", "tm_delta_chunk.hip", "tm_delta_backward.hip",
            "tm_group_norm.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I" + INCLUDE, "-I" + CSRC]
@@ -29,9 +29,9 @@ DEVICE = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang", "-p
           "-munsafe-fp-atomics"]
 
 
-# MFMA results in VGPRs: the MFMA kernel post-processes every accumulator on
-# the VALU and keeps the memory state in VGPRs
-PER_FILE = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for f in ("tm_mlp2_group.hip", "tm_delta_chunk.hip")}
+# MFMA results in VGPRs: these kernels post-process every accumulator on the
+# VALU and keep the memory state in VGPRs
+PER_FILE = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for f in ("tm_mlp2_group.hip", "tm_delta_chunk.hip", "tm_delta_backward.hip")}
 
 
 def hipcc() -> str:

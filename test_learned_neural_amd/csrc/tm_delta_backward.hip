@@ -1,0 +1,581 @@
+// Gradients through the gated delta memory (tm_delta_chunk.h has the forward
+// chunk form: F the residuals, T = (I + B)^-1, P, G, E, D).
+//
+// With dW the adjoint of the state after a chunk and dY that of its outputs,
+// and dE that of E = V - diag(G) K W^T (so dV = dE):
+//
+//   dF  = P^T dY + diag(E theta) K dW^T,   dE = T^T dF
+//   dW' = G_C dW + dY^T diag(G) Q - dE^T diag(G) K      (before the chunk)
+//   X[t,j] = D[t,j] dY_t.F_j (j <= t),   M[t,j] = -D[t,j] dE_t.F_j (j < t)
+//   dQ  = diag(G) dY W + (X theta) K
+//   dK  = (X theta)^T Q + ((M theta) + (M theta)^T) K - diag(G) dE W + diag(E theta) F dW
+//   Z[t,j] = X (q_t.k_j) + M (k_t.k_j),   e_j = E_j k_j.(F_j dW)
+//   dtheta_j = sum_t Z[t,j] + e_j
+//   dalpha_t = -(1/a_t) (what passes token t's decay): the sum over rows
+//     i >= t (a token, or the chunk's end) and columns before t (its start,
+//     or a token j < t) of Z theta, with q_i.dq_i + k_i.dk_i of the terms
+//     through W in the start's column, e theta in the end's row and
+//     G_C <W, dW> in their corner.
+//
+// The last sum is taken over the rectangle itself, by suffix sums down the
+// columns: as a difference of row and column sums it would cancel.  In it (and
+// nowhere else) a = 0 (alpha = 1) is held as 2^-64, which leaves the quotient
+// its limit; what passes two such tokens vanishes beside it.
+//
+// What is serial is W forwards and dW backwards, and neither needs the other:
+// one launch sweeps both ways, each on chain and builder waves as the forward
+// kernel has them, and leaves W and dW at every chunk's edges, F and dE.  A
+// second launch takes every chunk of a key head by itself, with the value
+// heads that share the key head in turn, so dQ and dK are sums in registers
+// in a fixed order.
+#include "tm_delta_chunk.h"
+
+namespace titans {
+namespace {
+
+constexpr float kForgetGrad = -64.f;
+
+// Per (stream, chunk) in the workspace: W and dW [ld x ld] fp32, row-major,
+// and F and dE as the chains' tiles, [ld / 16][64 lanes][8] fp32.
+struct GradParams {
+  const void *k, *v, *q, *dy;
+  const float *alpha, *theta, *W_in, *dW_out;
+  const int32_t* lengths;
+  void *dk, *dv, *dq;
+  float *dalpha, *dtheta, *dW_in;
+  float *ws_W, *ws_dW, *ws_F, *ws_dE;
+  int B, H, Hk, N, d, ld, chunks, parts;
+};
+
+template <int DP, bool F32>
+using GradLds = ChunkLds<DP, F32 ? 3 : 1, 3, 32>;
+
+// ---- the two sweeps: blocks of the first half forwards, of the second backwards ----
+template <int DP, bool F32, int PB, int NB, int VB>
+__global__ void __launch_bounds__((2 + PB) * 64) delta_sweep_kernel(GradParams p) {
+  constexpr int CW = 2, NP = F32 ? 3 : 1;
+  constexpr int NT = DP / 16, NK = DP / 32, kE = F32 ? 4 : 2;
+  using Lds = GradLds<DP, F32>;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  int* built = (int*)(smem + NB * Lds::BYTES);
+  int* used = built + PB;
+  const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = gridDim.x / 2;   // a multiple of 8
+  const bool back = (int)blockIdx.x >= half;
+  const int bid = back ? blockIdx.x - half : blockIdx.x, idx = bid >> 3;
+  const int s = (idx / p.parts) * 8 + (bid & 7), part = idx % p.parts;
+  if (s >= p.B * p.H) return;
+  const int b = s / p.H, h = s % p.H, d = p.d;
+  const int n = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
+  const int chunks = (n + kC - 1) / kC;
+  init_ring<Lds, NB, CW, PB>(smem, built, wave, lane);
+
+  if (wave >= CW) {
+    const int col0 = part * CW * 16;
+    const int64_t krow = ((int64_t)b * p.Hk + h / (p.H / p.Hk)) * p.N * d, vrow = (int64_t)s * p.N * d + col0;
+    const char *k = (const char*)p.k + krow * kE, *q = (const char*)p.q + krow * kE;
+    const float *alpha = p.alpha + (int64_t)s * p.N, *theta = p.theta + (int64_t)s * p.N;
+    if (back)
+      run_builder<DP, F32, CW, PB, NB, VB, 3, true, true>(smem, built, used, wave - CW, lane, chunks, n, d, d - col0, k, q,
+                                                          (const char*)p.dy + vrow * kE, alpha, theta, kForget);
+    else
+      run_builder<DP, F32, CW, PB, NB, VB, 3, false, false>(smem, built, used, wave - CW, lane, chunks, n, d, d - col0, k,
+                                                            q, (const char*)p.v + vrow * kE, alpha, theta, kForget);
+    return;
+  }
+
+  const int cg = part * CW + wave, col = cg * 16 + li;
+  const bool kept = cg * 16 < p.ld;   // a whole tile of columns, or none
+  f32x4 S[NT];
+  if (back && !p.dW_out) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  } else {
+    load_state<NT, VB>(S, back ? p.dW_out : p.W_in, s, col, d, g);
+  }
+  for (int i = 0; i < chunks; ++i) {
+    const int c = back ? chunks - 1 - i : i;
+    const int64_t at = (int64_t)s * p.chunks + c;
+    float* state = (back ? p.ws_dW : p.ws_W) + (at * p.ld + col) * p.ld + 4 * g;
+    f32x4* tiles = (f32x4*)((back ? p.ws_dE : p.ws_F) + ((at * (p.ld / 16) + cg) * 64 + lane) * 8);
+    if (kept) {
+#pragma unroll
+      for (int ti = 0; ti < NT; ++ti)
+        if (16 * ti < p.ld) *(f32x4*)(state + 16 * ti) = S[ti];
+    }
+    wait_for(built + i % PB, i + 1);
+    const Lds L{smem + i % NB * Lds::BYTES};
+    f32x4 ks[2], V[2], G[2], E[2], X[2];
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) ks[rt] = X[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    bf16x8 vp[3];
+    if constexpr (F32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        V[e >> 2][e & 3] = ((const float*)L.v())[(16 * (e >> 2) + 4 * g + (e & 3)) * Lds::VS + 16 * wave + li];
+    } else {
+      vp[0] = read_transposed<false>((const uint16_t*)L.v(), Lds::VS, 16 * wave, lane);
+      const u32x4 x = __builtin_bit_cast(u32x4, vp[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) V[e >> 2][e & 3] = e & 1 ? top(flt(x[e >> 1])) : flt(x[e >> 1] << 16);
+    }
+    const float gc = L.gc()[0], scale = L.gc()[1];
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) {
+      G[rt] = *(const f32x4*)(L.g() + 16 * rt + 4 * g);
+      E[rt] = *(const f32x4*)(L.eth() + 16 * rt + 4 * g);
+    }
+#pragma unroll
+    for (int kx = 0; kx < NK; ++kx) {
+      bf16x8 ra[2][NP], sp[3];
+      read2<NP>(L.k() + li * Lds::RS + 8 * g + 32 * kx, Lds::KP, 16 * Lds::RS, ra);
+      split8<3>(S[2 * kx], S[2 * kx + 1], sp);
+      mul2<false, 3>(ra, sp, ks);
+    }
+    // forwards: R = V - G K W^T, X = F = T R; backwards: R = dF, X = dE = T^T dF
+    f32x4 R[2];
+    bf16x8 ra[2][3], rp[3];
+    if (!back) {
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) R[rt] = V[rt] - G[rt] * ks[rt];
+      read2<3>(L.t() + li * kCS + 8 * g, Lds::CP, 16 * kCS, ra);
+    } else {
+      if constexpr (F32) split8<3>(V[0], V[1], vp);
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) ra[rt][e] = read_transposed<true>(L.p() + e * Lds::CP, kCS, 16 * rt, lane);
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) R[rt] = ks[rt] * E[rt] * scale;
+      if constexpr (F32) {
+        mul2<false, 3>(ra, vp, R);
+      } else {
+        bf16x8 one[1] = {vp[0]};
+        mul2<false, 1>(ra, one, R);
+      }
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) ra[rt][e] = read_transposed<true>(L.t() + e * Lds::CP, kCS, 16 * rt, lane);
+    }
+    split8<3>(R[0], R[1], rp);
+    mul2<false, 3>(ra, rp, X);
+    if (kept) tiles[0] = X[0], tiles[1] = X[1];
+    // forwards: W' = G_C W + K^T (E theta F); backwards: dW' = G_C dW + Q^T (G dY) - K^T (G dE)
+    f32x4 U[2], acc[NT];
+    bf16x8 up[3];
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) U[rt] = back ? X[rt] * -G[rt] : X[rt] * E[rt];
+    split8<3>(U[0], U[1], up);
+    const bool scaled = !back && __builtin_amdgcn_readfirstlane(bits(scale)) != 0x3f800000u;
+#pragma unroll
+    for (int ti = 0; ti < NT; ++ti) {
+      const f32x4 x = S[ti] * gc;
+      S[ti] = scaled ? x : f32x4{0.f, 0.f, 0.f, 0.f};
+      acc[ti] = scaled ? f32x4{0.f, 0.f, 0.f, 0.f} : x;
+    }
+    auto fold = [&](const uint16_t* rows) {
+#pragma unroll
+      for (int ti = 0; ti < NT; ++ti) {
+        bf16x8 kt[NP];
+#pragma unroll
+        for (int e = 0; e < NP; ++e) kt[e] = read_transposed<true>(rows + e * Lds::KP, Lds::RS, 16 * ti, lane);
+#pragma unroll
+        for (int o = 2; o >= 0; --o)
+#pragma unroll
+          for (int e = NP - 1; e >= 0; --e)
+            if (o - e >= 0) acc[ti] = mfma(kt[e], up[o - e], acc[ti]);
+      }
+    };
+    fold(L.k());
+    if (back) {
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) U[rt] = V[rt] * G[rt];
+      split8<3>(U[0], U[1], up);
+      fold(L.q());
+    }
+    raise_to(used + wave, i + 1, lane);
+#pragma unroll
+    for (int ti = 0; ti < NT; ++ti) S[ti] = scaled ? S[ti] + acc[ti] * scale : acc[ti];
+  }
+  if (back) store_state<NT, VB>(S, p.dW_in, s, col, d, g);
+}
+
+// ---- a chunk of a key head ----
+template <int DP, bool F32>
+struct PieceLds {
+  static constexpr int NP = F32 ? 3 : 1, NX = F32 ? 3 : 2, RS = DP + 8, KP = kC * RS, CP = kC * kCS, FP = DP * kCS,
+                       NW = DP / 16;
+  static constexpr int K = 0, Q = K + NP * KP * 2, DY = Q + NP * KP * 2, F = DY + NP * KP * 2, DE = F + 3 * FP * 2,
+                       X = DE + 3 * FP * 2, M = X + NX * CP * 2, Z = M + NX * CP * 2, GATES = Z + kC * kBS * 4,
+                       DOTS = GATES + 9 * kC * 4, BYTES = DOTS + NW * (2 * kC + 1) * 4;
+};
+
+// sum over the 16 lanes of a DPP row, in every lane
+__device__ __forceinline__ float row_sum(float x) {
+#define TM_ROR(n) flt(__builtin_amdgcn_update_dpp(0, (int)bits(x), 0x120 + n, 0xf, 0xf, true))
+  x += TM_ROR(8);
+  x += TM_ROR(4);
+  x += TM_ROR(2);
+  x += TM_ROR(1);
+#undef TM_ROR
+  return x;
+}
+
+template <bool F32>
+__device__ __forceinline__ void put(void* p, int64_t i, float x) {
+  if (F32)
+    ((float*)p)[i] = x;
+  else
+    ((__bf16*)p)[i] = (__bf16)x;
+}
+
+// the values that planes of one operand stand for
+template <int NP>
+__device__ __forceinline__ float whole(const bf16x8 (&x)[NP], int e) {
+  float sum = (float)x[NP - 1][e];
+#pragma unroll
+  for (int i = NP - 2; i >= 0; --i) sum += (float)x[i][e];
+  return sum;
+}
+
+template <int DP, bool F32, int VB>
+__global__ void __launch_bounds__(DP * 4) delta_piece_kernel(GradParams p) {
+  using L = PieceLds<DP, F32>;
+  constexpr int NP = L::NP, NX = L::NX, NW = L::NW, NK = DP / 32, RS = L::RS, KP = L::KP, CP = L::CP, FP = L::FP;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  uint16_t *Ks = (uint16_t*)(smem + L::K), *Qs = (uint16_t*)(smem + L::Q), *dYs = (uint16_t*)(smem + L::DY);
+  uint16_t *Fs = (uint16_t*)(smem + L::F), *dEs = (uint16_t*)(smem + L::DE);   // [channel][token]
+  uint16_t *Xs = (uint16_t*)(smem + L::X), *Ms = (uint16_t*)(smem + L::M);
+  float *Z = (float*)(smem + L::Z), *gates = (float*)(smem + L::GATES), *dots = (float*)(smem + L::DOTS);
+  // log2 G as float pairs, theta, G and E; the last four with a floored (what Z uses)
+  float *gh = gates, *gl = gates + kC, *th = gates + 2 * kC, *Gt = gates + 3 * kC, *Et = gates + 4 * kC;
+  float *zh = gates + 5 * kC, *zl = gates + 6 * kC, *Gz = gates + 7 * kC, *Ez = gates + 8 * kC;
+  const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = blockIdx.x % p.chunks, bk = blockIdx.x / p.chunks, b = bk / p.Hk, hk = bk % p.Hk;
+  const int share = p.H / p.Hk, d = p.d, t0 = c * kC;
+  const int n = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
+  const int live = min(max(n - t0, 0), kC), rows = min(kC, p.N - t0);   // tokens of the sequence, and of the tensors
+  const int64_t krow = ((int64_t)bk * p.N + t0) * d;
+  const int ch = 16 * w + li;   // this lane's channel: of v when tiles are staged, of k after
+  if (live == 0) {   // past the sequence: zeros
+    const int64_t s0 = (int64_t)b * p.H + hk * share;
+    for (int e = threadIdx.x; e < rows * d; e += NW * 64) {
+      put<F32>(p.dk, krow + e, 0.f);
+      put<F32>(p.dq, krow + e, 0.f);
+      for (int x = 0; x < share; ++x) put<F32>(p.dv, ((s0 + x) * p.N + t0) * d + e, 0.f);
+    }
+    if ((int)threadIdx.x < rows)
+      for (int x = 0; x < share; ++x) p.dalpha[(s0 + x) * p.N + t0 + threadIdx.x] = p.dtheta[(s0 + x) * p.N + t0 + threadIdx.x] = 0.f;
+    return;
+  }
+  const bool tile = 16 * w < p.ld;
+  float la_z = 0.f;   // the last wave's lane t: log2 a_t, floored
+  f32x4 dq[2], dk[2];
+#pragma unroll
+  for (int rt = 0; rt < 2; ++rt) dq[rt] = dk[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int x = 0; x < share; ++x) {
+    const int s = b * p.H + hk * share + x;
+    const int64_t at = (int64_t)s * p.chunks + c;
+    // W and dW as operands over their rows (value channels), this wave's 16
+    // key channels as columns; on their way while the rest is staged
+    f32x4 Wf[NK][2], dWf[NK][2];
+#pragma unroll
+    for (int kx = 0; kx < NK; ++kx)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int row = 32 * kx + 16 * (e >> 2) + 4 * g + (e & 3);
+        const bool in = tile && 32 * kx + 16 * (e >> 2) < p.ld;
+        const int64_t o = (at * p.ld + (in ? row : 0)) * p.ld + (in ? ch : 0);
+        const float a = p.ws_W[o], bb = p.ws_dW[o];
+        Wf[kx][e >> 2][e & 3] = in ? a : 0.f;
+        dWf[kx][e >> 2][e & 3] = in ? bb : 0.f;
+      }
+    if (x > 0) __syncthreads();   // the last head's LDS is done with
+    // stage: K and Q once, dY, F and dE, the gates
+    if (w == 0 && x == 0) {
+      RowLoad<DP, DP, F32, VB> r;
+      r.load((const char*)p.k + krow * (F32 ? 4 : 2), live, d, d, lane);
+      store_planes<DP, F32>(r, Ks, lane);
+    }
+    if (w == 1 && x == 0) {
+      RowLoad<DP, DP, F32, VB> r;
+      r.load((const char*)p.q + krow * (F32 ? 4 : 2), live, d, d, lane);
+      store_planes<DP, F32>(r, Qs, lane);
+    }
+    if (w == 2) {
+      RowLoad<DP, DP, F32, VB> r;
+      r.load((const char*)p.dy + ((int64_t)s * p.N + t0) * d * (F32 ? 4 : 2), live, d, d, lane);
+      store_planes<DP, F32>(r, dYs, lane);
+    }
+    if (w == NW - 1) {
+      const int64_t gt = (int64_t)s * p.N + t0 + min(lane, live - 1);
+      const bool in = lane < live;
+      const float la = in ? log2_keep(p.alpha[gt]) : 0.f, theta = in ? p.theta[gt] : 0.f;
+      la_z = la < kForgetGrad ? kForgetGrad : la;
+      double all, all_z;
+      const double sum = prefix_sums(la, lane, all), sum_z = prefix_sums(la_z, lane, all_z);
+      const float hi = (float)sum, hi_z = (float)sum_z;
+      if (lane < kC) {
+        gh[lane] = hi;
+        gl[lane] = (float)(sum - (double)hi);
+        th[lane] = theta;
+        Gt[lane] = exp2_of(hi);
+        Et[lane] = exp2_of((float)(all - sum));
+        zh[lane] = hi_z;
+        zl[lane] = (float)(sum_z - (double)hi_z);
+        Gz[lane] = exp2_of(hi_z);
+        Ez[lane] = exp2_of((float)(all_z - sum_z));
+      }
+      // X's upper right block
+#pragma unroll
+      for (int e = 0; e < NX; ++e) *(uint2*)(Xs + e * CP + li * kCS + 8 * g + 4) = make_uint2(0, 0);
+    }
+    {
+      f32x4 f[2], e[2];
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) f[rt] = e[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (tile) {
+        const int64_t o = ((at * (p.ld / 16) + w) * 64 + lane) * 8;
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) f[rt] = ((const f32x4*)(p.ws_F + o))[rt], e[rt] = ((const f32x4*)(p.ws_dE + o))[rt];
+      }
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        put4<3>(Fs + ch * kCS + 8 * g + 4 * rt, FP, f[rt][0], f[rt][1], f[rt][2], f[rt][3]);
+        put4<3>(dEs + ch * kCS + 8 * g + 4 * rt, FP, e[rt][0], e[rt][1], e[rt][2], e[rt][3]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * rt + 4 * g + r;
+          if (ch < d && t < rows) put<F32>(p.dv, ((int64_t)s * p.N + t0 + t) * d + ch, t < live ? e[rt][r] : 0.f);
+        }
+      }
+    }
+    __syncthreads();
+    // X, M and Z by tiles, transposed (rows j, columns t): wave 0 (t 0, j 0), 1 (t 1, j 0), 2 (t 1, j 1)
+    if (w < 3) {
+      const int tt = w > 0, jt = w > 1, t = 16 * tt + li, j0 = 16 * jt + 4 * g;
+      f32x4 xx = {0.f, 0.f, 0.f, 0.f}, mm = xx, kk = xx, qk = xx;
+#pragma unroll
+      for (int kx = 0; kx < NK; ++kx) {
+        bf16x8 f[3], e[3], y[NP], kj[NP], kt[NP], qt[NP];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          f[i] = read_transposed<true>(Fs + i * FP + 32 * kx * kCS, kCS, 16 * jt, lane);
+          e[i] = read_transposed<true>(dEs + i * FP + 32 * kx * kCS, kCS, 16 * tt, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int o = i * KP + li * RS + 32 * kx + 8 * g;
+          y[i] = *(const bf16x8*)(dYs + o + 16 * tt * RS);
+          kj[i] = *(const bf16x8*)(Ks + o + 16 * jt * RS);
+          kt[i] = *(const bf16x8*)(Ks + o + 16 * tt * RS);
+          qt[i] = *(const bf16x8*)(Qs + o + 16 * tt * RS);
+        }
+#pragma unroll
+        for (int o = 2; o >= 0; --o)
+#pragma unroll
+          for (int i = o; i >= 0; --i) {
+            if (o - i < NP) xx = mfma(f[i], y[o - i], xx);
+            mm = mfma(f[i], e[o - i], mm);
+            if (i < NP && o - i < NP) {
+              kk = mfma(kj[i], kt[o - i], kk);
+              qk = mfma(kj[i], qt[o - i], qk);
+            }
+          }
+      }
+      const float tg = gh[t], tl = gl[t], tg_z = zh[t], tl_z = zl[t];
+      f32x4 z;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int j = j0 + r;
+        // (above the diagonal the powers may be infinite: they are dropped, not multiplied by 0)
+        const float D = t < j ? 0.f : exp2_of((tg - gh[j]) + (tl - gl[j])) * th[j];
+        const float Dz = t < j ? 0.f : exp2_of((tg_z - zh[j]) + (tl_z - zl[j]));
+        if (t == j) mm[r] = 0.f;
+        z[r] = Dz * (xx[r] * qk[r] - mm[r] * kk[r]);
+        xx[r] *= D;
+        mm[r] *= -D;
+      }
+      *(f32x4*)(Z + t * kBS + j0) = z;
+      put4<NX>(Xs + t * kCS + 8 * g + 4 * jt, CP, xx[0], xx[1], xx[2], xx[3]);
+      // M and its transpose; the zeros of a diagonal tile's upper half are the transpose's places
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int j = j0 + r;
+        float v = mm[r];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+          const uint16_t u = (uint16_t)(bits(v) >> 16);
+          v -= top(v);
+          if (t >= j) Ms[i * CP + t * kCS + perm32(j)] = u;
+          if (t > j) Ms[i * CP + j * kCS + perm32(t)] = u;
+        }
+      }
+    }
+    // what goes through W and dW, and its dots with q and k
+    bf16x8 kT[NP], qT[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      kT[i] = read_transposed<true>(Ks + i * KP, RS, 16 * w, lane);
+      qT[i] = read_transposed<true>(Qs + i * KP, RS, 16 * w, lane);
+    }
+    {
+      f32x4 a[2], m[2], e[2];
+      float corner = 0.f;
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) a[rt] = m[rt] = e[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kx = 0; kx < NK; ++kx) {
+        bf16x8 wp[3], dp[3], y[2][NP], f[2][3], ee[2][3];
+        split8<3>(Wf[kx][0], Wf[kx][1], wp);
+        split8<3>(dWf[kx][0], dWf[kx][1], dp);
+        read2<NP>(dYs + li * RS + 32 * kx + 8 * g, KP, 16 * RS, y);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt) {
+            f[rt][i] = read_transposed<true>(Fs + i * FP + 32 * kx * kCS, kCS, 16 * rt, lane);
+            ee[rt][i] = read_transposed<true>(dEs + i * FP + 32 * kx * kCS, kCS, 16 * rt, lane);
+          }
+        mul2<false, 3>(y, wp, a);
+        mul2<false, 3>(ee, wp, m);
+        mul2<false, 3>(f, dp, e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) corner = fmaf(Wf[kx][i >> 2][i & 3], dWf[kx][i >> 2][i & 3], corner);
+      }
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * rt + 4 * g + r;
+          const float kv = whole<NP>(kT, 4 * rt + r), qv = whole<NP>(qT, 4 * rt + r);
+          const float start = row_sum(qv * a[rt][r] - kv * m[rt][r]) * Gz[t], end = row_sum(kv * e[rt][r]) * Ez[t];
+          if (li == 0) dots[w * 2 * kC + t] = start, dots[(w * 2 + 1) * kC + t] = end;
+          dq[rt][r] = fmaf(Gt[t], a[rt][r], dq[rt][r]);
+          dk[rt][r] += Et[t] * th[t] * e[rt][r] - Gt[t] * m[rt][r];
+        }
+      corner = row_sum(corner);
+      corner += __shfl_xor(corner, 16, 64);
+      corner += __shfl_xor(corner, 32, 64);
+      if (lane == 0) dots[NW * 2 * kC + w] = corner;
+    }
+    __syncthreads();
+    // through the chunk's own tokens
+    {
+      bf16x8 xr[2][NX], xt[2][NX], mr[2][NX];
+      read2<NX>(Xs + li * kCS + 8 * g, CP, 16 * kCS, xr);
+      read2<NX>(Ms + li * kCS + 8 * g, CP, 16 * kCS, mr);
+#pragma unroll
+      for (int i = 0; i < NX; ++i)
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) xt[rt][i] = read_transposed<true>(Xs + i * CP, kCS, 16 * rt, lane);
+      mul2<false, NP>(xr, kT, dq);
+      mul2<false, NP>(xt, qT, dk);
+      mul2<false, NP>(mr, kT, dk);
+    }
+    // the gates: lane j < 32 sums column j of Z theta up from the end's row, lane 32 the start's column
+    if (w == NW - 1) {
+      float sum = 0.f, dtheta = 0.f, end = 0.f;
+      const float tj = lane < kC ? th[lane] : 0.f;
+      if (lane < kC)
+        for (int i = 0; i < NW; ++i) end += dots[(i * 2 + 1) * kC + lane];
+      if (lane == kC)
+        for (int i = 0; i < NW; ++i) sum += dots[NW * 2 * kC + i];
+      if (lane < kC) sum = end * tj;
+      sum = lane == kC ? sum * Gz[kC - 1] : sum;
+      for (int i = kC - 1; i >= 0; --i) {
+        float z = 0.f;
+        if (lane < kC) {
+          if (i >= lane) z = Z[i * kBS + lane];
+          dtheta += z;
+          z *= tj;
+        } else if (lane == kC) {
+          for (int k = 0; k < NW; ++k) z += dots[k * 2 * kC + i];
+        }
+        sum += z;
+        if (lane <= kC) Z[i * kBS + lane] = sum;
+      }
+      wave_fence();
+      if (lane < rows) {
+        const int64_t gt = (int64_t)s * p.N + t0 + lane;
+        float through = Z[lane * kBS + kC];
+        for (int j = 0; j < lane; ++j) through += Z[lane * kBS + j];
+        p.dtheta[gt] = lane < live ? dtheta + end : 0.f;
+        p.dalpha[gt] = lane < live ? -through * exp2_of(-la_z) : 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * rt + 4 * g + r;
+      if (ch < d && t < rows) {
+        put<F32>(p.dq, krow + (int64_t)t * d + ch, t < live ? dq[rt][r] : 0.f);
+        put<F32>(p.dk, krow + (int64_t)t * d + ch, t < live ? dk[rt][r] : 0.f);
+      }
+    }
+}
+
+template <int DP, bool F32, int VB>
+hipError_t launch_grad(GradParams p, hipStream_t stream) {
+  constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : DP == 64 ? 3 : 4, PB = F32 && DP == 128 ? 1 : 2;
+  constexpr int lds = NB * GradLds<DP, F32>::BYTES + (PB + 2) * 4, piece = PieceLds<DP, F32>::BYTES;
+  static_assert(lds <= 160 * 1024 && piece <= 160 * 1024, "LDS of one workgroup");
+  auto sweep = delta_sweep_kernel<DP, F32, PB, NB, VB>;
+  auto pieces = delta_piece_kernel<DP, F32, VB>;
+  hipError_t err = hipFuncSetAttribute((const void*)sweep, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (err != hipSuccess) return err;
+  err = hipFuncSetAttribute((const void*)pieces, hipFuncAttributeMaxDynamicSharedMemorySize, piece);
+  if (err != hipSuccess) return err;
+  p.parts = ((p.d + 15) / 16 + 1) / 2;
+  const unsigned half = (unsigned)((p.B * p.H + 7) / 8 * 8 * p.parts);
+  sweep<<<2 * half, (2 + PB) * 64, lds, stream>>>(p);
+  err = hipGetLastError();
+  if (err != hipSuccess || p.chunks == 0) return err;
+  pieces<<<(unsigned)(p.B * p.Hk * p.chunks), DP * 4, piece, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <bool F32, int VB>
+hipError_t launch_width(const GradParams& p, hipStream_t stream) {
+  return p.d <= 64 ? launch_grad<64, F32, VB>(p, stream) : launch_grad<128, F32, VB>(p, stream);
+}
+
+int64_t state_floats(const DeltaShape& s) {
+  const int64_t ld = (s.d + 15) / 16 * 16;
+  return (int64_t)s.B * s.H * ((s.N + kC - 1) / kC) * ld * ld;
+}
+int64_t tile_floats(const DeltaShape& s) {
+  const int64_t ld = (s.d + 15) / 16 * 16;
+  return (int64_t)s.B * s.H * ((s.N + kC - 1) / kC) * kC * ld;
+}
+
+}  // namespace
+
+bool delta_backward_supported(const DeltaShape& s) {
+  return (int64_t)s.B * s.Hk * ((s.N + kC - 1) / kC) < (int64_t)1 << 31;
+}
+
+int64_t delta_backward_ws_bytes(const DeltaShape& s) { return 8 * (state_floats(s) + tile_floats(s)); }
+
+hipError_t launch_delta_backward(const DeltaShape& s, const void* k, const void* v, const void* q, const float* alpha,
+                                 const float* theta, const int32_t* lengths, const float* W_in, const void* dy,
+                                 const float* dW_out, void* dk, void* dv, void* dq, float* dalpha, float* dtheta,
+                                 float* dW_in, float* ws, hipStream_t stream) {
+  GradParams p = {k, v, q, dy, alpha, theta, W_in, dW_out, lengths, dk, dv, dq, dalpha, dtheta, dW_in};
+  p.ws_W = ws, p.ws_dW = ws + state_floats(s);
+  p.ws_F = ws + 2 * state_floats(s), p.ws_dE = p.ws_F + tile_floats(s);
+  p.B = s.B, p.H = s.H, p.Hk = s.Hk, p.N = s.N, p.d = s.d, p.ld = (s.d + 15) / 16 * 16;
+  p.chunks = (s.N + kC - 1) / kC;
+  if (s.io == TM_IO_BF16) {
+    if (s.d % 8 == 0) return launch_width<false, 16>(p, stream);
+    return s.d % 4 == 0 ? launch_width<false, 8>(p, stream) : launch_width<false, 0>(p, stream);
+  }
+  return s.d % 4 == 0 ? launch_width<true, 16>(p, stream) : launch_width<true, 0>(p, stream);
+}
+
+}  // namespace titans

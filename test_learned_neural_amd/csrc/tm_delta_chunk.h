@@ -150,13 +150,15 @@ __device__ __forceinline__ double lane_f64(double x, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// log2(1 - alpha); alpha = 1: -2000; above 1: NaN.  1 - alpha is rounded, by
+// log2(1 - alpha), at least `floor` (-2000: alpha = 1 gives exact zeros); NaN
+// for alpha above 1.  1 - alpha is rounded, by
 // u; log2 u (-alpha) / (u - 1) is log2(1 - alpha) to a few units in the last
 // place, as log x / (x - 1) hardly changes over one rounding of x.
-__device__ __forceinline__ float log2_keep(float alpha) {
+constexpr float kForget = -2000.f;
+__device__ __forceinline__ float log2_keep(float alpha, float floor = kForget) {
   const float u = 1.f - alpha, x = u - 1.f;
   const float l = x == 0.f ? -alpha * 1.44269504088896f : __builtin_amdgcn_logf(u) * (-alpha * __builtin_amdgcn_rcpf(x));
-  return l < -2000.f ? -2000.f : l;
+  return l < floor ? floor : l;
 }
 
 // LDS of one chunk: NP planes of K and Q, three of T = (I + B)^-1, NPP of P,
@@ -167,7 +169,7 @@ struct ChunkLds {
   static constexpr int KP = kC * RS, CP = kC * kCS; // plane sizes
   static constexpr int OFF_K = 0, OFF_Q = OFF_K + NP * KP * 2, OFF_T = OFF_Q + NP * KP * 2, OFF_P = OFF_T + 3 * CP * 2,
                        OFF_G = OFF_P + NPP * CP * 2, OFF_V = OFF_G + (2 * kC + 4) * 4,
-                       VS = VC + (NP == 1 ? 8 : 4),   // row stride of V: bf16, or fp32 where NP is 3
+                       VS = VC + 4,   // row stride of V: bf16, or fp32 where NP is 3
                        BYTES = OFF_V + kC * VS * (NP == 1 ? 2 : 4);
   static_assert(NPP * CP * 2 >= kC * kBS * 4, "the fp32 scratch lies where P comes to lie");
   static_assert(16 * kCS * 2 >= 3 * kC * 4, "the gates' scratch lies in T's lower half");
@@ -275,21 +277,28 @@ __device__ __forceinline__ void store_planes(Load& rows, uint16_t* dst, int lane
   });
 }
 
-// One wave builds a chunk's matrices in LDS from its K and Q (already stored)
-// and its gates (lane t < 32: token t's log2 a and theta; 0 past the end).
-template <int DP, int NP, int NPP, int VC>
-__device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP, VC>& L, float la, float th, int lane) {
-  using Lds = ChunkLds<DP, NP, NPP, VC>;
-  const int g = lane >> 4, li = lane & 15;
-  // prefix sums of log2 a in fp64 over lanes 0..31, by DPP (16 lanes a row)
-  double sum = la;
+// Prefix sums over lanes 0..31 and their total, in fp64, by DPP (16 lanes a row).
+__device__ __forceinline__ double prefix_sums(float x, int lane, double& all) {
+  double sum = x;
   sum += dpp_f64<0x111>(sum);
   sum += dpp_f64<0x112>(sum);
   sum += dpp_f64<0x114>(sum);
   sum += dpp_f64<0x118>(sum);
   const double half = lane_f64(sum, 15);
   if (lane >= 16) sum += half;
-  const double all = lane_f64(sum, kC - 1);
+  all = lane_f64(sum, kC - 1);
+  return sum;
+}
+
+// One wave builds a chunk's matrices in LDS from its K and Q (already stored)
+// and its gates (lane t < 32: token t's log2 a and theta; 0 past the end).
+// WITH_Q: P too.
+template <bool WITH_Q, int DP, int NP, int NPP, int VC>
+__device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP, VC>& L, float la, float th, int lane) {
+  using Lds = ChunkLds<DP, NP, NPP, VC>;
+  const int g = lane >> 4, li = lane & 15;
+  double all;
+  const double sum = prefix_sums(la, lane, all);
   const float hi = (float)sum;
   // E theta f is split into planes, whose last bits lie 2^-24 below it: where theta alone would bring them near the
   // least fp32 exponent (or theta f near the largest), a power of two is taken out of theta
@@ -324,8 +333,10 @@ __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP, VC>& L, 
     for (int i = 0; i < NP; ++i) {
       k0[i] = *(const bf16x8*)(L.k() + i * Lds::KP + at);
       k1[i] = *(const bf16x8*)(L.k() + i * Lds::KP + 16 * Lds::RS + at);
-      q0[i] = *(const bf16x8*)(L.q() + i * Lds::KP + at);
-      q1[i] = *(const bf16x8*)(L.q() + i * Lds::KP + 16 * Lds::RS + at);
+      if (WITH_Q) {
+        q0[i] = *(const bf16x8*)(L.q() + i * Lds::KP + at);
+        q1[i] = *(const bf16x8*)(L.q() + i * Lds::KP + 16 * Lds::RS + at);
+      }
     }
 #pragma unroll
     for (int o = NP - 1; o >= 0; --o)
@@ -334,9 +345,11 @@ __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP, VC>& L, 
         kk[0] = mfma(k0[i], k0[o - i], kk[0]);
         kk[1] = mfma(k0[i], k1[o - i], kk[1]);
         kk[2] = mfma(k1[i], k1[o - i], kk[2]);
-        qk[0] = mfma(k0[i], q0[o - i], qk[0]);
-        qk[1] = mfma(k0[i], q1[o - i], qk[1]);
-        qk[2] = mfma(k1[i], q1[o - i], qk[2]);
+        if (WITH_Q) {
+          qk[0] = mfma(k0[i], q0[o - i], qk[0]);
+          qk[1] = mfma(k0[i], q1[o - i], qk[1]);
+          qk[2] = mfma(k1[i], q1[o - i], qk[2]);
+        }
       }
   }
   // lane: token t = 16 tt + li, tokens j = 16 jt + 4 g + 0..3
@@ -407,11 +420,119 @@ __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP, VC>& L, 
   put4<3>(T, Lds::CP, t00[0], t00[1], t00[2], t00[3]);
   put4<3>(T + 16 * kCS, Lds::CP, -t10[0], -t10[1], -t10[2], -t10[3]);
   put4<3>(T + 16 * kCS + 4, Lds::CP, t11[0], t11[1], t11[2], t11[3]);
+  if (!WITH_Q) return;
   uint16_t* P = L.p() + li * kCS + 8 * g;
   put4<NPP>(P, Lds::CP, qk[0][0], qk[0][1], qk[0][2], qk[0][3]);
   put4<NPP>(P + 4, Lds::CP, 0.f, 0.f, 0.f, 0.f);
   put4<NPP>(P + 16 * kCS, Lds::CP, qk[1][0], qk[1][1], qk[1][2], qk[1][3]);
   put4<NPP>(P + 16 * kCS + 4, Lds::CP, qk[2][0], qk[2][1], qk[2][2], qk[2][3]);
+}
+
+// A counter in LDS that one wave raises and others wait for.
+__device__ __forceinline__ int seen(const int* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP); }
+__device__ __forceinline__ void wait_for(const int* p, int value) {
+  while (seen(p) < value) __builtin_amdgcn_s_sleep(1);
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+__device__ __forceinline__ void raise_to(int* p, int value, int lane) {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  if (lane == 0) __hip_atomic_store(p, value, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+
+// The chunk ring of a workgroup of CW chain and PB builder waves, NB buffers:
+// counters to zero and the blocks of T that stay zero; every wave calls it.
+template <class Lds, int NB, int CW, int PB>
+__device__ __forceinline__ void init_ring(unsigned char* smem, int* built, int wave, int lane) {
+  if (threadIdx.x < PB + CW) built[threadIdx.x] = 0;
+  for (int x = wave; x < 3 * NB; x += CW + PB) {
+    Lds L{smem + x / 3 * Lds::BYTES};
+    *(uint2*)(L.t() + x % 3 * Lds::CP + (lane & 15) * kCS + 8 * (lane >> 4) + 4) = make_uint2(0, 0);
+  }
+  __syncthreads();
+}
+
+// Builder wave pw: the ring's chunks pw, pw + PB, ... (BACK: counted from the
+// sequence's end), from a stream's K, Q (WITH_Q), V rows and gates.  floor:
+// log2_keep's.
+template <int DP, bool F32, int CW, int PB, int NB, int VB, int NPP, bool WITH_Q, bool BACK>
+__device__ __forceinline__ void run_builder(unsigned char* smem, int* built, const int* used, int pw, int lane,
+                                            int chunks, int n, int d, int vcols, const char* k, const char* q,
+                                            const char* v, const float* alpha, const float* theta, float floor) {
+  constexpr int NP = F32 ? 3 : 1, kE = F32 ? 4 : 2;
+  using Lds = ChunkLds<DP, NP, NPP, CW * 16>;
+  RowLoad<DP, DP, F32, VB> kr, qr;
+  RowLoad<DP, CW * 16, F32, VB> vr;
+  float al = 0.f, th = 0.f;
+  auto fetch = [&](int i) {
+    if (i >= chunks) return;
+    const int t0 = (BACK ? chunks - 1 - i : i) * kC, m = min(kC, n - t0);
+    const int64_t at = (int64_t)t0 * d * kE;
+    kr.load(k + at, m, d, d, lane);
+    if (WITH_Q) qr.load(q + at, m, d, d, lane);
+    vr.load(v + at, m, d, vcols, lane);
+    al = alpha[t0 + min(lane, m - 1)];   // (zeroed when used: nothing here waits)
+    th = theta[t0 + min(lane, m - 1)];
+  };
+  fetch(pw);
+  for (int i = pw; i < chunks; i += PB) {
+    Lds L{smem + i % NB * Lds::BYTES};
+    const bool in = (BACK ? chunks - 1 - i : i) * kC + lane < n;
+    const float la = in ? log2_keep(al, floor) : 0.f, th0 = in ? th : 0.f;
+#pragma unroll
+    for (int w = 0; w < CW; ++w) wait_for(used + w, i - NB + 1);
+    store_planes<DP, F32>(kr, L.k(), lane);
+    if (WITH_Q) store_planes<DP, F32>(qr, L.q(), lane);
+    vr.store(lane, [&](int r, int c, const uint32_t* x) {
+      if constexpr (F32)
+        *(uint4*)((float*)L.v() + r * Lds::VS + c) = make_uint4(x[0], x[1], x[2], x[3]);
+      else
+        *(uint2*)((uint16_t*)L.v() + r * Lds::VS + c) = make_uint2(x[0], x[1]);
+    });
+    fetch(i + PB);
+    wave_fence();
+    build_chunk<WITH_Q>(L, la, th0, lane);
+    raise_to(built + pw, i + 1, lane);
+  }
+}
+
+// A chain wave's 16 columns of W^T from and to the [d x d] state of stream s:
+// lane's column `col`, tile i's rows 16 i + 4 g + 0..3.
+template <int NT, int VB>
+__device__ __forceinline__ void load_state(f32x4 (&S)[NT], const float* W, int s, int col, int d, int g) {
+  const bool live = col < d;
+  const int64_t at = (int64_t)s * d * d + (int64_t)col * d;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int c = 16 * i + 4 * g;
+    S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (VB) {
+      if (live && c < d) S[i] = *(const f32x4*)(W + at + c);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool in = live && c + r < d;
+        const float w = W[in ? at + c + r : 0];
+        S[i][r] = in ? w : 0.f;
+      }
+    }
+  }
+}
+template <int NT, int VB>
+__device__ __forceinline__ void store_state(const f32x4 (&S)[NT], float* W, int s, int col, int d, int g) {
+  if (col >= d) return;
+  float* to = W + (int64_t)s * d * d + (int64_t)col * d;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int c = 16 * i + 4 * g;
+    if (VB) {
+      if (c < d) *(f32x4*)(to + c) = S[i];
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (c + r < d) to[c + r] = S[i][r];
+    }
+  }
 }
 
 }  // namespace

@@ -29,17 +29,6 @@ struct ChainParams {
   int streams, H, Hk, N, d, parts;
 };
 
-// A counter in LDS that one wave raises and others wait for.
-__device__ __forceinline__ int seen(const int* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP); }
-__device__ __forceinline__ void wait_for(const int* p, int value) {
-  while (seen(p) < value) __builtin_amdgcn_s_sleep(1);
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-__device__ __forceinline__ void raise_to(int* p, int value, int lane) {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  if (lane == 0) __hip_atomic_store(p, value, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-}
-
 template <int DP, bool F32, int CW, int PB, int NB, int VB>
 __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams p) {
   static_assert(NB > PB, "a chunk is consumed while PB are built");
@@ -58,74 +47,22 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
   const int b = s / p.H, h = s % p.H, d = p.d;
   const int n = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
   const int chunks = (n + kC - 1) / kC;
-  if (threadIdx.x < PB + CW) built[threadIdx.x] = 0;
-  // T's block that stays zero
-  for (int x = wave; x < 3 * NB; x += CW + PB) {
-    Lds L{smem + x / 3 * Lds::BYTES};
-    *(uint2*)(L.t() + x % 3 * Lds::CP + li * kCS + 8 * g + 4) = make_uint2(0, 0);
-  }
-  __syncthreads();
+  init_ring<Lds, NB, CW, PB>(smem, built, wave, lane);
 
   if (wave >= CW) {
-    // ---- builder ----
-    const int pw = wave - CW, col0 = part * CW * 16;
-    const int64_t krow = ((int64_t)b * p.Hk + h / (p.H / p.Hk)) * p.N;
-    const float *alpha = p.alpha + (int64_t)s * p.N, *theta = p.theta + (int64_t)s * p.N;
-    RowLoad<DP, DP, F32, VB> kr, qr;
-    RowLoad<DP, CW * 16, F32, VB> vr;
-    float al = 0.f, th = 0.f;
-    auto fetch = [&](int c) {
-      const int t0 = c * kC, m = min(kC, n - t0);
-      if (m <= 0) return;
-      kr.load((const char*)p.k + (krow + t0) * d * kE, m, d, d, lane);
-      qr.load((const char*)p.q + (krow + t0) * d * kE, m, d, d, lane);
-      vr.load((const char*)p.v + (((int64_t)s * p.N + t0) * d + col0) * kE, m, d, d - col0, lane);
-      al = alpha[t0 + min(lane, m - 1)];   // (zeroed when used: nothing here waits)
-      th = theta[t0 + min(lane, m - 1)];
-    };
-    fetch(pw);
-    for (int c = pw; c < chunks; c += PB) {
-      Lds L{smem + c % NB * Lds::BYTES};
-      const bool in = c * kC + lane < n;
-      const float la = in ? log2_keep(al) : 0.f, th0 = in ? th : 0.f;
-#pragma unroll
-      for (int w = 0; w < CW; ++w) wait_for(used + w, c - NB + 1);
-      store_planes<DP, F32>(kr, L.k(), lane);
-      store_planes<DP, F32>(qr, L.q(), lane);
-      vr.store(lane, [&](int r, int cc, const uint32_t* x) {
-        if constexpr (F32)
-          *(uint4*)((float*)L.v() + r * Lds::VS + cc) = make_uint4(x[0], x[1], x[2], x[3]);
-        else
-          *(uint2*)((uint16_t*)L.v() + r * Lds::VS + cc) = make_uint2(x[0], x[1]);
-      });
-      fetch(c + PB);
-      wave_fence();
-      build_chunk(L, la, th0, lane);
-      raise_to(built + pw, c + 1, lane);
-    }
+    const int col0 = part * CW * 16;
+    const int64_t krow = ((int64_t)b * p.Hk + h / (p.H / p.Hk)) * p.N * d, vrow = (int64_t)s * p.N * d + col0;
+    run_builder<DP, F32, CW, PB, NB, VB, NPP, true, false>(
+        smem, built, used, wave - CW, lane, chunks, n, d, d - col0, (const char*)p.k + krow * kE,
+        (const char*)p.q + krow * kE, (const char*)p.v + vrow * kE, p.alpha + (int64_t)s * p.N,
+        p.theta + (int64_t)s * p.N, kForget);
     return;
   }
 
   // ---- chain ----
   const int col = (part * CW + wave) * 16 + li;   // this lane's value channel
-  const bool live = col < d;
-  const float* W_in = p.W_in + (int64_t)s * d * d + (int64_t)col * d;
   f32x4 S[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int c = 16 * i + 4 * g;
-    S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (VB) {
-      if (live && c < d) S[i] = *(const f32x4*)(W_in + c);
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const bool in = live && c + r < d;
-        const float w = p.W_in[in ? (int64_t)s * d * d + col * d + c + r : 0];
-        S[i][r] = in ? w : 0.f;
-      }
-    }
-  }
+  load_state<NT, VB>(S, p.W_in, s, col, d, g);
   // y's tiles are computed transposed: a lane has 4 consecutive channels of
   // a token, stored in one piece at a uniform address per chunk plus this
   const int ych = (part * CW + wave) * 16 + 4 * g;
@@ -252,19 +189,7 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
       }
     }
   }
-  if (!live) return;
-  float* W_out = p.W_out + (int64_t)s * d * d + (int64_t)col * d;
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int c = 16 * i + 4 * g;
-    if (VB) {
-      if (c < d) *(f32x4*)(W_out + c) = S[i];
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (c + r < d) W_out[c + r] = S[i][r];
-    }
-  }
+  store_state<NT, VB>(S, p.W_out, s, col, d, g);
 }
 
 template <int DP, bool F32, int CW, int PB, int NB, int VB>

@@ -446,6 +446,52 @@ int titans_mem_delta_forward(const titans_delta_desc* desc, const void* k, const
   return err == hipSuccess ? TM_OK : TM_ERR_HIP;
 }
 
+int64_t titans_mem_delta_backward_workspace_bytes(const titans_delta_desc* desc) {
+  DeltaShape s;
+  int rc = build_delta(desc, &s);
+  if (rc) return rc;
+  return titans::delta_backward_supported(s) ? titans::delta_backward_ws_bytes(s) : TM_ERR_UNSUPPORTED;
+}
+
+int titans_mem_delta_backward(const titans_delta_desc* desc, const void* k, const void* v, const void* q,
+                              const float* alpha, const float* theta, const int32_t* lengths, const float* W_in,
+                              const void* dy, const float* dW_out, void* dk, void* dv, void* dq, float* dalpha,
+                              float* dtheta, float* dW_in, void* workspace, int64_t workspace_bytes, void* stream) {
+  DeltaShape s;
+  int rc = build_delta(desc, &s);
+  if (rc) return rc;
+  const int64_t esz = s.io == TM_IO_BF16 ? 2 : 4;
+  const int64_t keys = (int64_t)s.B * s.Hk * s.N * s.d * esz, vals = (int64_t)s.B * s.H * s.N * s.d * esz;
+  const int64_t gates = (int64_t)s.B * s.H * s.N * 4, state = (int64_t)s.B * s.H * s.d * s.d * 4;
+  const void* key_ptrs[] = {k, q, dk, dq};
+  const void* val_ptrs[] = {v, dy, dv};
+  const void* gate_ptrs[] = {alpha, theta, dalpha, dtheta};
+  for (const void* p : key_ptrs)
+    if (!needed(p, keys)) return TM_ERR_INVALID;
+  for (const void* p : val_ptrs)
+    if (!needed(p, vals)) return TM_ERR_INVALID;
+  for (const void* p : gate_ptrs)
+    if (!needed(p, gates)) return TM_ERR_INVALID;
+  if (!needed(W_in, state) || !needed(dW_in, state) || !aligned16(lengths) || !aligned16(dW_out) || !aligned16(workspace))
+    return TM_ERR_INVALID;
+  const int64_t need = titans_mem_delta_backward_workspace_bytes(desc);
+  if (need < 0) return (int)need;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return TM_ERR_WORKSPACE;
+  const Range r[] = {{(const char*)k, keys, false},       {(const char*)v, vals, false},
+                     {(const char*)q, keys, false},       {(const char*)alpha, gates, false},
+                     {(const char*)theta, gates, false},  {(const char*)lengths, (int64_t)s.B * 4, false},
+                     {(const char*)W_in, state, false},   {(const char*)dy, vals, false},
+                     {(const char*)dW_out, state, false}, {(const char*)dk, keys, true},
+                     {(const char*)dv, vals, true},       {(const char*)dq, keys, true},
+                     {(const char*)dalpha, gates, true},  {(const char*)dtheta, gates, true},
+                     {(const char*)dW_in, state, true},   {(const char*)workspace, need, true}};
+  if (!disjoint(r, 16)) return TM_ERR_ALIAS;
+  return titans::launch_delta_backward(s, k, v, q, alpha, theta, lengths, W_in, dy, dW_out, dk, dv, dq, dalpha, dtheta,
+                                       dW_in, (float*)workspace, (hipStream_t)stream) == hipSuccess
+             ? TM_OK
+             : TM_ERR_HIP;
+}
+
 int titans_mem_group_norm(const titans_norm_desc* desc, const void* x, const void* gate, const float* weight,
                           const float* bias, const int32_t* lengths, void* out, void* stream) {
   NormShape s;

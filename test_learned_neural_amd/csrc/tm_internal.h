@@ -135,6 +135,14 @@ hipError_t launch_delta_chunked(const DeltaShape& s, const void* k, const void* 
                                 const float* theta, const int32_t* lengths, const float* W_in, void* y, float* W_out,
                                 hipStream_t stream);
 
+// Gradients through the gated delta memory; dy and dk, dv, dq in the io type.
+bool delta_backward_supported(const DeltaShape& s);
+int64_t delta_backward_ws_bytes(const DeltaShape& s);
+hipError_t launch_delta_backward(const DeltaShape& s, const void* k, const void* v, const void* q, const float* alpha,
+                                 const float* theta, const int32_t* lengths, const float* W_in, const void* dy,
+                                 const float* dW_out, void* dk, void* dv, void* dq, float* dalpha, float* dtheta,
+                                 float* dW_in, float* ws, hipStream_t stream);
+
 // Group norm with an activation (one head's d channels of a token a group)
 // and its gradient.  gate, weight, bias and lengths may be null; first: x is
 // [B,H,N,d], else [B,N,H d].

@@ -31,6 +31,7 @@ EXPORTS = ("titans_mem_abi_version", "titans_mem_param_count", "titans_mem_selec
            "titans_mem_workspace_status", "titans_mem_retrieve",
            "titans_mem_input", "titans_mem_backward", "titans_mem_backward_workspace_bytes",
            "titans_mem_delta_select_path", "titans_mem_delta_workspace_bytes", "titans_mem_delta_forward",
+           "titans_mem_delta_backward", "titans_mem_delta_backward_workspace_bytes",
            "titans_mem_group_norm", "titans_mem_group_norm_backward",
            "titans_mem_group_norm_backward_workspace_bytes", "titans_mem_status_string")
 
@@ -131,6 +132,10 @@ def load():
     lib.titans_mem_delta_workspace_bytes.argtypes = [ep]
     lib.titans_mem_delta_forward.restype = ctypes.c_int
     lib.titans_mem_delta_forward.argtypes = [ep, vp, vp, vp, fp, fp, vp, fp, vp, fp, vp, i64, vp]
+    lib.titans_mem_delta_backward_workspace_bytes.restype = i64
+    lib.titans_mem_delta_backward_workspace_bytes.argtypes = [ep]
+    lib.titans_mem_delta_backward.restype = ctypes.c_int
+    lib.titans_mem_delta_backward.argtypes = [ep, vp, vp, vp, fp, fp, vp, fp, vp, fp, vp, vp, vp, fp, fp, fp, vp, i64, vp]
     lib.titans_mem_group_norm.restype = ctypes.c_int
     lib.titans_mem_group_norm.argtypes = [nq, vp, vp, fp, fp, vp, vp, vp]
     lib.titans_mem_group_norm_backward_workspace_bytes.restype = i64
@@ -215,6 +220,17 @@ def raw_delta_forward(desc: DeltaDesc, k, v, q, alpha, theta, lengths, W_in, y_o
     """Direct call of titans_mem_delta_forward with integer device addresses; returns the status."""
     return load().titans_mem_delta_forward(ctypes.byref(desc), k, v, q, alpha, theta, lengths, W_in, y_out, W_out,
                                            workspace, workspace_bytes_, stream)
+
+
+def delta_backward_workspace_bytes(desc: DeltaDesc) -> int:
+    return int(load().titans_mem_delta_backward_workspace_bytes(ctypes.byref(desc)))
+
+
+def raw_delta_backward(desc: DeltaDesc, k, v, q, alpha, theta, lengths, W_in, dy, dW_out, dk, dv, dq, dalpha, dtheta,
+                       dW_in, workspace, workspace_bytes_, stream) -> int:
+    """Direct call of titans_mem_delta_backward with integer device addresses; returns the status."""
+    return load().titans_mem_delta_backward(ctypes.byref(desc), k, v, q, alpha, theta, lengths, W_in, dy, dW_out, dk,
+                                            dv, dq, dalpha, dtheta, dW_in, workspace, workspace_bytes_, stream)
 
 
 def raw_group_norm(desc: NormDesc, x, gate, weight, bias, lengths, out, stream) -> int:
@@ -499,6 +515,31 @@ def delta_forward(k, v, q, alpha, theta, W_in, *, lengths=None, force_recurrent:
                alpha.data_ptr(), theta.data_ptr(), _ptr(lengths), W_in.data_ptr(), y_out.data_ptr(), W_out.data_ptr(),
                _ptr(ws), ws_bytes)
     return y_out, W_out
+
+
+def delta_backward(k, v, q, alpha, theta, W_in, *, dy, dW_out=None, lengths=None, workspace=None):
+    """Gradients through delta_forward() (titans_mem_delta_backward).
+
+    Same inputs as delta_forward(); dy: [B, H, N, d] in k's type; dW_out:
+    [B, H, d, d] float32 or None (zero).  Returns a dict: k, q [B, Hk, N, d]
+    (summed over the value heads of a key head) and v [B, H, N, d] in k's
+    type, alpha, theta [B, H, N] and W_in [B, H, d, d] float32.
+    """
+    torch = _torch()
+    B, H, Hk, N, d, dev = _check_delta(k, v, q, alpha, theta, W_in, lengths)
+    _check(dy, "dy", (B, H, N, d), k.dtype, dev)
+    if dW_out is not None:
+        _check(dW_out, "dW_out", (B, H, d, d), torch.float32, dev)
+    desc = make_delta_desc(B, H, Hk, N, d, _io_of(k))
+    g = {n: torch.empty_like(t) for n, t in
+         (("k", k), ("v", v), ("q", q), ("alpha", alpha), ("theta", theta), ("W_in", W_in))}
+    ws, ws_bytes = _workspace(workspace, delta_backward_workspace_bytes(desc), dev,
+                              "titans_mem_delta_backward_workspace_bytes")
+    _on_device(dev, "titans_mem_delta_backward", raw_delta_backward, desc, k.data_ptr(), v.data_ptr(), q.data_ptr(),
+               alpha.data_ptr(), theta.data_ptr(), _ptr(lengths), W_in.data_ptr(), dy.data_ptr(), _ptr(dW_out),
+               g["k"].data_ptr(), g["v"].data_ptr(), g["q"].data_ptr(), g["alpha"].data_ptr(), g["theta"].data_ptr(),
+               g["W_in"].data_ptr(), _ptr(ws), ws_bytes)
+    return g
 
 
 def _check_norm(x, weight, bias, H, gate, lengths, activation, eps):

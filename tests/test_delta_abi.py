@@ -151,3 +151,44 @@ def test_wrappers_refuse_before_the_library():
             tmm.group_norm(*args, **kw)
     with pytest.raises(ValueError):
         tmm.group_norm_backward(x, None, None, torch.zeros(2, 4, 23))
+
+
+class DeltaGrad(Delta):
+    def __init__(self, io="bf16", N=100, **kw):
+        super().__init__(io, N, **kw)
+        e = 2 if io == "bf16" else 4
+        key, val, gate, state = 2 * 3 * N * 64 * e, 2 * 6 * N * 64 * e, 2 * 6 * N * 4, 12 * 64 * 64 * 4
+        self.ws = tmm.delta_backward_workspace_bytes(self.desc)
+        self.p = _lay(dict(k=key, v=val, q=key, alpha=gate, theta=gate, lengths=8, W_in=state, dy=val, dW_out=state,
+                           dk=key, dv=val, dq=key, dalpha=gate, dtheta=gate, dW_in=state, ws=self.ws))
+
+    def call(self, **over):
+        p = {**self.p, "ws_bytes": self.ws, **over}
+        return tmm.raw_delta_backward(self.desc, *(p[n] for n in (
+            "k", "v", "q", "alpha", "theta", "lengths", "W_in", "dy", "dW_out", "dk", "dv", "dq", "dalpha", "dtheta",
+            "dW_in", "ws", "ws_bytes")), 0)
+
+
+@pytest.mark.parametrize("field,value,status", [
+    ("abi_version", 2, "INVALID"), ("H", 7, "INVALID"), ("N", -2, "INVALID"), ("io_dtype", -1, "INVALID"),
+    ("d", 200, "UNSUPPORTED"), ("B", 1 << 23, "UNSUPPORTED")])
+def test_delta_backward_descriptor(field, value, status):
+    c = DeltaGrad()
+    setattr(c.desc, field, value)
+    want = getattr(tmm, "ERR_" + status)
+    assert tmm.delta_backward_workspace_bytes(c.desc) == want and c.call() == want
+
+
+def test_delta_backward_pointers_and_overlaps():
+    c = DeltaGrad()
+    names = [n for n in c.p if n != "ws"]
+    for name in names:
+        assert c.call(**{name: c.p[name] + 8}) == tmm.ERR_INVALID, name
+        if name not in ("lengths", "dW_out"):
+            assert c.call(**{name: 0}) == tmm.ERR_INVALID, name
+    for out in ("dk", "dv", "dq", "dalpha", "dtheta", "dW_in", "ws"):
+        for name in names:
+            if name != out:
+                assert c.call(**{out: c.p[name]}) == tmm.ERR_ALIAS, (out, name)
+    assert c.call(ws=0) == tmm.ERR_WORKSPACE
+    assert c.call(ws_bytes=c.ws - 1) == tmm.ERR_WORKSPACE
