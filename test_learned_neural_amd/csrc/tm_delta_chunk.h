@@ -90,22 +90,42 @@ __device__ __forceinline__ void read2(const uint16_t* a, int plane, int step, bf
     for (int t = 0; t < 2; ++t) av[t][i] = *(const bf16x8*)(a + i * plane + t * step);
 }
 
-// c += A B for the two tiles; the products kept are those of planes
-// i + j < max(NA, NB), smallest first, the two tiles' accumulation chains in
-// turn.  B may have more planes than NB.  SWAP: the product's transpose (an
-// operand's lanes hold the same values on either side).
+// The products of planes kept for operands of NA and NB planes, those with
+// i + j < max(NA, NB), smallest first.
+struct Planes {
+  int i, j;
+};
+template <int NA, int NB>
+constexpr int products() {
+  int n = 0;
+  for (int i = 0; i < NA; ++i)
+    for (int j = 0; j < NB; ++j) n += i + j < (NA > NB ? NA : NB);
+  return n;
+}
+template <int NA, int NB>
+constexpr Planes product(int which) {
+  for (int o = (NA > NB ? NA : NB) - 1; o >= 0; --o)
+    for (int i = NA - 1; i >= 0; --i)
+      if (o - i >= 0 && o - i < NB && which-- == 0) return {i, o - i};
+  return {0, 0};
+}
+
+// c += A B for the two tiles, by the which-th of these products.  SWAP: the
+// product's transpose (an operand's lanes hold the same values on either side).
+template <bool SWAP, int NB, int NA, int MB>
+__device__ __forceinline__ void mul2_one(int which, const bf16x8 (&av)[2][NA], const bf16x8 (&b)[MB], f32x4 (&c)[2]) {
+  static_assert(NB <= MB, "planes of B");
+  const Planes x = product<NA, NB>(which);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) c[t] = SWAP ? mfma(b[x.j], av[t][x.i], c[t]) : mfma(av[t][x.i], b[x.j], c[t]);
+}
+
+// All of them, the two tiles' accumulation chains in turn.  B may have more
+// planes than the NB that take part.
 template <bool SWAP, int NB, int NA, int MB>
 __device__ __forceinline__ void mul2(const bf16x8 (&av)[2][NA], const bf16x8 (&b)[MB], f32x4 (&c)[2]) {
-  static_assert(NB <= MB, "planes of B");
-  constexpr int kMost = NA > NB ? NA : NB;
 #pragma unroll
-  for (int o = kMost - 1; o >= 0; --o)
-#pragma unroll
-    for (int i = NA - 1; i >= 0; --i)
-      if (o - i >= 0 && o - i < NB) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) c[t] = SWAP ? mfma(b[o - i], av[t][i], c[t]) : mfma(av[t][i], b[o - i], c[t]);
-      }
+  for (int which = 0; which < products<NA, NB>(); ++which) mul2_one<SWAP, NB>(which, av, b, c);
 }
 
 // Keeps what is written before it ahead of what is written after it.
@@ -430,9 +450,10 @@ __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP, VC>& L, 
 
 // A counter in LDS that one wave raises and others wait for.
 __device__ __forceinline__ int seen(const int* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP); }
+__device__ __forceinline__ void acquire() { __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local"); }
 __device__ __forceinline__ void wait_for(const int* p, int value) {
   while (seen(p) < value) __builtin_amdgcn_s_sleep(1);
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  acquire();
 }
 __device__ __forceinline__ void raise_to(int* p, int value, int lane) {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");

@@ -66,10 +66,12 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
   // y's tiles are computed transposed: a lane has 4 consecutive channels of
   // a token, stored in one piece at a uniform address per chunk plus this
   const int ych = (part * CW + wave) * 16 + 4 * g;
-  char* ydst = (char*)p.y + ((int64_t)s * p.N * d + ych) * kE;
-  const uint32_t yoff = (uint32_t)li * d * kE;
+  char* ydst = (char*)p.y + (int64_t)s * p.N * d * kE;
+  const uint32_t yoff = ((uint32_t)li * d + ych) * kE;
+  int ready = 0;   // what built[c % PB] was when last read
   for (int c = 0; c < chunks; ++c) {
-    wait_for(built + c % PB, c + 1);
+    if (ready <= c) wait_for(built + c % PB, c + 1);
+    acquire();
     const Lds L{smem + c % NB * Lds::BYTES};
     const uint16_t *ka = L.k() + li * Lds::RS + 8 * g, *qa = L.q() + li * Lds::RS + 8 * g;
     const uint16_t *ta = L.t() + li * kCS + 8 * g, *pa = L.p() + li * kCS + 8 * g;
@@ -113,70 +115,69 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
       for (int r = 0; r < 4; ++r) R[rt][r] = fmaf(-G[rt][r], ks[rt][r], V[rt][r]);
     bf16x8 rp[3];
     split8<3>(R[0], R[1], rp);
-    mul2<false, 3>(rt3, rp, F);
     if (!F32) in_order();
-    bf16x8 kt[NT][NP];
+    bf16x8 kt[NT][NP], rp2[2][NPP];
+    if (!F32) {
 #pragma unroll
-    for (int ti = 0; ti < NT; ++ti)
-#pragma unroll
-      for (int e = 0; e < NP; ++e) kt[ti][e] = read_transposed<true>(L.k() + e * Lds::KP, Lds::RS, 16 * ti, lane);
-#pragma unroll
-    for (int kx = 0; kx < NK; ++kx) mul2<true, NS>(rq[kx], sp[kx], qs);
+      for (int ti = 0; ti < NT; ++ti) kt[ti][0] = read_transposed<true>(L.k(), Lds::RS, 16 * ti, lane);
+      read2<NPP>(pa, Lds::CP, 16 * kCS, rp2);
+    }
     const float gc = L.gc()[0], scale = L.gc()[1];
-    if (!F32) in_order();
-    // W' = G_C W + K^T (E theta F)
+    // F = T R, with Q W^T between the steps of its accumulation chains
     {
-      f32x4 U[2];
+      constexpr int kF = products<3, 3>(), kQ = products<NP, NS>();
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt) U[rt] = F[rt] * E[rt];
-      bf16x8 up[3];
-      split8<3>(U[0], U[1], up);
-      const bool scaled = __builtin_amdgcn_readfirstlane(bits(scale)) != 0x3f800000u;
-      f32x4 acc[NT];
+      for (int f = 0; f < kF; ++f) {
+        mul2_one<false, 3>(f, rt3, rp, F);
 #pragma unroll
-      for (int ti = 0; ti < NT; ++ti) acc[ti] = S[ti] * gc;
-      if (scaled) {   // seldom: theta far from 1 all over the chunk
-#pragma unroll
-        for (int ti = 0; ti < NT; ++ti) S[ti] = acc[ti], acc[ti] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
-#pragma unroll
-      for (int o = 2; o >= 0; --o)
-#pragma unroll
-        for (int e = NP - 1; e >= 0; --e)
-          if (o - e >= 0) {
-#pragma unroll
-            for (int ti = 0; ti < NT; ++ti) acc[ti] = mfma(kt[ti][e], up[o - e], acc[ti]);
-          }
-      if (scaled) {
-#pragma unroll
-        for (int ti = 0; ti < NT; ++ti) S[ti] += acc[ti] * scale;
-      } else {
-#pragma unroll
-        for (int ti = 0; ti < NT; ++ti) S[ti] = acc[ti];
+        for (int x = f * NK * kQ / kF; x < (f + 1) * NK * kQ / kF; ++x) mul2_one<true, NS>(x % kQ, rq[x / kQ], sp[x / kQ], qs);
+        if (!F32) in_order();
       }
     }
+    // W' = G_C W + K^T (E theta F)
+    f32x4 U[2], acc[NT], out[2];
+    bf16x8 up[3], fp[NS];
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) U[rt] = F[rt] * E[rt];
+    split8<3>(U[0], U[1], up);
+    const bool scaled = __builtin_amdgcn_readfirstlane(bits(scale)) != 0x3f800000u;
+#pragma unroll
+    for (int ti = 0; ti < NT; ++ti) acc[ti] = S[ti] * gc;
+    if (scaled) {   // seldom: theta far from 1 all over the chunk
+#pragma unroll
+      for (int ti = 0; ti < NT; ++ti) S[ti] = acc[ti], acc[ti] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (F32) {
+#pragma unroll
+      for (int ti = 0; ti < NT; ++ti)
+#pragma unroll
+        for (int e = 0; e < NP; ++e) kt[ti][e] = read_transposed<true>(L.k() + e * Lds::KP, Lds::RS, 16 * ti, lane);
+      read2<NPP>(pa, Lds::CP, 16 * kCS, rp2);
+    }
+#pragma unroll
+    for (int f = 0; f < products<NP, 3>(); ++f) {
+      const Planes x = product<NP, 3>(f);
+#pragma unroll
+      for (int ti = 0; ti < NT; ++ti) acc[ti] = mfma(kt[ti][x.i], up[x.j], acc[ti]);
+    }
     // Y^T = W Q^T diag(G) + F^T P^T
-    f32x4 out[2];
-    bf16x8 fp[NS], rp2[2][NPP];
-    read2<NPP>(pa, Lds::CP, 16 * kCS, rp2);
     split8<NS>(F[0], F[1], fp);
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) out[rt] = qs[rt] * L.g()[16 * rt + li];
+    ready = seen(built + (c + 1) % PB);
     mul2<true, NS>(rp2, fp, out);
+#pragma unroll
+    for (int ti = 0; ti < NT; ++ti) S[ti] = scaled ? S[ti] + acc[ti] * scale : acc[ti];
     raise_to(used + wave, c + 1, lane);
     const int t0 = c * kC;
     char* at = ydst + (int64_t)t0 * d * kE;
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt) {
-      if (t0 + 16 * rt + li >= n) continue;
+    auto store = [&](int rt) {
       char* to = at + (yoff + 16u * rt * d * kE);
       if constexpr (VB > 0) {
-        if (ych < d) {
-          if constexpr (F32)
-            *(f32x4*)to = out[rt];
-          else
-            *(bf16x4*)to = __builtin_convertvector(out[rt], bf16x4);
-        }
+        if constexpr (F32)
+          *(f32x4*)to = out[rt];
+        else
+          *(bf16x4*)to = __builtin_convertvector(out[rt], bf16x4);
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -186,6 +187,16 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
             else
               ((__bf16*)to)[r] = (__bf16)out[rt][r];
           }
+      }
+    };
+    if (ych < d) {
+      if (t0 + kC <= n) {
+        store(0);
+        store(1);
+      } else {
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt)
+          if (t0 + 16 * rt + li < n) store(rt);
       }
     }
   }
