@@ -129,7 +129,10 @@ __device__ __forceinline__ void mul2(const bf16x8 (&av)[2][NA], const bf16x8 (&b
 }
 
 // Keeps what is written before it ahead of what is written after it.
-__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+__device__ __forceinline__ void in_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
 
 // The operand A[m][k] of a [k][m] array (row stride rs in bf16, k = 32 tokens in their natural row order, m0 the tile's
 // first column; PERM: its rows
@@ -386,55 +389,54 @@ __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP, VC>& L, 
       b[r] = x == 1 || t > j0 + r ? D * kk[x][r] : 0.f;
       qk[x][r] = x == 1 || t >= j0 + r ? D * qk[x][r] : 0.f;
     }
-    *(f32x4*)(sc + t * kBS + j0) = b;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sc[(j0 + r) * kBS + t] = b[r];
   }
   wave_fence();
   // the two diagonal blocks' inverses: lane (block, column) by forward
-  // substitution down the rows (stable for any B)
+  // substitution (stable for any B), a solved row taken out of all later ones
+  // at once; B's columns are read two ahead
   {
-    const int o = 16 * (g & 1);
-    f32x4 B[16][4];   // row r's first r entries, four rows read ahead
-    auto rows = [&](int r0) {
+    const float* Bt = sc + 16 * (g & 1) * (kBS + 1);   // this block of B^T
+    f32x4 col[15][4];
+    auto read = [&](int j) {
 #pragma unroll
-      for (int r = r0; r < r0 + 4; ++r)
-#pragma unroll
-        for (int j = 0; j < r; j += 4) B[r][j / 4] = *(const f32x4*)(sc + (o + r) * kBS + o + j);
+      for (int e = (j + 1) / 4; e < 4; ++e) col[j][e] = *(const f32x4*)(Bt + j * kBS + 4 * e);
     };
     float T[16];
-    rows(0);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      if (r % 4 == 0) {
+    for (int r = 0; r < 16; ++r) T[r] = r == li ? 1.f : 0.f;
+    read(0);
+    read(1);
+#pragma unroll
+    for (int j = 0; j < 15; ++j) {
+      if (j % 2 == 0) {
         in_order();
-        if (r < 12) rows(r + 4);
+        if (j + 2 < 15) read(j + 2);
+        if (j + 3 < 15) read(j + 3);
       }
-      float s0 = r == li ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-      for (int j = 0; j < r; ++j) {
-        if (j & 1)
-          s1 = fmaf(-B[r][j / 4][j % 4], T[j], s1);
-        else
-          s0 = fmaf(-B[r][j / 4][j % 4], T[j], s0);
-      }
-      T[r] = s0 + s1;
+      for (int r = j + 1; r < 16; ++r) T[r] = fmaf(-col[j][r / 4][r % 4], T[j], T[r]);
     }
     wave_fence();
-    if (lane < 32) {
+    if (lane < 32) {   // in B^T's place, transposed too
 #pragma unroll
-      for (int r = 0; r < 16; ++r) sc[(o + r) * kBS + o + li] = T[r];
+      for (int e = 0; e < 4; ++e)
+        *(f32x4*)(sc + (16 * (g & 1) + li) * kBS + 16 * (g & 1) + 4 * e) = f32x4{T[4 * e], T[4 * e + 1], T[4 * e + 2], T[4 * e + 3]};
     }
   }
   wave_fence();
   // T10^T = -T00^T (B10^T T11^T) in fp32 matrix instructions; the inner
   // product's tile is the second one's operand over rows 4 g + r
-  f32x4 x = {0.f, 0.f, 0.f, 0.f}, t10 = x;
+  f32x4 x = {0.f, 0.f, 0.f, 0.f}, t10 = x, t00, t11;
+  const f32x4 left = *(const f32x4*)(sc + li * kBS + 4 * g);
 #pragma unroll
   for (int s = 0; s < 4; ++s)
-    x = __builtin_amdgcn_mfma_f32_16x16x4f32(sc[(16 + 4 * s + g) * kBS + li], sc[(16 + li) * kBS + 16 + 4 * s + g], x, 0, 0, 0);
+    x = __builtin_amdgcn_mfma_f32_16x16x4f32(sc[li * kBS + 16 + 4 * s + g], sc[(16 + 4 * s + g) * kBS + 16 + li], x, 0, 0, 0);
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
-    t10 = __builtin_amdgcn_mfma_f32_16x16x4f32(sc[(4 * g + r) * kBS + li], x[r], t10, 0, 0, 0);
-  const f32x4 t00 = *(const f32x4*)(sc + li * kBS + 4 * g), t11 = *(const f32x4*)(sc + (16 + li) * kBS + 16 + 4 * g);
+  for (int r = 0; r < 4; ++r) t00[r] = sc[(4 * g + r) * kBS + li], t11[r] = sc[(16 + 4 * g + r) * kBS + 16 + li];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) t10 = __builtin_amdgcn_mfma_f32_16x16x4f32(left[r], x[r], t10, 0, 0, 0);
   wave_fence();
   uint16_t* T = L.t() + li * kCS + 8 * g;
   put4<3>(T, Lds::CP, t00[0], t00[1], t00[2], t00[3]);
