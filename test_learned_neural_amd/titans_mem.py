@@ -438,13 +438,23 @@ def backward(k, v, q, alpha, eta, theta, W_in, S_in, chunk: int, *, hidden: int,
     return g
 
 
+# A decode step's kernel runs for about 3 us, so the wrappers below keep the
+# host's share of a call small: one pass over the tensors' properties, and the
+# raw handle of the current stream (a torch.cuda.Stream object costs 2 us).
 def _io_of(t) -> str:
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return "bf16"
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return "f32"
     raise ValueError(f"float32 or bfloat16 expected, got {t.dtype}")
+
+
+def _want(tensors, device):
+    """Checks (name, tensor, shape, dtype) entries; a tensor may be None."""
+    for name, t, shape, dtype in tensors:
+        if t is not None and not (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+            _check(t, name, shape, dtype, device)
 
 
 def _on_device(dev, what, fn, *args):
@@ -453,10 +463,10 @@ def _on_device(dev, what, fn, *args):
     if dev.type != "cuda":
         raise ValueError(f"{what}: tensors must be on a GPU, got {dev}")
     if dev.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if rc != OK:
         raise TitansMemError(rc, what)
 
@@ -477,15 +487,10 @@ def _check_delta(k, v, q, alpha, theta, W_in, lengths):
     if k.dim() != 4 or v.dim() != 4:
         raise ValueError("k and v must be [B, heads, N, d]")
     B, Hk, N, d = k.shape
-    H, dev, f32 = v.shape[1], k.device, torch.float32
-    _check(v, "v", (B, H, N, d), k.dtype, dev)
-    _check(k, "k", (B, Hk, N, d), k.dtype, dev)
-    _check(q, "q", (B, Hk, N, d), k.dtype, dev)
-    _check(alpha, "alpha", (B, H, N), f32, dev)
-    _check(theta, "theta", (B, H, N), f32, dev)
-    _check(W_in, "W_in", (B, H, d, d), f32, dev)
-    if lengths is not None:
-        _check(lengths, "lengths", (B,), torch.int32, dev)
+    H, dev, io, f32 = v.shape[1], k.device, k.dtype, torch.float32
+    keys, gates = (B, Hk, N, d), (B, H, N)
+    _want((("v", v, (B, H, N, d), io), ("k", k, keys, io), ("q", q, keys, io), ("alpha", alpha, gates, f32),
+           ("theta", theta, gates, f32), ("W_in", W_in, (B, H, d, d), f32), ("lengths", lengths, (B,), torch.int32)), dev)
     return B, H, Hk, N, d, dev
 
 
@@ -502,14 +507,11 @@ def delta_forward(k, v, q, alpha, theta, W_in, *, lengths=None, force_recurrent:
     torch = _torch()
     B, H, Hk, N, d, dev = _check_delta(k, v, q, alpha, theta, W_in, lengths)
     desc = make_delta_desc(B, H, Hk, N, d, _io_of(k), FLAG_FORCE_GENERIC if force_recurrent else 0)
+    _want((("y_out", y_out, (B, H, N, d), k.dtype), ("W_out", W_out, (B, H, d, d), torch.float32)), dev)
     if y_out is None:
-        y_out = (torch.empty if lengths is None else torch.zeros)((B, H, N, d), dtype=k.dtype, device=dev)
-    else:
-        _check(y_out, "y_out", (B, H, N, d), k.dtype, dev)
+        y_out = torch.empty_like(v) if lengths is None else torch.zeros_like(v)
     if W_out is None:
-        W_out = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
-    else:
-        _check(W_out, "W_out", (B, H, d, d), torch.float32, dev)
+        W_out = torch.empty_like(W_in)
     ws, ws_bytes = _workspace(workspace, delta_workspace_bytes(desc), dev, "titans_mem_delta_workspace_bytes")
     _on_device(dev, "titans_mem_delta_forward", raw_delta_forward, desc, k.data_ptr(), v.data_ptr(), q.data_ptr(),
                alpha.data_ptr(), theta.data_ptr(), _ptr(lengths), W_in.data_ptr(), y_out.data_ptr(), W_out.data_ptr(),
@@ -555,14 +557,9 @@ def _check_norm(x, weight, bias, H, gate, lengths, activation, eps):
         d, flags = C // H, FLAG_CHANNELS_LAST
     else:
         raise ValueError("x must be [B, H, N, d], or [B, N, H*d] with H given")
-    _check(x, "x", tuple(x.shape), x.dtype, dev)
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _check(t, name, (H * d,), torch.float32, dev)
-    if gate is not None:
-        _check(gate, "gate", (B, N, H * d), x.dtype, dev)
-    if lengths is not None:
-        _check(lengths, "lengths", (B,), torch.int32, dev)
+    f32, C = torch.float32, H * d
+    _want((("x", x, x.shape, x.dtype), ("weight", weight, (C,), f32), ("bias", bias, (C,), f32),
+           ("gate", gate, (B, N, C), x.dtype), ("lengths", lengths, (B,), torch.int32)), dev)
     return make_norm_desc(B, H, N, d, io, activation, eps, flags), (B, N, H * d), dev
 
 
