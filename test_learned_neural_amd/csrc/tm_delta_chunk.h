@@ -225,7 +225,7 @@ struct RowLoad {
   __device__ __forceinline__ void load(const char* from, int rows, int width, int real, int lane) {
     src = from, n = rows, d = width, cols = real;
     if constexpr (VB > 0) {
-      if (n == kC && d == DP) {   // offsets that no chunk changes
+      if (n == kC && d == DP && cols >= COLS) {   // offsets that no chunk changes
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
           const int e = (i * 64 + lane) * PER;
@@ -411,6 +411,8 @@ __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP, VC>& L, 
 #pragma unroll
     for (int j = 0; j < 15; ++j) {
       if (j % 2 == 0) {
+        // (tied to the sums, so that the reads stay two columns ahead and no more)
+        asm volatile("" : "+v"(T[j]), "+v"(T[(j + 16) / 2]), "+v"(T[15]) : : "memory");
         in_order();
         if (j + 2 < 15) read(j + 2);
         if (j + 3 < 15) read(j + 3);

@@ -15,6 +15,14 @@
 // only for chunks built before its own to be consumed and a chain wave only
 // for the next chunk, so every wait ends.  Nothing but the inputs and outputs
 // touches memory.
+//
+// Few streams and many chunks: the sequence is cut into segments.  A segment
+// maps the state before it to the one after it by W -> W Phi + W_0; a first
+// launch finds every segment's Phi and W_0 at once (the chain run on the unit
+// vectors without values, and on the values from a zero state), a second
+// passes the state through them in order (delta_join_kernel), a third runs
+// the segments side by side from their true starts.  That is about 2.4 times
+// the work, for as many times the parallelism as there are segments.
 #include "tm_delta_chunk.h"
 
 namespace titans {
@@ -26,10 +34,31 @@ struct ChainParams {
   const int32_t* lengths;
   void* y;
   float* W_out;
-  int streams, H, Hk, N, d, parts;
+  // segments of seg_chunks chunks; ws_phi, ws_loc, ws_start: [stream][segment][ld x ld] (rows: value channels of
+  // W_0 and the starts, inputs of Phi)
+  float *ws_phi, *ws_loc, *ws_start;
+  int streams, H, Hk, N, d, parts, segments, seg_chunks, ld;
 };
 
-template <int DP, bool F32, int CW, int PB, int NB, int VB>
+// a state of the workspace, as a chain wave holds it
+template <int NT>
+__device__ __forceinline__ void load_ws(f32x4 (&S)[NT], const float* W, int row, int ld, int g) {
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (row < ld && 16 * i < ld) S[i] = *(const f32x4*)(W + row * ld + 16 * i + 4 * g);
+  }
+}
+template <int NT>
+__device__ __forceinline__ void store_ws(const f32x4 (&S)[NT], float* W, int row, int ld, int g) {
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+    if (row < ld && 16 * i < ld) *(f32x4*)(W + row * ld + 16 * i + 4 * g) = S[i];
+}
+
+// TRANS: the segments' maps instead of y: column groups up to d from zero with
+// the values, as many again from the unit vectors without.
+template <int DP, bool F32, int CW, int PB, int NB, int VB, bool TRANS>
 __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams p) {
   static_assert(NB > PB, "a chunk is consumed while PB are built");
   constexpr int NP = F32 ? 3 : 1, NPP = F32 ? 3 : 2, NS = F32 ? 3 : 2;   // planes: inputs, P, and W and F for y
@@ -42,31 +71,47 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // the parts of a stream read the same K and Q: workgroups 8 apart share an XCD's L2
   const int idx = blockIdx.x >> 3;
-  const int s = (idx / p.parts) * 8 + (blockIdx.x & 7), part = idx % p.parts;
+  const int segs = TRANS ? p.segments - 1 : p.segments, per = p.parts * segs;
+  const int s = idx / per * 8 + (blockIdx.x & 7), seg = idx % per / p.parts, part = idx % p.parts;
   if (s >= p.streams) return;
   const int b = s / p.H, h = s % p.H, d = p.d;
-  const int n = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
+  const int all = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
+  const int first = (int)min((int64_t)seg * p.seg_chunks * kC, (int64_t)all);   // the segment's tokens: first .. first + n - 1
+  const int n = seg + 1 < p.segments ? (int)min((int64_t)(all - first), (int64_t)p.seg_chunks * kC) : all - first;
   const int chunks = (n + kC - 1) / kC;
   init_ring<Lds, NB, CW, PB>(smem, built, wave, lane);
 
   if (wave >= CW) {
-    const int col0 = part * CW * 16;
-    const int64_t krow = ((int64_t)b * p.Hk + h / (p.H / p.Hk)) * p.N * d, vrow = (int64_t)s * p.N * d + col0;
-    run_builder<DP, F32, CW, PB, NB, VB, NPP, true, false>(
-        smem, built, used, wave - CW, lane, chunks, n, d, d - col0, (const char*)p.k + krow * kE,
-        (const char*)p.q + krow * kE, (const char*)p.v + vrow * kE, p.alpha + (int64_t)s * p.N,
-        p.theta + (int64_t)s * p.N, kForget);
+    const int col0 = part * CW * 16, vcols = max(d - col0, 0);
+    const int64_t t0 = first;
+    const int64_t krow = (((int64_t)b * p.Hk + h / (p.H / p.Hk)) * p.N + t0) * d;
+    const int64_t vrow = ((int64_t)s * p.N + t0) * d + (vcols > 0 ? col0 : 0), gate = (int64_t)s * p.N + t0;
+    run_builder<DP, F32, CW, PB, NB, VB, NPP, !TRANS, false>(
+        smem, built, used, wave - CW, lane, chunks, n, d, vcols, (const char*)p.k + krow * kE,
+        (const char*)p.q + krow * kE, (const char*)p.v + vrow * kE, p.alpha + gate, p.theta + gate, kForget);
     return;
   }
 
   // ---- chain ----
-  const int col = (part * CW + wave) * 16 + li;   // this lane's value channel
+  const int cg = part * CW + wave, groups = (d + 15) / 16;
+  const int col = cg * 16 + li;   // this lane's value channel
+  const int unit = col - groups * 16;   // TRANS: its unit vector, if not negative
+  const int64_t at_ws = ((int64_t)s * p.segments + seg) * p.ld * p.ld;
   f32x4 S[NT];
-  load_state<NT, VB>(S, p.W_in, s, col, d, g);
+  if (TRANS) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = 16 * i + 4 * g + r == unit ? 1.f : 0.f;
+  } else if (p.segments > 1) {
+    load_ws(S, p.ws_start + at_ws, col, p.ld, g);
+  } else {
+    load_state<NT, VB>(S, p.W_in, s, col, d, g);
+  }
   // y's tiles are computed transposed: a lane has 4 consecutive channels of
   // a token, stored in one piece at a uniform address per chunk plus this
-  const int ych = (part * CW + wave) * 16 + 4 * g;
-  char* ydst = (char*)p.y + (int64_t)s * p.N * d * kE;
+  const int ych = cg * 16 + 4 * g;
+  char* ydst = (char*)p.y + ((int64_t)s * p.N + first) * d * kE;
   const uint32_t yoff = ((uint32_t)li * d + ych) * kE;
   int ready = 0;   // what built[c % PB] was when last read
   for (int c = 0; c < chunks; ++c) {
@@ -107,6 +152,7 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
     for (int rt = 0; rt < 2; ++rt) E[rt] = *(const f32x4*)(L.eth() + 16 * rt + 4 * g);
     if (!F32) in_order();
     bf16x8 rq[NK][2][NP];
+    if (!TRANS)
 #pragma unroll
     for (int kx = 0; kx < NK; ++kx) read2<NP>(qa + 32 * kx, Lds::KP, 16 * Lds::RS, rq[kx]);
 #pragma unroll
@@ -120,7 +166,7 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
     if (!F32) {
 #pragma unroll
       for (int ti = 0; ti < NT; ++ti) kt[ti][0] = read_transposed<true>(L.k(), Lds::RS, 16 * ti, lane);
-      read2<NPP>(pa, Lds::CP, 16 * kCS, rp2);
+      if (!TRANS) read2<NPP>(pa, Lds::CP, 16 * kCS, rp2);
     }
     const float gc = L.gc()[0], scale = L.gc()[1];
     // F = T R, with Q W^T between the steps of its accumulation chains
@@ -129,6 +175,7 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
 #pragma unroll
       for (int f = 0; f < kF; ++f) {
         mul2_one<false, 3>(f, rt3, rp, F);
+        if (TRANS) continue;
 #pragma unroll
         for (int x = f * NK * kQ / kF; x < (f + 1) * NK * kQ / kF; ++x) mul2_one<true, NS>(x % kQ, rq[x / kQ], sp[x / kQ], qs);
         if (!F32) in_order();
@@ -152,7 +199,7 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
       for (int ti = 0; ti < NT; ++ti)
 #pragma unroll
         for (int e = 0; e < NP; ++e) kt[ti][e] = read_transposed<true>(L.k() + e * Lds::KP, Lds::RS, 16 * ti, lane);
-      read2<NPP>(pa, Lds::CP, 16 * kCS, rp2);
+      if (!TRANS) read2<NPP>(pa, Lds::CP, 16 * kCS, rp2);
     }
 #pragma unroll
     for (int f = 0; f < products<NP, 3>(); ++f) {
@@ -161,11 +208,13 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
       for (int ti = 0; ti < NT; ++ti) acc[ti] = mfma(kt[ti][x.i], up[x.j], acc[ti]);
     }
     // Y^T = W Q^T diag(G) + F^T P^T
-    split8<NS>(F[0], F[1], fp);
+    if (!TRANS) {
+      split8<NS>(F[0], F[1], fp);
 #pragma unroll
-    for (int rt = 0; rt < 2; ++rt) out[rt] = qs[rt] * L.g()[16 * rt + li];
+      for (int rt = 0; rt < 2; ++rt) out[rt] = qs[rt] * L.g()[16 * rt + li];
+    }
     ready = seen(built + (c + 1) % PB);
-    mul2<true, NS>(rp2, fp, out);
+    if (!TRANS) mul2<true, NS>(rp2, fp, out);
 #pragma unroll
     for (int ti = 0; ti < NT; ++ti) S[ti] = scaled ? S[ti] + acc[ti] * scale : acc[ti];
     raise_to(used + wave, c + 1, lane);
@@ -189,7 +238,7 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
           }
       }
     };
-    if (ych < d) {
+    if (!TRANS && ych < d) {
       if (t0 + kC <= n) {
         store(0);
         store(1);
@@ -200,46 +249,146 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
       }
     }
   }
-  store_state<NT, VB>(S, p.W_out, s, col, d, g);
+  if (TRANS) {
+    if (unit < 0)
+      store_ws(S, p.ws_loc + at_ws, col, p.ld, g);
+    else
+      store_ws(S, p.ws_phi + at_ws, unit, p.ld, g);
+  } else if (seg + 1 == p.segments) {
+    store_state<NT, VB>(S, p.W_out, s, col, d, g);
+  }
 }
 
-template <int DP, bool F32, int CW, int PB, int NB, int VB>
+// The state before every segment: a workgroup takes 16 rows (value channels)
+// of a stream through W <- W Phi + W_0, in fp32 matrix instructions, the
+// rows in LDS between segments.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(ChainParams p) {
+  __shared__ float rows[16][kMaxWidthDelta + 1];
+  const int ld = p.ld, blocks = ld / 16, s = blockIdx.x / blocks, row0 = blockIdx.x % blocks * 16, d = p.d;
+  const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15, w = threadIdx.x >> 6;
+  const int64_t base = (int64_t)s * p.segments * ld * ld;
+  for (int e = threadIdx.x; e < 16 * ld; e += kJoinThreads) {
+    const int r = e / ld, c = e % ld;
+    const bool in = row0 + r < d && c < d;
+    const float x = in ? p.W_in[((int64_t)s * d + row0 + r) * d + c] : 0.f;
+    rows[r][c] = x;
+    p.ws_start[base + (row0 + r) * ld + c] = x;
+  }
+  for (int seg = 0; seg + 1 < p.segments; ++seg) {
+    const float *phi = p.ws_phi + base + (int64_t)seg * ld * ld, *loc = p.ws_loc + base + (int64_t)seg * ld * ld;
+    float* next = p.ws_start + base + (int64_t)(seg + 1) * ld * ld;
+    __syncthreads();
+    f32x4 acc[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {   // this wave's column tiles
+      const int c = (w + 4 * i) * 16 + li;
+      acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if ((w + 4 * i) * 16 >= ld) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[i][r] = loc[(row0 + 4 * g + r) * ld + c];
+#pragma unroll 8
+      for (int k = 0; k < ld; k += 4)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(rows[li][k + g], phi[(k + g) * ld + c], acc[i], 0, 0, 0);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = (w + 4 * i) * 16 + li;
+      if ((w + 4 * i) * 16 >= ld) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) rows[4 * g + r][c] = acc[i][r], next[(row0 + 4 * g + r) * ld + c] = acc[i][r];
+    }
+  }
+}
+
+template <int DP, bool F32, int CW, int VB, bool TRANS>
 hipError_t launch_as(ChainParams p, hipStream_t stream) {
+  // as many buffers as LDS holds, and builders as keep the chain fed
+  constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : 4, PB = F32 ? (DP == 128 ? 1 : 2) : DP == 64 ? 3 : 2;
   constexpr int lds = NB * ChunkLds<DP, F32 ? 3 : 1, F32 ? 3 : 2, CW * 16>::BYTES + (PB + CW) * 4;
   static_assert(lds <= 160 * 1024, "LDS of one workgroup");
-  p.parts = ((p.d + 15) / 16 + CW - 1) / CW;
-  auto kernel = delta_chain_kernel<DP, F32, CW, PB, NB, VB>;
+  p.parts = ((p.d + 15) / 16 * (TRANS ? 2 : 1) + CW - 1) / CW;
+  auto kernel = delta_chain_kernel<DP, F32, CW, PB, NB, VB, TRANS>;
   hipError_t err = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (err != hipSuccess) return err;
-  const unsigned grid = (unsigned)((p.streams + 7) / 8 * 8 * p.parts);
+  const unsigned grid = (unsigned)((p.streams + 7) / 8 * 8 * p.parts * (TRANS ? p.segments - 1 : p.segments));
   kernel<<<grid, (CW + PB) * 64, lds, stream>>>(p);
   return hipGetLastError();
 }
 
+// How a call is cut.  Times of a chunk of 32 tokens in a workgroup that has a
+// CU to itself, in tenths of a microsecond, as measured on 16 to 512 streams:
+// d up to 64 with 2 chain waves 12, with 4 18 (128: 17 and 24; fp32: 21 and
+// 29, 60 and 107), two thirds of that without y.
+struct Plan {
+  int wide;       // 4 chain waves in a workgroup of the (last) launch
+  int segments;   // 1: one launch
+  int seg_chunks;
+};
+constexpr int kCus = 256;
+int chunk_cost(const DeltaShape& s, int cw) {
+  if (s.io == TM_IO_BF16) return s.d <= 64 ? (cw == 2 ? 12 : 18) : cw == 2 ? 17 : 24;
+  return s.d <= 64 ? (cw == 2 ? 21 : 29) : cw == 2 ? 60 : 107;
+}
+Plan plan_of(const DeltaShape& s) {
+  const int64_t streams = (int64_t)s.B * s.H, chunks = (s.N + kC - 1) / kC, groups = (s.d + 15) / 16;
+  auto rounds = [&](int64_t segs, int64_t columns, int cw) {
+    return (streams * segs * ((columns + cw - 1) / cw) + kCus - 1) / kCus * chunk_cost(s, cw);
+  };
+  Plan best = {0, 1, (int)chunks};
+  int64_t cost = chunks * rounds(1, groups, 2);
+  if (chunks * rounds(1, groups, 4) < cost) cost = chunks * rounds(1, groups, 4), best.wide = 1;
+  for (int segs = 2; segs <= 32; segs *= 2) {
+    const int64_t per = (chunks + segs - 1) / segs, n = (chunks + per - 1) / per;
+    if (n < 2) break;
+    for (int wide = 0; wide < 2; ++wide) {
+      // the maps' launch, the joins (20 each) and two more launches
+      const int64_t c = per * (rounds(n - 1, 2 * groups, 4) * 2 / 3 + rounds(n, groups, wide ? 4 : 2)) + 20 * n + 150;
+      if (c < cost) cost = c, best = {wide, (int)n, (int)per};
+    }
+  }
+  return best;
+}
+
+int64_t segment_floats(const DeltaShape& s, const Plan& plan) {
+  const int64_t ld = (s.d + 15) / 16 * 16;
+  return plan.segments > 1 ? (int64_t)s.B * s.H * plan.segments * ld * ld : 0;
+}
+
 template <int DP, bool F32, int VB>
-hipError_t launch_chain(const ChainParams& p, hipStream_t stream) {
-  // as many buffers as LDS holds, a builder less
-  constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : 4, PB = F32 && DP == 128 ? 1 : 2;
-  if (p.streams >= 256) return launch_as<DP, F32, 4, PB, NB, VB>(p, stream);
-  return launch_as<DP, F32, 2, PB, NB, VB>(p, stream);
+hipError_t launch_chain(const ChainParams& p, bool wide, hipStream_t stream) {
+  if (p.segments > 1) {
+    hipError_t err = launch_as<DP, F32, 4, VB, true>(p, stream);
+    if (err != hipSuccess) return err;
+    delta_join_kernel<<<p.streams * (p.ld / 16), kJoinThreads, 0, stream>>>(p);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+  }
+  return wide ? launch_as<DP, F32, 4, VB, false>(p, stream) : launch_as<DP, F32, 2, VB, false>(p, stream);
 }
 
 template <bool F32, int VB>
-hipError_t launch_width(const ChainParams& p, hipStream_t stream) {
-  return p.d <= 64 ? launch_chain<64, F32, VB>(p, stream) : launch_chain<128, F32, VB>(p, stream);
+hipError_t launch_width(const ChainParams& p, bool wide, hipStream_t stream) {
+  return p.d <= 64 ? launch_chain<64, F32, VB>(p, wide, stream) : launch_chain<128, F32, VB>(p, wide, stream);
 }
 
 }  // namespace
 
+int64_t delta_chunked_ws_bytes(const DeltaShape& s) { return 12 * segment_floats(s, plan_of(s)); }
+
 hipError_t launch_delta_chunked(const DeltaShape& s, const void* k, const void* v, const void* q, const float* alpha,
                                 const float* theta, const int32_t* lengths, const float* W_in, void* y, float* W_out,
-                                hipStream_t stream) {
-  const ChainParams p = {k, v, q, alpha, theta, W_in, lengths, y, W_out, s.B * s.H, s.H, s.Hk, s.N, s.d, 0};
+                                float* ws, hipStream_t stream) {
+  const Plan plan = plan_of(s);
+  ChainParams p = {k, v, q, alpha, theta, W_in, lengths, y, W_out};
+  p.ws_phi = ws, p.ws_loc = ws + segment_floats(s, plan), p.ws_start = ws + 2 * segment_floats(s, plan);
+  p.streams = s.B * s.H, p.H = s.H, p.Hk = s.Hk, p.N = s.N, p.d = s.d, p.ld = (s.d + 15) / 16 * 16;
+  p.segments = plan.segments, p.seg_chunks = plan.seg_chunks;
   if (s.io == TM_IO_BF16) {
-    if (s.d % 8 == 0) return launch_width<false, 16>(p, stream);
-    return s.d % 4 == 0 ? launch_width<false, 8>(p, stream) : launch_width<false, 0>(p, stream);
+    if (s.d % 8 == 0) return launch_width<false, 16>(p, plan.wide, stream);
+    return s.d % 4 == 0 ? launch_width<false, 8>(p, plan.wide, stream) : launch_width<false, 0>(p, plan.wide, stream);
   }
-  return s.d % 4 == 0 ? launch_width<true, 16>(p, stream) : launch_width<true, 0>(p, stream);
+  return s.d % 4 == 0 ? launch_width<true, 16>(p, plan.wide, stream) : launch_width<true, 0>(p, plan.wide, stream);
 }
 
 }  // namespace titans

@@ -418,7 +418,8 @@ int32_t titans_mem_delta_select_path(const titans_delta_desc* desc) {
 int64_t titans_mem_delta_workspace_bytes(const titans_delta_desc* desc) {
   DeltaShape s;
   int rc = build_delta(desc, &s);
-  return rc ? rc : 0;
+  if (rc) return rc;
+  return delta_path(s) == TM_PATH_DELTA_CHUNKED ? titans::delta_chunked_ws_bytes(s) : 0;
 }
 
 int titans_mem_delta_forward(const titans_delta_desc* desc, const void* k, const void* v, const void* q,
@@ -441,8 +442,11 @@ int titans_mem_delta_forward(const titans_delta_desc* desc, const void* k, const
                      {(const char*)W_in, state, false},      {(const char*)W_out, state, true},
                      {(const char*)y_out, vals, true},       {(const char*)workspace, need, true}};
   if (!disjoint(r, 10, 6, 7)) return TM_ERR_ALIAS;
-  const auto launch = delta_path(s) == TM_PATH_DELTA_CHUNKED ? titans::launch_delta_chunked : titans::launch_delta_recurrent;
-  hipError_t err = launch(s, k, v, q, alpha, theta, lengths, W_in, y_out, W_out, (hipStream_t)stream);
+  hipError_t err = delta_path(s) == TM_PATH_DELTA_CHUNKED
+                       ? titans::launch_delta_chunked(s, k, v, q, alpha, theta, lengths, W_in, y_out, W_out,
+                                                      (float*)workspace, (hipStream_t)stream)
+                       : titans::launch_delta_recurrent(s, k, v, q, alpha, theta, lengths, W_in, y_out, W_out,
+                                                        (hipStream_t)stream);
   return err == hipSuccess ? TM_OK : TM_ERR_HIP;
 }
 

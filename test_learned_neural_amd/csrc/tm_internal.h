@@ -133,7 +133,8 @@ hipError_t launch_delta_recurrent(const DeltaShape& s, const void* k, const void
 constexpr int kMinTokensDeltaChunked = 24;
 hipError_t launch_delta_chunked(const DeltaShape& s, const void* k, const void* v, const void* q, const float* alpha,
                                 const float* theta, const int32_t* lengths, const float* W_in, void* y, float* W_out,
-                                hipStream_t stream);
+                                float* ws, hipStream_t stream);
+int64_t delta_chunked_ws_bytes(const DeltaShape& s);
 
 // Gradients through the gated delta memory; dy and dk, dv, dq in the io type.
 bool delta_backward_supported(const DeltaShape& s);

@@ -52,6 +52,62 @@ def test_forward(shape, recurrent):
     print(shape, "y", check("y", y, yr, io, tol), "W", check("W", W, Wr, "f32", tol), flush=True)
 
 
+#          B  H  Hk N     d    io      lengths
+SEGMENTS = [(1, 1, 1, 2500, 64, "bf16", None),
+            (1, 2, 1, 3000, 128, "bf16", None),
+            (3, 1, 1, 2100, 40, "f32", [2100, 0, 77]),
+            (2, 2, 2, 2049, 33, "bf16", [1, 2049]),
+            (1, 1, 1, 3001, 100, "f32", [1999])]
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("shape", SEGMENTS, ids=str)
+def test_long_sequences_of_few_streams_in_segments(shape, inplace):
+    """Cut into segments side by side (the only calls with a workspace): the same recurrence."""
+    import torch
+    from test_learned_neural_amd import titans_mem as tmm
+    B, H, Hk, N, d, io, lengths = shape
+    assert tmm.delta_workspace_bytes(tmm.make_delta_desc(B, H, Hk, N, d, io)) > 0
+    t, f = make(20, B, H, Hk, N, d, io, resets=True, lengths=lengths)
+    g = cuda(t)
+    W0 = g["W_in"].clone()
+    y, W = _run(g, W_out=g["W_in"] if inplace else None)
+    assert not inplace or W is g["W_in"]
+    yr, Wr = _oracle(f)
+    check("y", y, yr, io, tol32(N, d))
+    check("W", W, Wr, "f32", tol32(N, d))
+    if lengths is not None:
+        for b, n in enumerate(lengths):
+            if n == 0:
+                assert torch.equal(W[b], W0[b])
+
+
+def test_a_segmented_call_replayed_beside_another():
+    """Two captured segmented calls keep a workspace each: replayed on two streams at once."""
+    import torch
+    t, _ = make(21, 1, 2, 2, 2600, 64, "bf16")
+    g = cuda(t)
+    calls = []
+    for i in range(2):
+        x = {n: None if v is None else v.clone() for n, v in g.items()}
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = _run(x)
+        calls.append((graph, x, out, torch.cuda.Stream()))
+    for rep in range(3):
+        want = []
+        for i, (graph, x, out, s) in enumerate(calls):
+            x["v"].copy_(g["v"] * (rep + 2 * i + 1))
+            want.append(_run({**g, "v": g["v"] * (rep + 2 * i + 1)}))
+        torch.cuda.synchronize()
+        for graph, x, out, s in calls:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (graph, x, out, s), w in zip(calls, want):
+            assert torch.equal(out[0], w[0]) and torch.equal(out[1], w[1])
+
+
 def test_rows_past_a_length_are_left_as_they_were():
     import torch
     t, f = make(12, 4, 2, 2, 70, 64, "bf16", lengths=[0, 70, 1, 33])
