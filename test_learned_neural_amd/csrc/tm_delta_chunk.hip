@@ -69,11 +69,11 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
   int* used = built + PB;                        // [CW]: chunks a chain wave has finished
   const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // the parts of a stream read the same K and Q: workgroups 8 apart share an XCD's L2
-  const int idx = blockIdx.x >> 3;
-  const int segs = TRANS ? p.segments - 1 : p.segments, per = p.parts * segs;
-  const int s = idx / per * 8 + (blockIdx.x & 7), seg = idx % per / p.parts, part = idx % p.parts;
-  if (s >= p.streams) return;
+  // the parts of a stream's segment read the same K and Q: workgroups 8 apart share an XCD's L2
+  const int segs = TRANS ? p.segments - 1 : p.segments, idx = blockIdx.x >> 3;
+  const int unit_id = idx / p.parts * 8 + (blockIdx.x & 7), part = idx % p.parts;
+  if (unit_id >= p.streams * segs) return;
+  const int s = unit_id / segs, seg = unit_id % segs;
   const int b = s / p.H, h = s % p.H, d = p.d;
   const int all = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
   const int first = (int)min((int64_t)seg * p.seg_chunks * kC, (int64_t)all);   // the segment's tokens: first .. first + n - 1
@@ -260,45 +260,75 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
 }
 
 // The state before every segment: a workgroup takes 16 rows (value channels)
-// of a stream through W <- W Phi + W_0, in fp32 matrix instructions, the
-// rows in LDS between segments.
+// of a stream through W <- W Phi + W_0, in fp32 matrix instructions, the rows
+// in LDS between segments.  The next segment's Phi and W_0 are read while one
+// is computed: what remains serial is a product's 16 or 32 steps (in two
+// accumulation chains) and the rows' way through LDS.
 constexpr int kJoinThreads = 256;
+template <int DP>
 __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(ChainParams p) {
-  __shared__ float rows[16][kMaxWidthDelta + 1];
+  constexpr int T = DP / 64, K = DP / 4;   // column tiles of a wave, steps of a product
+  __shared__ float rows[16][DP + 4];
   const int ld = p.ld, blocks = ld / 16, s = blockIdx.x / blocks, row0 = blockIdx.x % blocks * 16, d = p.d;
-  const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t base = (int64_t)s * p.segments * ld * ld;
-  for (int e = threadIdx.x; e < 16 * ld; e += kJoinThreads) {
-    const int r = e / ld, c = e % ld;
+  for (int e = threadIdx.x; e < 16 * DP; e += kJoinThreads) {
+    const int r = e / DP, c = e % DP;
     const bool in = row0 + r < d && c < d;
     const float x = in ? p.W_in[((int64_t)s * d + row0 + r) * d + c] : 0.f;
     rows[r][c] = x;
-    p.ws_start[base + (row0 + r) * ld + c] = x;
+    if (c < ld) p.ws_start[base + (row0 + r) * ld + c] = x;
   }
-  for (int seg = 0; seg + 1 < p.segments; ++seg) {
+  struct Step {
+    float phi[T][K];
+    f32x4 loc[T];
+  };
+  // columns past ld read the last tile's (and are not stored); steps past it multiply zeros of `rows` by finite values
+  auto read = [&](int seg, Step& x) {
     const float *phi = p.ws_phi + base + (int64_t)seg * ld * ld, *loc = p.ws_loc + base + (int64_t)seg * ld * ld;
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      const int c = min((w + 4 * i) * 16, ld - 16) + li;
+#pragma unroll
+      for (int k = 0; k < K; ++k) x.phi[i][k] = phi[min(4 * k + g, ld - 1) * ld + c];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x.loc[i][r] = loc[(row0 + 4 * g + r) * ld + c];
+    }
+  };
+  auto step = [&](int seg, const Step& x) {
     float* next = p.ws_start + base + (int64_t)(seg + 1) * ld * ld;
-    __syncthreads();
-    f32x4 acc[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {   // this wave's column tiles
-      const int c = (w + 4 * i) * 16 + li;
-      acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if ((w + 4 * i) * 16 >= ld) continue;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[i][r] = loc[(row0 + 4 * g + r) * ld + c];
-#pragma unroll 8
-      for (int k = 0; k < ld; k += 4)
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(rows[li][k + g], phi[(k + g) * ld + c], acc[i], 0, 0, 0);
-    }
+    f32x4 acc[T][2];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < T; ++i) acc[i][0] = x.loc[i], acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+        acc[i][k & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(rows[li][4 * k + g], x.phi[i][k], acc[i][k & 1], 0, 0, 0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
       const int c = (w + 4 * i) * 16 + li;
       if ((w + 4 * i) * 16 >= ld) continue;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) rows[4 * g + r][c] = acc[i][r], next[(row0 + 4 * g + r) * ld + c] = acc[i][r];
+      for (int r = 0; r < 4; ++r) {
+        const float v = acc[i][0][r] + acc[i][1][r];
+        rows[4 * g + r][c] = v;
+        next[(row0 + 4 * g + r) * ld + c] = v;
+      }
     }
+  };
+  const int n = p.segments - 1;
+  Step a, b;
+  read(0, a);
+  for (int seg = 0; seg < n; seg += 2) {
+    read(min(seg + 1, n - 1), b);
+    step(seg, a);
+    if (seg + 1 >= n) break;
+    read(min(seg + 2, n - 1), a);
+    step(seg + 1, b);
   }
 }
 
@@ -312,7 +342,8 @@ hipError_t launch_as(ChainParams p, hipStream_t stream) {
   auto kernel = delta_chain_kernel<DP, F32, CW, PB, NB, VB, TRANS>;
   hipError_t err = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (err != hipSuccess) return err;
-  const unsigned grid = (unsigned)((p.streams + 7) / 8 * 8 * p.parts * (TRANS ? p.segments - 1 : p.segments));
+  const int units = p.streams * (TRANS ? p.segments - 1 : p.segments);
+  const unsigned grid = (unsigned)((units + 7) / 8 * 8 * p.parts);
   kernel<<<grid, (CW + PB) * 64, lds, stream>>>(p);
   return hipGetLastError();
 }
@@ -339,12 +370,13 @@ Plan plan_of(const DeltaShape& s) {
   Plan best = {0, 1, (int)chunks};
   int64_t cost = chunks * rounds(1, groups, 2);
   if (chunks * rounds(1, groups, 4) < cost) cost = chunks * rounds(1, groups, 4), best.wide = 1;
-  for (int segs = 2; segs <= 32; segs *= 2) {
+  for (int segs : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128}) {
     const int64_t per = (chunks + segs - 1) / segs, n = (chunks + per - 1) / per;
     if (n < 2) break;
     for (int wide = 0; wide < 2; ++wide) {
-      // the maps' launch, the joins (20 each) and two more launches
-      const int64_t c = per * (rounds(n - 1, 2 * groups, 4) * 2 / 3 + rounds(n, groups, wide ? 4 : 2)) + 20 * n + 150;
+      // the maps' launch and the segments', the joins (0.5 and 0.8 us each), and two more launches
+      const int64_t c = per * (rounds(n - 1, 2 * groups, 4) * 2 / 3 + rounds(n, groups, wide ? 4 : 2)) +
+                        (s.d <= 64 ? 5 : 8) * n + 120;
       if (c < cost) cost = c, best = {wide, (int)n, (int)per};
     }
   }
@@ -361,7 +393,7 @@ hipError_t launch_chain(const ChainParams& p, bool wide, hipStream_t stream) {
   if (p.segments > 1) {
     hipError_t err = launch_as<DP, F32, 4, VB, true>(p, stream);
     if (err != hipSuccess) return err;
-    delta_join_kernel<<<p.streams * (p.ld / 16), kJoinThreads, 0, stream>>>(p);
+    delta_join_kernel<DP><<<p.streams * (p.ld / 16), kJoinThreads, 0, stream>>>(p);
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
   return wide ? launch_as<DP, F32, 4, VB, false>(p, stream) : launch_as<DP, F32, 2, VB, false>(p, stream);

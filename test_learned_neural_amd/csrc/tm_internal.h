@@ -129,8 +129,11 @@ struct DeltaShape {
 hipError_t launch_delta_recurrent(const DeltaShape& s, const void* k, const void* v, const void* q,
                                   const float* alpha, const float* theta, const int32_t* lengths, const float* W_in,
                                   void* y, float* W_out, hipStream_t stream);
-// Chunks of 32 tokens on the matrix cores, for sequences.
-constexpr int kMinTokensDeltaChunked = 24;
+// Chunks of 32 tokens on the matrix cores, for sequences.  Below 12 tokens
+// the token-by-token kernel is the faster one: of 512 streams, d 64, bf16, 8
+// tokens take it 12 us and 16 tokens 20, a chunk of up to 32 tokens takes 14
+// (256 streams, d 128, fp32: 26 and 43, 32).
+constexpr int kMinTokensDeltaChunked = 12;
 hipError_t launch_delta_chunked(const DeltaShape& s, const void* k, const void* v, const void* q, const float* alpha,
                                 const float* theta, const int32_t* lengths, const float* W_in, void* y, float* W_out,
                                 float* ws, hipStream_t stream);
