@@ -212,17 +212,6 @@ struct PieceLds {
                        DOTS = GATES + 9 * kC * 4, BYTES = DOTS + NW * (2 * kC + 1) * 4;
 };
 
-// sum over the 16 lanes of a DPP row, in every lane
-__device__ __forceinline__ float row_sum(float x) {
-#define TM_ROR(n) flt(__builtin_amdgcn_update_dpp(0, (int)bits(x), 0x120 + n, 0xf, 0xf, true))
-  x += TM_ROR(8);
-  x += TM_ROR(4);
-  x += TM_ROR(2);
-  x += TM_ROR(1);
-#undef TM_ROR
-  return x;
-}
-
 template <bool F32>
 __device__ __forceinline__ void put(void* p, int64_t i, float x) {
   if (F32)
@@ -231,19 +220,48 @@ __device__ __forceinline__ void put(void* p, int64_t i, float x) {
     ((__bf16*)p)[i] = (__bf16)x;
 }
 
-// the values that planes of one operand stand for
-template <int NP>
-__device__ __forceinline__ float whole(const bf16x8 (&x)[NP], int e) {
-  float sum = (float)x[NP - 1][e];
+// four consecutive channels from c on at element `at`; VB 0: rows that may not be aligned, or end within the four
+template <bool F32, int VB>
+__device__ __forceinline__ void put_four(void* p, int64_t at, const f32x4& x, int c, int d) {
+  if constexpr (VB > 0) {
+    if (c >= d) return;
+    if constexpr (F32)
+      *(f32x4*)((float*)p + at + c) = x;
+    else
+      *(bf16x4*)((__bf16*)p + at + c) = __builtin_convertvector(x, bf16x4);
+  } else {
 #pragma unroll
-  for (int i = NP - 2; i >= 0; --i) sum += (float)x[i][e];
+    for (int r = 0; r < 4; ++r)
+      if (c + r < d) put<F32>(p, at + c + r, x[r]);
+  }
+}
+
+// the values that NP planes (`plane` apart) of four neighbours stand for
+template <int NP>
+__device__ __forceinline__ f32x4 whole(const uint16_t* at, int plane) {
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = NP - 1; i >= 0; --i) {
+    const uint2 u = *(const uint2*)(at + i * plane);
+    sum += f32x4{flt(u.x << 16), top(flt(u.x)), flt(u.y << 16), top(flt(u.y))};
+  }
   return sum;
 }
 
+// sum over the four lane groups, in every lane
+__device__ __forceinline__ float groups_sum(float x) {
+  x += __shfl_xor(x, 16, 64);
+  return x + __shfl_xor(x, 32, 64);
+}
+
+// A wave has 16 channels of its own: of K's for dQ and dK (and, when staging,
+// of V's).  Products of tokens by those channels are computed transposed, so
+// that a lane has four neighbouring channels of one token.
 template <int DP, bool F32, int VB>
-__global__ void __launch_bounds__(DP * 4) delta_piece_kernel(GradParams p) {
+__global__ void __launch_bounds__(DP * 4, 2) delta_piece_kernel(GradParams p) {
   using L = PieceLds<DP, F32>;
   constexpr int NP = L::NP, NX = L::NX, NW = L::NW, NK = DP / 32, RS = L::RS, KP = L::KP, CP = L::CP, FP = L::FP;
+  constexpr int kE = F32 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   uint16_t *Ks = (uint16_t*)(smem + L::K), *Qs = (uint16_t*)(smem + L::Q), *dYs = (uint16_t*)(smem + L::DY);
   uint16_t *Fs = (uint16_t*)(smem + L::F), *dEs = (uint16_t*)(smem + L::DE);   // [channel][token]
@@ -259,7 +277,7 @@ __global__ void __launch_bounds__(DP * 4) delta_piece_kernel(GradParams p) {
   const int n = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
   const int live = min(max(n - t0, 0), kC), rows = min(kC, p.N - t0);   // tokens of the sequence, and of the tensors
   const int64_t krow = ((int64_t)bk * p.N + t0) * d;
-  const int ch = 16 * w + li;   // this lane's channel: of v when tiles are staged, of k after
+  const int ch = 16 * w + li, ch4 = 16 * w + 4 * g;
   if (live == 0) {   // past the sequence: zeros
     const int64_t s0 = (int64_t)b * p.H + hk * share;
     for (int e = threadIdx.x; e < rows * d; e += NW * 64) {
@@ -279,37 +297,36 @@ __global__ void __launch_bounds__(DP * 4) delta_piece_kernel(GradParams p) {
   for (int x = 0; x < share; ++x) {
     const int s = b * p.H + hk * share + x;
     const int64_t at = (int64_t)s * p.chunks + c;
-    // W and dW as operands over their rows (value channels), this wave's 16
-    // key channels as columns; on their way while the rest is staged
-    f32x4 Wf[NK][2], dWf[NK][2];
+    // what a wave reads is on its way before any of it is staged: its rows
+    // (waves 0 to 2: K and Q, once, and dY), its tiles of F and dE, and W and
+    // dW as operands over their rows with the wave's channels as columns
+    RowLoad<DP, DP, F32, VB> row;
+    const bool staged = w == 2 || (w < 2 && x == 0);
+    if (staged)
+      row.load(w == 2 ? (const char*)p.dy + ((int64_t)s * p.N + t0) * d * kE
+                      : (const char*)(w == 0 ? p.k : p.q) + krow * kE,
+               live, d, d, lane);
+    f32x4 f[2], e[2], Wf[NK][2], dWf[NK][2];
+    {
+      const int64_t o = ((at * (p.ld / 16) + (tile ? w : 0)) * 64 + lane) * 8;
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        f[rt] = ((const f32x4*)(p.ws_F + o))[rt];
+        e[rt] = ((const f32x4*)(p.ws_dE + o))[rt];
+      }
+    }
 #pragma unroll
     for (int kx = 0; kx < NK; ++kx)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int row = 32 * kx + 16 * (e >> 2) + 4 * g + (e & 3);
-        const bool in = tile && 32 * kx + 16 * (e >> 2) < p.ld;
-        const int64_t o = (at * p.ld + (in ? row : 0)) * p.ld + (in ? ch : 0);
-        const float a = p.ws_W[o], bb = p.ws_dW[o];
-        Wf[kx][e >> 2][e & 3] = in ? a : 0.f;
-        dWf[kx][e >> 2][e & 3] = in ? bb : 0.f;
+      for (int i = 0; i < 8; ++i) {
+        const int r = 32 * kx + 16 * (i >> 2) + 4 * g + (i & 3);
+        const bool in = tile && 32 * kx + 16 * (i >> 2) < p.ld;
+        const int64_t o = (at * p.ld + (in ? r : 0)) * p.ld + (in ? ch : 0);
+        Wf[kx][i >> 2][i & 3] = p.ws_W[o];
+        dWf[kx][i >> 2][i & 3] = p.ws_dW[o];
       }
     if (x > 0) __syncthreads();   // the last head's LDS is done with
-    // stage: K and Q once, dY, F and dE, the gates
-    if (w == 0 && x == 0) {
-      RowLoad<DP, DP, F32, VB> r;
-      r.load((const char*)p.k + krow * (F32 ? 4 : 2), live, d, d, lane);
-      store_planes<DP, F32>(r, Ks, lane);
-    }
-    if (w == 1 && x == 0) {
-      RowLoad<DP, DP, F32, VB> r;
-      r.load((const char*)p.q + krow * (F32 ? 4 : 2), live, d, d, lane);
-      store_planes<DP, F32>(r, Qs, lane);
-    }
-    if (w == 2) {
-      RowLoad<DP, DP, F32, VB> r;
-      r.load((const char*)p.dy + ((int64_t)s * p.N + t0) * d * (F32 ? 4 : 2), live, d, d, lane);
-      store_planes<DP, F32>(r, dYs, lane);
-    }
+    if (staged) store_planes<DP, F32>(row, w == 0 ? Ks : w == 1 ? Qs : dYs, lane);
     if (w == NW - 1) {
       const int64_t gt = (int64_t)s * p.N + t0 + min(lane, live - 1);
       const bool in = lane < live;
@@ -331,28 +348,19 @@ __global__ void __launch_bounds__(DP * 4) delta_piece_kernel(GradParams p) {
       }
       // X's upper right block
 #pragma unroll
-      for (int e = 0; e < NX; ++e) *(uint2*)(Xs + e * CP + li * kCS + 8 * g + 4) = make_uint2(0, 0);
+      for (int i = 0; i < NX; ++i) *(uint2*)(Xs + i * CP + li * kCS + 8 * g + 4) = make_uint2(0, 0);
     }
-    {
-      f32x4 f[2], e[2];
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt) f[rt] = e[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (tile) {
-        const int64_t o = ((at * (p.ld / 16) + w) * 64 + lane) * 8;
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) f[rt] = ((const f32x4*)(p.ws_F + o))[rt], e[rt] = ((const f32x4*)(p.ws_dE + o))[rt];
-      }
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) {
-        put4<3>(Fs + ch * kCS + 8 * g + 4 * rt, FP, f[rt][0], f[rt][1], f[rt][2], f[rt][3]);
-        put4<3>(dEs + ch * kCS + 8 * g + 4 * rt, FP, e[rt][0], e[rt][1], e[rt][2], e[rt][3]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = 16 * rt + 4 * g + r;
-          if (ch < d && t < rows) put<F32>(p.dv, ((int64_t)s * p.N + t0 + t) * d + ch, t < live ? e[rt][r] : 0.f);
-        }
-      }
+    for (int rt = 0; rt < 2; ++rt) {
+      if (!tile) f[rt] = e[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      put4<3>(Fs + ch * kCS + 8 * g + 4 * rt, FP, f[rt][0], f[rt][1], f[rt][2], f[rt][3]);
+      put4<3>(dEs + ch * kCS + 8 * g + 4 * rt, FP, e[rt][0], e[rt][1], e[rt][2], e[rt][3]);
     }
+#pragma unroll
+    for (int kx = 0; kx < NK; ++kx)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (!tile || 32 * kx + 16 * i >= p.ld) Wf[kx][i] = dWf[kx][i] = f32x4{0.f, 0.f, 0.f, 0.f};
     __syncthreads();
     // X, M and Z by tiles, transposed (rows j, columns t): wave 0 (t 0, j 0), 1 (t 1, j 0), 2 (t 1, j 1)
     if (w < 3) {
@@ -360,11 +368,11 @@ __global__ void __launch_bounds__(DP * 4) delta_piece_kernel(GradParams p) {
       f32x4 xx = {0.f, 0.f, 0.f, 0.f}, mm = xx, kk = xx, qk = xx;
 #pragma unroll
       for (int kx = 0; kx < NK; ++kx) {
-        bf16x8 f[3], e[3], y[NP], kj[NP], kt[NP], qt[NP];
+        bf16x8 fo[3], eo[3], y[NP], kj[NP], kt[NP], qt[NP];
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-          f[i] = read_transposed<true>(Fs + i * FP + 32 * kx * kCS, kCS, 16 * jt, lane);
-          e[i] = read_transposed<true>(dEs + i * FP + 32 * kx * kCS, kCS, 16 * tt, lane);
+          fo[i] = read_transposed<true>(Fs + i * FP + 32 * kx * kCS, kCS, 16 * jt, lane);
+          eo[i] = read_transposed<true>(dEs + i * FP + 32 * kx * kCS, kCS, 16 * tt, lane);
         }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -378,8 +386,8 @@ __global__ void __launch_bounds__(DP * 4) delta_piece_kernel(GradParams p) {
         for (int o = 2; o >= 0; --o)
 #pragma unroll
           for (int i = o; i >= 0; --i) {
-            if (o - i < NP) xx = mfma(f[i], y[o - i], xx);
-            mm = mfma(f[i], e[o - i], mm);
+            if (o - i < NP) xx = mfma(fo[i], y[o - i], xx);
+            mm = mfma(fo[i], eo[o - i], mm);
             if (i < NP && o - i < NP) {
               kk = mfma(kj[i], kt[o - i], kk);
               qk = mfma(kj[i], qt[o - i], qk);
@@ -416,108 +424,128 @@ __global__ void __launch_bounds__(DP * 4) delta_piece_kernel(GradParams p) {
       }
     }
     // what goes through W and dW, and its dots with q and k
-    bf16x8 kT[NP], qT[NP];
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      kT[i] = read_transposed<true>(Ks + i * KP, RS, 16 * w, lane);
-      qT[i] = read_transposed<true>(Qs + i * KP, RS, 16 * w, lane);
-    }
     {
-      f32x4 a[2], m[2], e[2];
+      f32x4 a[2], m[2], u[2];
       float corner = 0.f;
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt) a[rt] = m[rt] = e[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int rt = 0; rt < 2; ++rt) a[rt] = m[rt] = u[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kx = 0; kx < NK; ++kx) {
-        bf16x8 wp[3], dp[3], y[2][NP], f[2][3], ee[2][3];
+        bf16x8 wp[3], y[2][NP], o[2][3];
         split8<3>(Wf[kx][0], Wf[kx][1], wp);
-        split8<3>(dWf[kx][0], dWf[kx][1], dp);
         read2<NP>(dYs + li * RS + 32 * kx + 8 * g, KP, 16 * RS, y);
 #pragma unroll
         for (int i = 0; i < 3; ++i)
 #pragma unroll
-          for (int rt = 0; rt < 2; ++rt) {
-            f[rt][i] = read_transposed<true>(Fs + i * FP + 32 * kx * kCS, kCS, 16 * rt, lane);
-            ee[rt][i] = read_transposed<true>(dEs + i * FP + 32 * kx * kCS, kCS, 16 * rt, lane);
-          }
-        mul2<false, 3>(y, wp, a);
-        mul2<false, 3>(ee, wp, m);
-        mul2<false, 3>(f, dp, e);
+          for (int rt = 0; rt < 2; ++rt) o[rt][i] = read_transposed<true>(dEs + i * FP + 32 * kx * kCS, kCS, 16 * rt, lane);
+        mul2<true, 3>(y, wp, a);
+        mul2<true, 3>(o, wp, m);
+        split8<3>(dWf[kx][0], dWf[kx][1], wp);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt) o[rt][i] = read_transposed<true>(Fs + i * FP + 32 * kx * kCS, kCS, 16 * rt, lane);
+        mul2<true, 3>(o, wp, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) corner = fmaf(Wf[kx][i >> 2][i & 3], dWf[kx][i >> 2][i & 3], corner);
       }
+      const int pos = (ch4 & ~31) + perm32(ch4 & 31);
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt)
+      for (int rt = 0; rt < 2; ++rt) {
+        const int t = 16 * rt + li;
+        const f32x4 kv = whole<NP>(Ks + t * RS + pos, KP), qv = whole<NP>(Qs + t * RS + pos, KP);
+        float start = 0.f, end = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int t = 16 * rt + 4 * g + r;
-          const float kv = whole<NP>(kT, 4 * rt + r), qv = whole<NP>(qT, 4 * rt + r);
-          const float start = row_sum(qv * a[rt][r] - kv * m[rt][r]) * Gz[t], end = row_sum(kv * e[rt][r]) * Ez[t];
-          if (li == 0) dots[w * 2 * kC + t] = start, dots[(w * 2 + 1) * kC + t] = end;
-          dq[rt][r] = fmaf(Gt[t], a[rt][r], dq[rt][r]);
-          dk[rt][r] += Et[t] * th[t] * e[rt][r] - Gt[t] * m[rt][r];
+          start = fmaf(qv[r], a[rt][r], fmaf(-kv[r], m[rt][r], start));
+          end = fmaf(kv[r], u[rt][r], end);
         }
-      corner = row_sum(corner);
-      corner += __shfl_xor(corner, 16, 64);
-      corner += __shfl_xor(corner, 32, 64);
+        start = groups_sum(start) * Gz[t];
+        end = groups_sum(end) * Ez[t];
+        if (g == 0) dots[w * 2 * kC + t] = start, dots[(w * 2 + 1) * kC + t] = end;
+        dq[rt] += a[rt] * Gt[t];
+        dk[rt] += u[rt] * (Et[t] * th[t]) - m[rt] * Gt[t];
+        // dV, from dE's planes
+        const uint16_t* from = dEs + (ch4 + (li >> 2)) * kCS;
+        f32x4 dv = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 2; i >= 0; --i) {
+          typedef __attribute__((address_space(3))) bf16x4 lds4;
+          const bf16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(from + i * FP + perm32(16 * rt + 4 * (li & 3))));
+          dv += __builtin_convertvector(v, f32x4);
+        }
+        if (t < rows) put_four<F32, VB>(p.dv, ((int64_t)s * p.N + t0 + t) * d, t < live ? dv : f32x4{0.f, 0.f, 0.f, 0.f}, ch4, d);
+      }
+#pragma unroll
+      for (int i = 1; i < 64; i *= 2) corner += __shfl_xor(corner, i, 64);
       if (lane == 0) dots[NW * 2 * kC + w] = corner;
     }
     __syncthreads();
     // through the chunk's own tokens
     {
-      bf16x8 xr[2][NX], xt[2][NX], mr[2][NX];
+      bf16x8 xr[2][NX], xt[2][NX], mr[2][NX], kT[NP], qT[NP];
       read2<NX>(Xs + li * kCS + 8 * g, CP, 16 * kCS, xr);
       read2<NX>(Ms + li * kCS + 8 * g, CP, 16 * kCS, mr);
 #pragma unroll
       for (int i = 0; i < NX; ++i)
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) xt[rt][i] = read_transposed<true>(Xs + i * CP, kCS, 16 * rt, lane);
-      mul2<false, NP>(xr, kT, dq);
-      mul2<false, NP>(xt, qT, dk);
-      mul2<false, NP>(mr, kT, dk);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        kT[i] = read_transposed<true>(Ks + i * KP, RS, 16 * w, lane);
+        qT[i] = read_transposed<true>(Qs + i * KP, RS, 16 * w, lane);
+      }
+      mul2<true, NP>(xr, kT, dq);
+      mul2<true, NP>(xt, qT, dk);
+      mul2<true, NP>(mr, kT, dk);
     }
     // the gates: lane j < 32 sums column j of Z theta up from the end's row, lane 32 the start's column
     if (w == NW - 1) {
-      float sum = 0.f, dtheta = 0.f, end = 0.f;
-      const float tj = lane < kC ? th[lane] : 0.f;
-      if (lane < kC)
-        for (int i = 0; i < NW; ++i) end += dots[(i * 2 + 1) * kC + lane];
-      if (lane == kC)
-        for (int i = 0; i < NW; ++i) sum += dots[NW * 2 * kC + i];
-      if (lane < kC) sum = end * tj;
-      sum = lane == kC ? sum * Gz[kC - 1] : sum;
+      const float tj = lane < kC ? th[lane] : 1.f;
+      float end = 0.f, start = 0.f, corner = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        start += dots[i * 2 * kC + (lane & 31)];
+        end += dots[(i * 2 + 1) * kC + (lane & 31)];
+        corner += dots[NW * 2 * kC + i];
+      }
+      if (lane < kC) Z[lane * kBS + kC] = start;
+      wave_fence();
+      const int col = min(lane, kC);
+      float z[kC], dtheta = 0.f, sum = lane < kC ? end * tj : corner * Gz[kC - 1];
+#pragma unroll
+      for (int i = 0; i < kC; ++i) z[i] = Z[i * kBS + col];
+      wave_fence();
+#pragma unroll
       for (int i = kC - 1; i >= 0; --i) {
-        float z = 0.f;
-        if (lane < kC) {
-          if (i >= lane) z = Z[i * kBS + lane];
-          dtheta += z;
-          z *= tj;
-        } else if (lane == kC) {
-          for (int k = 0; k < NW; ++k) z += dots[k * 2 * kC + i];
-        }
-        sum += z;
-        if (lane <= kC) Z[i * kBS + lane] = sum;
+        const float v = lane >= kC || i >= lane ? z[i] : 0.f;   // (above the diagonal nothing was written)
+        dtheta += v;
+        sum = fmaf(v, tj, sum);
+        if (lane <= kC) Z[i * kBS + col] = sum;
       }
       wave_fence();
+      const int t = lane & 31;
+      float through = Z[t * kBS + kC];
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        const float v = Z[t * kBS + j];
+        through += j < t ? v : 0.f;
+      }
       if (lane < rows) {
         const int64_t gt = (int64_t)s * p.N + t0 + lane;
-        float through = Z[lane * kBS + kC];
-        for (int j = 0; j < lane; ++j) through += Z[lane * kBS + j];
         p.dtheta[gt] = lane < live ? dtheta + end : 0.f;
         p.dalpha[gt] = lane < live ? -through * exp2_of(-la_z) : 0.f;
       }
     }
   }
 #pragma unroll
-  for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * rt + 4 * g + r;
-      if (ch < d && t < rows) {
-        put<F32>(p.dq, krow + (int64_t)t * d + ch, t < live ? dq[rt][r] : 0.f);
-        put<F32>(p.dk, krow + (int64_t)t * d + ch, t < live ? dk[rt][r] : 0.f);
-      }
-    }
+  for (int rt = 0; rt < 2; ++rt) {
+    const int t = 16 * rt + li;
+    if (t >= rows) continue;
+    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    put_four<F32, VB>(p.dq, krow + (int64_t)t * d, t < live ? dq[rt] : none, ch4, d);
+    put_four<F32, VB>(p.dk, krow + (int64_t)t * d, t < live ? dk[rt] : none, ch4, d);
+  }
 }
 
 template <int DP, bool F32, int VB>
