@@ -315,15 +315,16 @@ __global__ void __launch_bounds__(DP * 4, 2) delta_piece_kernel(GradParams p) {
         e[rt] = ((const f32x4*)(p.ws_dE + o))[rt];
       }
     }
+    // (uniform row addresses and one offset a lane)
+    const float *W = p.ws_W + at * p.ld * p.ld, *dW = p.ws_dW + at * p.ld * p.ld;
+    const uint32_t lane_off = 4 * g * p.ld + (tile ? ch : li);
 #pragma unroll
     for (int kx = 0; kx < NK; ++kx)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int r = 32 * kx + 16 * (i >> 2) + 4 * g + (i & 3);
-        const bool in = tile && 32 * kx + 16 * (i >> 2) < p.ld;
-        const int64_t o = (at * p.ld + (in ? r : 0)) * p.ld + (in ? ch : 0);
-        Wf[kx][i >> 2][i & 3] = p.ws_W[o];
-        dWf[kx][i >> 2][i & 3] = p.ws_dW[o];
+        const int r = 32 * kx + 16 * (i >> 2), at_row = (r < p.ld ? r + (i & 3) : i & 3) * p.ld;
+        Wf[kx][i >> 2][i & 3] = (W + at_row)[lane_off];
+        dWf[kx][i >> 2][i & 3] = (dW + at_row)[lane_off];
       }
     if (x > 0) __syncthreads();   // the last head's LDS is done with
     if (staged) store_planes<DP, F32>(row, w == 0 ? Ks : w == 1 ? Qs : dYs, lane);
@@ -368,6 +369,7 @@ __global__ void __launch_bounds__(DP * 4, 2) delta_piece_kernel(GradParams p) {
       f32x4 xx = {0.f, 0.f, 0.f, 0.f}, mm = xx, kk = xx, qk = xx;
 #pragma unroll
       for (int kx = 0; kx < NK; ++kx) {
+        asm volatile("" : "+v"(xx), "+v"(mm), "+v"(kk), "+v"(qk) : : "memory");
         bf16x8 fo[3], eo[3], y[NP], kj[NP], kt[NP], qt[NP];
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
@@ -431,6 +433,8 @@ __global__ void __launch_bounds__(DP * 4, 2) delta_piece_kernel(GradParams p) {
       for (int rt = 0; rt < 2; ++rt) a[rt] = m[rt] = u[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kx = 0; kx < NK; ++kx) {
+        // (tied to the sums: the reads of later steps stay behind, and in registers)
+        asm volatile("" : "+v"(a[0]), "+v"(m[0]), "+v"(u[0]) : : "memory");
         bf16x8 wp[3], y[2][NP], o[2][3];
         split8<3>(Wf[kx][0], Wf[kx][1], wp);
         read2<NP>(dYs + li * RS + 32 * kx + 8 * g, KP, 16 * RS, y);
