@@ -52,13 +52,12 @@ using GradLds = ChunkLds<DP, F32 ? 3 : 1, 3, 32>;
 
 // ---- the two sweeps: blocks of the first half forwards, of the second backwards ----
 template <int DP, bool F32, int PB, int NB, int VB>
-__global__ void __launch_bounds__((2 + PB) * 64) delta_sweep_kernel(GradParams p) {
+__global__ void __launch_bounds__((2 + PB * (F32 ? 2 : 1)) * 64) delta_sweep_kernel(GradParams p) {
   constexpr int CW = 2, NP = F32 ? 3 : 1;
   constexpr int NT = DP / 16, NK = DP / 32, kE = F32 ? 4 : 2;
   using Lds = GradLds<DP, F32>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  int* built = (int*)(smem + NB * Lds::BYTES);
-  int* used = built + PB;
+  const Ring<Lds, CW, PB, NB, F32> ring{smem};
   const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = gridDim.x / 2;   // a multiple of 8
@@ -69,19 +68,17 @@ __global__ void __launch_bounds__((2 + PB) * 64) delta_sweep_kernel(GradParams p
   const int b = s / p.H, h = s % p.H, d = p.d;
   const int n = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
   const int chunks = (n + kC - 1) / kC;
-  init_ring<Lds, NB, CW, PB>(smem, built, wave, lane);
+  ring.init(wave, lane);
 
   if (wave >= CW) {
     const int col0 = part * CW * 16;
     const int64_t krow = ((int64_t)b * p.Hk + h / (p.H / p.Hk)) * p.N * d, vrow = (int64_t)s * p.N * d + col0;
-    const char *k = (const char*)p.k + krow * kE, *q = (const char*)p.q + krow * kE;
-    const float *alpha = p.alpha + (int64_t)s * p.N, *theta = p.theta + (int64_t)s * p.N;
+    const Rows in = {(const char*)p.k + krow * kE,   (const char*)p.q + krow * kE,  (const char*)(back ? p.dy : p.v) + vrow * kE,
+                     p.alpha + (int64_t)s * p.N, p.theta + (int64_t)s * p.N, chunks, n, d, d - col0};
     if (back)
-      run_builder<DP, F32, CW, PB, NB, VB, 3, true, true>(smem, built, used, wave - CW, lane, chunks, n, d, d - col0, k, q,
-                                                          (const char*)p.dy + vrow * kE, alpha, theta, kForget);
+      run_builder<DP, F32, VB, 32, true, true>(ring, wave, lane, in);
     else
-      run_builder<DP, F32, CW, PB, NB, VB, 3, false, false>(smem, built, used, wave - CW, lane, chunks, n, d, d - col0, k,
-                                                            q, (const char*)p.v + vrow * kE, alpha, theta, kForget);
+      run_builder<DP, F32, VB, 32, false, false>(ring, wave, lane, in);
     return;
   }
 
@@ -104,8 +101,8 @@ __global__ void __launch_bounds__((2 + PB) * 64) delta_sweep_kernel(GradParams p
       for (int ti = 0; ti < NT; ++ti)
         if (16 * ti < p.ld) *(f32x4*)(state + 16 * ti) = S[ti];
     }
-    wait_for(built + i % PB, i + 1);
-    const Lds L{smem + i % NB * Lds::BYTES};
+    wait_for(ring.built() + i % PB, i + 1);
+    const Lds L = ring.buffer(i);
     f32x4 ks[2], V[2], G[2], E[2], X[2];
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) ks[rt] = X[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -195,7 +192,7 @@ __global__ void __launch_bounds__((2 + PB) * 64) delta_sweep_kernel(GradParams p
       split8<3>(U[0], U[1], up);
       fold(L.q());
     }
-    raise_to(used + wave, i + 1, lane);
+    raise_to(ring.used() + wave, i + 1, lane);
 #pragma unroll
     for (int ti = 0; ti < NT; ++ti) S[ti] = scaled ? S[ti] + acc[ti] * scale : acc[ti];
   }
@@ -555,7 +552,8 @@ __global__ void __launch_bounds__(DP * 4, 2) delta_piece_kernel(GradParams p) {
 template <int DP, bool F32, int VB>
 hipError_t launch_grad(GradParams p, hipStream_t stream) {
   constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : DP == 64 ? 3 : 4, PB = F32 && DP == 128 ? 1 : 2;
-  constexpr int lds = NB * GradLds<DP, F32>::BYTES + (PB + 2) * 4, piece = PieceLds<DP, F32>::BYTES;
+  using R = Ring<GradLds<DP, F32>, 2, PB, NB, F32>;
+  constexpr int lds = R::BYTES, piece = PieceLds<DP, F32>::BYTES;
   static_assert(lds <= 160 * 1024 && piece <= 160 * 1024, "LDS of one workgroup");
   auto sweep = delta_sweep_kernel<DP, F32, PB, NB, VB>;
   auto pieces = delta_piece_kernel<DP, F32, VB>;
@@ -565,7 +563,7 @@ hipError_t launch_grad(GradParams p, hipStream_t stream) {
   if (err != hipSuccess) return err;
   p.parts = ((p.d + 15) / 16 + 1) / 2;
   const unsigned half = (unsigned)((p.B * p.H + 7) / 8 * 8 * p.parts);
-  sweep<<<2 * half, (2 + PB) * 64, lds, stream>>>(p);
+  sweep<<<2 * half, R::WAVES * 64, lds, stream>>>(p);
   err = hipGetLastError();
   if (err != hipSuccess || p.chunks == 0) return err;
   pieces<<<(unsigned)(p.B * p.Hk * p.chunks), DP * 4, piece, stream>>>(p);

@@ -465,48 +465,59 @@ __device__ __forceinline__ void raise_to(int* p, int value, int lane) {
 }
 
 
-// The chunk ring of a workgroup of CW chain and PB builder waves, NB buffers:
-// counters to zero and the blocks of T that stay zero; every wave calls it.
-template <class Lds, int NB, int CW, int PB>
-__device__ __forceinline__ void init_ring(unsigned char* smem, int* built, int wave, int lane) {
-  if (threadIdx.x < PB + CW) built[threadIdx.x] = 0;
-  for (int x = wave; x < 3 * NB; x += CW + PB) {
-    Lds L{smem + x / 3 * Lds::BYTES};
-    *(uint2*)(L.t() + x % 3 * Lds::CP + (lane & 15) * kCS + 8 * (lane >> 4) + 4) = make_uint2(0, 0);
+// A workgroup's waves around a ring of NB chunk buffers: CW chain waves, PB
+// builders and, for fp32 inputs, a helper for every builder, which splits and
+// stores Q and V (a third of a builder's time, and half of its registers).
+// Their counters, after the buffers: chunks that a builder has finished, that
+// a chain wave has, that a helper has.
+template <class Lds, int CW, int PB, int NB, bool HELP>
+struct Ring {
+  static_assert(NB > PB, "a chunk is consumed while PB are built");
+  static constexpr int WAVES = CW + PB * (HELP ? 2 : 1), COUNTERS = CW + 2 * PB,
+                       BYTES = NB * Lds::BYTES + COUNTERS * 4;
+  unsigned char* smem;
+  __device__ int* built() const { return (int*)(smem + NB * Lds::BYTES); }
+  __device__ int* used() const { return built() + PB; }
+  __device__ int* stored() const { return used() + CW; }
+  __device__ Lds buffer(int i) const { return Lds{smem + i % NB * Lds::BYTES}; }
+  // counters to zero, and the blocks of T that stay zero; every wave calls it
+  __device__ __forceinline__ void init(int wave, int lane) const {
+    if (threadIdx.x < COUNTERS) built()[threadIdx.x] = 0;
+    for (int x = wave; x < 3 * NB; x += WAVES)
+      *(uint2*)(buffer(x / 3).t() + x % 3 * Lds::CP + (lane & 15) * kCS + 8 * (lane >> 4) + 4) = make_uint2(0, 0);
+    __syncthreads();
   }
-  __syncthreads();
-}
+};
 
-// Builder wave pw: the ring's chunks pw, pw + PB, ... (BACK: counted from the
-// sequence's end), from a stream's K, Q (WITH_Q), V rows and gates.  floor:
-// log2_keep's.
-template <int DP, bool F32, int CW, int PB, int NB, int VB, int NPP, bool WITH_Q, bool BACK>
-__device__ __forceinline__ void run_builder(unsigned char* smem, int* built, const int* used, int pw, int lane,
-                                            int chunks, int n, int d, int vcols, const char* k, const char* q,
-                                            const char* v, const float* alpha, const float* theta, float floor) {
-  constexpr int NP = F32 ? 3 : 1, kE = F32 ? 4 : 2;
-  using Lds = ChunkLds<DP, NP, NPP, CW * 16>;
-  RowLoad<DP, DP, F32, VB> kr, qr;
-  RowLoad<DP, CW * 16, F32, VB> vr;
-  float al = 0.f, th = 0.f;
-  auto fetch = [&](int i) {
-    if (i >= chunks) return;
-    const int t0 = (BACK ? chunks - 1 - i : i) * kC, m = min(kC, n - t0);
-    const int64_t at = (int64_t)t0 * d * kE;
-    kr.load(k + at, m, d, d, lane);
-    if (WITH_Q) qr.load(q + at, m, d, d, lane);
-    vr.load(v + at, m, d, vcols, lane);
-    al = alpha[t0 + min(lane, m - 1)];   // (zeroed when used: nothing here waits)
-    th = theta[t0 + min(lane, m - 1)];
-  };
-  fetch(pw);
-  for (int i = pw; i < chunks; i += PB) {
-    Lds L{smem + i % NB * Lds::BYTES};
-    const bool in = (BACK ? chunks - 1 - i : i) * kC + lane < n;
-    const float la = in ? log2_keep(al, floor) : 0.f, th0 = in ? th : 0.f;
+// A stream's (or a segment's) rows and gates, for its builders.
+struct Rows {
+  const char *k, *q, *v;
+  const float *alpha, *theta;
+  int chunks, n, d, vcols;   // vcols: real columns of v from its address on
+};
+
+// Wave `wave` >= CW of a ring: builder pw builds the chunks pw, pw + PB, ...
+// (BACK: counted from the sequence's end).  WITH_Q: Q and P too.
+template <int DP, bool F32, int VB, int VC, bool WITH_Q, bool BACK, class Lds, int CW, int PB, int NB, bool HELP>
+__device__ __forceinline__ void run_builder(const Ring<Lds, CW, PB, NB, HELP>& ring, int wave, int lane, const Rows& in) {
+  constexpr int kE = F32 ? 4 : 2;
+  const bool helps = HELP && wave >= CW + PB;
+  const int pw = wave - CW - (helps ? PB : 0);
+  auto first = [&](int i) { return (BACK ? in.chunks - 1 - i : i) * kC; };
+  auto wait_free = [&](int i) {
 #pragma unroll
-    for (int w = 0; w < CW; ++w) wait_for(used + w, i - NB + 1);
-    store_planes<DP, F32>(kr, L.k(), lane);
+    for (int w = 0; w < CW; ++w) wait_for(ring.used() + w, i - NB + 1);
+  };
+  RowLoad<DP, DP, F32, VB> qr;
+  RowLoad<DP, VC, F32, VB> vr;
+  auto fetch_qv = [&](int i) {
+    if (i >= in.chunks) return;
+    const int t0 = first(i), m = min(kC, in.n - t0);
+    const int64_t at = (int64_t)t0 * in.d * kE;
+    if (WITH_Q) qr.load(in.q + at, m, in.d, in.d, lane);
+    vr.load(in.v + at, m, in.d, in.vcols, lane);
+  };
+  auto store_qv = [&](const Lds& L) {
     if (WITH_Q) store_planes<DP, F32>(qr, L.q(), lane);
     vr.store(lane, [&](int r, int c, const uint32_t* x) {
       if constexpr (F32)
@@ -514,10 +525,43 @@ __device__ __forceinline__ void run_builder(unsigned char* smem, int* built, con
       else
         *(uint2*)((uint16_t*)L.v() + r * Lds::VS + c) = make_uint2(x[0], x[1]);
     });
+  };
+  if (helps) {
+    fetch_qv(pw);
+    for (int i = pw; i < in.chunks; i += PB) {
+      wait_free(i);
+      store_qv(ring.buffer(i));
+      fetch_qv(i + PB);
+      raise_to(ring.stored() + pw, i + 1, lane);
+    }
+    return;
+  }
+  RowLoad<DP, DP, F32, VB> kr;
+  float al = 0.f, th = 0.f;
+  auto fetch = [&](int i) {
+    if (i >= in.chunks) return;
+    const int t0 = first(i), m = min(kC, in.n - t0);
+    kr.load(in.k + (int64_t)t0 * in.d * kE, m, in.d, in.d, lane);
+    al = in.alpha[t0 + min(lane, m - 1)];   // (zeroed when used: nothing here waits)
+    th = in.theta[t0 + min(lane, m - 1)];
+  };
+  fetch(pw);
+  if (!HELP) fetch_qv(pw);
+  for (int i = pw; i < in.chunks; i += PB) {
+    const Lds L = ring.buffer(i);
+    const bool real = first(i) + lane < in.n;
+    const float la = real ? log2_keep(al) : 0.f, th0 = real ? th : 0.f;
+    wait_free(i);
+    store_planes<DP, F32>(kr, L.k(), lane);
+    if (!HELP) store_qv(L);
     fetch(i + PB);
+    if (HELP)
+      wait_for(ring.stored() + pw, i + 1);
+    else
+      fetch_qv(i + PB);
     wave_fence();
     build_chunk<WITH_Q>(L, la, th0, lane);
-    raise_to(built + pw, i + 1, lane);
+    raise_to(ring.built() + pw, i + 1, lane);
   }
 }
 

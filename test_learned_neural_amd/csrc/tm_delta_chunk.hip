@@ -59,14 +59,12 @@ __device__ __forceinline__ void store_ws(const f32x4 (&S)[NT], float* W, int row
 // TRANS: the segments' maps instead of y: column groups up to d from zero with
 // the values, as many again from the unit vectors without.
 template <int DP, bool F32, int CW, int PB, int NB, int VB, bool TRANS>
-__global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams p) {
-  static_assert(NB > PB, "a chunk is consumed while PB are built");
+__global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_kernel(ChainParams p) {
   constexpr int NP = F32 ? 3 : 1, NPP = F32 ? 3 : 2, NS = F32 ? 3 : 2;   // planes: inputs, P, and W and F for y
   constexpr int NT = DP / 16, NK = DP / 32, kE = F32 ? 4 : 2;
   using Lds = ChunkLds<DP, NP, NPP, CW * 16>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  int* built = (int*)(smem + NB * Lds::BYTES);   // [PB]: chunks a builder has finished, counted from the sequence's start
-  int* used = built + PB;                        // [CW]: chunks a chain wave has finished
+  const Ring<Lds, CW, PB, NB, F32> ring{smem};
   const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // the parts of a stream's segment read the same K and Q: workgroups 8 apart share an XCD's L2
@@ -79,16 +77,15 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
   const int first = (int)min((int64_t)seg * p.seg_chunks * kC, (int64_t)all);   // the segment's tokens: first .. first + n - 1
   const int n = seg + 1 < p.segments ? (int)min((int64_t)(all - first), (int64_t)p.seg_chunks * kC) : all - first;
   const int chunks = (n + kC - 1) / kC;
-  init_ring<Lds, NB, CW, PB>(smem, built, wave, lane);
+  ring.init(wave, lane);
 
   if (wave >= CW) {
     const int col0 = part * CW * 16, vcols = max(d - col0, 0);
-    const int64_t t0 = first;
-    const int64_t krow = (((int64_t)b * p.Hk + h / (p.H / p.Hk)) * p.N + t0) * d;
-    const int64_t vrow = ((int64_t)s * p.N + t0) * d + (vcols > 0 ? col0 : 0), gate = (int64_t)s * p.N + t0;
-    run_builder<DP, F32, CW, PB, NB, VB, NPP, !TRANS, false>(
-        smem, built, used, wave - CW, lane, chunks, n, d, vcols, (const char*)p.k + krow * kE,
-        (const char*)p.q + krow * kE, (const char*)p.v + vrow * kE, p.alpha + gate, p.theta + gate, kForget);
+    const int64_t krow = (((int64_t)b * p.Hk + h / (p.H / p.Hk)) * p.N + first) * d;
+    const int64_t vrow = ((int64_t)s * p.N + first) * d + (vcols > 0 ? col0 : 0), gate = (int64_t)s * p.N + first;
+    const Rows in = {(const char*)p.k + krow * kE, (const char*)p.q + krow * kE, (const char*)p.v + vrow * kE,
+                     p.alpha + gate, p.theta + gate, chunks, n, d, vcols};
+    run_builder<DP, F32, VB, CW * 16, !TRANS, false>(ring, wave, lane, in);
     return;
   }
 
@@ -115,9 +112,9 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
   const uint32_t yoff = ((uint32_t)li * d + ych) * kE;
   int ready = 0;   // what built[c % PB] was when last read
   for (int c = 0; c < chunks; ++c) {
-    if (ready <= c) wait_for(built + c % PB, c + 1);
+    if (ready <= c) wait_for(ring.built() + c % PB, c + 1);
     acquire();
-    const Lds L{smem + c % NB * Lds::BYTES};
+    const Lds L = ring.buffer(c);
     const uint16_t *ka = L.k() + li * Lds::RS + 8 * g, *qa = L.q() + li * Lds::RS + 8 * g;
     const uint16_t *ta = L.t() + li * kCS + 8 * g, *pa = L.p() + li * kCS + 8 * g;
     // The order below keeps LDS reads a product ahead of their use, and
@@ -213,11 +210,11 @@ __global__ void __launch_bounds__((CW + PB) * 64) delta_chain_kernel(ChainParams
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) out[rt] = qs[rt] * L.g()[16 * rt + li];
     }
-    ready = seen(built + (c + 1) % PB);
+    ready = seen(ring.built() + (c + 1) % PB);
     if (!TRANS) mul2<true, NS>(rp2, fp, out);
 #pragma unroll
     for (int ti = 0; ti < NT; ++ti) S[ti] = scaled ? S[ti] + acc[ti] * scale : acc[ti];
-    raise_to(used + wave, c + 1, lane);
+    raise_to(ring.used() + wave, c + 1, lane);
     const int t0 = c * kC;
     char* at = ydst + (int64_t)t0 * d * kE;
     auto store = [&](int rt) {
@@ -336,7 +333,8 @@ template <int DP, bool F32, int CW, int VB, bool TRANS>
 hipError_t launch_as(ChainParams p, hipStream_t stream) {
   // as many buffers as LDS holds, and builders as keep the chain fed
   constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : 4, PB = F32 ? (DP == 128 ? 1 : 2) : DP == 64 ? 3 : 2;
-  constexpr int lds = NB * ChunkLds<DP, F32 ? 3 : 1, F32 ? 3 : 2, CW * 16>::BYTES + (PB + CW) * 4;
+  using R = Ring<ChunkLds<DP, F32 ? 3 : 1, F32 ? 3 : 2, CW * 16>, CW, PB, NB, F32>;
+  constexpr int lds = R::BYTES;
   static_assert(lds <= 160 * 1024, "LDS of one workgroup");
   p.parts = ((p.d + 15) / 16 * (TRANS ? 2 : 1) + CW - 1) / CW;
   auto kernel = delta_chain_kernel<DP, F32, CW, PB, NB, VB, TRANS>;
@@ -344,7 +342,7 @@ hipError_t launch_as(ChainParams p, hipStream_t stream) {
   if (err != hipSuccess) return err;
   const int units = p.streams * (TRANS ? p.segments - 1 : p.segments);
   const unsigned grid = (unsigned)((units + 7) / 8 * 8 * p.parts);
-  kernel<<<grid, (CW + PB) * 64, lds, stream>>>(p);
+  kernel<<<grid, R::WAVES * 64, lds, stream>>>(p);
   return hipGetLastError();
 }
 
