@@ -47,15 +47,15 @@ struct GradParams {
   int B, H, Hk, N, d, ld, chunks, parts;
 };
 
-template <int DP, bool F32>
-using GradLds = ChunkLds<DP, F32 ? 3 : 1, 3, 32>;
+template <int DP, bool F32, int CW>
+using GradLds = ChunkLds<DP, F32 ? 3 : 1, 3, CW * 16>;
 
 // ---- the two sweeps: blocks of the first half forwards, of the second backwards ----
-template <int DP, bool F32, int PB, int NB, int VB>
-__global__ void __launch_bounds__((2 + PB * (F32 ? 2 : 1)) * 64) delta_sweep_kernel(GradParams p) {
-  constexpr int CW = 2, NP = F32 ? 3 : 1;
+template <int DP, bool F32, int CW, int PB, int NB, int VB>
+__global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_sweep_kernel(GradParams p) {
+  constexpr int NP = F32 ? 3 : 1;
   constexpr int NT = DP / 16, NK = DP / 32, kE = F32 ? 4 : 2;
-  using Lds = GradLds<DP, F32>;
+  using Lds = GradLds<DP, F32, CW>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const Ring<Lds, CW, PB, NB, F32> ring{smem};
   const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
@@ -76,9 +76,9 @@ __global__ void __launch_bounds__((2 + PB * (F32 ? 2 : 1)) * 64) delta_sweep_ker
     const Rows in = {(const char*)p.k + krow * kE,   (const char*)p.q + krow * kE,  (const char*)(back ? p.dy : p.v) + vrow * kE,
                      p.alpha + (int64_t)s * p.N, p.theta + (int64_t)s * p.N, chunks, n, d, d - col0};
     if (back)
-      run_builder<DP, F32, VB, 32, true, true>(ring, wave, lane, in);
+      run_builder<DP, F32, VB, CW * 16, true, true>(ring, wave, lane, in);
     else
-      run_builder<DP, F32, VB, 32, false, false>(ring, wave, lane, in);
+      run_builder<DP, F32, VB, CW * 16, false, false>(ring, wave, lane, in);
     return;
   }
 
@@ -549,23 +549,36 @@ __global__ void __launch_bounds__(DP * 4, 2) delta_piece_kernel(GradParams p) {
   }
 }
 
+template <int DP, bool F32, int CW, int VB>
+hipError_t launch_sweep(GradParams p, hipStream_t stream) {
+  // (two workgroups of 2 chain waves share a CU where LDS allows)
+  constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : DP == 64 && CW == 2 ? 3 : 4,
+                PB = F32 ? (DP == 128 ? 1 : 2) : DP == 64 && CW == 4 ? 3 : 2;
+  using R = Ring<GradLds<DP, F32, CW>, CW, PB, NB, F32>;
+  static_assert(R::BYTES <= 160 * 1024, "LDS of one workgroup");
+  p.parts = ((p.d + 15) / 16 + CW - 1) / CW;
+  auto sweep = delta_sweep_kernel<DP, F32, CW, PB, NB, VB>;
+  hipError_t err = hipFuncSetAttribute((const void*)sweep, hipFuncAttributeMaxDynamicSharedMemorySize, R::BYTES);
+  if (err != hipSuccess) return err;
+  const unsigned half = (unsigned)((p.B * p.H + 7) / 8 * 8 * p.parts);
+  sweep<<<2 * half, R::WAVES * 64, R::BYTES, stream>>>(p);
+  return hipGetLastError();
+}
+
+// Four chain waves in a workgroup share one builder's work, two take less time
+// a chunk: four where the device is full either way (128 streams x 1024, d 64,
+// bf16: 60 us against 87; 8 streams x 2048: 135 against 104).
 template <int DP, bool F32, int VB>
 hipError_t launch_grad(GradParams p, hipStream_t stream) {
-  constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : DP == 64 ? 3 : 4, PB = F32 && DP == 128 ? 1 : 2;
-  using R = Ring<GradLds<DP, F32>, 2, PB, NB, F32>;
-  constexpr int lds = R::BYTES, piece = PieceLds<DP, F32>::BYTES;
-  static_assert(lds <= 160 * 1024 && piece <= 160 * 1024, "LDS of one workgroup");
-  auto sweep = delta_sweep_kernel<DP, F32, PB, NB, VB>;
+  constexpr int kCus = 256, piece = PieceLds<DP, F32>::BYTES;
+  static_assert(piece <= 160 * 1024, "LDS of one workgroup");
+  const int groups = (p.d + 15) / 16;
+  hipError_t err = 2 * p.B * p.H * ((groups + 1) / 2) > kCus ? launch_sweep<DP, F32, 4, VB>(p, stream)
+                                                             : launch_sweep<DP, F32, 2, VB>(p, stream);
+  if (err != hipSuccess || p.chunks == 0) return err;
   auto pieces = delta_piece_kernel<DP, F32, VB>;
-  hipError_t err = hipFuncSetAttribute((const void*)sweep, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (err != hipSuccess) return err;
   err = hipFuncSetAttribute((const void*)pieces, hipFuncAttributeMaxDynamicSharedMemorySize, piece);
   if (err != hipSuccess) return err;
-  p.parts = ((p.d + 15) / 16 + 1) / 2;
-  const unsigned half = (unsigned)((p.B * p.H + 7) / 8 * 8 * p.parts);
-  sweep<<<2 * half, R::WAVES * 64, lds, stream>>>(p);
-  err = hipGetLastError();
-  if (err != hipSuccess || p.chunks == 0) return err;
   pieces<<<(unsigned)(p.B * p.Hk * p.chunks), DP * 4, piece, stream>>>(p);
   return hipGetLastError();
 }

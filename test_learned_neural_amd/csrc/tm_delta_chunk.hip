@@ -348,8 +348,8 @@ hipError_t launch_as(ChainParams p, hipStream_t stream) {
 
 // How a call is cut.  Times of a chunk of 32 tokens in a workgroup that has a
 // CU to itself, in tenths of a microsecond, as measured on 16 to 512 streams:
-// d up to 64 with 2 chain waves 12, with 4 18 (128: 17 and 24; fp32: 21 and
-// 29, 60 and 107), two thirds of that without y.
+// d up to 64 with 2 chain waves 13, with 4 18 (128: 17 and 24; fp32: 20 and
+// 30, 46 and 62), two thirds of that without y.
 struct Plan {
   int wide;       // 4 chain waves in a workgroup of the (last) launch
   int segments;   // 1: one launch
@@ -357,8 +357,8 @@ struct Plan {
 };
 constexpr int kCus = 256;
 int chunk_cost(const DeltaShape& s, int cw) {
-  if (s.io == TM_IO_BF16) return s.d <= 64 ? (cw == 2 ? 12 : 18) : cw == 2 ? 17 : 24;
-  return s.d <= 64 ? (cw == 2 ? 21 : 29) : cw == 2 ? 60 : 107;
+  if (s.io == TM_IO_BF16) return s.d <= 64 ? (cw == 2 ? 13 : 18) : cw == 2 ? 17 : 24;
+  return s.d <= 64 ? (cw == 2 ? 20 : 30) : cw == 2 ? 46 : 62;
 }
 Plan plan_of(const DeltaShape& s) {
   const int64_t streams = (int64_t)s.B * s.H, chunks = (s.N + kC - 1) / kC, groups = (s.d + 15) / 16;

@@ -72,27 +72,38 @@ __device__ __forceinline__ void store_piece(void* p, int64_t i, const float (&x)
     else
       ((float*)p)[i] = x[0];
   } else if constexpr (BF16) {
-    uint32_t u[VEC / 2];
+    typedef __attribute__((ext_vector_type(VEC))) float fv;
+    typedef __attribute__((ext_vector_type(VEC))) __bf16 bv;
+    fv v;
 #pragma unroll
-    for (int j = 0; j < VEC / 2; ++j) u[j] = to_bf16(x[2 * j]) | (uint32_t)to_bf16(x[2 * j + 1]) << 16;
-    if constexpr (VEC == 4)
-      *(uint2*)((uint16_t*)p + i) = make_uint2(u[0], u[1]);
-    else
-      *(uint4*)((uint16_t*)p + i) = make_uint4(u[0], u[1], u[2], u[3]);
+    for (int j = 0; j < VEC; ++j) v[j] = x[j];
+    *(bv*)((uint16_t*)p + i) = __builtin_convertvector(v, bv);
   } else {
     *(float4*)((float*)p + i) = make_float4(x[0], x[1], x[2], x[3]);
   }
 }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+
+// sum over L neighbouring lanes, in every lane: DPP within a row of 16 (each
+// step adds the other half, mirrored), which stays out of LDS
 template <int L>
 __device__ __forceinline__ float group_sum(float x) {
-#pragma unroll
-  for (int m = L / 2; m >= 1; m /= 2) x += __shfl_xor(x, m, 64);
+  if (L >= 2) x = dpp_add<0xB1>(x);    // quad_perm 1 0 3 2
+  if (L >= 4) x = dpp_add<0x4E>(x);    // quad_perm 2 3 0 1
+  if (L >= 8) x = dpp_add<0x141>(x);   // row_half_mirror
+  if (L >= 16) x = dpp_add<0x140>(x);  // row_mirror
+  if (L >= 32) x += __shfl_xor(x, 16, 64);
+  if (L >= 64) x += __shfl_xor(x, 32, 64);
   return x;
 }
 
-// 1 / (1 + exp(-z)), to a few units in the last place; 0 and 1 at the ends
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + __expf(-z)); }
+// 1 / (1 + exp(-z)), to a few units in the last place (a reciprocal
+// instruction: a division is ten); 0 and 1 at the ends
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 template <bool BF16, int VEC, int L, int IT, bool GRAD>
 __global__ void __launch_bounds__(kThreads) group_norm_kernel(NormParams p) {
@@ -111,15 +122,22 @@ __global__ void __launch_bounds__(kThreads) group_norm_kernel(NormParams p) {
       dw[i][j] = db[i][j] = 0.f;
     }
   const int64_t r0 = (int64_t)blockIdx.x * p.per, r1 = min(r0 + p.per, p.rows);
-  // every lane of a wave runs the same rounds: groups past the end do no loads, but take part in the shuffles
+  // every lane of a wave runs the same rounds: groups past the end do no loads, but take part in the sums
+  const uint32_t N = max(p.N, 1);
+  int64_t b = (r0 + g) / N;
+  uint32_t t = (uint32_t)((r0 + g) - b * N);
   for (int64_t rb = r0; rb < r1; rb += kGroups) {
     const int64_t r = rb + g;
-    bool live = r < r1;
-    const int64_t b = live ? r / p.N : 0, t = live ? r - b * p.N : 0;
-    bool past = false;
-    if (live && p.lengths && t >= p.lengths[b]) live = false, past = true;
+    bool live = r < r1, past = false;
+    if (live && p.lengths && (int64_t)t >= p.lengths[b]) live = false, past = true;
     const int64_t ct = r * C + (int64_t)h * p.d;
     const int64_t xt = p.first ? ((b * p.H + h) * (int64_t)p.N + t) * p.d : ct;
+    t += kGroups;
+    if (t >= N) {
+      const uint32_t more = t / N;
+      b += more;
+      t -= more * N;
+    }
     float x[IT][VEC], z[IT][VEC], go[IT][VEC], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
@@ -263,12 +281,12 @@ hipError_t launch(const NormParams& p, int slices, bool grad, hipStream_t stream
   }
 }
 
-// Workgroups along the tokens: enough of them that the grid (times H) fills
-// the device several times over, none with fewer than 64 tokens.
+// Workgroups along the tokens: 2048 in all (the device holds about as many;
+// 4096 or 8192 cost the gradient 4% and 9%), none with fewer than 64 tokens.
 int slices_of(const NormShape& s) {
   const int64_t rows = (int64_t)s.B * s.N;
   int64_t n = (rows + 63) / 64;
-  const int64_t most = (4096 + s.H - 1) / s.H;
+  const int64_t most = (2048 + s.H - 1) / s.H;
   if (n > most) n = most;
   if (n > kMaxSlices) n = kMaxSlices;
   return n < 1 ? 1 : (int)n;
