@@ -10,11 +10,12 @@
 //
 // A row of W meets nothing of another row: row i needs v_i, and k, q and the
 // gates that all rows share.  So a row lives in 16 lanes' registers (float4
-// pieces), a wave holds 4 * kSets rows, a workgroup of 4 waves a slice of
+// pieces), a wave holds 4 rows, a workgroup of 4 waves a slice of
 // the state's rows, and the two dot products of a token are sums over 16
 // lanes by DPP.  Nothing is exchanged between waves.  The state is read and
 // written once; for a few tokens that traffic (8 d^2 bytes a stream) is the
-// bound.
+// bound: a step of 192 x 16 heads of 128 x 128 takes 72 us, 5.6 TB/s (a large
+// copy reaches 5.2).  A small call is launch and latency, about 3 us.
 #include "tm_internal.h"
 
 namespace titans {

@@ -28,6 +28,11 @@
 // second launch takes every chunk of a key head by itself, with the value
 // heads that share the key head in turn, so dQ and dK are sums in registers
 // in a fixed order.
+//
+// 128 streams x 1024 tokens, d 64, bf16: 75 us for the sweeps (2.3 us a chunk,
+// the chain's and builders' latencies: a third of the cycles issue vector
+// instructions) and 109 us for the pieces (two workgroups a CU, again a third;
+// 124 MB read and 50 MB written, so not bound by memory).
 #include "tm_delta_chunk.h"
 
 namespace titans {
@@ -103,10 +108,13 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_sweep_ke
     }
     wait_for(ring.built() + i % PB, i + 1);
     const Lds L = ring.buffer(i);
+    // (as in the forward kernel, LDS reads go out a product ahead of their use)
     f32x4 ks[2], V[2], G[2], E[2], X[2];
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) ks[rt] = X[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    bf16x8 vp[3];
+    bf16x8 ka[NK][2][NP], vp[3];
+#pragma unroll
+    for (int kx = 0; kx < NK; ++kx) read2<NP>(L.k() + li * Lds::RS + 8 * g + 32 * kx, Lds::KP, 16 * Lds::RS, ka[kx]);
     if constexpr (F32) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -123,48 +131,64 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_sweep_ke
       G[rt] = *(const f32x4*)(L.g() + 16 * rt + 4 * g);
       E[rt] = *(const f32x4*)(L.eth() + 16 * rt + 4 * g);
     }
+    if (!F32) in_order();
 #pragma unroll
     for (int kx = 0; kx < NK; ++kx) {
-      bf16x8 ra[2][NP], sp[3];
-      read2<NP>(L.k() + li * Lds::RS + 8 * g + 32 * kx, Lds::KP, 16 * Lds::RS, ra);
+      bf16x8 sp[3];
       split8<3>(S[2 * kx], S[2 * kx + 1], sp);
-      mul2<false, 3>(ra, sp, ks);
+      mul2<false, 3>(ka[kx], sp, ks);
     }
     // forwards: R = V - G K W^T, X = F = T R; backwards: R = dF, X = dE = T^T dF
     f32x4 R[2];
-    bf16x8 ra[2][3], rp[3];
+    bf16x8 ta[2][3], rp[3];
     if (!back) {
+      read2<3>(L.t() + li * kCS + 8 * g, Lds::CP, 16 * kCS, ta);
+      if (!F32) in_order();
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) R[rt] = V[rt] - G[rt] * ks[rt];
-      read2<3>(L.t() + li * kCS + 8 * g, Lds::CP, 16 * kCS, ra);
     } else {
-      if constexpr (F32) split8<3>(V[0], V[1], vp);
+      bf16x8 pt[2][3];
 #pragma unroll
       for (int e = 0; e < 3; ++e)
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt) ra[rt][e] = read_transposed<true>(L.p() + e * Lds::CP, kCS, 16 * rt, lane);
+        for (int rt = 0; rt < 2; ++rt) pt[rt][e] = read_transposed<true>(L.p() + e * Lds::CP, kCS, 16 * rt, lane);
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt) R[rt] = ks[rt] * E[rt] * scale;
+      for (int e = 0; e < 3; ++e)
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) ta[rt][e] = read_transposed<true>(L.t() + e * Lds::CP, kCS, 16 * rt, lane);
+      if (!F32) in_order();
       if constexpr (F32) {
-        mul2<false, 3>(ra, vp, R);
+        split8<3>(V[0], V[1], vp);
+        mul2<false, 3>(pt, vp, X);
       } else {
-        bf16x8 one[1] = {vp[0]};
-        mul2<false, 1>(ra, one, R);
+        mul2<false, 1>(pt, vp, X);
       }
 #pragma unroll
-      for (int e = 0; e < 3; ++e)
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) ra[rt][e] = read_transposed<true>(L.t() + e * Lds::CP, kCS, 16 * rt, lane);
+      for (int rt = 0; rt < 2; ++rt) {
+        R[rt] = ks[rt] * E[rt] * scale + X[rt];
+        X[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
     }
     split8<3>(R[0], R[1], rp);
-    mul2<false, 3>(ra, rp, X);
-    if (kept) tiles[0] = X[0], tiles[1] = X[1];
+    if (!F32) in_order();
+    bf16x8 kt[NT][NP];
+    auto read_rows = [&](const uint16_t* rows) {
+#pragma unroll
+      for (int ti = 0; ti < NT; ++ti)
+#pragma unroll
+        for (int e = 0; e < NP; ++e) kt[ti][e] = read_transposed<true>(rows + e * Lds::KP, Lds::RS, 16 * ti, lane);
+    };
     // forwards: W' = G_C W + K^T (E theta F); backwards: dW' = G_C dW + Q^T (G dY) - K^T (G dE)
     f32x4 U[2], acc[NT];
     bf16x8 up[3];
+    auto fold = [&] {
 #pragma unroll
-    for (int rt = 0; rt < 2; ++rt) U[rt] = back ? X[rt] * -G[rt] : X[rt] * E[rt];
-    split8<3>(U[0], U[1], up);
+      for (int f = 0; f < products<NP, 3>(); ++f) {
+        const Planes x = product<NP, 3>(f);
+#pragma unroll
+        for (int ti = 0; ti < NT; ++ti) acc[ti] = mfma(kt[ti][x.i], up[x.j], acc[ti]);
+      }
+    };
     const bool scaled = !back && __builtin_amdgcn_readfirstlane(bits(scale)) != 0x3f800000u;
 #pragma unroll
     for (int ti = 0; ti < NT; ++ti) {
@@ -172,26 +196,20 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_sweep_ke
       S[ti] = scaled ? x : f32x4{0.f, 0.f, 0.f, 0.f};
       acc[ti] = scaled ? f32x4{0.f, 0.f, 0.f, 0.f} : x;
     }
-    auto fold = [&](const uint16_t* rows) {
-#pragma unroll
-      for (int ti = 0; ti < NT; ++ti) {
-        bf16x8 kt[NP];
-#pragma unroll
-        for (int e = 0; e < NP; ++e) kt[e] = read_transposed<true>(rows + e * Lds::KP, Lds::RS, 16 * ti, lane);
-#pragma unroll
-        for (int o = 2; o >= 0; --o)
-#pragma unroll
-          for (int e = NP - 1; e >= 0; --e)
-            if (o - e >= 0) acc[ti] = mfma(kt[e], up[o - e], acc[ti]);
-      }
-    };
-    fold(L.k());
-    if (back) {
+    if (back) {   // Q's part does not wait for dE
+      read_rows(L.q());
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) U[rt] = V[rt] * G[rt];
       split8<3>(U[0], U[1], up);
-      fold(L.q());
+      fold();
     }
+    read_rows(L.k());
+    mul2<false, 3>(ta, rp, X);
+    if (kept) tiles[0] = X[0], tiles[1] = X[1];
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) U[rt] = back ? X[rt] * -G[rt] : X[rt] * E[rt];
+    split8<3>(U[0], U[1], up);
+    fold();
     raise_to(ring.used() + wave, i + 1, lane);
 #pragma unroll
     for (int ti = 0; ti < NT; ++ti) S[ti] = scaled ? S[ti] + acc[ti] * scale : acc[ti];
@@ -565,9 +583,10 @@ hipError_t launch_sweep(GradParams p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Four chain waves in a workgroup share one builder's work, two take less time
-// a chunk: four where the device is full either way (128 streams x 1024, d 64,
-// bf16: 60 us against 87; 8 streams x 2048: 135 against 104).
+// Four chain waves in a workgroup share the builders' work, two take less time
+// a chunk: four where there are more workgroups of two than CUs (128 streams
+// x 1024, d 64, bf16: 75 us against 87; 32 x 2048, d 128: 192 against 162,
+// and 64 x 1024, d 64, as long either way).
 template <int DP, bool F32, int VB>
 hipError_t launch_grad(GradParams p, hipStream_t stream) {
   constexpr int kCus = 256, piece = PieceLds<DP, F32>::BYTES;

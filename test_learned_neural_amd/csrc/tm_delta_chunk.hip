@@ -10,11 +10,17 @@
 // triangular inverse, the bf16 planes) "builder" waves of the same workgroup
 // prepare in a ring of NB chunk buffers in LDS, PB chunks at once, with the
 // loads of the chunks after those in flight in their registers.  The waves
-// meet through two kinds of counters in LDS: a builder's last finished chunk,
-// and a chain wave's.  All waves of a workgroup are resident, a builder waits
-// only for chunks built before its own to be consumed and a chain wave only
-// for the next chunk, so every wait ends.  Nothing but the inputs and outputs
+// meet through counters in LDS: a builder's last finished chunk, a chain
+// wave's, and for fp32 inputs that of a builder's helper (Q and V).  All waves
+// of a workgroup are resident, a builder and its helper wait only for chunks
+// built before their own to be consumed and a chain wave only for the next
+// chunk, so every wait ends.  Nothing but the inputs and outputs
 // touches memory.
+//
+// Measured at 128 streams x 16384 tokens, d 64, bf16: 700 us, 1.37 us a chunk
+// against a serial path of about 250 vector instructions and 50 matrix
+// instructions (2000 cycles of issue, 0.85 us); the inputs and outputs alone
+// would take 210 us at a copy's rate.
 //
 // Few streams and many chunks: the sequence is cut into segments.  A segment
 // maps the state before it to the one after it by W -> W Phi + W_0; a first
@@ -22,7 +28,8 @@
 // vectors without values, and on the values from a zero state), a second
 // passes the state through them in order (delta_join_kernel), a third runs
 // the segments side by side from their true starts.  That is about 2.4 times
-// the work, for as many times the parallelism as there are segments.
+// the work, for as many times the parallelism as there are segments: 16
+// streams x 65536 tokens take 510 us so and 2740 in one piece.
 #include "tm_delta_chunk.h"
 
 namespace titans {

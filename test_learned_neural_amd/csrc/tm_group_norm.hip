@@ -22,6 +22,8 @@
 // takes 1/grid.x of the tokens.  The gradient's workgroup sums its tokens'
 // shares of dw and db in registers and LDS, in a fixed order, into one row of
 // the workspace; a second kernel sums the rows, again in a fixed order.
+// 8 x 16384 tokens x 1024 channels, bf16, gated: 174 us, 4.6 TB/s (a large copy
+// reaches 5.2); the gradient at 8 x 16384: 278 us, 4.8 TB/s.
 #include "tm_internal.h"
 
 namespace titans {
