@@ -32,7 +32,7 @@
 // 128 streams x 1024 tokens, d 64, bf16: 75 us for the sweeps (2.3 us a chunk,
 // the chain's and builders' latencies: a third of the cycles issue vector
 // instructions) and 109 us for the pieces (two workgroups a CU, again a third;
-// 124 MB read and 50 MB written, so not bound by memory).
+// 247 MB read and 50 MB written, half of a copy's rate).
 #include "tm_delta_chunk.h"
 
 namespace titans {
