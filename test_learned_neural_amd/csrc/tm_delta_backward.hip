@@ -96,6 +96,7 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_sweep_ke
   } else {
     load_state<NT, VB>(S, back ? p.dW_out : p.W_in, s, col, d, g);
   }
+  arrived(S);
   for (int i = 0; i < chunks; ++i) {
     const int c = back ? chunks - 1 - i : i;
     const int64_t at = (int64_t)s * p.chunks + c;
@@ -121,9 +122,6 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_sweep_ke
         V[e >> 2][e & 3] = ((const float*)L.v())[(16 * (e >> 2) + 4 * g + (e & 3)) * Lds::VS + 16 * wave + li];
     } else {
       vp[0] = read_transposed<false>((const uint16_t*)L.v(), Lds::VS, 16 * wave, lane);
-      const u32x4 x = __builtin_bit_cast(u32x4, vp[0]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) V[e >> 2][e & 3] = e & 1 ? top(flt(x[e >> 1])) : flt(x[e >> 1] << 16);
     }
     const float gc = L.gc()[0], scale = L.gc()[1];
 #pragma unroll
@@ -137,6 +135,11 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_sweep_ke
       bf16x8 sp[3];
       split8<3>(S[2 * kx], S[2 * kx + 1], sp);
       mul2<false, 3>(ka[kx], sp, ks);
+    }
+    if constexpr (!F32) {
+      const u32x4 x = __builtin_bit_cast(u32x4, vp[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) V[e >> 2][e & 3] = e & 1 ? top(flt(x[e >> 1])) : flt(x[e >> 1] << 16);
     }
     // forwards: R = V - G K W^T, X = F = T R; backwards: R = dF, X = dE = T^T dF
     f32x4 R[2];

@@ -587,6 +587,13 @@ __device__ __forceinline__ void load_state(f32x4 (&S)[NT], const float* W, int s
     }
   }
 }
+// Waits for the state's loads here.  Left to its first use, in the chain's
+// loop, the wait would be taken every time round, for the loop's own stores.
+template <int NT>
+__device__ __forceinline__ void arrived(f32x4 (&S)[NT]) {
+#pragma unroll
+  for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(S[i]));
+}
 template <int NT, int VB>
 __device__ __forceinline__ void store_state(const f32x4 (&S)[NT], float* W, int s, int col, int d, int g) {
   if (col >= d) return;

@@ -112,6 +112,7 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
   } else {
     load_state<NT, VB>(S, p.W_in, s, col, d, g);
   }
+  arrived(S);
   // y's tiles are computed transposed: a lane has 4 consecutive channels of
   // a token, stored in one piece at a uniform address per chunk plus this
   const int ych = cg * 16 + 4 * g;
@@ -132,14 +133,13 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
     bf16x8 ra[NK][2][NP];
 #pragma unroll
     for (int kx = 0; kx < NK; ++kx) read2<NP>(ka + 32 * kx, Lds::KP, 16 * Lds::RS, ra[kx]);
+    bf16x8 vr;
     if constexpr (F32) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         V[e >> 2][e & 3] = ((const float*)L.v())[(16 * (e >> 2) + 4 * g + (e & 3)) * Lds::VS + 16 * wave + li];
     } else {
-      const u32x4 x = __builtin_bit_cast(u32x4, read_transposed<false>((const uint16_t*)L.v(), Lds::VS, 16 * wave, lane));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) V[e >> 2][e & 3] = e & 1 ? top(flt(x[e >> 1])) : flt(x[e >> 1] << 16);
+      vr = read_transposed<false>((const uint16_t*)L.v(), Lds::VS, 16 * wave, lane);
     }
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) G[rt] = *(const f32x4*)(L.g() + 16 * rt + 4 * g);
@@ -159,6 +159,11 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
     if (!TRANS)
 #pragma unroll
     for (int kx = 0; kx < NK; ++kx) read2<NP>(qa + 32 * kx, Lds::KP, 16 * Lds::RS, rq[kx]);
+    if constexpr (!F32) {
+      const u32x4 x = __builtin_bit_cast(u32x4, vr);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) V[e >> 2][e & 3] = e & 1 ? top(flt(x[e >> 1])) : flt(x[e >> 1] << 16);
+    }
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
