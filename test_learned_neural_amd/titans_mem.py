@@ -9,6 +9,7 @@ there is no Python or CPU fallback -- a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -439,34 +440,35 @@ def backward(k, v, q, alpha, eta, theta, W_in, S_in, chunk: int, *, hidden: int,
 
 
 # A decode step's kernel runs for about 3 us, so the wrappers below keep the
-# host's share of a call small: one pass over the tensors' properties, and the
-# raw handle of the current stream (a torch.cuda.Stream object costs 2 us).
-def _io_of(t) -> str:
+# host's share of a call small: descriptors, shapes and workspace sizes are
+# kept per shape (they follow from it alone), a tensor's properties are read
+# once, and the stream is the raw handle (a torch.cuda.Stream object costs 2 us).
+def _io_of(dtype) -> str:
     torch = _torch()
-    if t.dtype is torch.bfloat16:
+    if dtype is torch.bfloat16:
         return "bf16"
-    if t.dtype is torch.float32:
+    if dtype is torch.float32:
         return "f32"
-    raise ValueError(f"float32 or bfloat16 expected, got {t.dtype}")
+    raise ValueError(f"float32 or bfloat16 expected, got {dtype}")
 
 
-def _want(tensors, device):
+def _want(device, index, *tensors):
     """Checks (name, tensor, shape, dtype) entries; a tensor may be None."""
     for name, t, shape, dtype in tensors:
-        if t is not None and not (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+        if t is not None and not (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
             _check(t, name, shape, dtype, device)
 
 
-def _on_device(dev, what, fn, *args):
-    """fn(*args, stream) on torch's current stream of ``dev``, with ``dev`` current; raises on a bad status."""
+def _on_device(index, what, fn, *args):
+    """fn(*args, stream) on torch's current stream of GPU ``index``, with that GPU current; raises on a bad status."""
     torch = _torch()
-    if dev.type != "cuda":
-        raise ValueError(f"{what}: tensors must be on a GPU, got {dev}")
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if index < 0:
+        raise ValueError(f"{what}: tensors must be on a GPU")
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.device(index):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != OK:
         raise TitansMemError(rc, what)
 
@@ -482,16 +484,32 @@ def _workspace(workspace, need, dev, what):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _check_delta(k, v, q, alpha, theta, W_in, lengths):
+class _DeltaPlan:
+    """What a call's shapes and type fix."""
+
+    def __init__(self, keys, vals, dtype, flags):
+        if len(keys) != 4 or len(vals) != 4:
+            raise ValueError("k and v must be [B, heads, N, d]")
+        B, Hk, N, d = keys
+        H = vals[1]
+        self.keys, self.vals, self.gates, self.state, self.batch = keys, (B, H, N, d), (B, H, N), (B, H, d, d), (B,)
+        self.desc = make_delta_desc(B, H, Hk, N, d, _io_of(dtype), flags)
+        self.ref = ctypes.byref(self.desc)
+        self.need = delta_workspace_bytes(self.desc)
+        self.back = delta_backward_workspace_bytes(self.desc)
+
+
+_delta_plan = functools.lru_cache(maxsize=256)(_DeltaPlan)
+
+
+def _check_delta(k, v, q, alpha, theta, W_in, lengths, flags=0):
     torch = _torch()
-    if k.dim() != 4 or v.dim() != 4:
-        raise ValueError("k and v must be [B, heads, N, d]")
-    B, Hk, N, d = k.shape
-    H, dev, io, f32 = v.shape[1], k.device, k.dtype, torch.float32
-    keys, gates = (B, Hk, N, d), (B, H, N)
-    _want((("v", v, (B, H, N, d), io), ("k", k, keys, io), ("q", q, keys, io), ("alpha", alpha, gates, f32),
-           ("theta", theta, gates, f32), ("W_in", W_in, (B, H, d, d), f32), ("lengths", lengths, (B,), torch.int32)), dev)
-    return B, H, Hk, N, d, dev
+    io, f32, index = k.dtype, torch.float32, k.get_device()
+    plan = _delta_plan(k.shape, v.shape, io, flags)
+    _want(k.device, index, ("v", v, plan.vals, io), ("k", k, plan.keys, io), ("q", q, plan.keys, io),
+          ("alpha", alpha, plan.gates, f32), ("theta", theta, plan.gates, f32), ("W_in", W_in, plan.state, f32),
+          ("lengths", lengths, plan.batch, torch.int32))
+    return plan, index
 
 
 def delta_forward(k, v, q, alpha, theta, W_in, *, lengths=None, force_recurrent: bool = False, y_out=None, W_out=None,
@@ -505,17 +523,19 @@ def delta_forward(k, v, q, alpha, theta, W_in, *, lengths=None, force_recurrent:
     y_out that is passed in are left as they were there.
     """
     torch = _torch()
-    B, H, Hk, N, d, dev = _check_delta(k, v, q, alpha, theta, W_in, lengths)
-    desc = make_delta_desc(B, H, Hk, N, d, _io_of(k), FLAG_FORCE_GENERIC if force_recurrent else 0)
-    _want((("y_out", y_out, (B, H, N, d), k.dtype), ("W_out", W_out, (B, H, d, d), torch.float32)), dev)
+    plan, index = _check_delta(k, v, q, alpha, theta, W_in, lengths, FLAG_FORCE_GENERIC if force_recurrent else 0)
     if y_out is None:
         y_out = torch.empty_like(v) if lengths is None else torch.zeros_like(v)
+    else:
+        _want(k.device, index, ("y_out", y_out, plan.vals, k.dtype))
     if W_out is None:
         W_out = torch.empty_like(W_in)
-    ws, ws_bytes = _workspace(workspace, delta_workspace_bytes(desc), dev, "titans_mem_delta_workspace_bytes")
-    _on_device(dev, "titans_mem_delta_forward", raw_delta_forward, desc, k.data_ptr(), v.data_ptr(), q.data_ptr(),
-               alpha.data_ptr(), theta.data_ptr(), _ptr(lengths), W_in.data_ptr(), y_out.data_ptr(), W_out.data_ptr(),
-               _ptr(ws), ws_bytes)
+    else:
+        _want(k.device, index, ("W_out", W_out, plan.state, torch.float32))
+    ws, ws_bytes = _workspace(workspace, plan.need, k.device, "titans_mem_delta_workspace_bytes")
+    _on_device(index, "titans_mem_delta_forward", load().titans_mem_delta_forward, plan.ref, k.data_ptr(), v.data_ptr(),
+               q.data_ptr(), alpha.data_ptr(), theta.data_ptr(), _ptr(lengths), W_in.data_ptr(), y_out.data_ptr(),
+               W_out.data_ptr(), _ptr(ws), ws_bytes)
     return y_out, W_out
 
 
@@ -528,39 +548,49 @@ def delta_backward(k, v, q, alpha, theta, W_in, *, dy, dW_out=None, lengths=None
     type, alpha, theta [B, H, N] and W_in [B, H, d, d] float32.
     """
     torch = _torch()
-    B, H, Hk, N, d, dev = _check_delta(k, v, q, alpha, theta, W_in, lengths)
-    _check(dy, "dy", (B, H, N, d), k.dtype, dev)
-    if dW_out is not None:
-        _check(dW_out, "dW_out", (B, H, d, d), torch.float32, dev)
-    desc = make_delta_desc(B, H, Hk, N, d, _io_of(k))
+    plan, index = _check_delta(k, v, q, alpha, theta, W_in, lengths)
+    _want(k.device, index, ("dy", dy, plan.vals, k.dtype), ("dW_out", dW_out, plan.state, torch.float32))
     g = {n: torch.empty_like(t) for n, t in
          (("k", k), ("v", v), ("q", q), ("alpha", alpha), ("theta", theta), ("W_in", W_in))}
-    ws, ws_bytes = _workspace(workspace, delta_backward_workspace_bytes(desc), dev,
-                              "titans_mem_delta_backward_workspace_bytes")
-    _on_device(dev, "titans_mem_delta_backward", raw_delta_backward, desc, k.data_ptr(), v.data_ptr(), q.data_ptr(),
-               alpha.data_ptr(), theta.data_ptr(), _ptr(lengths), W_in.data_ptr(), dy.data_ptr(), _ptr(dW_out),
-               g["k"].data_ptr(), g["v"].data_ptr(), g["q"].data_ptr(), g["alpha"].data_ptr(), g["theta"].data_ptr(),
-               g["W_in"].data_ptr(), _ptr(ws), ws_bytes)
+    ws, ws_bytes = _workspace(workspace, plan.back, k.device, "titans_mem_delta_backward_workspace_bytes")
+    _on_device(index, "titans_mem_delta_backward", load().titans_mem_delta_backward, plan.ref, k.data_ptr(),
+               v.data_ptr(), q.data_ptr(), alpha.data_ptr(), theta.data_ptr(), _ptr(lengths), W_in.data_ptr(),
+               dy.data_ptr(), _ptr(dW_out), g["k"].data_ptr(), g["v"].data_ptr(), g["q"].data_ptr(),
+               g["alpha"].data_ptr(), g["theta"].data_ptr(), g["W_in"].data_ptr(), _ptr(ws), ws_bytes)
     return g
+
+
+class _NormPlan:
+    """What a call's shape, type and options fix."""
+
+    def __init__(self, shape, dtype, H, activation, eps):
+        if len(shape) == 4:
+            B, heads, N, d = shape
+            if H is not None and H != heads:
+                raise ValueError(f"x has {heads} heads, H is {H}")
+            H, flags = heads, 0
+        elif len(shape) == 3 and H is not None and H > 0 and shape[2] % H == 0:
+            B, N, C = shape
+            d, flags = C // H, FLAG_CHANNELS_LAST
+        else:
+            raise ValueError("x must be [B, H, N, d], or [B, N, H*d] with H given")
+        self.out, self.channels, self.batch = (B, N, H * d), (H * d,), (B,)
+        self.desc = make_norm_desc(B, H, N, d, _io_of(dtype), activation, eps, flags)
+        self.ref = ctypes.byref(self.desc)
+        self.back = group_norm_backward_workspace_bytes(self.desc)
+
+
+_norm_plan = functools.lru_cache(maxsize=256)(_NormPlan)
 
 
 def _check_norm(x, weight, bias, H, gate, lengths, activation, eps):
     torch = _torch()
-    io, dev = _io_of(x), x.device
-    if x.dim() == 4:
-        B, heads, N, d = x.shape
-        if H is not None and H != heads:
-            raise ValueError(f"x has {heads} heads, H is {H}")
-        H, flags = heads, 0
-    elif x.dim() == 3 and H is not None and H > 0 and x.shape[2] % H == 0:
-        B, N, C = x.shape
-        d, flags = C // H, FLAG_CHANNELS_LAST
-    else:
-        raise ValueError("x must be [B, H, N, d], or [B, N, H*d] with H given")
-    f32, C = torch.float32, H * d
-    _want((("x", x, x.shape, x.dtype), ("weight", weight, (C,), f32), ("bias", bias, (C,), f32),
-           ("gate", gate, (B, N, C), x.dtype), ("lengths", lengths, (B,), torch.int32)), dev)
-    return make_norm_desc(B, H, N, d, io, activation, eps, flags), (B, N, H * d), dev
+    f32, index = torch.float32, x.get_device()
+    plan = _norm_plan(x.shape, x.dtype, H, activation, eps)
+    _want(x.device, index, ("x", x, x.shape, x.dtype), ("weight", weight, plan.channels, f32),
+          ("bias", bias, plan.channels, f32), ("gate", gate, plan.out, x.dtype),
+          ("lengths", lengths, plan.batch, torch.int32))
+    return plan, index
 
 
 def group_norm(x, weight=None, bias=None, *, H: Optional[int] = None, gate=None, activation: int = ACT_SILU,
@@ -573,13 +603,13 @@ def group_norm(x, weight=None, bias=None, *, H: Optional[int] = None, gate=None,
     a gate, as [B, N, H*d].  A new out holds zeros past a sequence's length.
     """
     torch = _torch()
-    desc, shape, dev = _check_norm(x, weight, bias, H, gate, lengths, activation, eps)
+    plan, index = _check_norm(x, weight, bias, H, gate, lengths, activation, eps)
     if out is None:
-        out = (torch.empty if lengths is None else torch.zeros)(shape, dtype=x.dtype, device=dev)
+        out = (torch.empty if lengths is None else torch.zeros)(plan.out, dtype=x.dtype, device=x.device)
     else:
-        _check(out, "out", shape, x.dtype, dev)
-    _on_device(dev, "titans_mem_group_norm", raw_group_norm, desc, x.data_ptr(), _ptr(gate), _ptr(weight), _ptr(bias),
-               _ptr(lengths), out.data_ptr())
+        _want(x.device, index, ("out", out, plan.out, x.dtype))
+    _on_device(index, "titans_mem_group_norm", load().titans_mem_group_norm, plan.ref, x.data_ptr(), _ptr(gate),
+               _ptr(weight), _ptr(bias), _ptr(lengths), out.data_ptr())
     return out
 
 
@@ -592,16 +622,15 @@ def group_norm_backward(x, weight, bias, dout, *, H: Optional[int] = None, gate=
     float32.
     """
     torch = _torch()
-    desc, shape, dev = _check_norm(x, weight, bias, H, gate, lengths, activation, eps)
-    _check(dout, "dout", shape, x.dtype, dev)
+    plan, index = _check_norm(x, weight, bias, H, gate, lengths, activation, eps)
+    _want(x.device, index, ("dout", dout, plan.out, x.dtype))
     g = {"x": torch.empty_like(x)}
     if gate is not None:
         g["gate"] = torch.empty_like(gate)
-    g["weight"] = torch.empty(shape[2], dtype=torch.float32, device=dev)
-    g["bias"] = torch.empty(shape[2], dtype=torch.float32, device=dev)
-    ws, ws_bytes = _workspace(workspace, group_norm_backward_workspace_bytes(desc), dev,
-                              "titans_mem_group_norm_backward_workspace_bytes")
-    _on_device(dev, "titans_mem_group_norm_backward", raw_group_norm_backward, desc, x.data_ptr(), _ptr(gate),
-               _ptr(weight), _ptr(bias), _ptr(lengths), dout.data_ptr(), g["x"].data_ptr(), _ptr(g.get("gate")),
-               g["weight"].data_ptr(), g["bias"].data_ptr(), _ptr(ws), ws_bytes)
+    g["weight"] = torch.empty(plan.channels, dtype=torch.float32, device=x.device)
+    g["bias"] = torch.empty_like(g["weight"])
+    ws, ws_bytes = _workspace(workspace, plan.back, x.device, "titans_mem_group_norm_backward_workspace_bytes")
+    _on_device(index, "titans_mem_group_norm_backward", load().titans_mem_group_norm_backward, plan.ref, x.data_ptr(),
+               _ptr(gate), _ptr(weight), _ptr(bias), _ptr(lengths), dout.data_ptr(), g["x"].data_ptr(),
+               _ptr(g.get("gate")), g["weight"].data_ptr(), g["bias"].data_ptr(), _ptr(ws), ws_bytes)
     return g
