@@ -89,10 +89,12 @@ def test_delta_overlaps(out, other):
 
 
 def test_delta_small_workspace_is_refused():
-    c = Delta()
-    if tmm.delta_workspace_bytes(c.desc) > 0:
-        assert c.call(ws_bytes=c.ws - 1) == tmm.ERR_WORKSPACE
-        assert c.call(ws=0) == tmm.ERR_WORKSPACE
+    c = Delta(N=20000)      # few streams and many tokens: cut into segments, which need one
+    assert tmm.delta_workspace_bytes(c.desc) == c.ws > 0
+    assert c.call(ws_bytes=c.ws - 1) == tmm.ERR_WORKSPACE
+    assert c.call(ws=0) == tmm.ERR_WORKSPACE
+    assert c.call(ws=c.p["v"]) == tmm.ERR_ALIAS
+    assert tmm.delta_workspace_bytes(Delta(N=100).desc) == 0
 
 
 @pytest.mark.parametrize("field,value,status", [

@@ -232,3 +232,30 @@ def test_same_bits_every_time():
     for _ in range(3):
         again = _run(g)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last tokens against a short run over them (alpha = 0.5: 64 tokens forget 2^-64)."""
+    import torch
+    from test_learned_neural_amd import titans_mem as tmm
+    d, tile, reps = 128, 1 << 16, 257
+    N = tile * reps
+    assert N * d > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def rows(unit):
+        x = torch.randn(tile, d, generator=g, device="cuda")
+        x = torch.nn.functional.normalize(x, dim=-1) if unit else x
+        return x.bfloat16().repeat(reps, 1).reshape(1, 1, N, d)
+
+    k, q, v = rows(True), rows(True), rows(False)
+    v[0, 0, -1000:] *= 2          # unlike any tile before
+    alpha = torch.full((1, 1, N), 0.5, device="cuda")
+    theta = torch.rand(tile, generator=g, device="cuda").repeat(reps).reshape(1, 1, N)
+    W0 = torch.zeros(1, 1, d, d, device="cuda")
+    y, W = tmm.delta_forward(k, v, q, alpha, theta, W0)
+    tail = lambda t: t[:, :, -1200:].contiguous()
+    f = [tail(t).double().cpu().numpy() for t in (k, v, q, alpha, theta)] + [W0.double().cpu().numpy()]
+    yr, Wr = do.delta_forward(*f)
+    check("W", W, Wr, "f32", tol32(1200, d))
+    check("y", y[:, :, -1100:], yr[:, :, 100:], "bf16", tol32(1200, d))

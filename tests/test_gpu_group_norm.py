@@ -162,3 +162,30 @@ def test_empty_and_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(want[n], out[n]) for n in want)
+
+
+@pytest.mark.parametrize("first", [True, False])
+def test_offsets_past_32_bits(first):
+    """More than 2^31 elements: the last rows are those of a short call over them; so are the gradient's."""
+    import torch
+    from test_learned_neural_amd import titans_mem as tmm
+    B, H, N, d = 2, 2, (1 << 19) + 64, 1024
+    assert B * H * N * d > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(4)
+    shape = (B, H, N, d) if first else (B, N, H * d)
+    x = torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+    gate = torch.zeros(B, N, H * d, dtype=torch.bfloat16, device="cuda")
+    dout = torch.zeros_like(gate)
+    tail = lambda t: (t[-1:, :, -50:] if t.dim() == 4 else t[-1:, -50:])
+    for t in (x, gate, dout):
+        tail(t).copy_(torch.randn(tail(t).shape, generator=g, device="cuda"))
+    out = tmm.group_norm(x, gate=gate, H=H)
+    want = tmm.group_norm(tail(x).contiguous(), gate=tail(gate).contiguous(), H=H)
+    assert torch.equal(tail(out), want)
+    got = tmm.group_norm_backward(x, None, None, dout, gate=gate, H=H)
+    ref = tmm.group_norm_backward(tail(x).contiguous(), None, None, tail(dout).contiguous(), gate=tail(gate).contiguous(), H=H)
+    for name in ("x", "gate"):
+        assert torch.equal(tail(got[name]), ref[name])
+        assert not tail(got[name]).isnan().any()
+    for name in ("weight", "bias"):    # zeros besides, summed in another order
+        assert torch.allclose(got[name], ref[name], rtol=1e-5, atol=1e-5)
