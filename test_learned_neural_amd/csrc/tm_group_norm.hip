@@ -267,7 +267,11 @@ template <bool BF16>
 hipError_t launch(const NormParams& p, int slices, bool grad, hipStream_t stream) {
   const int d = p.d;
   if (d % 4) {
+    if (d <= 16) return launch_as<BF16, 1, 16, 1>(p, slices, grad, stream);
+    if (d <= 32) return launch_as<BF16, 1, 16, 2>(p, slices, grad, stream);
+    if (d <= 48) return launch_as<BF16, 1, 16, 3>(p, slices, grad, stream);
     if (d <= 64) return launch_as<BF16, 1, 16, 4>(p, slices, grad, stream);
+    if (d <= 128) return launch_as<BF16, 1, 32, 4>(p, slices, grad, stream);
     if (d <= 256) return launch_as<BF16, 1, 64, 4>(p, slices, grad, stream);
     return launch_as<BF16, 1, 64, 16>(p, slices, grad, stream);
   }
