@@ -287,11 +287,12 @@ struct RowLoad {
   }
 };
 
-// Rows of K or Q into their permuted planes.
+// Rows of K or Q (from column col0 on) into their permuted planes.
 template <int DP, bool F32, class Load>
-__device__ __forceinline__ void store_planes(Load& rows, uint16_t* dst, int lane) {
+__device__ __forceinline__ void store_planes(Load& rows, uint16_t* dst, int lane, int col0 = 0) {
   constexpr int RS = DP + 8, KP = kC * RS;
   rows.store(lane, [&](int r, int c, const uint32_t* x) {
+    c += col0;
     uint16_t* at = dst + r * RS + (c & ~31) + perm32(c & 31);
     if constexpr (F32)
       put4<3>(at, KP, flt(x[0]), flt(x[1]), flt(x[2]), flt(x[3]));
