@@ -367,10 +367,13 @@ int titans_mem_input(const titans_input_desc* desc,
  *              scratch (may be NULL when that is 0)
  *
  * State, sums and gates are fp32; products of bf16 inputs are exact.  y is
- * rounded once.  d <= 128 (TM_ERR_UNSUPPORTED otherwise); N == 0 copies the
- * state.  Where chunks are used, a NaN or infinity of a token may reach the
- * 31 tokens before it (of its stream) too.  TM_FLAG_FORCE_GENERIC runs the token-by-token kernel at any N.
- * titans_mem_delta_select_path reports the kernel that a call runs.
+ * rounded once.  d <= 128 and B*H <= 2^20 (TM_ERR_UNSUPPORTED otherwise);
+ * N == 0 copies the state.  Where chunks are used, a NaN or infinity of a
+ * token may reach the 31 tokens before it (of its stream) too, and the product
+ * of 1 - alpha over up to 32 tokens in a row has to be a finite float (a gate
+ * never makes it larger than 1; a negative alpha can).  TM_FLAG_FORCE_GENERIC runs the
+ * token-by-token kernel at any N.  titans_mem_delta_select_path reports the
+ * kernel that a call runs.
  */
 #define TM_PATH_DELTA_RECURRENT 0   /* token by token */
 #define TM_PATH_DELTA_CHUNKED   1   /* by chunks, on the matrix cores */
@@ -410,6 +413,7 @@ int titans_mem_delta_forward(const titans_delta_desc* desc,
  * there.  Arithmetic is fp32; dk, dv and dq are rounded once.  Any overlap of
  * a written buffer is TM_ERR_ALIAS.  The workspace holds W and its adjoint at
  * every 32nd token: titans_mem_delta_backward_workspace_bytes(desc) bytes.
+ * TM_ERR_UNSUPPORTED from B*Hk*ceil(N/32) = 2^24 on (2^23 where d > 64).
  */
 int64_t titans_mem_delta_backward_workspace_bytes(const titans_delta_desc* desc);
 

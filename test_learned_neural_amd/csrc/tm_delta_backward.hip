@@ -72,7 +72,7 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_sweep_ke
   if (s >= p.B * p.H) return;
   const int b = s / p.H, h = s % p.H, d = p.d;
   const int n = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
-  const int chunks = (n + kC - 1) / kC;
+  const int chunks = chunks_of(n);
   ring.init(wave, lane);
 
   if (wave >= CW) {
@@ -630,17 +630,18 @@ hipError_t launch_width(const GradParams& p, hipStream_t stream) {
 
 int64_t state_floats(const DeltaShape& s) {
   const int64_t ld = (s.d + 15) / 16 * 16;
-  return (int64_t)s.B * s.H * ((s.N + kC - 1) / kC) * ld * ld;
+  return (int64_t)s.B * s.H * chunks_of(s.N) * ld * ld;
 }
 int64_t tile_floats(const DeltaShape& s) {
   const int64_t ld = (s.d + 15) / 16 * 16;
-  return (int64_t)s.B * s.H * ((s.N + kC - 1) / kC) * kC * ld;
+  return (int64_t)s.B * s.H * chunks_of(s.N) * kC * ld;
 }
 
 }  // namespace
 
 bool delta_backward_supported(const DeltaShape& s) {
-  return (int64_t)s.B * s.Hk * ((s.N + kC - 1) / kC) < (int64_t)1 << 31;
+  // the pieces' launch: a workgroup a chunk, and fewer than 2^32 threads
+  return (int64_t)s.B * s.Hk * chunks_of(s.N) * (s.d <= 64 ? 256 : 512) < (int64_t)1 << 32;
 }
 
 int64_t delta_backward_ws_bytes(const DeltaShape& s) { return 8 * (state_floats(s) + tile_floats(s)); }
@@ -653,7 +654,7 @@ hipError_t launch_delta_backward(const DeltaShape& s, const void* k, const void*
   p.ws_W = ws, p.ws_dW = ws + state_floats(s);
   p.ws_F = ws + 2 * state_floats(s), p.ws_dE = p.ws_F + tile_floats(s);
   p.B = s.B, p.H = s.H, p.Hk = s.Hk, p.N = s.N, p.d = s.d, p.ld = (s.d + 15) / 16 * 16;
-  p.chunks = (s.N + kC - 1) / kC;
+  p.chunks = chunks_of(s.N);
   if (s.io == TM_IO_BF16) {
     if (s.d % 8 == 0) return launch_width<false, 16>(p, stream);
     return s.d % 4 == 0 ? launch_width<false, 8>(p, stream) : launch_width<false, 0>(p, stream);

@@ -34,6 +34,8 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
 constexpr int kC = 32;          // tokens per chunk
+// (n up to 2^31 - 1: n + 31 would not be an int)
+__host__ __device__ inline int chunks_of(int n) { return n / kC + (n % kC != 0); }
 constexpr int kCS = kC + 8;     // row stride of a [32][32] plane, in bf16
 constexpr int kBS = kC + 4;     // row stride of the fp32 scratch
 
@@ -550,7 +552,7 @@ __device__ __forceinline__ void run_builder(const Ring<Lds, CW, PB, NB, HELP>& r
   if (!HELP) fetch_qv(pw);
   for (int i = pw; i < in.chunks; i += PB) {
     const Lds L = ring.buffer(i);
-    const bool real = first(i) + lane < in.n;
+    const bool real = lane < in.n - first(i);
     const float la = real ? log2_keep(al) : 0.f, th0 = real ? th : 0.f;
     wait_free(i);
     store_planes<DP, F32>(kr, L.k(), lane);

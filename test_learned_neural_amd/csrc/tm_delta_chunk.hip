@@ -83,7 +83,7 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
   const int all = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
   const int first = (int)min((int64_t)seg * p.seg_chunks * kC, (int64_t)all);   // the segment's tokens: first .. first + n - 1
   const int n = seg + 1 < p.segments ? (int)min((int64_t)(all - first), (int64_t)p.seg_chunks * kC) : all - first;
-  const int chunks = (n + kC - 1) / kC;
+  const int chunks = chunks_of(n);
   ring.init(wave, lane);
 
   if (wave >= CW) {
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
       }
     };
     if (!TRANS && ych < d) {
-      if (t0 + kC <= n) {
+      if (n - t0 >= kC) {
         store(0);
         store(1);
       } else {
@@ -373,7 +373,7 @@ int chunk_cost(const DeltaShape& s, int cw) {
   return s.d <= 64 ? (cw == 2 ? 20 : 30) : cw == 2 ? 46 : 62;
 }
 Plan plan_of(const DeltaShape& s) {
-  const int64_t streams = (int64_t)s.B * s.H, chunks = (s.N + kC - 1) / kC, groups = (s.d + 15) / 16;
+  const int64_t streams = (int64_t)s.B * s.H, chunks = chunks_of(s.N), groups = (s.d + 15) / 16;
   auto rounds = [&](int64_t segs, int64_t columns, int cw) {
     return (streams * segs * ((columns + cw - 1) / cw) + kCus - 1) / kCus * chunk_cost(s, cw);
   };

@@ -366,7 +366,7 @@ int build_delta(const titans_delta_desc* desc, DeltaShape* s) {
     return TM_ERR_INVALID;
   if (desc->io_dtype != TM_IO_F32 && desc->io_dtype != TM_IO_BF16) return TM_ERR_INVALID;
   if (desc->flags & ~TM_FLAG_FORCE_GENERIC) return TM_ERR_INVALID;
-  if (desc->d > titans::kMaxWidthDelta || (int64_t)desc->B * desc->H > (int64_t)1 << 24) return TM_ERR_UNSUPPORTED;
+  if (desc->d > titans::kMaxWidthDelta || (int64_t)desc->B * desc->H > titans::kMaxStreamsDelta) return TM_ERR_UNSUPPORTED;
   if ((double)desc->B * desc->H * desc->N * desc->d > kMostElements) return TM_ERR_UNSUPPORTED;
   *s = {desc->B, desc->H, desc->Hk, desc->N, desc->d, desc->io_dtype, desc->flags};
   return TM_OK;

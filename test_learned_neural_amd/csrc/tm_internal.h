@@ -122,6 +122,7 @@ hipError_t launch_input(int B, int N, int D, int H, int d, int w, const void* x,
 // The gated delta memory (token-exact linear memory).  W [B,H,d,d] fp32;
 // lengths may be null.  W_out == W_in is allowed.
 constexpr int kMaxWidthDelta = 128;
+constexpr int64_t kMaxStreamsDelta = 1 << 20;   // every launch stays under 2^32 threads
 struct DeltaShape {
   int B, H, Hk, N, d, io;
   unsigned flags;

@@ -484,6 +484,12 @@ def _workspace(workspace, need, dev, what):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _fits(*dims):
+    """A descriptor's fields are int32; ctypes would take a larger one modulo 2^32."""
+    if max(dims) >= 1 << 31:
+        raise ValueError(f"dimensions must be below 2^31, got {dims}")
+
+
 class _DeltaPlan:
     """What a call's shapes and type fix."""
 
@@ -492,6 +498,7 @@ class _DeltaPlan:
             raise ValueError("k and v must be [B, heads, N, d]")
         B, Hk, N, d = keys
         H = vals[1]
+        _fits(B, H, Hk, N, d)
         self.keys, self.vals, self.gates, self.state, self.batch = keys, (B, H, N, d), (B, H, N), (B, H, d, d), (B,)
         self.desc = make_delta_desc(B, H, Hk, N, d, _io_of(dtype), flags)
         self.ref = ctypes.byref(self.desc)
@@ -574,6 +581,7 @@ class _NormPlan:
             d, flags = C // H, FLAG_CHANNELS_LAST
         else:
             raise ValueError("x must be [B, H, N, d], or [B, N, H*d] with H given")
+        _fits(B, H, N, d)
         self.out, self.channels, self.batch = (B, N, H * d), (H * d,), (B,)
         self.desc = make_norm_desc(B, H, N, d, _io_of(dtype), activation, eps, flags)
         self.ref = ctypes.byref(self.desc)

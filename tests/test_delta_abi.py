@@ -194,3 +194,39 @@ def test_delta_backward_pointers_and_overlaps():
                 assert c.call(**{out: c.p[name]}) == tmm.ERR_ALIAS, (out, name)
     assert c.call(ws=0) == tmm.ERR_WORKSPACE
     assert c.call(ws_bytes=c.ws - 1) == tmm.ERR_WORKSPACE
+
+
+def test_delta_limits_of_a_launch():
+    """A launch has fewer than 2^32 threads: streams up to 2^20, a gradient's chunks times 256 (512 past d = 64)."""
+    def desc(B=1, H=1, N=64, d=16):
+        return tmm.make_delta_desc(B, H, H, N, d)
+
+    for N in (4, 64):
+        assert tmm.delta_select_path(desc(B=1 << 19, H=2, N=N)) >= 0
+        assert tmm.delta_select_path(desc(B=1 << 19, H=2 + 1, N=N)) == tmm.ERR_UNSUPPORTED
+    for d, threads in ((64, 256), (65, 512)):
+        chunks = (1 << 32) // threads
+        ld = (d + 15) // 16 * 16
+        fits = desc(N=32 * (chunks - 1), d=d)
+        assert tmm.delta_backward_workspace_bytes(fits) == (chunks - 1) * 8 * (ld * ld + 32 * ld)
+        assert tmm.delta_backward_workspace_bytes(desc(N=32 * chunks, d=d)) == tmm.ERR_UNSUPPORTED
+        assert tmm.delta_backward_workspace_bytes(desc(B=2, N=16 * chunks, d=d)) == tmm.ERR_UNSUPPORTED
+
+
+def test_delta_longest_sequence_is_cut_as_others_are():
+    longest, long = (tmm.delta_workspace_bytes(tmm.make_delta_desc(1, 1, 1, N, 64)) for N in (0x7fffffff, 1 << 30))
+    assert longest == long > 0
+    assert tmm.delta_backward_workspace_bytes(tmm.make_delta_desc(1, 1, 1, 0x7fffffff, 64)) == tmm.ERR_UNSUPPORTED
+
+
+def test_dimensions_past_32_bits_do_not_wrap():
+    """A tensor can have 2^32 tokens; the descriptors' fields cannot hold that many."""
+    import torch
+    big = 1 << 32
+    for keys, vals in (((1, 1, big, 1), (1, 1, big, 1)), ((big + 1, 1, 4, 4), (big + 1, 1, 4, 4)),
+                       ((1, 1, 4, 4), (1, big + 1, 4, 4))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            tmm._DeltaPlan(keys, vals, torch.bfloat16, 0)
+    for shape, H in (((1, 1, big, 1), None), ((big + 1, 4, 8), 2), ((1, 4, big * 8), 2)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            tmm._NormPlan(shape, torch.float32, H, tmm.ACT_SILU, 1e-5)
