@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) group_norm_kernel(NormParams p) {
           o[j] = gated ? f * n : f;
         } else {
           const float slope = p.silu ? sg * fmaf(a, 1.f - sg, 1.f) : 1.f;
-          const float dn = go[i][j] * (gated ? f : slope);
+          const float dn = live ? go[i][j] * (gated ? f : slope) : 0.f;   // (the slope at an infinite bias is NaN)
           o[j] = live ? go[i][j] * n * slope : 0.f;   // dgate
           dw[i][j] = fmaf(dn, xh, dw[i][j]);
           db[i][j] += dn;
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) group_norm_kernel(NormParams p) {
         const int c = (i * L + l) * VEC;
         float o[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = rstd * (go[i][j] - s1 - x[i][j] * s2);
+        for (int j = 0; j < VEC; ++j) o[j] = live ? rstd * (go[i][j] - s1 - x[i][j] * s2) : 0.f;
         if ((live || past) && c < p.d) store_piece<BF16, VEC>(p.dx, xt + c, o);
       }
     }

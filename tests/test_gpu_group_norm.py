@@ -189,3 +189,23 @@ def test_offsets_past_32_bits(first):
         assert not tail(got[name]).isnan().any()
     for name in ("weight", "bias"):    # zeros besides, summed in another order
         assert torch.allclose(got[name], ref[name], rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("io,d", [("bf16", 64), ("f32", 33)])
+def test_rows_past_a_length_get_zeros_whatever_the_affine_parameters_are(io, d, gated):
+    """weight and bias are no input of a row that is masked: not its zeros, nor dweight and dbias, see their infinities."""
+    import torch
+    from test_learned_neural_amd import titans_mem as tmm
+    B, H, N = 3, 2, 150
+    t = _draw(91, B, H, N, d, io, gated, True)
+    t["weight"][3], t["weight"][5], t["bias"][4] = float("inf"), float("nan"), float("-inf")
+    lengths = torch.tensor([N, 0, 70], dtype=torch.int32, device="cuda")
+    for own in (lengths, torch.zeros_like(lengths)):
+        g = tmm.group_norm_backward(t["x"], t["weight"], t["bias"], t["dout"], gate=t["gate"], lengths=own)
+        for b, n in enumerate(own.tolist()):
+            assert torch.all(g["x"][b, :, n:] == 0)
+            assert not gated or torch.all(g["gate"][b, n:] == 0)
+            assert torch.isfinite(g["x"][b, 1]).all()   # the other head's parameters are finite
+        if not own.any():
+            assert torch.all(g["weight"] == 0) and torch.all(g["bias"] == 0)
