@@ -34,8 +34,8 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
 constexpr int kC = 32;          // tokens per chunk
-// (n up to 2^31 - 1: n + 31 would not be an int)
-__host__ __device__ inline int chunks_of(int n) { return n / kC + (n % kC != 0); }
+// (unsigned: n may be 2^31 - 1)
+__host__ __device__ inline int chunks_of(int n) { return (int)(((unsigned)n + kC - 1) / kC); }
 constexpr int kCS = kC + 8;     // row stride of a [32][32] plane, in bf16
 constexpr int kBS = kC + 4;     // row stride of the fp32 scratch
 
