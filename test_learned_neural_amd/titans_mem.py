@@ -99,6 +99,12 @@ def load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           "`python -m test_learned_neural_amd.build` (hipcc, gfx950)")
+    # torch first, where it is there: it brings a HIP runtime of its own, which
+    # the library then shares; loaded the other way round the process has two
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        pass
     lib = ctypes.CDLL(LIB_PATH)
     vp, fp, i32, i64 = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     dp = ctypes.POINTER(Desc)

@@ -230,3 +230,17 @@ def test_dimensions_past_32_bits_do_not_wrap():
     for shape, H in (((1, 1, big, 1), None), ((big + 1, 4, 8), 2), ((1, 4, big * 8), 2)):
         with pytest.raises(ValueError, match="2\\^31"):
             tmm._NormPlan(shape, torch.float32, H, tmm.ACT_SILU, 1e-5)
+
+
+def test_a_query_before_torch_is_imported_leaves_one_hip_runtime():
+    """torch brings a HIP runtime of its own: with two in a process no launch on torch's tensors works."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("from test_learned_neural_amd import titans_mem as t\n"
+            "t.delta_workspace_bytes(t.make_delta_desc(1, 1, 1, 64, 64))\n"
+            "import torch\n"
+            "files = {l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}\n"
+            "assert len(files) == 1, files\n")
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=300)
