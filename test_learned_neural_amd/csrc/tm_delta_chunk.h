@@ -220,6 +220,13 @@ template <int DP, int COLS, bool F32, int VB>
 struct RowLoad {
   static constexpr int PER = VB ? VB / (F32 ? 4 : 2) : 4;    // elements per piece
   static constexpr int PIECES = kC * COLS / PER / 64;        // per lane
+  // a lane's i-th piece is at row r, column c; the offsets repeat every P pieces, ROWS rows further down
+  static constexpr int ROW = COLS / PER, P = ROW % 3 ? 1 : 3, ROWS = P * 64 / ROW;
+  static_assert(P * 64 % ROW == 0 && PIECES % P == 0, "whole rows");
+  static __device__ __forceinline__ void place(int i, int lane, int& r, int& c) {
+    const int e = i % P * 64 + lane;
+    r = e / ROW + i / P * ROWS, c = e % ROW * PER;
+  }
   uint32_t raw[VB ? PIECES : 1][VB ? VB / 4 : 1];
   const char* src;
   int n, d, cols;
@@ -230,13 +237,15 @@ struct RowLoad {
       if (n == kC && d == DP && cols >= COLS) {   // offsets that no chunk changes
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-          const int e = (i * 64 + lane) * PER;
-          take(i, (e / COLS * DP + e % COLS) * (F32 ? 4 : 2));
+          int r, c;
+          place(i, lane, r, c);
+          take(i, (r * DP + c) * (F32 ? 4 : 2));
         }
       } else {   // clamped addresses: no branch between the loads
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-          const int e = (i * 64 + lane) * PER, r = e / COLS, c = e % COLS;
+          int r, c;
+          place(i, lane, r, c);
           take(i, (min(r, n - 1) * d + max(min(c, cols - PER), 0)) * (F32 ? 4 : 2));
         }
       }
@@ -259,21 +268,24 @@ struct RowLoad {
       if (n != kC || cols < COLS) {
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-          const int e = (i * 64 + lane) * PER, r = e / COLS, c = e % COLS;
+          int r, c;
+          place(i, lane, r, c);
 #pragma unroll
           for (int j = 0; j < VB / 4; ++j) raw[i][j] = r < n && c < cols ? raw[i][j] : 0u;
         }
       }
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        const int e = (i * 64 + lane) * PER, r = e / COLS, c = e % COLS;
+        int r, c;
+        place(i, lane, r, c);
 #pragma unroll
         for (int j = 0; j < PER; j += 4) put(r, c + j, raw[i] + (F32 ? j : j / 2));
       }
     } else {
 #pragma unroll 1
       for (int i = 0; i < PIECES; ++i) {
-        const int e = (i * 64 + lane) * PER, r = e / COLS, c = e % COLS;
+        int r, c;
+        place(i, lane, r, c);
         uint32_t x[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < 4; ++j)

@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(ChainParams p)
 template <int DP, bool F32, int CW, int VB, bool TRANS>
 hipError_t launch_as(ChainParams p, hipStream_t stream) {
   // as many buffers as LDS holds, and builders as keep the chain fed
-  constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : 4, PB = F32 ? (DP == 128 ? 1 : 2) : DP == 64 ? 3 : 2;
+  constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : 4, PB = F32 ? (DP == 64 ? 2 : 1) : DP == 64 ? 3 : 2;
   using R = Ring<ChunkLds<DP, F32 ? 3 : 1, F32 ? 3 : 2, CW * 16>, CW, PB, NB, F32>;
   constexpr int lds = R::BYTES;
   static_assert(lds <= 160 * 1024, "LDS of one workgroup");
@@ -361,7 +361,8 @@ hipError_t launch_as(ChainParams p, hipStream_t stream) {
 // How a call is cut.  Times of a chunk of 32 tokens in a workgroup that has a
 // CU to itself, in tenths of a microsecond, as measured on 16 to 512 streams:
 // d up to 64 with 2 chain waves 13, with 4 18 (128: 17 and 24; fp32: 20 and
-// 30, 46 and 62), two thirds of that without y.
+// 30, 46 and 62), two thirds of that without y (d from 65 to 96 takes a fifth
+// less than 128, whichever way it is cut).
 struct Plan {
   int wide;       // 4 chain waves in a workgroup of the (last) launch
   int segments;   // 1: one launch
@@ -403,15 +404,19 @@ hipError_t launch_chain(const ChainParams& p, bool wide, hipStream_t stream) {
   if (p.segments > 1) {
     hipError_t err = launch_as<DP, F32, 4, VB, true>(p, stream);
     if (err != hipSuccess) return err;
-    delta_join_kernel<DP><<<p.streams * (p.ld / 16), kJoinThreads, 0, stream>>>(p);
+    delta_join_kernel<DP == 64 ? 64 : 128><<<p.streams * (p.ld / 16), kJoinThreads, 0, stream>>>(p);
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
   return wide ? launch_as<DP, F32, 4, VB, false>(p, stream) : launch_as<DP, F32, 2, VB, false>(p, stream);
 }
 
+// Widths from 65 to 96 have kernels of their own: 3 of 4 tiles' work, 30
+// streams x 777 x 96, fp32, in 116 us against 137 with rows padded to 128
+// (256 x 1024 x 80, bf16: 150 against 166).
 template <bool F32, int VB>
 hipError_t launch_width(const ChainParams& p, bool wide, hipStream_t stream) {
-  return p.d <= 64 ? launch_chain<64, F32, VB>(p, wide, stream) : launch_chain<128, F32, VB>(p, wide, stream);
+  if (p.d <= 64) return launch_chain<64, F32, VB>(p, wide, stream);
+  return p.d <= 96 ? launch_chain<96, F32, VB>(p, wide, stream) : launch_chain<128, F32, VB>(p, wide, stream);
 }
 
 }  // namespace

@@ -259,3 +259,29 @@ def test_offsets_past_32_bits():
     yr, Wr = do.delta_forward(*f)
     check("W", W, Wr, "f32", tol32(1200, d))
     check("y", y[:, :, -1100:], yr[:, :, 100:], "bf16", tol32(1200, d))
+
+
+#         B  H  Hk N     d   io      lengths      (both ends of the kernels' 65 to 96, rows of every alignment)
+MIDDLE = [(2, 2, 1, 100, 65, "f32", None),
+          (2, 2, 1, 100, 67, "bf16", [100, 33]),
+          (2, 4, 2, 131, 96, "f32", [131, 64]),
+          (2, 4, 2, 131, 96, "bf16", None),
+          (1, 2, 2, 97, 92, "bf16", None),
+          (1, 2, 2, 97, 88, "bf16", [96]),
+          (2, 2, 2, 97, 97, "f32", None),
+          (1, 1, 1, 2600, 96, "f32", [2599]),
+          (1, 2, 1, 2600, 72, "bf16", None),
+          (1, 1, 1, 2600, 68, "bf16", [1300]),
+          (1, 1, 1, 2600, 95, "f32", None)]
+
+
+@pytest.mark.parametrize("shape", MIDDLE, ids=str)
+def test_widths_between_64_and_128(shape):
+    from test_learned_neural_amd import titans_mem as tmm
+    B, H, Hk, N, d, io, lengths = shape
+    assert (tmm.delta_workspace_bytes(tmm.make_delta_desc(B, H, Hk, N, d, io)) > 0) == (N == 2600)
+    t, f = make(51, B, H, Hk, N, d, io, resets=True, lengths=lengths)
+    y, W = _run(cuda(t))
+    yr, Wr = _oracle(f)
+    check("y", y, yr, io, tol32(N, d))
+    check("W", W, Wr, "f32", tol32(N, d))
