@@ -592,7 +592,7 @@ template <int DP, bool F32, int CW, int VB>
 hipError_t launch_sweep(GradParams p, hipStream_t stream) {
   // (two workgroups of 2 chain waves share a CU where LDS allows)
   constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : DP == 64 && CW == 2 ? 3 : 4,
-                PB = F32 ? (DP == 128 ? 1 : 2) : DP == 64 && CW == 4 ? 3 : 2;
+                PB = F32 ? (DP == 64 ? 2 : 1) : DP == 64 && CW == 4 ? 3 : 2;
   using R = Ring<GradLds<DP, F32, CW>, CW, PB, NB, F32>;
   static_assert(R::BYTES <= 160 * 1024, "LDS of one workgroup");
   p.parts = ((p.d + 15) / 16 + CW - 1) / CW;
@@ -623,9 +623,12 @@ hipError_t launch_grad(GradParams p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// (128 streams x 512 x 96: 357 us in fp32 and 210 in bf16, padded to 128 445
+// and 261)
 template <bool F32, int VB>
 hipError_t launch_width(const GradParams& p, hipStream_t stream) {
-  return p.d <= 64 ? launch_grad<64, F32, VB>(p, stream) : launch_grad<128, F32, VB>(p, stream);
+  if (p.d <= 64) return launch_grad<64, F32, VB>(p, stream);
+  return p.d <= 96 ? launch_grad<96, F32, VB>(p, stream) : launch_grad<128, F32, VB>(p, stream);
 }
 
 int64_t state_floats(const DeltaShape& s) {

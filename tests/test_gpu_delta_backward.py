@@ -121,3 +121,15 @@ def test_same_bits_streams_and_replayed_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(want[n], out[n]) for n in NAMES)
+
+
+@pytest.mark.parametrize("B,H,Hk,N,d,io,lengths", [
+    (2, 2, 1, 70, 65, "f32", None), (2, 2, 1, 70, 67, "bf16", [70, 33]), (2, 4, 2, 99, 96, "f32", [99, 64]),
+    (2, 4, 2, 99, 96, "bf16", None), (1, 2, 2, 65, 92, "bf16", None), (1, 2, 1, 65, 88, "bf16", [64]),
+    (2, 2, 2, 40, 97, "f32", None), (40, 4, 2, 40, 84, "f32", None), (40, 4, 2, 40, 96, "bf16", None)])
+def test_widths_between_64_and_128(B, H, Hk, N, d, io, lengths):
+    t, f = make(61, B, H, Hk, N, d, io, resets=True, lengths=lengths)
+    got = _run(cuda(t))
+    want = do.delta_backward(*(f[n] for n in NAMES), f["dy"], f["dW"], f["lengths"])
+    for name in NAMES:
+        check(name, got[name], want[name], io, 4 * tol32(N, d))
