@@ -53,7 +53,7 @@ struct GradParams {
 };
 
 template <int DP, bool F32, int CW>
-using GradLds = ChunkLds<DP, F32 ? 3 : 1, 3, CW * 16>;
+using GradLds = ChunkLds<DP, F32 ? 3 : 1, CW * 16>;
 
 // ---- the two sweeps: blocks of the first half forwards, of the second backwards ----
 template <int DP, bool F32, int CW, int PB, int NB, int VB>
@@ -223,10 +223,10 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_sweep_ke
 // ---- a chunk of a key head ----
 template <int DP, bool F32>
 struct PieceLds {
-  static constexpr int NP = F32 ? 3 : 1, NX = F32 ? 3 : 2, RS = DP + 8, KP = kC * RS, CP = kC * kCS, FP = DP * kCS,
+  static constexpr int NP = F32 ? 3 : 1, RS = DP + 8, KP = kC * RS, CP = kC * kCS, FP = DP * kCS,
                        NW = DP / 16;
   static constexpr int K = 0, Q = K + NP * KP * 2, DY = Q + NP * KP * 2, F = DY + NP * KP * 2, DE = F + 3 * FP * 2,
-                       X = DE + 3 * FP * 2, M = X + NX * CP * 2, Z = M + NX * CP * 2, GATES = Z + kC * kBS * 4,
+                       X = DE + 3 * FP * 2, M = X + 3 * CP * 2, Z = M + 3 * CP * 2, GATES = Z + kC * kBS * 4,
                        DOTS = GATES + 9 * kC * 4, BYTES = DOTS + NW * (2 * kC + 1) * 4;
 };
 
@@ -278,7 +278,7 @@ __device__ __forceinline__ float groups_sum(float x) {
 template <int DP, bool F32, int VB>
 __global__ void __launch_bounds__(DP * 4, 2) delta_piece_kernel(GradParams p) {
   using L = PieceLds<DP, F32>;
-  constexpr int NP = L::NP, NX = L::NX, NW = L::NW, NK = DP / 32, RS = L::RS, KP = L::KP, CP = L::CP, FP = L::FP;
+  constexpr int NP = L::NP, NW = L::NW, NK = DP / 32, RS = L::RS, KP = L::KP, CP = L::CP, FP = L::FP;
   constexpr int kE = F32 ? 4 : 2;
   // K, Q and dY are staged by blocks of kCols columns, kParts waves to a tensor, kRows blocks to a wave (blocks of 32
   // columns keep the wide rows in few registers: 284 us against 361 for 128 streams x 512, d 128, fp32)
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(DP * 4, 2) delta_piece_kernel(GradParams p) {
       }
       // X's upper right block
 #pragma unroll
-      for (int i = 0; i < NX; ++i) *(uint2*)(Xs + i * CP + li * kCS + 8 * g + 4) = make_uint2(0, 0);
+      for (int i = 0; i < 3; ++i) *(uint2*)(Xs + i * CP + li * kCS + 8 * g + 4) = make_uint2(0, 0);
     }
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
@@ -446,14 +446,14 @@ __global__ void __launch_bounds__(DP * 4, 2) delta_piece_kernel(GradParams p) {
         mm[r] *= -D;
       }
       *(f32x4*)(Z + t * kBS + j0) = z;
-      put4<NX>(Xs + t * kCS + 8 * g + 4 * jt, CP, xx[0], xx[1], xx[2], xx[3]);
+      put4<3>(Xs + t * kCS + 8 * g + 4 * jt, CP, xx[0], xx[1], xx[2], xx[3]);
       // M and its transpose; the zeros of a diagonal tile's upper half are the transpose's places
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int j = j0 + r;
         float v = mm[r];
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
+        for (int i = 0; i < 3; ++i) {
           const uint16_t u = (uint16_t)(bits(v) >> 16);
           v -= top(v);
           if (t >= j) Ms[i * CP + t * kCS + perm32(j)] = u;
@@ -523,11 +523,11 @@ __global__ void __launch_bounds__(DP * 4, 2) delta_piece_kernel(GradParams p) {
     __syncthreads();
     // through the chunk's own tokens
     {
-      bf16x8 xr[2][NX], xt[2][NX], mr[2][NX], kT[NP], qT[NP];
-      read2<NX>(Xs + li * kCS + 8 * g, CP, 16 * kCS, xr);
-      read2<NX>(Ms + li * kCS + 8 * g, CP, 16 * kCS, mr);
+      bf16x8 xr[2][3], xt[2][3], mr[2][3], kT[NP], qT[NP];
+      read2<3>(Xs + li * kCS + 8 * g, CP, 16 * kCS, xr);
+      read2<3>(Ms + li * kCS + 8 * g, CP, 16 * kCS, mr);
 #pragma unroll
-      for (int i = 0; i < NX; ++i)
+      for (int i = 0; i < 3; ++i)
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) xt[rt][i] = read_transposed<true>(Xs + i * CP, kCS, 16 * rt, lane);
 #pragma unroll

@@ -21,6 +21,9 @@
 // down to 2^-16 (the three dropped ones are below 2^-24 of it), a product
 // with a bf16 input, which is its own first plane, the three that exist: so
 // the bf16 matrix cores (16 times the fp32 ones' rate) give fp32 results.
+// That holds for bf16 outputs too: where a large old association is
+// overwritten, y is a small difference of terms of the old one's size, and
+// factors of two planes would leave it 2^-17 of that size off.
 #pragma once
 
 #include "tm_internal.h"
@@ -186,17 +189,17 @@ __device__ __forceinline__ float log2_keep(float alpha, float floor = kForget) {
   return l < floor ? floor : l;
 }
 
-// LDS of one chunk: NP planes of K and Q, three of T = (I + B)^-1, NPP of P,
+// LDS of one chunk: NP planes of K and Q, three of T = (I + B)^-1 and of P,
 // per-token factors, and VC columns of V.  T's upper right block is zeroed once.
-template <int DP, int NP, int NPP, int VC>
+template <int DP, int NP, int VC>
 struct ChunkLds {
   static constexpr int RS = DP + 8;                 // row stride of K and Q in bf16
   static constexpr int KP = kC * RS, CP = kC * kCS; // plane sizes
   static constexpr int OFF_K = 0, OFF_Q = OFF_K + NP * KP * 2, OFF_T = OFF_Q + NP * KP * 2, OFF_P = OFF_T + 3 * CP * 2,
-                       OFF_G = OFF_P + NPP * CP * 2, OFF_V = OFF_G + (2 * kC + 4) * 4,
+                       OFF_G = OFF_P + 3 * CP * 2, OFF_V = OFF_G + (2 * kC + 4) * 4,
                        VS = VC + 4,   // row stride of V: bf16, or fp32 where NP is 3
                        BYTES = OFF_V + kC * VS * (NP == 1 ? 2 : 4);
-  static_assert(NPP * CP * 2 >= kC * kBS * 4, "the fp32 scratch lies where P comes to lie");
+  static_assert(3 * CP * 2 >= kC * kBS * 4, "the fp32 scratch lies where P comes to lie");
   static_assert(16 * kCS * 2 >= 3 * kC * 4, "the gates' scratch lies in T's lower half");
   unsigned char* base;
   __device__ uint16_t* k() const { return (uint16_t*)(base + OFF_K); }
@@ -331,9 +334,9 @@ __device__ __forceinline__ double prefix_sums(float x, int lane, double& all) {
 // One wave builds a chunk's matrices in LDS from its K and Q (already stored)
 // and its gates (lane t < 32: token t's log2 a and theta; 0 past the end).
 // WITH_Q: P too.
-template <bool WITH_Q, int DP, int NP, int NPP, int VC>
-__device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP, VC>& L, float la, float th, int lane) {
-  using Lds = ChunkLds<DP, NP, NPP, VC>;
+template <bool WITH_Q, int DP, int NP, int VC>
+__device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, VC>& L, float la, float th, int lane) {
+  using Lds = ChunkLds<DP, NP, VC>;
   const int g = lane >> 4, li = lane & 15;
   double all;
   const double sum = prefix_sums(la, lane, all);
@@ -461,10 +464,10 @@ __device__ __forceinline__ void build_chunk(const ChunkLds<DP, NP, NPP, VC>& L, 
   put4<3>(T + 16 * kCS + 4, Lds::CP, t11[0], t11[1], t11[2], t11[3]);
   if (!WITH_Q) return;
   uint16_t* P = L.p() + li * kCS + 8 * g;
-  put4<NPP>(P, Lds::CP, qk[0][0], qk[0][1], qk[0][2], qk[0][3]);
-  put4<NPP>(P + 4, Lds::CP, 0.f, 0.f, 0.f, 0.f);
-  put4<NPP>(P + 16 * kCS, Lds::CP, qk[1][0], qk[1][1], qk[1][2], qk[1][3]);
-  put4<NPP>(P + 16 * kCS + 4, Lds::CP, qk[2][0], qk[2][1], qk[2][2], qk[2][3]);
+  put4<3>(P, Lds::CP, qk[0][0], qk[0][1], qk[0][2], qk[0][3]);
+  put4<3>(P + 4, Lds::CP, 0.f, 0.f, 0.f, 0.f);
+  put4<3>(P + 16 * kCS, Lds::CP, qk[1][0], qk[1][1], qk[1][2], qk[1][3]);
+  put4<3>(P + 16 * kCS + 4, Lds::CP, qk[2][0], qk[2][1], qk[2][2], qk[2][3]);
 }
 
 // A counter in LDS that one wave raises and others wait for.

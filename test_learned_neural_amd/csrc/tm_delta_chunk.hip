@@ -67,9 +67,9 @@ __device__ __forceinline__ void store_ws(const f32x4 (&S)[NT], float* W, int row
 // the values, as many again from the unit vectors without.
 template <int DP, bool F32, int CW, int PB, int NB, int VB, bool TRANS>
 __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_kernel(ChainParams p) {
-  constexpr int NP = F32 ? 3 : 1, NPP = F32 ? 3 : 2, NS = F32 ? 3 : 2;   // planes: inputs, P, and W and F for y
+  constexpr int NP = F32 ? 3 : 1;   // planes of an input
   constexpr int NT = DP / 16, NK = DP / 32, kE = F32 ? 4 : 2;
-  using Lds = ChunkLds<DP, NP, NPP, CW * 16>;
+  using Lds = ChunkLds<DP, NP, CW * 16>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const Ring<Lds, CW, PB, NB, F32> ring{smem};
   const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
@@ -171,28 +171,28 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
     bf16x8 rp[3];
     split8<3>(R[0], R[1], rp);
     if (!F32) in_order();
-    bf16x8 kt[NT][NP], rp2[2][NPP];
+    bf16x8 kt[NT][NP], rp2[2][3];
     if (!F32) {
 #pragma unroll
       for (int ti = 0; ti < NT; ++ti) kt[ti][0] = read_transposed<true>(L.k(), Lds::RS, 16 * ti, lane);
-      if (!TRANS) read2<NPP>(pa, Lds::CP, 16 * kCS, rp2);
+      if (!TRANS) read2<3>(pa, Lds::CP, 16 * kCS, rp2);
     }
     const float gc = L.gc()[0], scale = L.gc()[1];
     // F = T R, with Q W^T between the steps of its accumulation chains
     {
-      constexpr int kF = products<3, 3>(), kQ = products<NP, NS>();
+      constexpr int kF = products<3, 3>(), kQ = products<NP, 3>();
 #pragma unroll
       for (int f = 0; f < kF; ++f) {
         mul2_one<false, 3>(f, rt3, rp, F);
         if (TRANS) continue;
 #pragma unroll
-        for (int x = f * NK * kQ / kF; x < (f + 1) * NK * kQ / kF; ++x) mul2_one<true, NS>(x % kQ, rq[x / kQ], sp[x / kQ], qs);
+        for (int x = f * NK * kQ / kF; x < (f + 1) * NK * kQ / kF; ++x) mul2_one<true, 3>(x % kQ, rq[x / kQ], sp[x / kQ], qs);
         if (!F32) in_order();
       }
     }
     // W' = G_C W + K^T (E theta F)
     f32x4 U[2], acc[NT], out[2];
-    bf16x8 up[3], fp[NS];
+    bf16x8 up[3], fp[3];
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) U[rt] = F[rt] * E[rt];
     split8<3>(U[0], U[1], up);
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
       for (int ti = 0; ti < NT; ++ti)
 #pragma unroll
         for (int e = 0; e < NP; ++e) kt[ti][e] = read_transposed<true>(L.k() + e * Lds::KP, Lds::RS, 16 * ti, lane);
-      if (!TRANS) read2<NPP>(pa, Lds::CP, 16 * kCS, rp2);
+      if (!TRANS) read2<3>(pa, Lds::CP, 16 * kCS, rp2);
     }
 #pragma unroll
     for (int f = 0; f < products<NP, 3>(); ++f) {
@@ -218,12 +218,12 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
     }
     // Y^T = W Q^T diag(G) + F^T P^T
     if (!TRANS) {
-      split8<NS>(F[0], F[1], fp);
+      split8<3>(F[0], F[1], fp);
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) out[rt] = qs[rt] * L.g()[16 * rt + li];
     }
     ready = seen(ring.built() + (c + 1) % PB);
-    if (!TRANS) mul2<true, NS>(rp2, fp, out);
+    if (!TRANS) mul2<true, 3>(rp2, fp, out);
 #pragma unroll
     for (int ti = 0; ti < NT; ++ti) S[ti] = scaled ? S[ti] + acc[ti] * scale : acc[ti];
     raise_to(ring.used() + wave, c + 1, lane);
@@ -345,7 +345,7 @@ template <int DP, bool F32, int CW, int VB, bool TRANS>
 hipError_t launch_as(ChainParams p, hipStream_t stream) {
   // as many buffers as LDS holds, and builders as keep the chain fed
   constexpr int NB = F32 ? (DP == 64 ? 3 : 2) : 4, PB = F32 ? (DP == 64 ? 2 : 1) : DP == 64 ? 3 : 2;
-  using R = Ring<ChunkLds<DP, F32 ? 3 : 1, F32 ? 3 : 2, CW * 16>, CW, PB, NB, F32>;
+  using R = Ring<ChunkLds<DP, F32 ? 3 : 1, CW * 16>, CW, PB, NB, F32>;
   constexpr int lds = R::BYTES;
   static_assert(lds <= 160 * 1024, "LDS of one workgroup");
   p.parts = ((p.d + 15) / 16 * (TRANS ? 2 : 1) + CW - 1) / CW;
