@@ -83,6 +83,9 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
   const int all = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
   const int first = (int)min((int64_t)seg * p.seg_chunks * kC, (int64_t)all);   // the segment's tokens: first .. first + n - 1
   const int n = seg + 1 < p.segments ? (int)min((int64_t)(all - first), (int64_t)p.seg_chunks * kC) : all - first;
+  // the segment with the sequence's last token leaves the final state (W_in itself, if there is no token)
+  if (!TRANS && seg > 0 && n == 0) return;
+  const bool last = first + n == all;
   const int chunks = chunks_of(n);
   ring.init(wave, lane);
 
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
       store_ws(S, p.ws_loc + at_ws, col, p.ld, g);
     else
       store_ws(S, p.ws_phi + at_ws, unit, p.ld, g);
-  } else if (seg + 1 == p.segments) {
+  } else if (last) {
     store_state<NT, VB>(S, p.W_out, s, col, d, g);
   }
 }
