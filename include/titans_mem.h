@@ -371,7 +371,8 @@ int titans_mem_input(const titans_input_desc* desc,
  * N == 0 copies the state.  Where chunks are used, a NaN or infinity of a
  * token may reach the 31 tokens before it (of its stream) too, and the product
  * of 1 - alpha over up to 32 tokens in a row has to be a finite float (a gate
- * never makes it larger than 1; a negative alpha can).  TM_FLAG_FORCE_GENERIC runs the
+ * never makes it larger than 1; a negative alpha can, and multiplies rounding
+ * errors by up to that product).  TM_FLAG_FORCE_GENERIC runs the
  * token-by-token kernel at any N.  titans_mem_delta_select_path reports the
  * kernel that a call runs.
  */

@@ -29,7 +29,8 @@
 // passes the state through them in order (delta_join_kernel), a third runs
 // the segments side by side from their true starts.  That is about 2.4 times
 // the work, for as many times the parallelism as there are segments: 16
-// streams x 65536 tokens take 510 us so and 2740 in one piece.
+// streams x 65536 tokens take 510 us so and 2740 in one piece.  (Rows whose
+// maps overflow are run in one piece: delta_join_kernel.)
 #include "tm_delta_chunk.h"
 
 namespace titans {
@@ -44,6 +45,7 @@ struct ChainParams {
   // segments of seg_chunks chunks; ws_phi, ws_loc, ws_start: [stream][segment][ld x ld] (rows: value channels of
   // W_0 and the starts, inputs of Phi)
   float *ws_phi, *ws_loc, *ws_start;
+  int32_t* ws_whole;   // [stream][ld / 16]: value channels whose sequence is run in one piece
   int streams, H, Hk, N, d, parts, segments, seg_chunks, ld;
 };
 
@@ -82,7 +84,14 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
   const int b = s / p.H, h = s % p.H, d = p.d;
   const int all = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
   const int first = (int)min((int64_t)seg * p.seg_chunks * kC, (int64_t)all);   // the segment's tokens: first .. first + n - 1
-  const int n = seg + 1 < p.segments ? (int)min((int64_t)(all - first), (int64_t)p.seg_chunks * kC) : all - first;
+  int n = seg + 1 < p.segments ? (int)min((int64_t)(all - first), (int64_t)p.seg_chunks * kC) : all - first;
+  if (!TRANS && p.segments > 1) {   // the first segment takes the sequence, where its maps are of no use
+    const int tiles = p.ld / 16, end = min((part + 1) * CW, tiles);
+    int whole = 0;
+    for (int i = part * CW; i < end; ++i) whole |= p.ws_whole[s * tiles + i];
+    if (whole && seg > 0) return;
+    if (whole) n = all;
+  }
   // the segment with the sequence's last token leaves the final state (W_in itself, if there is no token)
   if (!TRANS && seg > 0 && n == 0) return;
   const bool last = first + n == all;
@@ -109,7 +118,7 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[i][r] = 16 * i + 4 * g + r == unit ? 1.f : 0.f;
+      for (int r = 0; r < 4; ++r) S[i][r] = 16 * i + 4 * g + r == unit && unit < d ? 1.f : 0.f;
   } else if (p.segments > 1) {
     load_ws(S, p.ws_start + at_ws, col, p.ld, g);
   } else {
@@ -276,6 +285,11 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
 // in LDS between segments.  The next segment's Phi and W_0 are read while one
 // is computed: what remains serial is a product's 16 or 32 steps (in two
 // accumulation chains) and the rows' way through LDS.
+//
+// A map may overflow where no state does: with a > 1 a direction that no key
+// touches grows over the whole segment, and a state without a part in it meets
+// 0 x inf.  Rows that come out of a join not finite are therefore taken
+// through the sequence in one piece.
 constexpr int kJoinThreads = 256;
 template <int DP>
 __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(ChainParams p) {
@@ -296,7 +310,8 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(ChainParams p)
     float phi[T][K];
     f32x4 loc[T];
   };
-  // columns past ld read the last tile's (and are not stored); steps past it multiply zeros of `rows` by finite values
+  // columns past ld read the last tile's (and are not stored), steps past it the last row, for zeros of `rows`
+  int lost = 0;   // a value that is not finite
   auto read = [&](int seg, Step& x) {
     const float *phi = p.ws_phi + base + (int64_t)seg * ld * ld, *loc = p.ws_loc + base + (int64_t)seg * ld * ld;
 #pragma unroll
@@ -327,6 +342,7 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(ChainParams p)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float v = acc[i][0][r] + acc[i][1][r];
+        lost |= (bits(v) & 0x7f800000u) == 0x7f800000u;
         rows[4 * g + r][c] = v;
         next[(row0 + 4 * g + r) * ld + c] = v;
       }
@@ -342,6 +358,8 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(ChainParams p)
     read(min(seg + 2, n - 1), a);
     step(seg + 1, b);
   }
+  lost = __syncthreads_or(lost);
+  if (threadIdx.x == 0) p.ws_whole[blockIdx.x] = lost;
 }
 
 template <int DP, bool F32, int CW, int VB, bool TRANS>
@@ -424,7 +442,10 @@ hipError_t launch_width(const ChainParams& p, bool wide, hipStream_t stream) {
 
 }  // namespace
 
-int64_t delta_chunked_ws_bytes(const DeltaShape& s) { return 12 * segment_floats(s, plan_of(s)); }
+int64_t delta_chunked_ws_bytes(const DeltaShape& s) {
+  const Plan plan = plan_of(s);
+  return 12 * segment_floats(s, plan) + (plan.segments > 1 ? (int64_t)s.B * s.H * ((s.d + 15) / 16) * 4 : 0);
+}
 
 hipError_t launch_delta_chunked(const DeltaShape& s, const void* k, const void* v, const void* q, const float* alpha,
                                 const float* theta, const int32_t* lengths, const float* W_in, void* y, float* W_out,
@@ -432,6 +453,7 @@ hipError_t launch_delta_chunked(const DeltaShape& s, const void* k, const void* 
   const Plan plan = plan_of(s);
   ChainParams p = {k, v, q, alpha, theta, W_in, lengths, y, W_out};
   p.ws_phi = ws, p.ws_loc = ws + segment_floats(s, plan), p.ws_start = ws + 2 * segment_floats(s, plan);
+  p.ws_whole = (int32_t*)(ws + 3 * segment_floats(s, plan));
   p.streams = s.B * s.H, p.H = s.H, p.Hk = s.Hk, p.N = s.N, p.d = s.d, p.ld = (s.d + 15) / 16 * 16;
   p.segments = plan.segments, p.seg_chunks = plan.seg_chunks;
   if (s.io == TM_IO_BF16) {

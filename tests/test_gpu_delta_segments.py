@@ -1,9 +1,24 @@
-"""Calls that are cut into segments: sequences that end before the last one."""
+"""Calls that are cut into segments, where a segment's map is not what a token
+meets: growth that overflows over a segment and nowhere in the recurrence, and
+sequences that end before the last segment."""
 import numpy as np
 import pytest
 
+from delta_util import U32, check, tol32
+
 pytestmark = pytest.mark.gpu
-N = 60000     # 2 streams of 60000 tokens: 125 segments of 15 chunks
+N, SEG = 60000, 480     # 2 streams of 60000 tokens: 125 segments of 15 chunks
+GROWTH = -0.25          # 1.25^480 is 2^154; over 32 tokens it is 1262
+
+
+def recurrence(k, v, q, alpha, theta, W):
+    """fp64, one stream: y and W."""
+    y = np.zeros_like(v)
+    for t in range(len(k)):
+        W = (1 - alpha[t]) * W
+        W = W + theta[t] * np.outer(v[t] - W @ k[t], k[t])
+        y[t] = W @ q[t]
+    return y, W
 
 
 def problem(d, used, io, alpha, seed=1):
@@ -18,6 +33,79 @@ def problem(d, used, io, alpha, seed=1):
          "q": torch.from_numpy(q).to(dt), "alpha": torch.from_numpy(np.broadcast_to(alpha, (1, 2, N)).copy()).float(),
          "theta": torch.ones(1, 2, N), "W_in": torch.from_numpy(rng.standard_normal((1, 2, d, d))).float()}
     return t
+
+
+def run(t, **kw):
+    from test_learned_neural_amd import titans_mem as tmm
+    B, H, _, d = t["v"].shape
+    assert tmm.delta_workspace_bytes(tmm.make_delta_desc(B, H, t["k"].shape[1], N, d, "bf16" if t["k"].element_size() == 2 else "f32")) > 0
+    return tmm.delta_forward(*(t[n].cuda() for n in ("k", "v", "q", "alpha", "theta", "W_in")), **kw)
+
+
+def compare(t, y, W, io, d, used):
+    """A column grows by 1.25 `used` times before it is replaced by v, in a chunk of 32 tokens 1 + 31 // used times.
+    The chunk's form has every one of them as terms of its own: the column of its start grown past all replacements,
+    and each residual grown past the later ones.  They are up to 1.25^(used (1 + 31 // used)) times what is left after
+    the last replacement, and each is rounded less than 16 times (the decay's exponent and power, the products and
+    their sums): 16 u of that factor, relative to the new column, beside what any recurrence of N tokens is off."""
+    ref = [recurrence(*(t[n][0, h].double().numpy() for n in ("k", "v", "q", "alpha", "theta", "W_in"))) for h in range(2)]
+    yr, Wr = (np.stack([r[i] for r in ref])[None] for i in range(2))
+    assert np.abs(Wr).max() < 1e30
+    tol = tol32(N, d) + 16 * U32 * (1 - GROWTH) ** (used * (1 + 31 // used))
+    check("y", y, yr, io, tol)
+    check("W", W, Wr, "f32", tol)
+
+
+@pytest.mark.parametrize("d,io", [(40, "bf16"), (24, "f32"), (100, "f32")])
+def test_growth_in_the_padding_of_a_width(d, io):
+    """d is no multiple of 16: the rows that pad a map are no input of the memory."""
+    used = min(d, 40)       # (d = 100: the other columns start at zero and stay so)
+    t = problem(d, used, io, GROWTH)
+    t["W_in"][..., used:] = 0
+    y, W = run(t)
+    compare(t, y, W, io, d, used)
+
+
+@pytest.mark.parametrize("d,io", [(48, "bf16"), (64, "f32"), (128, "bf16")])
+def test_growth_where_no_key_reaches(d, io):
+    """A column that no key touches and that is zero stays zero, however far its map has grown."""
+    t = problem(d, 40, io, GROWTH)
+    t["W_in"][..., 40:] = 0
+    y, W = run(t)
+    assert (W[..., 40:] == 0).all()
+    compare(t, y, W, io, d, 40)
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+def test_growth_of_a_column_that_starts_small(inplace):
+    """2^154 over one segment, from 1e-30: finite in the recurrence.  A second stream that only decays is unharmed."""
+    d = 48
+    alpha = np.full((1, 2, N), 0.01)
+    alpha[0, 0, 21 * SEG:22 * SEG] = GROWTH
+    alpha[:, :, :21 * SEG] = 0.0
+    t = problem(d, 40, "f32", alpha)
+    t["W_in"][..., 40:] *= 1e-30
+    t["q"][:, :, 20 * SEG:, 44] = 1e-12
+    if inplace:
+        from test_learned_neural_amd import titans_mem as tmm
+        g = {n: x.cuda() for n, x in t.items()}
+        y, W = tmm.delta_forward(*(g[n] for n in ("k", "v", "q", "alpha", "theta", "W_in")), W_out=g["W_in"])
+        assert W is g["W_in"]
+    else:
+        y, W = run(t)
+    compare(t, y, W, "f32", d, 40)
+
+
+def test_a_nan_in_a_late_segment_leaves_the_tokens_before_it():
+    t = problem(64, 40, "bf16", 0.01)
+    t["v"][0, 1, 30000, 3] = float("nan")
+    y, W = run(t)
+    t["v"][0, 1, 30000, 3] = 0
+    want, _ = run(t)
+    assert y[0, 1, 30000:, 3].isnan().any() and W[0, 1, 3].isnan().any()
+    y[0, 1, 30000 // 32 * 32:, 3] = want[0, 1, 30000 // 32 * 32:, 3]
+    e = (y.double() - want.double()).norm() / want.double().norm()
+    assert float(e) <= 2 * (tol32(N, 64) + 2.0 ** -8), float(e)
 
 
 @pytest.mark.parametrize("inplace", [False, True])
