@@ -361,7 +361,9 @@ int titans_mem_input(const titans_input_desc* desc,
  *              after the last token of its sequence (W_in for length 0).
  *   W_in, W_out  [B,H,d,d] fp32, device, row-major [n_out x n_in]; W_out ==
  *              W_in (exact in-place) is allowed, any other overlap of a
- *              written buffer is TM_ERR_ALIAS
+ *              written buffer is TM_ERR_ALIAS.  In place the states of
+ *              sequences of length 0 are not written: calls on several
+ *              streams may share one state, if no sequence has tokens in two
  *   y_out      [B,H,N,d]   io dtype, device, written
  *   workspace  titans_mem_delta_workspace_bytes(desc) bytes of device
  *              scratch (may be NULL when that is 0)

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__((CW + PB * (F32 ? 2 : 1)) * 64) delta_chain_ke
     if (whole) n = all;
   }
   // the segment with the sequence's last token leaves the final state (W_in itself, if there is no token)
-  if (!TRANS && seg > 0 && n == 0) return;
+  if (!TRANS && n == 0 && (seg > 0 || p.W_in == p.W_out)) return;   // (in place another call may be at such a state)
   const bool last = first + n == all;
   const int chunks = chunks_of(n);
   ring.init(wave, lane);
