@@ -458,10 +458,20 @@ def _io_of(dtype) -> str:
     raise ValueError(f"float32 or bfloat16 expected, got {dtype}")
 
 
+_OPTIONAL = frozenset(("lengths", "dW_out", "weight", "bias", "gate"))
+
+
+def _missing(name):
+    raise ValueError(f"{name} must be a tensor, got None")
+
+
 def _want(device, index, *tensors):
-    """Checks (name, tensor, shape, dtype) entries; a tensor may be None."""
+    """Checks (name, tensor, shape, dtype) entries; the optional ones may be None."""
     for name, t, shape, dtype in tensors:
-        if t is not None and not (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+        if t is None:
+            if name not in _OPTIONAL:
+                _missing(name)
+        elif not (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
             _check(t, name, shape, dtype, device)
 
 
@@ -517,6 +527,8 @@ _delta_plan = functools.lru_cache(maxsize=256)(_DeltaPlan)
 
 def _check_delta(k, v, q, alpha, theta, W_in, lengths, flags=0):
     torch = _torch()
+    if k is None or v is None:
+        _missing("k" if k is None else "v")
     io, f32, index = k.dtype, torch.float32, k.get_device()
     plan = _delta_plan(k.shape, v.shape, io, flags)
     _want(k.device, index, ("v", v, plan.vals, io), ("k", k, plan.keys, io), ("q", q, plan.keys, io),
@@ -599,6 +611,8 @@ _norm_plan = functools.lru_cache(maxsize=256)(_NormPlan)
 
 def _check_norm(x, weight, bias, H, gate, lengths, activation, eps):
     torch = _torch()
+    if x is None:
+        _missing("x")
     f32, index = torch.float32, x.get_device()
     plan = _norm_plan(x.shape, x.dtype, H, activation, eps)
     _want(x.device, index, ("x", x, x.shape, x.dtype), ("weight", weight, plan.channels, f32),
