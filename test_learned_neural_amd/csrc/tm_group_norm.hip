@@ -19,10 +19,10 @@
 // A group lies in L lanes (a power of two), each with IT pieces of VEC
 // consecutive channels in registers, so the sums over a group are log2 L
 // shuffles.  A workgroup keeps one head, so w and b are loaded once, and
-// takes 1/grid.x of the tokens.  The gradient's workgroup sums its tokens'
+// takes 1/grid.x of the tokens (slices_of).  The gradient's workgroup sums its tokens'
 // shares of dw and db in registers and LDS, in a fixed order, into one row of
 // the workspace; a second kernel sums the rows, again in a fixed order (a
-// single row, up to 64 tokens, is the result).
+// single row, of a few tokens, is the result).
 // 8 x 16384 tokens x 1024 channels, bf16, gated: 174 us, 4.6 TB/s (a large copy
 // reaches 5.2); the gradient at 8 x 16384: 278 us, 4.8 TB/s.
 #include "tm_internal.h"
@@ -31,7 +31,6 @@ namespace titans {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxSlices = 256;   // rows of partial sums
 
 struct NormParams {
   const void *x, *gate, *dout;
@@ -293,14 +292,37 @@ hipError_t launch(const NormParams& p, int slices, bool grad, hipStream_t stream
   }
 }
 
-// Workgroups along the tokens: 2048 in all (the device holds about as many;
-// 4096 or 8192 cost the gradient 4% and 9%), none with fewer than 64 tokens.
-int slices_of(const NormShape& s) {
-  const int64_t rows = (int64_t)s.B * s.N;
-  int64_t n = (rows + 63) / 64;
-  const int64_t most = (2048 + s.H - 1) / s.H;
-  if (n > most) n = most;
-  if (n > kMaxSlices) n = kMaxSlices;
+// Groups that a workgroup holds at a time, as launch() lays them out.
+int groups_of(const NormShape& s) {
+  const int vec = s.d % 4 ? 1 : s.io == TM_IO_BF16 && s.d % 8 == 0 ? 8 : 4, held = vec == 1 ? 4 : vec;
+  int lanes = 16 / vec;
+  while (lanes < 64 && lanes * held < s.d) lanes *= 2;
+  return kThreads / lanes;
+}
+
+// Workgroups along the tokens, none with less than 2 rounds of its groups (4
+// in the gradient, whose slices are summed again: 1 x 32 heads x 2048 x 128,
+// bf16, 23.7 us, with 2 26.0).
+//
+// From 8 heads on 2048 in all (the device holds about as many; 4096 or 8192
+// cost the gradient 4% and 9%, 1024 the norm 2% to 25%).  With fewer heads the
+// norm takes 1024 (one head x 65536 x 1024, bf16: 86 us, in 256 workgroups
+// 176, in 4096 79; 2 heads x 65536 x 512, fp32: 164, in 2048 193), the
+// gradient 256 a head (2 heads x 131072 x 64, bf16: 41, in 1024 43 and in 2048
+// 52) and 512 for a single one (one head x 65536 x 1024, bf16: 179, in 256 280
+// and in 1024 194).
+//
+// With thousands of heads one slice a head would do, but its thousands of
+// tokens would be summed one after the other: the gradient's slices have 2048
+// rows at most (4096 heads x 16384 x 16, bf16: 2739 us, in one slice 4358),
+// as far as a launch of fewer than 2^32 threads goes.
+int slices_of(const NormShape& s, bool grad) {
+  const int64_t rows = (int64_t)s.B * s.N, least = (grad ? 4 : 2) * groups_of(s);
+  const int all = s.H >= 8 ? 2048 : !grad ? 1024 : s.H == 1 ? 512 : 256 * s.H;
+  int64_t n = (rows + least - 1) / least;
+  if (n > (all + s.H - 1) / s.H) n = (all + s.H - 1) / s.H;
+  if (grad && n < (rows + 2047) / 2048) n = (rows + 2047) / 2048;
+  if (n > (1 << 23) / s.H) n = (1 << 23) / s.H;
   return n < 1 ? 1 : (int)n;
 }
 
@@ -314,11 +336,11 @@ NormParams params_of(const NormShape& s, int slices) {
 
 }  // namespace
 
-int64_t norm_backward_ws_bytes(const NormShape& s) { return (int64_t)slices_of(s) * 2 * s.H * s.d * 4; }
+int64_t norm_backward_ws_bytes(const NormShape& s) { return (int64_t)slices_of(s, true) * 2 * s.H * s.d * 4; }
 
 hipError_t launch_group_norm(const NormShape& s, const void* x, const void* gate, const float* weight,
                              const float* bias, const int32_t* lengths, void* out, hipStream_t stream) {
-  const int slices = slices_of(s);
+  const int slices = slices_of(s, false);
   NormParams p = params_of(s, slices);
   p.x = x, p.gate = gate, p.weight = weight, p.bias = bias, p.lengths = lengths, p.out = out;
   return s.io == TM_IO_BF16 ? launch<true>(p, slices, false, stream) : launch<false>(p, slices, false, stream);
@@ -327,7 +349,7 @@ hipError_t launch_group_norm(const NormShape& s, const void* x, const void* gate
 hipError_t launch_group_norm_backward(const NormShape& s, const void* x, const void* gate, const float* weight,
                                       const float* bias, const int32_t* lengths, const void* dout, void* dx,
                                       void* dgate, float* dweight, float* dbias, float* ws, hipStream_t stream) {
-  const int slices = slices_of(s), C = s.H * s.d;
+  const int slices = slices_of(s, true), C = s.H * s.d;
   NormParams p = params_of(s, slices);
   p.x = x, p.gate = gate, p.weight = weight, p.bias = bias, p.lengths = lengths, p.dout = dout;
   p.dx = dx, p.dgate = dgate, p.partial = ws, p.dweight = dweight, p.dbias = dbias;
