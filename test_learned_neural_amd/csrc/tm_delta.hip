@@ -15,7 +15,8 @@
 // lanes by DPP.  Nothing is exchanged between waves.  The state is read and
 // written once; for a few tokens that traffic (8 d^2 bytes a stream) is the
 // bound: a step of 192 x 16 heads of 128 x 128 takes 72 us, 5.6 TB/s (a large
-// copy reaches 5.2).  A small call is launch and latency, about 3 us.
+// copy reaches 5.2), and 37 in place with every other slot idle.  A small call is
+// launch and latency, about 3 us.
 #include "tm_internal.h"
 
 namespace titans {

@@ -31,8 +31,11 @@
 //
 // 128 streams x 1024 tokens, d 64, bf16: 75 us for the sweeps (2.3 us a chunk,
 // the chain's and builders' latencies: a third of the cycles issue vector
-// instructions) and 109 us for the pieces (two workgroups a CU, again a third;
-// 247 MB read and 50 MB written, half of a copy's rate).
+// instructions; 86 MB read and 203 MB written) and 110 us for the pieces (two
+// workgroups a CU, again a third; 253 MB read and 52 MB written, half of a
+// copy's rate).  The 594 MB alone would take 115 us at a copy's rate, the
+// inputs and outputs 24: W and its adjoint at every chunk's edges are most of
+// it.
 #include "tm_delta_chunk.h"
 
 namespace titans {
@@ -605,9 +608,13 @@ hipError_t launch_sweep(GradParams p, hipStream_t stream) {
 }
 
 // Four chain waves in a workgroup share the builders' work, two take less time
-// a chunk: four where there are more workgroups of two than CUs (128 streams
-// x 1024, d 64, bf16: 75 us against 87; 32 x 2048, d 128: 192 against 162,
-// and 64 x 1024, d 64, as long either way).
+// a chunk: four where there are more workgroups of two than CUs.  Whole calls
+// with two and with four, in us, 512 tokens of the most streams that take two
+// and of the next that were tried:
+//   bf16  d 64   64: 64 66     96: 81 78      fp32  d 64   64: 100 109   96: 148 134
+//         d 80   32: 70 74     64: 120 102          d 80   32: 121 138   64: 217 181
+//         d 96   32: 72 76     64: 125 106          d 96   32: 119 136   64: 216 183
+//         d 128  32: 94 96     64: 165 147          d 128  32: 151 175   64: 282 241
 template <int DP, bool F32, int VB>
 hipError_t launch_grad(GradParams p, hipStream_t stream) {
   constexpr int kCus = 256, piece = PieceLds<DP, F32>::BYTES;
@@ -623,8 +630,8 @@ hipError_t launch_grad(GradParams p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// (128 streams x 512 x 96: 357 us in fp32 and 210 in bf16, padded to 128 445
-// and 261)
+// (128 streams x 512 x 96: 355 us in fp32 and 201 in bf16, padded to 128 444
+// and 253)
 template <bool F32, int VB>
 hipError_t launch_width(const GradParams& p, hipStream_t stream) {
   if (p.d <= 64) return launch_grad<64, F32, VB>(p, stream);

@@ -17,10 +17,11 @@
 // chunk, so every wait ends.  Nothing but the inputs and outputs
 // touches memory.
 //
-// Measured at 128 streams x 16384 tokens, d 64, bf16: 700 us, 1.37 us a chunk
-// against a serial path of about 250 vector instructions and 50 matrix
-// instructions (2000 cycles of issue, 0.85 us); the inputs and outputs alone
-// would take 210 us at a copy's rate.
+// Measured at 128 streams x 16384 tokens, d 64, bf16: 721 us, 1.41 us a chunk
+// against a serial path of 320 vector and 60 matrix instructions (2250 cycles
+// of issue, 0.94 us); the inputs and outputs alone would take 210 us at a
+// copy's rate.  y from two planes of W, F and P instead of three took 682 us,
+// and was off by 2^-17 of the largest term.
 //
 // Few streams and many chunks: the sequence is cut into segments.  A segment
 // maps the state before it to the one after it by W -> W Phi + W_0; a first
@@ -29,7 +30,7 @@
 // passes the state through them in order (delta_join_kernel), a third runs
 // the segments side by side from their true starts.  That is about 2.4 times
 // the work, for as many times the parallelism as there are segments: 16
-// streams x 65536 tokens take 510 us so and 2740 in one piece.  (Rows whose
+// streams x 65536 tokens take 511 us so and 2810 in one piece.  (Rows whose
 // maps overflow are run in one piece: delta_join_kernel.)
 #include "tm_delta_chunk.h"
 
@@ -380,10 +381,12 @@ hipError_t launch_as(ChainParams p, hipStream_t stream) {
 }
 
 // How a call is cut.  Times of a chunk of 32 tokens in a workgroup that has a
-// CU to itself, in tenths of a microsecond, as measured on 16 to 512 streams:
-// d up to 64 with 2 chain waves 13, with 4 18 (128: 17 and 24; fp32: 20 and
-// 30, 46 and 62), two thirds of that without y (d from 65 to 96 takes a fifth
-// less than 128, whichever way it is cut).
+// CU to itself, in tenths of a microsecond: d up to 64 with 2 chain waves 13,
+// with 4 18 (128: 17 and 24; fp32: 20 and 30, 46 and 62), two thirds of that
+// without y.  They are those of a full device; alone, 16 to 64 streams take 13
+// and 14 to 15 (128: 18 and 25; fp32: 18 to 19 and 25, 44 and 58), and d from
+// 65 to 96 a fifth less than 128, whichever way it is cut (15 to 18 and 22;
+// fp32: 36 and 47), so it is cut as 128 is.
 struct Plan {
   int wide;       // 4 chain waves in a workgroup of the (last) launch
   int segments;   // 1: one launch
@@ -432,8 +435,8 @@ hipError_t launch_chain(const ChainParams& p, bool wide, hipStream_t stream) {
 }
 
 // Widths from 65 to 96 have kernels of their own: 3 of 4 tiles' work, 30
-// streams x 777 x 96, fp32, in 116 us against 137 with rows padded to 128
-// (256 x 1024 x 80, bf16: 150 against 166).
+// streams x 777 x 96, fp32, in 115 us against 136 with rows padded to 128
+// (256 x 1024 x 80, bf16: 163 against 189).
 template <bool F32, int VB>
 hipError_t launch_width(const ChainParams& p, bool wide, hipStream_t stream) {
   if (p.d <= 64) return launch_chain<64, F32, VB>(p, wide, stream);

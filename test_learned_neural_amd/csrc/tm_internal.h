@@ -130,10 +130,14 @@ struct DeltaShape {
 hipError_t launch_delta_recurrent(const DeltaShape& s, const void* k, const void* v, const void* q,
                                   const float* alpha, const float* theta, const int32_t* lengths, const float* W_in,
                                   void* y, float* W_out, hipStream_t stream);
-// Chunks of 32 tokens on the matrix cores, for sequences.  Below 12 tokens
-// the token-by-token kernel is the faster one: of 512 streams, d 64, bf16, 8
-// tokens take it 12 us and 16 tokens 20, a chunk of up to 32 tokens takes 14
-// (256 streams, d 128, fp32: 26 and 43, 32).
+// Chunks of 32 tokens on the matrix cores, for sequences of 12 tokens or more:
+// one border for all.  bf16 alone would change over at 8 to 11 tokens, fp32 at
+// 12 to 15.  11 and 16 tokens one by one against a chunk of up to 32, in us:
+//   bf16  d 64, 512 streams   15  19  15    fp32  d 64, 512 streams   16  21  17
+//         d 64, 2048          61  82  52          d 64, 2048          49  67  63
+//         d 96, 512           40  53  31          d 96, 512           33  44  40
+//         d 128, 128          15  19  11          d 128, 128          13  18  14
+//         d 128, 2048        178 245 138          d 128, 2048        167 225 198
 constexpr int kMinTokensDeltaChunked = 12;
 hipError_t launch_delta_chunked(const DeltaShape& s, const void* k, const void* v, const void* q, const float* alpha,
                                 const float* theta, const int32_t* lengths, const float* W_in, void* y, float* W_out,

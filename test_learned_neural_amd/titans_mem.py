@@ -545,7 +545,8 @@ def delta_forward(k, v, q, alpha, theta, W_in, *, lengths=None, force_recurrent:
     value head h reads key head h // (H // Hk)); alpha, theta: [B, H, N]
     float32; W_in: [B, H, d, d] float32; lengths: [B] int32 or None.  Returns
     (y, W_out).  A new y_out holds zeros past a sequence's length; rows of a
-    y_out that is passed in are left as they were there.
+    y_out that is passed in are left as they were there.  W_out may be W_in: the
+    states of sequences of length 0 are then not written.
     """
     torch = _torch()
     plan, index = _check_delta(k, v, q, alpha, theta, W_in, lengths, FLAG_FORCE_GENERIC if force_recurrent else 0)
