@@ -125,3 +125,27 @@ def test_a_state_without_tokens_is_copied_bit_by_bit(d, io, inplace):
                              W_out=two["W_in"] if inplace else None)
     assert torch.equal(W[1].view(torch.int32), before.view(torch.int32))
     assert torch.isfinite(W[0]).all() and (y[1] == 0).all()
+
+
+def test_replays_with_and_without_growth():
+    """Captured once, over lengths that end inside a segment: maps that overflow in one replay are of use in the next."""
+    import torch
+    from test_learned_neural_amd import titans_mem as tmm
+    names = ("k", "v", "q", "alpha", "theta", "W_in")
+    x = {n: t.cuda() for n, t in problem(48, 40, "bf16", GROWTH).items()}
+    x["W_in"][..., 40:] = 0
+    lengths = torch.tensor([30011], dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    call = lambda: tmm.delta_forward(*(x[n] for n in names), lengths=lengths)
+    call()
+    with torch.cuda.graph(graph):
+        y, W = call()
+    for rep, (alpha, n) in enumerate(((GROWTH, 30011), (0.05, 30011), (GROWTH, N), (GROWTH, 100), (0.05, N))):
+        x["alpha"].fill_(alpha)
+        lengths.fill_(n)
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = tmm.delta_forward(*(x[i] for i in names), lengths=lengths)
+        assert torch.equal(y, want[0]) and torch.equal(W, want[1]), rep
+        assert torch.isfinite(W).all() and torch.isfinite(y).all() and (y[:, :, n:] == 0).all(), rep
