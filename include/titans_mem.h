@@ -491,6 +491,56 @@ int titans_mem_group_norm_backward(const titans_norm_desc* desc, const void* x,
                                    void* workspace, int64_t workspace_bytes,
                                    void* stream);
 
+/*
+ * titans_mem_attention -- causal softmax attention over whole prompts: the
+ * short-term memory that the architectures set beside the neural one (section
+ * 2.1 for the formula, 4.2 "Memory as a Gate" and 4.3 for the sliding window
+ * over persistent tokens and the sequence).  Token i of a sequence sees token
+ * j of it where
+ *
+ *   j <= i  and  (window == 0  or  i - j < window  or  j < prefix)
+ *
+ *   lse_i = log sum_j exp(scale q_i . k_j),  out_i = sum_j exp(scale q_i . k_j - lse_i) v_j
+ *
+ * The first `prefix` tokens of a sequence are the persistent ones.
+ *
+ *   q          [B,H,N,d]   io dtype, device, read-only
+ *   k, v       [B,Hk,N,d]  io dtype, device, read-only; query head h reads
+ *              key head h / (H / Hk)
+ *              with TM_FLAG_CHANNELS_LAST [B,N,H*d] and [B,N,Hk*d]
+ *   offsets    [B+1] int32, device, read-only, or NULL.  With it the tensors
+ *              hold one row of N tokens ([H,N,d]; [N,H*d] with the flag), and
+ *              sequence s is its tokens offsets[s] .. offsets[s+1] - 1, in
+ *              order, clamped to 0..N
+ *   lengths    [B] int32, device, read-only, or NULL (all N; NULL with
+ *              offsets): tokens of each sequence, clamped to 0..N
+ *   out        [B,N,H*d]   ([N,H*d]) io dtype, device, written: channels last
+ *              in either layout, as titans_mem_group_norm reads a gate
+ *   lse        [B,H,N] ([H,N]) fp32, device, written, or NULL
+ *
+ * Tokens of no sequence are not read, and their rows of out and lse are left
+ * as they were.  Sums and the softmax are fp32; for bf16 tensors the weights
+ * are rounded to bf16 before they meet v, and out is rounded once.  A NaN or
+ * infinity in v may reach other queries too that come up to 127 tokens
+ * before it, or that it is out of the window of by up to 127.
+ * d <= 128, scale > 0 (TM_ERR_UNSUPPORTED, TM_ERR_INVALID otherwise).
+ */
+typedef struct {
+    int32_t abi_version;  /* must equal TITANS_MEM_ABI_VERSION */
+    int32_t B, H, Hk;     /* sequences, query heads, key heads (Hk divides H) */
+    int32_t N, d;         /* tokens of a row (N >= 0), width of a head */
+    int32_t io_dtype;     /* TM_IO_F32 or TM_IO_BF16 */
+    int32_t window;       /* 0: all tokens before */
+    int32_t prefix;       /* tokens that every later one sees (>= 0) */
+    float scale;          /* of the scores, 1/sqrt(d) as a rule */
+    uint32_t flags;       /* 0 or TM_FLAG_CHANNELS_LAST */
+} titans_attention_desc;
+
+int titans_mem_attention(const titans_attention_desc* desc, const void* q,
+                         const void* k, const void* v, const int32_t* offsets,
+                         const int32_t* lengths, void* out, float* lse,
+                         void* stream);
+
 /* Static text for a status code. */
 const char* titans_mem_status_string(int status);
 

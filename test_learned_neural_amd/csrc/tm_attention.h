@@ -1,0 +1,335 @@
+// What the attention kernels share: the call's parameters, how a workgroup
+// finds its rows, tiles in LDS and the operands that the matrix cores take
+// from them.
+//
+// Matrix products are 32x32 tiles with a contraction in steps of 16, bf16 in
+// one instruction (v_mfma_f32_32x32x16_bf16) and fp32 in eight
+// (v_mfma_f32_32x32x2_f32).  Either way a lane holds 8 elements of its row (or
+// column) lane % 32 a step, the lower half of the wave the first 8 of a step's
+// 16 and the upper half the others; any order will do that both operands keep.
+// An accumulator has its column in lane % 32 and its rows 8 (r / 4) + 4 (lane /
+// 32) + r % 4 in registers r = 0..15.  So a tile of scores, keys in rows and
+// queries in columns, is by itself the second operand of the product over the
+// keys: registers 8 s .. 8 s + 7 are step s, whose keys are 16 s + 4 (lane /
+// 32) + {0..3, 8..11}, and no lane hands anything to another.
+#pragma once
+
+#include <type_traits>
+
+#include "tm_internal.h"
+
+namespace titans {
+namespace att {
+
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(8))) float f32x8;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((address_space(3))) void* lds_void_ptr;
+typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+typedef __attribute__((ext_vector_type(2))) unsigned u32x2;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -1e30f;   // a running maximum before its first score
+
+struct Params {
+  const void *q, *k, *v, *dout;
+  void *out, *dq, *dk, *dv;
+  float *lse, *delta;
+  const int32_t *offsets, *lengths;
+  // elements from one sequence, head and token to the next (offsets: one row of N tokens, no sequence stride)
+  int64_t q_seq, q_head, q_tok, k_seq, k_head, k_tok, o_seq, o_tok;
+  int B, H, Hk, N, d, window, prefix;
+  float scale;
+  int streams, units;   // key heads by sequences (offsets: key heads), tiles of each
+};
+
+// How rows lie in memory: as whole 16-byte pieces that fill the padded width
+// DP, as whole pieces, or as anything.
+constexpr int kOdd = 0, kPieces = 1, kFull = 2;
+
+template <bool BF16>
+struct Types;
+template <>
+struct Types<true> {
+  typedef __bf16 elem;
+  typedef bf16x8 frag;
+};
+template <>
+struct Types<false> {
+  typedef float elem;
+  typedef f32x8 frag;
+};
+
+__device__ __forceinline__ void mma(f32x16& acc, bf16x8 a, bf16x8 b) {
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x16& acc, f32x8 a, f32x8 b) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], acc, 0, 0, 0);
+}
+
+// registers 8 s .. 8 s + 7 of an accumulator as an operand, rounded to bf16
+// for bf16 tensors: a weight keeps 8 bits, as the values that it multiplies
+__device__ __forceinline__ void operand(const f32x16& x, int s, bf16x8& f) {
+  f32x8 t;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) t[j] = x[8 * s + j];
+  f = __builtin_convertvector(t, bf16x8);
+}
+__device__ __forceinline__ void operand(const f32x16& x, int s, f32x8& f) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = x[8 * s + j];
+}
+
+// the other half wave's value
+__device__ __forceinline__ float other_half(float x) {
+  const unsigned u = __builtin_bit_cast(unsigned, x);
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, (threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// A tile's rows in LDS: LS elements each (the padded width up to the next
+// power of two), 16-byte chunk c of row r at c ^ swz(r).  A row's own chunks
+// are then read by 8 or 16 rows at once from different banks, and so are the
+// 4 rows x 4 chunks of a transposing read.
+template <bool BF16, int DP>
+struct Tile {
+  typedef typename Types<BF16>::elem elem;
+  typedef typename Types<BF16>::frag frag;
+  static constexpr int kSize = BF16 ? 2 : 4;
+  static constexpr int LS = DP == 96 ? 128 : DP;
+  static constexpr int RB = LS * kSize;       // bytes of a row
+  static constexpr int NC = RB / 16;          // its chunks
+  static constexpr int PC = 16 / kSize;       // elements of a chunk
+
+  static __device__ __forceinline__ int swz(int r) {
+    if (NC == 4) return (r >> 1) & 3;
+    if (NC == 8) return (r & 1) << 2 | ((r >> 1) & 3);
+    return (r & 3) << 2 | ((r >> 2) & 3);
+  }
+
+  // step s of row r, contraction along the row
+  static __device__ __forceinline__ frag along(const unsigned char* t, int r, int s, int half) {
+    if constexpr (BF16) {
+      return *(const frag*)(t + r * RB + ((2 * s + half) ^ swz(r)) * 16);
+    } else {
+      const f32x4 a = *(const f32x4*)(t + r * RB + ((4 * s + 2 * half) ^ swz(r)) * 16);
+      const f32x4 b = *(const f32x4*)(t + r * RB + ((4 * s + 2 * half + 1) ^ swz(r)) * 16);
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+
+  // step s of column c0 + lane % 32, contraction over rows r0 + 16 s + .. in an accumulator's order
+  static __device__ __forceinline__ frag across(const unsigned char* t, int r0, int s, int c0, int lane) {
+    const int half = lane >> 5;
+    if constexpr (BF16) {
+      const int l = lane & 15, col = c0 + (lane & 16) + 4 * (l & 3);
+      const int r = r0 + 16 * s + 4 * half + (l >> 2);
+      const unsigned char* p0 = t + r * RB + ((col / 8) ^ swz(r)) * 16 + (l & 1) * 8;
+      const unsigned char* p1 = t + (r + 8) * RB + ((col / 8) ^ swz(r + 8)) * 16 + (l & 1) * 8;
+      const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)p0);
+      const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)p1);
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      frag f;
+      const int col = c0 + (lane & 31);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = r0 + 16 * s + 4 * half + (j & 3) + 8 * (j >> 2);
+        f[j] = *(const float*)(t + r * RB + ((col / 4) ^ swz(r)) * 16 + (col & 3) * 4);
+      }
+      return f;
+    }
+  }
+
+  // Rows j0 .. j0 + ROWS - 1 of a tensor (its rows `tok` elements apart, rows
+  // past `last` as row `last`) into LDS by THREADS threads: wide pieces
+  // straight to LDS, or element by element where rows are not made of 16-byte
+  // pieces.  Columns from d on are zero: cleared once (clear()) where pieces
+  // go straight to LDS, which then leaves them alone.
+  template <int ROWS, int THREADS, int VEC>
+  static __device__ __forceinline__ void load(unsigned char* t, const elem* src, int64_t tok, int j0, int last, int d,
+                                              int tid) {
+    constexpr int kChunks = ROWS * NC;
+    if constexpr (VEC != kOdd) {
+      static_assert(kChunks % THREADS == 0, "");
+      const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+#pragma unroll
+      for (int i = 0; i < kChunks / THREADS; ++i) {
+        const int base = i * THREADS + wave * 64, at = base + lane;
+        const int r = at / NC, c = (at % NC) ^ swz(r);
+        const int j = j0 + r < last ? j0 + r : last;
+        if (VEC == kFull && DP == LS ? true : c * PC < d)
+          __builtin_amdgcn_global_load_lds((const void*)(src + (int64_t)j * tok + c * PC), (lds_void_ptr)(t + base * 16), 16, 0,
+                                           0);
+      }
+    } else {
+      for (int at = tid; at < kChunks; at += THREADS) {
+        const int r = at / NC, c = (at % NC) ^ swz(r);
+        const int j = j0 + r < last ? j0 + r : last;
+        const elem* s = src + (int64_t)j * tok + c * PC;
+        elem x[PC];
+#pragma unroll
+        for (int e = 0; e < PC; ++e) x[e] = c * PC + e < d ? s[e] : (elem)0.f;
+#pragma unroll
+        for (int e = 0; e < PC; ++e) ((elem*)(t + at * 16))[e] = x[e];
+      }
+    }
+  }
+
+  // row j (clamped) of a tensor as an operand's DP / 16 steps, straight from memory
+  template <int VEC>
+  static __device__ __forceinline__ void row(frag (&f)[DP / 16], const elem* src, int d, int half) {
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) {
+      const int c = 16 * s + 8 * half;
+      if (VEC != kOdd) {
+        frag z = {};
+        if constexpr (BF16) {
+          if (VEC == kFull || c < d) z = *(const frag*)(src + c);
+        } else {
+          f32x4 a = {}, b = {};
+          if (VEC == kFull || c < d) a = *(const f32x4*)(src + c);
+          if (VEC == kFull || c + 4 < d) b = *(const f32x4*)(src + c + 4);
+          z = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+        f[s] = z;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[s][e] = c + e < d ? src[c + e] : (elem)0.f;
+      }
+    }
+  }
+
+  // an accumulator's four rows 8 g + 4 half + 0..3 (columns c.. of a row in memory)
+  template <int VEC>
+  static __device__ __forceinline__ void store4(elem* dst, int c, int d, const f32x4 x) {
+    if (VEC != kOdd) {
+      if (VEC != kFull && c >= d) return;
+      if constexpr (BF16)
+        *(bf16x4*)(dst + c) = __builtin_convertvector(x, bf16x4);
+      else
+        *(f32x4*)(dst + c) = x;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < d) dst[c + e] = (elem)x[e];
+    }
+  }
+};
+
+// A barrier behind which every wave's LDS writes are there, the loads straight
+// to LDS among them: a plain barrier does not wait for those.
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+__device__ __forceinline__ void clear(unsigned char* t, int bytes, int tid, int threads) {
+  for (int i = tid * 16; i < bytes; i += threads * 16) *(f32x4*)(t + i) = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+// The tile of rows that unit `unit` of stream `stream` stands for.
+struct Place {
+  int seq, head0, key_head;   // the sequence's row of the tensors, first query head, key head
+  int t0, n, tile;            // its first token, its tokens, the tile
+};
+
+// Sequences packed one behind the other: sequence s has the units from
+// offsets[s] / ROWS + s on, as many as it needs at least, so that a unit's
+// sequence is found by comparing the starts that the lanes hold.  The rest
+// are empty.  Offsets are clamped to what memory holds.
+template <int ROWS>
+__device__ __forceinline__ bool find(const Params& p, int stream, int unit, Place& at) {
+  const int G = p.H / p.Hk;
+  if (p.offsets) {
+    at.key_head = stream;
+    at.seq = 0;
+    int lo = 0, hi = p.B;    // the last sequence in [lo, hi) that starts at or before the unit
+    const int lane = threadIdx.x & 63;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 63) / 64, s = lo + lane * step;
+      bool before = false;
+      if (s < hi) {
+        const int o = min(max(p.offsets[s], 0), p.N);
+        before = o / ROWS + s <= unit;
+      }
+      const int c = max(__popcll(__ballot(before)), 1);
+      lo += (c - 1) * step;
+      hi = min(hi, lo + step);
+    }
+    const int a = min(max(p.offsets[lo], 0), p.N);
+    at.t0 = __builtin_amdgcn_readfirstlane(a);
+    at.n = __builtin_amdgcn_readfirstlane(min(max(p.offsets[lo + 1], a), p.N)) - at.t0;
+    unit -= at.t0 / ROWS + __builtin_amdgcn_readfirstlane(lo);
+  } else {
+    at.key_head = stream % p.Hk;
+    at.seq = stream / p.Hk;
+    at.t0 = 0;
+    at.n = p.N;
+    if (p.lengths) at.n = __builtin_amdgcn_readfirstlane(min(max(p.lengths[at.seq], 0), p.N));
+  }
+  at.head0 = at.key_head * G;
+  const int tiles = (at.n + ROWS - 1) / ROWS;
+  at.tile = unit;
+  return unit >= 0 && unit < tiles;
+}
+
+// Block -> (stream, unit, head of the group).  Blocks go round the 8 XCDs.
+// With streams in eights every XCD takes whole streams, one after the other,
+// so that their keys stay in its L2; otherwise units go round the XCDs.  The
+// heads that share keys are neighbours on one XCD in both.
+__device__ __forceinline__ bool place_of(const Params& p, int heads, int& stream, int& unit, int& head) {
+  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  head = slot % heads;
+  const int u = slot / heads;
+  if (p.streams % 8 == 0) {
+    stream = xcd + 8 * (u / p.units);
+    unit = u % p.units;
+    return true;
+  }
+  const int64_t v = (int64_t)u * 8 + xcd;
+  stream = (int)(v % p.streams);
+  unit = (int)(v / p.streams);
+  return unit < p.units;
+}
+
+// Scores that the mask takes away, registers of one 32 x 32 tile.  j0: the
+// key of register 0 in this lane; i: the query (KEYS_IN_ROWS; otherwise j0 and i change places).
+template <bool KEYS_IN_ROWS>
+__device__ __forceinline__ void mask_tile(f32x16& x, int row0, int col, int window, int prefix) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int row = row0 + 8 * (r >> 2) + (r & 3);
+    const int i = KEYS_IN_ROWS ? col : row, j = KEYS_IN_ROWS ? row : col;
+    const bool seen = (j <= i) & ((i - j < window) | (j < prefix));
+    x[r] = seen ? x[r] : -__builtin_inff();
+  }
+}
+
+// DP and the rows' kind for a width, f(integral constants BF16, DP, VEC)
+template <bool BF16, int DP, typename F>
+hipError_t by_rows(int d, F f) {
+  typedef std::integral_constant<bool, BF16> B;
+  typedef std::integral_constant<int, DP> W;
+  if constexpr (DP != 96)
+    if (d == DP) return f(B(), W(), std::integral_constant<int, kFull>());
+  return d % (BF16 ? 8 : 4) == 0 ? f(B(), W(), std::integral_constant<int, kPieces>())
+                                 : f(B(), W(), std::integral_constant<int, kOdd>());
+}
+template <bool BF16, typename F>
+hipError_t by_width(int d, F f) {
+  return d <= 32   ? by_rows<BF16, 32>(d, f)
+         : d <= 64 ? by_rows<BF16, 64>(d, f)
+         : d <= 96 ? by_rows<BF16, 96>(d, f)
+                   : by_rows<BF16, 128>(d, f);
+}
+template <typename F>
+hipError_t by_type(int io, int d, F f) {
+  return io == TM_IO_BF16 ? by_width<true>(d, f) : by_width<false>(d, f);
+}
+
+}  // namespace att
+}  // namespace titans

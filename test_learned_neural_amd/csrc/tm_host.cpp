@@ -355,6 +355,7 @@ int titans_mem_input(const titans_input_desc* desc, const void* x, const void* w
 
 namespace {
 
+using titans::AttentionShape;
 using titans::DeltaShape;
 using titans::NormShape;
 
@@ -383,6 +384,29 @@ int build_norm(const titans_norm_desc* desc, NormShape* s) {
   if ((double)desc->B * desc->H * desc->N * desc->d > kMostElements) return TM_ERR_UNSUPPORTED;
   *s = {desc->B, desc->H, desc->N, desc->d, desc->io_dtype, desc->activation == TM_ACT_SILU,
         !(desc->flags & TM_FLAG_CHANNELS_LAST), desc->eps};
+  return TM_OK;
+}
+
+struct AttentionBytes {
+  int64_t q, k, lse;   // of q and out, of k and v, of lse
+};
+
+int build_attention(const titans_attention_desc* desc, const int32_t* offsets, AttentionShape* s, AttentionBytes* n) {
+  if (!desc || desc->abi_version != TITANS_MEM_ABI_VERSION) return TM_ERR_INVALID;
+  if (desc->B <= 0 || desc->H <= 0 || desc->Hk <= 0 || desc->H % desc->Hk || desc->N < 0 || desc->d <= 0)
+    return TM_ERR_INVALID;
+  if (desc->io_dtype != TM_IO_F32 && desc->io_dtype != TM_IO_BF16) return TM_ERR_INVALID;
+  if (desc->window < 0 || desc->prefix < 0 || !(desc->scale > 0.f) || desc->scale > 3.0e38f) return TM_ERR_INVALID;
+  if (desc->flags & ~TM_FLAG_CHANNELS_LAST) return TM_ERR_INVALID;
+  if (desc->d > titans::kMaxWidthAttention) return TM_ERR_UNSUPPORTED;
+  const int64_t rows = (offsets ? 1 : (int64_t)desc->B) * desc->N;
+  if ((double)rows * desc->H * desc->d > kMostElements) return TM_ERR_UNSUPPORTED;
+  *s = {desc->B, desc->H, desc->Hk, desc->N, desc->d, desc->io_dtype,
+        desc->window < desc->N ? desc->window : 0, desc->prefix < desc->N ? desc->prefix : desc->N,
+        offsets != nullptr, (desc->flags & TM_FLAG_CHANNELS_LAST) != 0, desc->scale};
+  if (!titans::attention_supported(*s)) return TM_ERR_UNSUPPORTED;
+  const int64_t esz = s->io == TM_IO_BF16 ? 2 : 4;
+  *n = {rows * s->H * s->d * esz, rows * s->Hk * s->d * esz, rows * s->H * 4};
   return TM_OK;
 }
 
@@ -546,6 +570,24 @@ int titans_mem_group_norm_backward(const titans_norm_desc* desc, const void* x, 
                                             (float*)workspace, (hipStream_t)stream) == hipSuccess
              ? TM_OK
              : TM_ERR_HIP;
+}
+
+int titans_mem_attention(const titans_attention_desc* desc, const void* q, const void* k, const void* v,
+                         const int32_t* offsets, const int32_t* lengths, void* out, float* lse, void* stream) {
+  AttentionShape s;
+  AttentionBytes n;
+  int rc = build_attention(desc, offsets, &s, &n);
+  if (rc) return rc;
+  if (!needed(q, n.q) || !needed(k, n.k) || !needed(v, n.k) || !needed(out, n.q) || !aligned16(lse) ||
+      !aligned16(offsets) || !aligned16(lengths) || (offsets && lengths))
+    return TM_ERR_INVALID;
+  const Range r[] = {{(const char*)q, n.q, false},       {(const char*)k, n.k, false},
+                     {(const char*)v, n.k, false},       {(const char*)offsets, ((int64_t)s.B + 1) * 4, false},
+                     {(const char*)lengths, (int64_t)s.B * 4, false}, {(const char*)out, n.q, true},
+                     {(const char*)lse, n.lse, true}};
+  if (!disjoint(r, 7)) return TM_ERR_ALIAS;
+  return titans::launch_attention(s, q, k, v, offsets, lengths, out, lse, (hipStream_t)stream) == hipSuccess ? TM_OK
+                                                                                                            : TM_ERR_HIP;
 }
 
 const char* titans_mem_status_string(int status) {

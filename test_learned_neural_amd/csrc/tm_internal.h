@@ -168,4 +168,18 @@ hipError_t launch_group_norm_backward(const NormShape& s, const void* x, const v
                                       const float* bias, const int32_t* lengths, const void* dout, void* dx,
                                       void* dgate, float* dweight, float* dbias, float* ws, hipStream_t stream);
 
+// Causal attention over prompts, its gradient, and single tokens over a cache.
+// packed: one row of N tokens, cut by offsets (then B sequences); last: heads
+// behind tokens.  window is 0 or less than N, prefix at most N.
+constexpr int kMaxWidthAttention = 128;
+constexpr int64_t kMostBlocks = 1 << 24;   // of 256 threads: a launch stays under 2^32
+struct AttentionShape {
+  int B, H, Hk, N, d, io, window, prefix, packed, last;
+  float scale;
+};
+bool attention_supported(const AttentionShape& s);
+hipError_t launch_attention(const AttentionShape& s, const void* q, const void* k, const void* v,
+                            const int32_t* offsets, const int32_t* lengths, void* out, float* lse,
+                            hipStream_t stream);
+
 }  // namespace titans

@@ -34,7 +34,7 @@ EXPORTS = ("titans_mem_abi_version", "titans_mem_param_count", "titans_mem_selec
            "titans_mem_delta_select_path", "titans_mem_delta_workspace_bytes", "titans_mem_delta_forward",
            "titans_mem_delta_backward", "titans_mem_delta_backward_workspace_bytes",
            "titans_mem_group_norm", "titans_mem_group_norm_backward",
-           "titans_mem_group_norm_backward_workspace_bytes", "titans_mem_status_string")
+           "titans_mem_group_norm_backward_workspace_bytes", "titans_mem_attention", "titans_mem_status_string")
 
 
 class Desc(ctypes.Structure):
@@ -61,6 +61,19 @@ class NormDesc(ctypes.Structure):
     _fields_ = [("abi_version", ctypes.c_int32), ("B", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("N", ctypes.c_int32), ("d", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
                 ("activation", ctypes.c_int32), ("eps", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class AttentionDesc(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("B", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("window", ctypes.c_int32), ("prefix", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+def make_attention_desc(B: int, H: int, Hk: int, N: int, d: int, io: str = "bf16", window: int = 0, prefix: int = 0,
+                        scale: Optional[float] = None, flags: int = 0) -> AttentionDesc:
+    return AttentionDesc(ABI_VERSION, B, H, Hk, N, d, IO_BF16 if io == "bf16" else IO_F32, window, prefix,
+                         max(d, 1) ** -0.5 if scale is None else scale, flags)
 
 
 def make_delta_desc(B: int, H: int, Hk: int, N: int, d: int, io: str = "bf16", flags: int = 0) -> DeltaDesc:
@@ -147,6 +160,9 @@ def load():
     lib.titans_mem_group_norm.argtypes = [nq, vp, vp, fp, fp, vp, vp, vp]
     lib.titans_mem_group_norm_backward_workspace_bytes.restype = i64
     lib.titans_mem_group_norm_backward_workspace_bytes.argtypes = [nq]
+    aq = ctypes.POINTER(AttentionDesc)
+    lib.titans_mem_attention.restype = ctypes.c_int
+    lib.titans_mem_attention.argtypes = [aq, vp, vp, vp, vp, vp, vp, fp, vp]
     lib.titans_mem_group_norm_backward.restype = ctypes.c_int
     lib.titans_mem_group_norm_backward.argtypes = [nq, vp, vp, fp, fp, vp, vp, vp, vp, fp, fp, vp, i64, vp]
     lib.titans_mem_status_string.restype = ctypes.c_char_p
@@ -238,6 +254,11 @@ def raw_delta_backward(desc: DeltaDesc, k, v, q, alpha, theta, lengths, W_in, dy
     """Direct call of titans_mem_delta_backward with integer device addresses; returns the status."""
     return load().titans_mem_delta_backward(ctypes.byref(desc), k, v, q, alpha, theta, lengths, W_in, dy, dW_out, dk,
                                             dv, dq, dalpha, dtheta, dW_in, workspace, workspace_bytes_, stream)
+
+
+def raw_attention(desc: AttentionDesc, q, k, v, offsets, lengths, out, lse, stream) -> int:
+    """Direct call of titans_mem_attention with integer device addresses; returns the status."""
+    return load().titans_mem_attention(ctypes.byref(desc), q, k, v, offsets, lengths, out, lse, stream)
 
 
 def raw_group_norm(desc: NormDesc, x, gate, weight, bias, lengths, out, stream) -> int:
@@ -458,7 +479,7 @@ def _io_of(dtype) -> str:
     raise ValueError(f"float32 or bfloat16 expected, got {dtype}")
 
 
-_OPTIONAL = frozenset(("lengths", "dW_out", "weight", "bias", "gate"))
+_OPTIONAL = frozenset(("lengths", "dW_out", "weight", "bias", "gate", "offsets"))
 
 
 def _missing(name):
@@ -663,3 +684,71 @@ def group_norm_backward(x, weight, bias, dout, *, H: Optional[int] = None, gate=
                _ptr(gate), _ptr(weight), _ptr(bias), _ptr(lengths), dout.data_ptr(), g["x"].data_ptr(),
                _ptr(g.get("gate")), g["weight"].data_ptr(), g["bias"].data_ptr(), _ptr(ws), ws_bytes)
     return g
+
+
+class _AttentionPlan:
+    """What a call's shapes, type and options fix."""
+
+    def __init__(self, queries, keys, dtype, sequences, window, prefix, scale):
+        if sequences is not None:
+            if len(queries) != 3 or len(keys) != 3:
+                raise ValueError("with offsets q must be [N, H, d], k and v [N, Hk, d]")
+            (N, H, d), Hk, B, flags = queries, keys[1], sequences, FLAG_CHANNELS_LAST
+            self.keys, self.out, self.lse = (N, Hk, d), (N, H * d), (H, N)
+        else:
+            if len(queries) != 4 or len(keys) != 4:
+                raise ValueError("q must be [B, H, N, d], k and v [B, Hk, N, d] (or three dimensions, and offsets)")
+            (B, H, N, d), Hk, flags = queries, keys[1], 0
+            self.keys, self.out, self.lse = (B, Hk, N, d), (B, N, H * d), (B, H, N)
+        window, prefix = min(window, (1 << 31) - 1), min(prefix, (1 << 31) - 1)
+        _fits(B + 1, H, Hk, N, d)
+        self.batch, self.cuts = (B,), (B + 1,)
+        self.desc = make_attention_desc(B, H, Hk, N, d, _io_of(dtype), window, prefix, scale, flags)
+        self.ref = ctypes.byref(self.desc)
+
+
+_attention_plan = functools.lru_cache(maxsize=256)(_AttentionPlan)
+
+
+def _check_attention(q, k, v, offsets, lengths, window, prefix, scale):
+    torch = _torch()
+    for name, t in (("q", q), ("k", k)):
+        if t is None:
+            _missing(name)
+    if offsets is not None and (lengths is not None or offsets.dim() != 1 or offsets.shape[0] < 2):
+        raise ValueError("offsets must be [sequences + 1], and come without lengths")
+    io, index = q.dtype, q.get_device()
+    plan = _attention_plan(q.shape, k.shape, io, None if offsets is None else offsets.shape[0] - 1, window, prefix, scale)
+    _want(q.device, index, ("q", q, q.shape, io), ("k", k, plan.keys, io), ("v", v, plan.keys, io),
+          ("offsets", offsets, plan.cuts, torch.int32), ("lengths", lengths, plan.batch, torch.int32))
+    return plan, index
+
+
+def attention(q, k, v, *, offsets=None, lengths=None, window: int = 0, prefix: int = 0, scale: Optional[float] = None,
+              out=None, lse_out=None) -> Tuple:
+    """Causal attention over whole prompts (titans_mem_attention).
+
+    q: [B, H, N, d], k, v: [B, Hk, N, d] (float32 or bfloat16, Hk divides H:
+    query head h reads key head h // (H // Hk)) with lengths [B] int32 or None;
+    or sequences one behind the other, q: [N, H, d], k, v: [N, Hk, d] with
+    offsets [sequences + 1] int32.  Token i sees token j <= i of its sequence
+    where window is 0, i - j < window or j < prefix.  scale is 1/sqrt(d) by
+    default.  Returns (out, lse): [B, N, H*d] in q's type and [B, H, N]
+    float32, or [N, H*d] and [H, N].  New ones hold zeros for tokens of no
+    sequence; such rows of an out or lse_out that is passed in are left as they
+    were.
+    """
+    torch = _torch()
+    plan, index = _check_attention(q, k, v, offsets, lengths, window, prefix, scale)
+    new = torch.empty if offsets is None and lengths is None else torch.zeros
+    if out is None:
+        out = new(plan.out, dtype=q.dtype, device=q.device)
+    else:
+        _want(q.device, index, ("out", out, plan.out, q.dtype))
+    if lse_out is None:
+        lse_out = new(plan.lse, dtype=torch.float32, device=q.device)
+    else:
+        _want(q.device, index, ("lse_out", lse_out, plan.lse, torch.float32))
+    _on_device(index, "titans_mem_attention", load().titans_mem_attention, plan.ref, q.data_ptr(), k.data_ptr(),
+               v.data_ptr(), _ptr(offsets), _ptr(lengths), out.data_ptr(), lse_out.data_ptr())
+    return out, lse_out
