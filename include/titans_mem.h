@@ -541,6 +541,32 @@ int titans_mem_attention(const titans_attention_desc* desc, const void* q,
                          const int32_t* lengths, void* out, float* lse,
                          void* stream);
 
+/*
+ * titans_mem_attention_backward -- gradients through titans_mem_attention:
+ * the vector-Jacobian products with
+ *   out, lse         what the forward call wrote, device, read-only
+ *   dout             out's layout, io dtype, device, read-only: dL/dout
+ * into
+ *   dq, dk, dv       the layouts of q, k and v, io dtype, device, written; dk
+ *                    and dv are sums over the query heads of a key head
+ * Same inputs as the forward call.  Tokens of no sequence get zero gradients.
+ * Sums are fp32 and in a fixed order; for bf16 tensors the weights and their
+ * derivatives are rounded to bf16 before they meet q, k and dout, and results
+ * once.  A NaN or infinity in q, k, v or dout may reach the gradients of the
+ * 255 tokens before it and behind it too.  Any overlap of a written buffer is
+ * TM_ERR_ALIAS.
+ * packed: whether the call has offsets.
+ */
+int64_t titans_mem_attention_backward_workspace_bytes(const titans_attention_desc* desc, int32_t packed);
+
+int titans_mem_attention_backward(const titans_attention_desc* desc,
+                                  const void* q, const void* k, const void* v,
+                                  const int32_t* offsets, const int32_t* lengths,
+                                  const void* out, const float* lse, const void* dout,
+                                  void* dq, void* dk, void* dv,
+                                  void* workspace, int64_t workspace_bytes,
+                                  void* stream);
+
 /* Static text for a status code. */
 const char* titans_mem_status_string(int status);
 

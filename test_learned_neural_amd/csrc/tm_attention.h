@@ -39,7 +39,8 @@ constexpr float kLowest = -1e30f;   // a running maximum before its first score
 struct Params {
   const void *q, *k, *v, *dout;
   void *out, *dq, *dk, *dv;
-  float *lse, *delta;
+  float *lse, *stats;       // stats: the gradient's two fp32 values a query and head, stat_rows apart
+  int64_t stat_rows;
   const int32_t *offsets, *lengths;
   // elements from one sequence, head and token to the next (offsets: one row of N tokens, no sequence stride)
   int64_t q_seq, q_head, q_tok, k_seq, k_head, k_tok, o_seq, o_tok;
@@ -332,4 +333,9 @@ hipError_t by_type(int io, int d, F f) {
 }
 
 }  // namespace att
+
+att::Params attention_params(const AttentionShape& s);
+int64_t attention_units(const AttentionShape& s, int rows);
+int64_t attention_blocks(const AttentionShape& s, int rows, int heads);
+
 }  // namespace titans

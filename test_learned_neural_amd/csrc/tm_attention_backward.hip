@@ -1,0 +1,312 @@
+// Gradient of the causal attention (tm_attention.hip has the forward pass and
+// the mask).  With P_ij = exp(scale q_i . k_j - lse_i) where j is seen:
+//
+//   D_i = dout_i . out_i,  dS_ij = P_ij (dout_i . v_j - D_i)
+//   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
+//
+// dk_j and dv_j are sums over the query heads that share the key head, too.
+//
+// Two kernels, so that every sum stays in one workgroup's registers, in a
+// fixed order, with no atomics: one owns queries and runs over keys (D, dq),
+// the other owns keys and runs over queries and heads (dk, dv).  Scores and
+// dout . v are formed in both: seven products a tile instead of five, against
+// an fp32 copy of dq in memory and an order of its sums that changes from call
+// to call.
+//
+// Either kernel forms its scores so that what it owns lies in the lanes, and
+// what it sums over in the registers, where P and dS are operands as they lie
+// (tm_attention.h).  P and dS are rounded to bf16 there for bf16 tensors.
+#include <limits.h>
+
+#include "tm_attention.h"
+
+namespace titans {
+namespace {
+
+using namespace att;
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;     // queries, or keys, of a workgroup
+
+// rows of a tile in LDS
+template <bool BF16, int DP>
+constexpr int tile_of() { return BF16 ? 64 : 32; }
+
+// Packed rows before the first sequence and behind the last: the gradient is
+// zero.  Workgroup `unit` has rows unit * kRows .. of one head.
+template <typename elem>
+__device__ __forceinline__ void zero_rows(const Params& p, int unit, elem* a, elem* b, int64_t tok) {
+  const int first = min(max(p.offsets[0], 0), p.N), end = min(max(p.offsets[p.B], 0), p.N);
+  const int64_t r0 = (int64_t)unit * kRows;
+  if (r0 >= first && r0 + kRows <= end) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int i = wave; i < kRows; i += kWaves) {
+    const int64_t r = r0 + i;
+    if (r >= p.N || (r >= first && r < end)) continue;
+    for (int c = lane; c < p.d; c += 64) {
+      a[r * tok + c] = (elem)0.f;
+      if (b) b[r * tok + c] = (elem)0.f;
+    }
+  }
+}
+
+// Padded rows past a sequence's length.
+template <typename elem>
+__device__ __forceinline__ void zero_past(const Params& p, int row0, int n, elem* a, elem* b, int64_t tok) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int r = max(row0, n) + wave; r < min(row0 + kRows, p.N); r += kWaves)
+    for (int c = lane; c < p.d; c += 64) {
+      a[(int64_t)r * tok + c] = (elem)0.f;
+      if (b) b[(int64_t)r * tok + c] = (elem)0.f;
+    }
+}
+
+// dq, and per query lse log2 e and D for the other kernel.
+template <bool BF16, int DP, int VEC>
+__global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_dq_kernel(Params p) {
+  typedef Tile<BF16, DP> T;
+  typedef typename T::elem elem;
+  typedef typename T::frag frag;
+  constexpr int KT = tile_of<BF16, DP>(), kBytes = KT * T::RB;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2][K, V]
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int stream, unit, head;
+  if (!place_of(p, p.H / p.Hk, stream, unit, head)) return;
+  Place at;
+  const bool found = find<kRows>(p, stream, unit, at);
+  const int h = at.head0 + head;
+  if (p.offsets) zero_rows(p, unit, (elem*)p.dq + h * p.q_head, (elem*)nullptr, p.q_tok);
+  // units of a padded row count tiles from its end; those past the length are all padding
+  const int tiles = (at.n + kRows - 1) / kRows, tile = found ? tiles - 1 - at.tile : at.tile;
+  elem* dq = (elem*)p.dq + at.seq * p.q_seq + h * p.q_head + (int64_t)at.t0 * p.q_tok;
+  if (p.lengths) zero_past(p, tile * kRows, at.n, dq, (elem*)nullptr, p.q_tok);
+  if (!found) return;
+  const int i0 = tile * kRows, w0 = i0 + 32 * wave, qi = w0 + (lane & 31), last = at.n - 1;
+  const int64_t qt = at.t0 + min(qi, last), kv = at.seq * p.k_seq + at.key_head * p.k_head + (int64_t)at.t0 * p.k_tok;
+  const elem* kp = (const elem*)p.k + kv;
+  const elem* vp = (const elem*)p.v + kv;
+
+  const int top = min(i0 + kRows - 1, last) / KT;
+  const int lo = p.window ? max(0, i0 - p.window + 1) / KT : 0;
+  const int pre = min((p.prefix + KT - 1) / KT, lo);
+  int t = pre > 0 ? 0 : lo;
+  if (VEC == kPieces && p.d < DP) {
+    clear(smem, 4 * kBytes, tid, kThreads);
+    __syncthreads();
+  }
+  T::template load<KT, kThreads, VEC>(smem, kp, p.k_tok, t * KT, last, p.d, tid);
+  T::template load<KT, kThreads, VEC>(smem + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
+
+  frag q[DP / 16], go[DP / 16];
+  T::template row<VEC>(q, (const elem*)p.q + at.seq * p.q_seq + h * p.q_head + qt * p.q_tok, p.d, half);
+  const int64_t ot = at.seq * p.o_seq + qt * p.o_tok + h * p.d, stat = ((int64_t)at.seq * p.H + h) * p.N + qt;
+  T::template row<VEC>(go, (const elem*)p.dout + ot, p.d, half);
+  float D = 0.f;
+  {
+    frag o[DP / 16];
+    T::template row<VEC>(o, (const elem*)p.out + ot, p.d, half);
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) D = fmaf((float)go[s][e], (float)o[s][e], D);
+  }
+  D += other_half(D);
+  const float lse = p.lse[stat] * kLog2e;
+  if (half == 0 && qi <= last) {
+    p.stats[stat] = lse;
+    p.stats[p.stat_rows + stat] = D;
+  }
+
+  const int window = p.window ? p.window : INT_MAX;
+  const float c = p.scale * kLog2e;
+  f32x16 acc[DP / 32] = {};
+  for (int buf = 0; t <= top; buf ^= 1) {
+    const int k0 = t * KT;
+    t = t + 1 == pre ? lo : t + 1;
+    landed();
+    unsigned char* kb = smem + buf * 2 * kBytes;
+    unsigned char* vb = kb + kBytes;
+    if (t <= top) {
+      unsigned char* nb = smem + (buf ^ 1) * 2 * kBytes;
+      T::template load<KT, kThreads, VEC>(nb, kp, p.k_tok, t * KT, last, p.d, tid);
+      T::template load<KT, kThreads, VEC>(nb + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
+    }
+#pragma unroll
+    for (int g = 0; g < KT / 32; ++g) {
+      const int g0 = k0 + 32 * g;
+      if (w0 > last || g0 > w0 + 31 || (w0 - (g0 + 31) >= window && g0 >= p.prefix)) continue;
+      f32x16 x = {}, y = {};
+#pragma unroll
+      for (int s = 0; s < DP / 16; ++s) {
+        mma(x, T::along(kb, 32 * g + (lane & 31), s, half), q[s]);
+        mma(y, T::along(vb, 32 * g + (lane & 31), s, half), go[s]);
+      }
+      if (g0 + 31 > w0 || w0 + 31 - g0 >= window) mask_tile<true>(x, g0 + 4 * half, qi, window, p.prefix);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse)) * (y[r] - D);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        frag w;
+        operand(x, s, w);
+#pragma unroll
+        for (int e = 0; e < DP / 32; ++e) mma(acc[e], T::across(kb, 32 * g, s, 32 * e, lane), w);
+      }
+    }
+  }
+  if (qi > last) return;
+  dq += (int64_t)qi * p.q_tok;
+#pragma unroll
+  for (int e = 0; e < DP / 32; ++e)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      T::template store4<VEC>(dq, 32 * e + 8 * g + 4 * half, p.d,
+                              f32x4{acc[e][4 * g], acc[e][4 * g + 1], acc[e][4 * g + 2], acc[e][4 * g + 3]} * p.scale);
+}
+
+// dk and dv of one key head.
+template <bool BF16, int DP, int VEC>
+__global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_dkv_kernel(Params p) {
+  typedef Tile<BF16, DP> T;
+  typedef typename T::elem elem;
+  typedef typename T::frag frag;
+  constexpr int QT = tile_of<BF16, DP>(), kBytes = QT * T::RB, kStage = 2 * kBytes + 2 * 64 * 4;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2][Q, dout, lse[64], D[64]]
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int stream, unit, head;
+  if (!place_of(p, 1, stream, unit, head)) return;
+  Place at;
+  const bool found = find<kRows>(p, stream, unit, at);
+  if (p.offsets) zero_rows(p, unit, (elem*)p.dk + at.key_head * p.k_head, (elem*)p.dv + at.key_head * p.k_head, p.k_tok);
+  const int64_t kv = at.seq * p.k_seq + at.key_head * p.k_head + (int64_t)at.t0 * p.k_tok;
+  elem* dk = (elem*)p.dk + kv;
+  elem* dv = (elem*)p.dv + kv;
+  if (p.lengths) zero_past(p, at.tile * kRows, at.n, dk, dv, p.k_tok);
+  if (!found) return;
+  const int j0 = at.tile * kRows, w0 = j0 + 32 * wave, kj = w0 + (lane & 31), last = at.n - 1, G = p.H / p.Hk;
+  const int window = p.window ? p.window : INT_MAX;
+
+  // tiles of queries: from the workgroup's first key to the last query in reach of its last one
+  const int lo = j0 / QT;
+  const int end = p.window && j0 >= p.prefix ? (int)min((int64_t)last, (int64_t)j0 + kRows - 1 + p.window - 1) : last;
+  const int per = end / QT - lo + 1, all = per * G;
+  if (VEC == kPieces && p.d < DP) {
+    clear(smem, 2 * kStage, tid, kThreads);
+    __syncthreads();
+  }
+  // tile number n of all: head n / per, query tile lo + n % per
+  int lh = 0, lt = lo;
+  auto issue = [&](int buf) {
+    const int h = at.head0 + lh;
+    unsigned char* b = smem + buf * kStage;
+    const elem* qp = (const elem*)p.q + at.seq * p.q_seq + h * p.q_head + (int64_t)at.t0 * p.q_tok;
+    const elem* op = (const elem*)p.dout + at.seq * p.o_seq + (int64_t)at.t0 * p.o_tok + h * p.d;
+    T::template load<QT, kThreads, VEC>(b, qp, p.q_tok, lt * QT, last, p.d, tid);
+    T::template load<QT, kThreads, VEC>(b + kBytes, op, p.o_tok, lt * QT, last, p.d, tid);
+    if (wave < 2) {   // 64 rows of lse, of D (QT of them are used)
+      const float* st = p.stats + (wave ? p.stat_rows : 0) + ((int64_t)at.seq * p.H + h) * p.N + at.t0;
+      __builtin_amdgcn_global_load_lds((const void*)(st + min(lt * QT + lane, last)),
+                                       (lds_void_ptr)(b + 2 * kBytes + wave * 256), 4, 0, 0);
+    }
+    if (++lt == lo + per) lt = lo, ++lh;
+  };
+  issue(0);
+  frag k[DP / 16], v[DP / 16];
+  T::template row<VEC>(k, (const elem*)p.k + kv + (int64_t)min(kj, last) * p.k_tok, p.d, half);
+  T::template row<VEC>(v, (const elem*)p.v + kv + (int64_t)min(kj, last) * p.k_tok, p.d, half);
+
+  const float c = p.scale * kLog2e;
+  f32x16 ak[DP / 32] = {}, av[DP / 32] = {};
+  int qt = lo;
+  for (int n = 0; n < all; ++n) {
+    const int q0 = qt * QT;
+    if (++qt == lo + per) qt = lo;
+    landed();
+    unsigned char* qb = smem + (n & 1) * kStage;
+    unsigned char* ob = qb + kBytes;
+    const float* ls = (const float*)(qb + 2 * kBytes);
+    if (n + 1 < all) issue((n + 1) & 1);
+#pragma unroll
+    for (int g = 0; g < QT / 32; ++g) {
+      const int g0 = q0 + 32 * g;
+      if (w0 > last || g0 > last || g0 + 31 < w0 || (g0 - (w0 + 31) >= window && w0 >= p.prefix)) continue;
+      f32x16 x = {}, y = {};
+#pragma unroll
+      for (int s = 0; s < DP / 16; ++s) {
+        mma(x, T::along(qb, 32 * g + (lane & 31), s, half), k[s]);
+        mma(y, T::along(ob, 32 * g + (lane & 31), s, half), v[s]);
+      }
+      if (g0 < w0 + 31 || g0 + 31 > last || g0 + 31 - w0 >= window) {
+        mask_tile<false>(x, g0 + 4 * half, kj, window, p.prefix);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          x[r] = g0 + 4 * half + 8 * (r >> 2) + (r & 3) <= last ? x[r] : -__builtin_inff();
+      }
+      f32x16 ds;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const f32x4 l4 = *(const f32x4*)(ls + 32 * g + 8 * u + 4 * half), d4 = *(const f32x4*)(ls + 64 + 32 * g + 8 * u + 4 * half);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 4 * u + e;
+          x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -l4[e]));
+          ds[r] = x[r] * (y[r] - d4[e]);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        frag w, z;
+        operand(x, s, w);
+        operand(ds, s, z);
+#pragma unroll
+        for (int e = 0; e < DP / 32; ++e) {
+          mma(av[e], T::across(ob, 32 * g, s, 32 * e, lane), w);
+          mma(ak[e], T::across(qb, 32 * g, s, 32 * e, lane), z);
+        }
+      }
+    }
+  }
+  if (kj > last) return;
+  dk += (int64_t)kj * p.k_tok;
+  dv += (int64_t)kj * p.k_tok;
+#pragma unroll
+  for (int e = 0; e < DP / 32; ++e)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int ch = 32 * e + 8 * g + 4 * half;
+      T::template store4<VEC>(dk, ch, p.d, f32x4{ak[e][4 * g], ak[e][4 * g + 1], ak[e][4 * g + 2], ak[e][4 * g + 3]} * p.scale);
+      T::template store4<VEC>(dv, ch, p.d, f32x4{av[e][4 * g], av[e][4 * g + 1], av[e][4 * g + 2], av[e][4 * g + 3]});
+    }
+}
+
+}  // namespace
+
+int64_t attention_backward_ws_bytes(const AttentionShape& s) {
+  return 2 * (s.packed ? 1 : (int64_t)s.B) * s.H * s.N * 4;
+}
+
+hipError_t launch_attention_backward(const AttentionShape& s, const void* q, const void* k, const void* v,
+                                     const int32_t* offsets, const int32_t* lengths, const void* out, const float* lse,
+                                     const void* dout, void* dq, void* dk, void* dv, float* ws, hipStream_t stream) {
+  if (s.N == 0) return hipSuccess;
+  Params p = attention_params(s);
+  p.q = q, p.k = k, p.v = v, p.out = (void*)out, p.lse = (float*)lse, p.dout = dout, p.offsets = offsets, p.lengths = lengths;
+  p.dq = dq, p.dk = dk, p.dv = dv, p.stats = ws, p.stat_rows = attention_backward_ws_bytes(s) / 8;
+  p.streams = s.packed ? s.Hk : s.B * s.Hk, p.units = (int)attention_units(s, kRows);
+  return by_type(s.io, s.d, [&](auto bf16, auto dp, auto vec) {
+    constexpr bool BF16 = decltype(bf16)::value;
+    constexpr int DP = decltype(dp)::value, VEC = decltype(vec)::value;
+    constexpr int lds = 4 * tile_of<BF16, DP>() * Tile<BF16, DP>::RB;
+    attention_dq_kernel<BF16, DP, VEC>
+        <<<(unsigned)attention_blocks(s, kRows, s.H / s.Hk), kThreads, lds, stream>>>(p);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    attention_dkv_kernel<BF16, DP, VEC>
+        <<<(unsigned)attention_blocks(s, kRows, 1), kThreads, lds + 4 * 64 * 4, stream>>>(p);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace titans

@@ -391,7 +391,7 @@ struct AttentionBytes {
   int64_t q, k, lse;   // of q and out, of k and v, of lse
 };
 
-int build_attention(const titans_attention_desc* desc, const int32_t* offsets, AttentionShape* s, AttentionBytes* n) {
+int build_attention(const titans_attention_desc* desc, bool packed, AttentionShape* s, AttentionBytes* n) {
   if (!desc || desc->abi_version != TITANS_MEM_ABI_VERSION) return TM_ERR_INVALID;
   if (desc->B <= 0 || desc->H <= 0 || desc->Hk <= 0 || desc->H % desc->Hk || desc->N < 0 || desc->d <= 0)
     return TM_ERR_INVALID;
@@ -399,11 +399,11 @@ int build_attention(const titans_attention_desc* desc, const int32_t* offsets, A
   if (desc->window < 0 || desc->prefix < 0 || !(desc->scale > 0.f) || desc->scale > 3.0e38f) return TM_ERR_INVALID;
   if (desc->flags & ~TM_FLAG_CHANNELS_LAST) return TM_ERR_INVALID;
   if (desc->d > titans::kMaxWidthAttention) return TM_ERR_UNSUPPORTED;
-  const int64_t rows = (offsets ? 1 : (int64_t)desc->B) * desc->N;
+  const int64_t rows = (packed ? 1 : (int64_t)desc->B) * desc->N;
   if ((double)rows * desc->H * desc->d > kMostElements) return TM_ERR_UNSUPPORTED;
   *s = {desc->B, desc->H, desc->Hk, desc->N, desc->d, desc->io_dtype,
         desc->window < desc->N ? desc->window : 0, desc->prefix < desc->N ? desc->prefix : desc->N,
-        offsets != nullptr, (desc->flags & TM_FLAG_CHANNELS_LAST) != 0, desc->scale};
+        packed, (desc->flags & TM_FLAG_CHANNELS_LAST) != 0, desc->scale};
   if (!titans::attention_supported(*s)) return TM_ERR_UNSUPPORTED;
   const int64_t esz = s->io == TM_IO_BF16 ? 2 : 4;
   *n = {rows * s->H * s->d * esz, rows * s->Hk * s->d * esz, rows * s->H * 4};
@@ -576,7 +576,7 @@ int titans_mem_attention(const titans_attention_desc* desc, const void* q, const
                          const int32_t* offsets, const int32_t* lengths, void* out, float* lse, void* stream) {
   AttentionShape s;
   AttentionBytes n;
-  int rc = build_attention(desc, offsets, &s, &n);
+  int rc = build_attention(desc, offsets != nullptr, &s, &n);
   if (rc) return rc;
   if (!needed(q, n.q) || !needed(k, n.k) || !needed(v, n.k) || !needed(out, n.q) || !aligned16(lse) ||
       !aligned16(offsets) || !aligned16(lengths) || (offsets && lengths))
@@ -588,6 +588,44 @@ int titans_mem_attention(const titans_attention_desc* desc, const void* q, const
   if (!disjoint(r, 7)) return TM_ERR_ALIAS;
   return titans::launch_attention(s, q, k, v, offsets, lengths, out, lse, (hipStream_t)stream) == hipSuccess ? TM_OK
                                                                                                             : TM_ERR_HIP;
+}
+
+int64_t titans_mem_attention_backward_workspace_bytes(const titans_attention_desc* desc, int32_t packed) {
+  AttentionShape s;
+  AttentionBytes n;
+  int rc = build_attention(desc, packed != 0, &s, &n);
+  return rc ? rc : titans::attention_backward_ws_bytes(s);
+}
+
+int titans_mem_attention_backward(const titans_attention_desc* desc, const void* q, const void* k, const void* v,
+                                  const int32_t* offsets, const int32_t* lengths, const void* out, const float* lse,
+                                  const void* dout, void* dq, void* dk, void* dv, void* workspace,
+                                  int64_t workspace_bytes, void* stream) {
+  AttentionShape s;
+  AttentionBytes n;
+  int rc = build_attention(desc, offsets != nullptr, &s, &n);
+  if (rc) return rc;
+  const void* rows[] = {q, out, dout, dq};
+  const void* keys[] = {k, v, dk, dv};
+  for (const void* p : rows)
+    if (!needed(p, n.q)) return TM_ERR_INVALID;
+  for (const void* p : keys)
+    if (!needed(p, n.k)) return TM_ERR_INVALID;
+  if (!needed(lse, n.lse) || !aligned16(offsets) || !aligned16(lengths) || !aligned16(workspace) || (offsets && lengths))
+    return TM_ERR_INVALID;
+  const int64_t need = titans::attention_backward_ws_bytes(s);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return TM_ERR_WORKSPACE;
+  const Range r[] = {{(const char*)q, n.q, false},       {(const char*)k, n.k, false},
+                     {(const char*)v, n.k, false},       {(const char*)offsets, ((int64_t)s.B + 1) * 4, false},
+                     {(const char*)lengths, (int64_t)s.B * 4, false}, {(const char*)out, n.q, false},
+                     {(const char*)lse, n.lse, false},   {(const char*)dout, n.q, false},
+                     {(const char*)dq, n.q, true},       {(const char*)dk, n.k, true},
+                     {(const char*)dv, n.k, true},       {(const char*)workspace, need, true}};
+  if (!disjoint(r, 12)) return TM_ERR_ALIAS;
+  return titans::launch_attention_backward(s, q, k, v, offsets, lengths, out, lse, dout, dq, dk, dv, (float*)workspace,
+                                           (hipStream_t)stream) == hipSuccess
+             ? TM_OK
+             : TM_ERR_HIP;
 }
 
 const char* titans_mem_status_string(int status) {

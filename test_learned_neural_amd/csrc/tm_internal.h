@@ -181,5 +181,9 @@ bool attention_supported(const AttentionShape& s);
 hipError_t launch_attention(const AttentionShape& s, const void* q, const void* k, const void* v,
                             const int32_t* offsets, const int32_t* lengths, void* out, float* lse,
                             hipStream_t stream);
+int64_t attention_backward_ws_bytes(const AttentionShape& s);
+hipError_t launch_attention_backward(const AttentionShape& s, const void* q, const void* k, const void* v,
+                                     const int32_t* offsets, const int32_t* lengths, const void* out, const float* lse,
+                                     const void* dout, void* dq, void* dk, void* dv, float* ws, hipStream_t stream);
 
 }  // namespace titans

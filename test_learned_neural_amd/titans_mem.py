@@ -34,7 +34,8 @@ EXPORTS = ("titans_mem_abi_version", "titans_mem_param_count", "titans_mem_selec
            "titans_mem_delta_select_path", "titans_mem_delta_workspace_bytes", "titans_mem_delta_forward",
            "titans_mem_delta_backward", "titans_mem_delta_backward_workspace_bytes",
            "titans_mem_group_norm", "titans_mem_group_norm_backward",
-           "titans_mem_group_norm_backward_workspace_bytes", "titans_mem_attention", "titans_mem_status_string")
+           "titans_mem_group_norm_backward_workspace_bytes", "titans_mem_attention",
+           "titans_mem_attention_backward", "titans_mem_attention_backward_workspace_bytes", "titans_mem_status_string")
 
 
 class Desc(ctypes.Structure):
@@ -163,6 +164,10 @@ def load():
     aq = ctypes.POINTER(AttentionDesc)
     lib.titans_mem_attention.restype = ctypes.c_int
     lib.titans_mem_attention.argtypes = [aq, vp, vp, vp, vp, vp, vp, fp, vp]
+    lib.titans_mem_attention_backward_workspace_bytes.restype = i64
+    lib.titans_mem_attention_backward_workspace_bytes.argtypes = [aq, i32]
+    lib.titans_mem_attention_backward.restype = ctypes.c_int
+    lib.titans_mem_attention_backward.argtypes = [aq, vp, vp, vp, vp, vp, vp, fp, vp, vp, vp, vp, vp, i64, vp]
     lib.titans_mem_group_norm_backward.restype = ctypes.c_int
     lib.titans_mem_group_norm_backward.argtypes = [nq, vp, vp, fp, fp, vp, vp, vp, vp, fp, fp, vp, i64, vp]
     lib.titans_mem_status_string.restype = ctypes.c_char_p
@@ -259,6 +264,17 @@ def raw_delta_backward(desc: DeltaDesc, k, v, q, alpha, theta, lengths, W_in, dy
 def raw_attention(desc: AttentionDesc, q, k, v, offsets, lengths, out, lse, stream) -> int:
     """Direct call of titans_mem_attention with integer device addresses; returns the status."""
     return load().titans_mem_attention(ctypes.byref(desc), q, k, v, offsets, lengths, out, lse, stream)
+
+
+def attention_backward_workspace_bytes(desc: AttentionDesc, packed: bool = False) -> int:
+    return int(load().titans_mem_attention_backward_workspace_bytes(ctypes.byref(desc), int(packed)))
+
+
+def raw_attention_backward(desc: AttentionDesc, q, k, v, offsets, lengths, out, lse, dout, dq, dk, dv, workspace,
+                           workspace_bytes_, stream) -> int:
+    """Direct call of titans_mem_attention_backward with integer device addresses; returns the status."""
+    return load().titans_mem_attention_backward(ctypes.byref(desc), q, k, v, offsets, lengths, out, lse, dout, dq, dk, dv,
+                                                workspace, int(workspace_bytes_), stream)
 
 
 def raw_group_norm(desc: NormDesc, x, gate, weight, bias, lengths, out, stream) -> int:
@@ -705,6 +721,7 @@ class _AttentionPlan:
         self.batch, self.cuts = (B,), (B + 1,)
         self.desc = make_attention_desc(B, H, Hk, N, d, _io_of(dtype), window, prefix, scale, flags)
         self.ref = ctypes.byref(self.desc)
+        self.back = attention_backward_workspace_bytes(self.desc, sequences is not None)
 
 
 _attention_plan = functools.lru_cache(maxsize=256)(_AttentionPlan)
@@ -752,3 +769,23 @@ def attention(q, k, v, *, offsets=None, lengths=None, window: int = 0, prefix: i
     _on_device(index, "titans_mem_attention", load().titans_mem_attention, plan.ref, q.data_ptr(), k.data_ptr(),
                v.data_ptr(), _ptr(offsets), _ptr(lengths), out.data_ptr(), lse_out.data_ptr())
     return out, lse_out
+
+
+def attention_backward(q, k, v, out, lse, dout, *, offsets=None, lengths=None, window: int = 0, prefix: int = 0,
+                       scale: Optional[float] = None, workspace=None):
+    """Gradients through attention() (titans_mem_attention_backward).
+
+    Same inputs as attention(), what it returned, and dout in out's shape and
+    type.  Returns a dict: q, k, v in their shapes and type (k and v summed over
+    the query heads of a key head; zero for tokens of no sequence).
+    """
+    torch = _torch()
+    plan, index = _check_attention(q, k, v, offsets, lengths, window, prefix, scale)
+    _want(q.device, index, ("out", out, plan.out, q.dtype), ("lse", lse, plan.lse, torch.float32),
+          ("dout", dout, plan.out, q.dtype))
+    g = {n: torch.empty_like(t) for n, t in (("q", q), ("k", k), ("v", v))}
+    ws, ws_bytes = _workspace(workspace, plan.back, q.device, "titans_mem_attention_backward_workspace_bytes")
+    _on_device(index, "titans_mem_attention_backward", load().titans_mem_attention_backward, plan.ref, q.data_ptr(),
+               k.data_ptr(), v.data_ptr(), _ptr(offsets), _ptr(lengths), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+               g["q"].data_ptr(), g["k"].data_ptr(), g["v"].data_ptr(), _ptr(ws), ws_bytes)
+    return g
