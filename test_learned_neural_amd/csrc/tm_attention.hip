@@ -74,19 +74,17 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(Params p) {
   const float c = p.scale * kLog2e;
   float m = kLowest, l = 0.f;
   f32x16 o[DP / 32] = {};
-  for (int buf = 0; t <= top; buf ^= 1) {
-    const int k0 = t * KT;
-    t = t + 1 == pre ? lo : t + 1;
-    landed();   // this tile is there, and nobody reads the other any more
-    unsigned char* kb = smem + buf * 2 * kBytes;
-    unsigned char* vb = kb + kBytes;
+  // The tile in kb, while tile t goes to nb.  That the two are apart is said to
+  // the compiler (restrict): its transposing reads would wait for the loads
+  // under way otherwise.
+  auto step = [&](const unsigned char* __restrict__ kb, unsigned char* __restrict__ nb, int t, int k0) {
+    const unsigned char* vb = kb + kBytes;
     if (t <= top) {
-      unsigned char* nb = smem + (buf ^ 1) * 2 * kBytes;
       T::template load<KT, kThreads, VEC>(nb, kp, p.k_tok, t * KT, last, p.d, tid);
       T::template load<KT, kThreads, VEC>(nb + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
     }
     // nothing of the tile is seen by this wave's queries
-    if (w0 > last || k0 > w0 + 31 || (p.window && w0 - (k0 + KT - 1) >= p.window && k0 >= p.prefix)) continue;
+    if (w0 > last || k0 > w0 + 31 || (p.window && w0 - (k0 + KT - 1) >= p.window && k0 >= p.prefix)) return;
     f32x16 x[KT / 32] = {};
 #pragma unroll
     for (int s = 0; s < DP / 16; ++s)
@@ -127,6 +125,12 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(Params p) {
 #pragma unroll
       for (int e = 0; e < DP / 32; ++e) mma(o[e], T::across(vb, 0, s, 32 * e, lane), w);
     }
+    };
+  for (int buf = 0; t <= top; buf ^= 1) {
+    const int k0 = t * KT;
+    t = t + 1 == pre ? lo : t + 1;
+    landed();   // this tile is there, and nobody reads the other any more
+    step(smem + buf * 2 * kBytes, smem + (buf ^ 1) * 2 * kBytes, t, k0);
   }
   if (qi > last) return;
   l += other_half(l);

@@ -122,14 +122,10 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
   const int window = p.window ? p.window : INT_MAX;
   const float c = p.scale * kLog2e;
   f32x16 acc[DP / 32] = {};
-  for (int buf = 0; t <= top; buf ^= 1) {
-    const int k0 = t * KT;
-    t = t + 1 == pre ? lo : t + 1;
-    landed();
-    unsigned char* kb = smem + buf * 2 * kBytes;
-    unsigned char* vb = kb + kBytes;
+  // (restrict: the transposing reads do not wait for the loads under way)
+  auto step = [&](const unsigned char* __restrict__ kb, unsigned char* __restrict__ nb, int t, int k0) {
+    const unsigned char* vb = kb + kBytes;
     if (t <= top) {
-      unsigned char* nb = smem + (buf ^ 1) * 2 * kBytes;
       T::template load<KT, kThreads, VEC>(nb, kp, p.k_tok, t * KT, last, p.d, tid);
       T::template load<KT, kThreads, VEC>(nb + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
     }
@@ -154,6 +150,12 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
         for (int e = 0; e < DP / 32; ++e) mma(acc[e], T::across(kb, 32 * g, s, 32 * e, lane), w);
       }
     }
+    };
+  for (int buf = 0; t <= top; buf ^= 1) {
+    const int k0 = t * KT;
+    t = t + 1 == pre ? lo : t + 1;
+    landed();
+    step(smem + buf * 2 * kBytes, smem + (buf ^ 1) * 2 * kBytes, t, k0);
   }
   if (qi > last) return;
   dq += (int64_t)qi * p.q_tok;
@@ -198,9 +200,8 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
   }
   // tile number n of all: head n / per, query tile lo + n % per
   int lh = 0, lt = lo;
-  auto issue = [&](int buf) {
+  auto issue = [&](unsigned char* b) {
     const int h = at.head0 + lh;
-    unsigned char* b = smem + buf * kStage;
     const elem* qp = (const elem*)p.q + at.seq * p.q_seq + h * p.q_head + (int64_t)at.t0 * p.q_tok;
     const elem* op = (const elem*)p.dout + at.seq * p.o_seq + (int64_t)at.t0 * p.o_tok + h * p.d;
     T::template load<QT, kThreads, VEC>(b, qp, p.q_tok, lt * QT, last, p.d, tid);
@@ -212,22 +213,17 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
     }
     if (++lt == lo + per) lt = lo, ++lh;
   };
-  issue(0);
+  issue(smem);
   frag k[DP / 16], v[DP / 16];
   T::template row<VEC>(k, (const elem*)p.k + kv + (int64_t)min(kj, last) * p.k_tok, p.d, half);
   T::template row<VEC>(v, (const elem*)p.v + kv + (int64_t)min(kj, last) * p.k_tok, p.d, half);
 
   const float c = p.scale * kLog2e;
   f32x16 ak[DP / 32] = {}, av[DP / 32] = {};
-  int qt = lo;
-  for (int n = 0; n < all; ++n) {
-    const int q0 = qt * QT;
-    if (++qt == lo + per) qt = lo;
-    landed();
-    unsigned char* qb = smem + (n & 1) * kStage;
-    unsigned char* ob = qb + kBytes;
+  auto step = [&](const unsigned char* __restrict__ qb, unsigned char* __restrict__ nb, int n, int q0) {
+    const unsigned char* ob = qb + kBytes;
     const float* ls = (const float*)(qb + 2 * kBytes);
-    if (n + 1 < all) issue((n + 1) & 1);
+    if (n + 1 < all) issue(nb);
 #pragma unroll
     for (int g = 0; g < QT / 32; ++g) {
       const int g0 = q0 + 32 * g;
@@ -267,6 +263,13 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
         }
       }
     }
+    };
+  int qt = lo;
+  for (int n = 0; n < all; ++n) {
+    const int q0 = qt * QT;
+    if (++qt == lo + per) qt = lo;
+    landed();
+    step(smem + (n & 1) * kStage, smem + (~n & 1) * kStage, n, q0);
   }
   if (kj > last) return;
   dk += (int64_t)kj * p.k_tok;
