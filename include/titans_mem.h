@@ -567,6 +567,45 @@ int titans_mem_attention_backward(const titans_attention_desc* desc,
                                   void* workspace, int64_t workspace_bytes,
                                   void* stream);
 
+/*
+ * titans_mem_attention_step -- the attention of N new tokens a sequence (one,
+ * as a rule) over a cache of what came before them.  Row b's cache has
+ * lengths[b] tokens, the new ones the last N among them: new token i is token
+ * lengths[b] - N + i of the sequence, and sees what titans_mem_attention's
+ * mask lets it see.
+ *
+ *   q          [B,H,N,d]   io dtype, device, read-only
+ *   k, v       [B,Hk,C,d]  io dtype, device: the cache, room for C tokens
+ *   k_new, v_new  [B,Hk,N,d] io dtype, device, read-only, or both NULL.  With
+ *              them the call stores the new tokens' keys and values at their
+ *              places; without them the cache holds them already
+ *   lengths    [B] int32, device, read-only, clamped to 0..C
+ *   out        [B,N,H*d]   io dtype, device, written; zeros for a token whose
+ *              place would be before the first (an idle row has length 0)
+ * Nothing else of the cache is written, and nothing past a length is read.
+ * Arithmetic and limits as in titans_mem_attention.  A call reads the cache
+ * once for every 32 of the H/Hk * N queries of a key head.  Any overlap of a
+ * written buffer is TM_ERR_ALIAS (the cache is one if k_new is there).
+ */
+typedef struct {
+    int32_t abi_version;  /* must equal TITANS_MEM_ABI_VERSION */
+    int32_t B, H, Hk;     /* sequences, query heads, key heads (Hk divides H) */
+    int32_t N, C, d;      /* new tokens (N >= 0), the cache's room, width of a head */
+    int32_t io_dtype;     /* TM_IO_F32 or TM_IO_BF16 */
+    int32_t window, prefix;   /* as in titans_attention_desc */
+    float scale;
+    uint32_t flags;       /* must be 0 */
+} titans_attention_step_desc;
+
+int64_t titans_mem_attention_step_workspace_bytes(const titans_attention_step_desc* desc);
+
+int titans_mem_attention_step(const titans_attention_step_desc* desc,
+                              const void* q, void* k, void* v,
+                              const void* k_new, const void* v_new,
+                              const int32_t* lengths, void* out,
+                              void* workspace, int64_t workspace_bytes,
+                              void* stream);
+
 /* Static text for a status code. */
 const char* titans_mem_status_string(int status);
 

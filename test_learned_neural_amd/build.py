@@ -21,7 +21,7 @@ ARCH = "gfx950"
 
 SOURCES = ["tm_host.cpp", "tm_generic.hip", "tm_linear.hip", "tm_mlp2_group.hip", "tm_input.hip", "tm_backward.hip",
            "tm_retrieve.hip", "tm_deep.hip", "tm_delta.hip", "tm_delta_chunk.hip", "tm_delta_backward.hip",
-           "tm_group_norm.hip", "tm_attention.hip", "tm_attention_backward.hip"]
+           "tm_group_norm.hip", "tm_attention.hip", "tm_attention_backward.hip", "tm_attention_step.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I" + INCLUDE, "-I" + CSRC]
 # no packed fp32 instructions in device code (v_pk_* fp32 forms)
@@ -32,7 +32,8 @@ DEVICE = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang", "-p
 # MFMA results in VGPRs: these kernels post-process every accumulator on the
 # VALU and keep the memory state in VGPRs
 PER_FILE = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for f in ("tm_mlp2_group.hip", "tm_delta_chunk.hip", "tm_delta_backward.hip",
-                                                                    "tm_attention.hip", "tm_attention_backward.hip")}
+                                                                    "tm_attention.hip", "tm_attention_backward.hip",
+                                                                    "tm_attention_step.hip")}
 
 
 def hipcc() -> str:

@@ -228,6 +228,14 @@ struct Tile {
 // to LDS among them: a plain barrier does not wait for those.
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// The same for what this wave alone reads.  (vmcnt and lgkmcnt zero; as a
+// builtin, so that the compiler knows too that its own loads have come.)
+__device__ __forceinline__ void landed_in_wave() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  asm volatile("" ::: "memory");
+}
+
 __device__ __forceinline__ void clear(unsigned char* t, int bytes, int tid, int threads) {
   for (int i = tid * 16; i < bytes; i += threads * 16) *(f32x4*)(t + i) = f32x4{0.f, 0.f, 0.f, 0.f};
 }

@@ -356,6 +356,7 @@ int titans_mem_input(const titans_input_desc* desc, const void* x, const void* w
 namespace {
 
 using titans::AttentionShape;
+using titans::AttentionStepShape;
 using titans::DeltaShape;
 using titans::NormShape;
 
@@ -408,6 +409,21 @@ int build_attention(const titans_attention_desc* desc, bool packed, AttentionSha
   const int64_t esz = s->io == TM_IO_BF16 ? 2 : 4;
   *n = {rows * s->H * s->d * esz, rows * s->Hk * s->d * esz, rows * s->H * 4};
   return TM_OK;
+}
+
+int build_step(const titans_attention_step_desc* desc, AttentionStepShape* s) {
+  if (!desc || desc->abi_version != TITANS_MEM_ABI_VERSION) return TM_ERR_INVALID;
+  if (desc->B <= 0 || desc->H <= 0 || desc->Hk <= 0 || desc->H % desc->Hk || desc->N < 0 || desc->C <= 0 || desc->d <= 0)
+    return TM_ERR_INVALID;
+  if (desc->io_dtype != TM_IO_F32 && desc->io_dtype != TM_IO_BF16) return TM_ERR_INVALID;
+  if (desc->window < 0 || desc->prefix < 0 || !(desc->scale > 0.f) || desc->scale > 3.0e38f) return TM_ERR_INVALID;
+  if (desc->flags) return TM_ERR_INVALID;
+  if (desc->d > titans::kMaxWidthAttention) return TM_ERR_UNSUPPORTED;
+  if ((double)desc->B * desc->Hk * desc->C * desc->d > kMostElements) return TM_ERR_UNSUPPORTED;
+  if ((double)desc->H / desc->Hk * desc->N > (double)(1 << 30)) return TM_ERR_UNSUPPORTED;
+  *s = {desc->B, desc->H, desc->Hk, desc->N, desc->C, desc->d, desc->io_dtype,
+        desc->window < desc->C ? desc->window : 0, desc->prefix < desc->C ? desc->prefix : desc->C, desc->scale};
+  return titans::attention_step_supported(*s) ? TM_OK : TM_ERR_UNSUPPORTED;
 }
 
 int delta_path(const DeltaShape& s) {
@@ -624,6 +640,37 @@ int titans_mem_attention_backward(const titans_attention_desc* desc, const void*
   if (!disjoint(r, 12)) return TM_ERR_ALIAS;
   return titans::launch_attention_backward(s, q, k, v, offsets, lengths, out, lse, dout, dq, dk, dv, (float*)workspace,
                                            (hipStream_t)stream) == hipSuccess
+             ? TM_OK
+             : TM_ERR_HIP;
+}
+
+int64_t titans_mem_attention_step_workspace_bytes(const titans_attention_step_desc* desc) {
+  AttentionStepShape s;
+  int rc = build_step(desc, &s);
+  return rc ? rc : titans::attention_step_ws_bytes(s);
+}
+
+int titans_mem_attention_step(const titans_attention_step_desc* desc, const void* q, void* k, void* v,
+                              const void* k_new, const void* v_new, const int32_t* lengths, void* out, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+  AttentionStepShape s;
+  int rc = build_step(desc, &s);
+  if (rc) return rc;
+  const int64_t esz = s.io == TM_IO_BF16 ? 2 : 4, need = titans::attention_step_ws_bytes(s);
+  const int64_t rows = (int64_t)s.B * s.H * s.n * s.d * esz, cache = (int64_t)s.B * s.Hk * s.C * s.d * esz;
+  const int64_t added = (int64_t)s.B * s.Hk * s.n * s.d * esz;
+  if (!needed(q, rows) || !needed(out, rows) || !needed(k, cache) || !needed(v, cache) || !needed(lengths, s.B) ||
+      !aligned16(k_new) || !aligned16(v_new) || !aligned16(workspace) || !k_new != !v_new)
+    return TM_ERR_INVALID;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return TM_ERR_WORKSPACE;
+  const bool stores = k_new != nullptr;
+  const Range r[] = {{(const char*)q, rows, false},      {(const char*)k, cache, stores},
+                     {(const char*)v, cache, stores},    {(const char*)k_new, added, false},
+                     {(const char*)v_new, added, false}, {(const char*)lengths, (int64_t)s.B * 4, false},
+                     {(const char*)out, rows, true},     {(const char*)workspace, need, true}};
+  if (!disjoint(r, 8)) return TM_ERR_ALIAS;
+  return titans::launch_attention_step(s, q, k, v, k_new, v_new, lengths, out, (float*)workspace, (hipStream_t)stream) ==
+                 hipSuccess
              ? TM_OK
              : TM_ERR_HIP;
 }

@@ -185,5 +185,15 @@ int64_t attention_backward_ws_bytes(const AttentionShape& s);
 hipError_t launch_attention_backward(const AttentionShape& s, const void* q, const void* k, const void* v,
                                      const int32_t* offsets, const int32_t* lengths, const void* out, const float* lse,
                                      const void* dout, void* dq, void* dk, void* dv, float* ws, hipStream_t stream);
+// n new tokens a sequence over a cache of C; k_new and v_new are both null or
+// both there.  window is 0 or less than C, prefix at most C.
+struct AttentionStepShape {
+  int B, H, Hk, n, C, d, io, window, prefix;
+  float scale;
+};
+bool attention_step_supported(const AttentionStepShape& s);
+int64_t attention_step_ws_bytes(const AttentionStepShape& s);
+hipError_t launch_attention_step(const AttentionStepShape& s, const void* q, void* k, void* v, const void* k_new,
+                                 const void* v_new, const int32_t* lengths, void* out, float* ws, hipStream_t stream);
 
 }  // namespace titans

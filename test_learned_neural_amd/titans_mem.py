@@ -35,7 +35,8 @@ EXPORTS = ("titans_mem_abi_version", "titans_mem_param_count", "titans_mem_selec
            "titans_mem_delta_backward", "titans_mem_delta_backward_workspace_bytes",
            "titans_mem_group_norm", "titans_mem_group_norm_backward",
            "titans_mem_group_norm_backward_workspace_bytes", "titans_mem_attention",
-           "titans_mem_attention_backward", "titans_mem_attention_backward_workspace_bytes", "titans_mem_status_string")
+           "titans_mem_attention_backward", "titans_mem_attention_backward_workspace_bytes", "titans_mem_attention_step",
+           "titans_mem_attention_step_workspace_bytes", "titans_mem_status_string")
 
 
 class Desc(ctypes.Structure):
@@ -69,6 +70,19 @@ class AttentionDesc(ctypes.Structure):
                 ("Hk", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
                 ("io_dtype", ctypes.c_int32), ("window", ctypes.c_int32), ("prefix", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class AttentionStepDesc(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("B", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("N", ctypes.c_int32), ("C", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("window", ctypes.c_int32), ("prefix", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+def make_attention_step_desc(B: int, H: int, Hk: int, N: int, C: int, d: int, io: str = "bf16", window: int = 0,
+                             prefix: int = 0, scale: Optional[float] = None, flags: int = 0) -> AttentionStepDesc:
+    return AttentionStepDesc(ABI_VERSION, B, H, Hk, N, C, d, IO_BF16 if io == "bf16" else IO_F32, window, prefix,
+                             max(d, 1) ** -0.5 if scale is None else scale, flags)
 
 
 def make_attention_desc(B: int, H: int, Hk: int, N: int, d: int, io: str = "bf16", window: int = 0, prefix: int = 0,
@@ -168,6 +182,11 @@ def load():
     lib.titans_mem_attention_backward_workspace_bytes.argtypes = [aq, i32]
     lib.titans_mem_attention_backward.restype = ctypes.c_int
     lib.titans_mem_attention_backward.argtypes = [aq, vp, vp, vp, vp, vp, vp, fp, vp, vp, vp, vp, vp, i64, vp]
+    sq = ctypes.POINTER(AttentionStepDesc)
+    lib.titans_mem_attention_step_workspace_bytes.restype = i64
+    lib.titans_mem_attention_step_workspace_bytes.argtypes = [sq]
+    lib.titans_mem_attention_step.restype = ctypes.c_int
+    lib.titans_mem_attention_step.argtypes = [sq, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]
     lib.titans_mem_group_norm_backward.restype = ctypes.c_int
     lib.titans_mem_group_norm_backward.argtypes = [nq, vp, vp, fp, fp, vp, vp, vp, vp, fp, fp, vp, i64, vp]
     lib.titans_mem_status_string.restype = ctypes.c_char_p
@@ -275,6 +294,17 @@ def raw_attention_backward(desc: AttentionDesc, q, k, v, offsets, lengths, out, 
     """Direct call of titans_mem_attention_backward with integer device addresses; returns the status."""
     return load().titans_mem_attention_backward(ctypes.byref(desc), q, k, v, offsets, lengths, out, lse, dout, dq, dk, dv,
                                                 workspace, int(workspace_bytes_), stream)
+
+
+def attention_step_workspace_bytes(desc: AttentionStepDesc) -> int:
+    return int(load().titans_mem_attention_step_workspace_bytes(ctypes.byref(desc)))
+
+
+def raw_attention_step(desc: AttentionStepDesc, q, k, v, k_new, v_new, lengths, out, workspace, workspace_bytes_,
+                       stream) -> int:
+    """Direct call of titans_mem_attention_step with integer device addresses; returns the status."""
+    return load().titans_mem_attention_step(ctypes.byref(desc), q, k, v, k_new, v_new, lengths, out, workspace,
+                                            int(workspace_bytes_), stream)
 
 
 def raw_group_norm(desc: NormDesc, x, gate, weight, bias, lengths, out, stream) -> int:
@@ -495,7 +525,7 @@ def _io_of(dtype) -> str:
     raise ValueError(f"float32 or bfloat16 expected, got {dtype}")
 
 
-_OPTIONAL = frozenset(("lengths", "dW_out", "weight", "bias", "gate", "offsets"))
+_OPTIONAL = frozenset(("lengths", "dW_out", "weight", "bias", "gate", "offsets", "k_new", "v_new"))
 
 
 def _missing(name):
@@ -789,3 +819,51 @@ def attention_backward(q, k, v, out, lse, dout, *, offsets=None, lengths=None, w
                k.data_ptr(), v.data_ptr(), _ptr(offsets), _ptr(lengths), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                g["q"].data_ptr(), g["k"].data_ptr(), g["v"].data_ptr(), _ptr(ws), ws_bytes)
     return g
+
+
+class _AttentionStepPlan:
+    """What a call's shapes, type and options fix."""
+
+    def __init__(self, queries, cache, dtype, window, prefix, scale):
+        if len(queries) != 4 or len(cache) != 4:
+            raise ValueError("q must be [B, H, n, d], k and v [B, Hk, room, d]")
+        (B, H, N, d), Hk, C = queries, cache[1], cache[2]
+        window, prefix = min(window, (1 << 31) - 1), min(prefix, (1 << 31) - 1)
+        _fits(B, H, Hk, N, C, d)
+        self.cache, self.added, self.out, self.batch = (B, Hk, C, d), (B, Hk, N, d), (B, N, H * d), (B,)
+        self.desc = make_attention_step_desc(B, H, Hk, N, C, d, _io_of(dtype), window, prefix, scale)
+        self.ref = ctypes.byref(self.desc)
+        self.need = attention_step_workspace_bytes(self.desc)
+
+
+_attention_step_plan = functools.lru_cache(maxsize=256)(_AttentionStepPlan)
+
+
+def attention_step(q, k, v, lengths, *, k_new=None, v_new=None, window: int = 0, prefix: int = 0,
+                   scale: Optional[float] = None, out=None, workspace=None):
+    """Attention of a few new tokens over a cache (titans_mem_attention_step).
+
+    q: [B, H, n, d]; k, v: [B, Hk, room, d], the cache (float32 or bfloat16, as
+    in attention()); lengths: [B] int32, the tokens of each row's cache, the new
+    ones the last n among them.  k_new, v_new: [B, Hk, n, d], stored to the
+    cache at their places, or None where it holds them already.  Returns out
+    [B, n, H*d], zeros for new tokens before a row's first place.
+    """
+    torch = _torch()
+    for name, t in (("q", q), ("k", k), ("lengths", lengths)):
+        if t is None:
+            _missing(name)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new come together")
+    io, index = q.dtype, q.get_device()
+    plan = _attention_step_plan(q.shape, k.shape, io, window, prefix, scale)
+    _want(q.device, index, ("q", q, q.shape, io), ("k", k, plan.cache, io), ("v", v, plan.cache, io),
+          ("k_new", k_new, plan.added, io), ("v_new", v_new, plan.added, io), ("lengths", lengths, plan.batch, torch.int32))
+    if out is None:
+        out = torch.empty(plan.out, dtype=io, device=q.device)
+    else:
+        _want(q.device, index, ("out", out, plan.out, io))
+    ws, ws_bytes = _workspace(workspace, plan.need, q.device, "titans_mem_attention_step_workspace_bytes")
+    _on_device(index, "titans_mem_attention_step", load().titans_mem_attention_step, plan.ref, q.data_ptr(), k.data_ptr(),
+               v.data_ptr(), _ptr(k_new), _ptr(v_new), lengths.data_ptr(), out.data_ptr(), _ptr(ws), ws_bytes)
+    return out
