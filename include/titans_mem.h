@@ -606,6 +606,65 @@ int titans_mem_attention_step(const titans_attention_step_desc* desc,
                               void* workspace, int64_t workspace_bytes,
                               void* stream);
 
+/*
+ * titans_mem_projection -- the projection that closes a block (section 4.4,
+ * "Architectural Details": the output projection behind normalization and
+ * gating, and the residual connection), its bias, activation and residual in
+ * one pass:
+ *
+ *   z = x W^T + bias,  out = act(z) + residual
+ *
+ * act is SiLU (TM_ACT_SILU) or the identity (TM_ACT_NONE).
+ *
+ *   x          [rows,K]    io dtype, device, read-only
+ *   weight     [O,K]       io dtype, device, read-only (out = x . row)
+ *   bias       [O] fp32, device, read-only, or NULL
+ *   residual   [rows,O]    io dtype, device, read-only, or NULL
+ *   out        [rows,O]    io dtype, device, written; out == residual (exact
+ *              in-place) is allowed, any other overlap is TM_ERR_ALIAS
+ *   pre_out    [rows,O]    io dtype, device, written, or NULL: z, which the
+ *              gradient of an activation needs
+ * Products of bf16 inputs are exact, sums, bias and activation fp32, out is
+ * rounded once.  fp32 products keep 24 bits; a row or column of fp32 with an
+ * infinity in it comes out as NaN.
+ * TM_ERR_UNSUPPORTED where a launch would have 2^24 tiles of 64 x 64.
+ */
+typedef struct {
+    int32_t abi_version;  /* must equal TITANS_MEM_ABI_VERSION */
+    int32_t K, O;         /* channels in, channels out */
+    int32_t io_dtype;     /* TM_IO_F32 or TM_IO_BF16 */
+    int64_t rows;         /* tokens (>= 0) */
+    int32_t activation;   /* TM_ACT_SILU or TM_ACT_NONE */
+    uint32_t flags;       /* must be 0 */
+} titans_projection_desc;
+
+int titans_mem_projection(const titans_projection_desc* desc, const void* x,
+                          const void* weight, const float* bias,
+                          const void* residual, void* out, void* pre_out,
+                          void* stream);
+
+/*
+ * titans_mem_projection_backward -- its vector-Jacobian products with
+ *   dout       [rows,O]    io dtype, device, read-only: dL/dout
+ *   pre        [rows,O]    io dtype, device, read-only: pre_out of the forward
+ *              call with TM_ACT_SILU, NULL with TM_ACT_NONE
+ * into
+ *   dx         [rows,K]    io dtype, device, written
+ *   dweight    [O,K]       fp32, device, written
+ *   dbias      [O]         fp32, device, written
+ * (dL/dresidual is dout.)  dz = dout act'(z) is rounded to the io dtype once,
+ * before the products; sums are fp32, in a fixed order.  rows == 0 writes
+ * zeros.  Any overlap of a written buffer is TM_ERR_ALIAS.
+ */
+int64_t titans_mem_projection_backward_workspace_bytes(const titans_projection_desc* desc);
+
+int titans_mem_projection_backward(const titans_projection_desc* desc,
+                                   const void* x, const void* weight,
+                                   const void* pre, const void* dout,
+                                   void* dx, float* dweight, float* dbias,
+                                   void* workspace, int64_t workspace_bytes,
+                                   void* stream);
+
 /* Static text for a status code. */
 const char* titans_mem_status_string(int status);
 

@@ -21,7 +21,8 @@ ARCH = "gfx950"
 
 SOURCES = ["tm_host.cpp", "tm_generic.hip", "tm_linear.hip", "tm_mlp2_group.hip", "tm_input.hip", "tm_backward.hip",
            "tm_retrieve.hip", "tm_deep.hip", "tm_delta.hip", "tm_delta_chunk.hip", "tm_delta_backward.hip",
-           "tm_group_norm.hip", "tm_attention.hip", "tm_attention_backward.hip", "tm_attention_step.hip"]
+           "tm_group_norm.hip", "tm_attention.hip", "tm_attention_backward.hip", "tm_attention_step.hip",
+           "tm_projection.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I" + INCLUDE, "-I" + CSRC]
 # no packed fp32 instructions in device code (v_pk_* fp32 forms)

@@ -359,6 +359,7 @@ using titans::AttentionShape;
 using titans::AttentionStepShape;
 using titans::DeltaShape;
 using titans::NormShape;
+using titans::ProjectionShape;
 
 constexpr double kMostElements = 1e15;   // of one tensor: byte counts stay far inside 64 bits
 
@@ -424,6 +425,18 @@ int build_step(const titans_attention_step_desc* desc, AttentionStepShape* s) {
   *s = {desc->B, desc->H, desc->Hk, desc->N, desc->C, desc->d, desc->io_dtype,
         desc->window < desc->C ? desc->window : 0, desc->prefix < desc->C ? desc->prefix : desc->C, desc->scale};
   return titans::attention_step_supported(*s) ? TM_OK : TM_ERR_UNSUPPORTED;
+}
+
+int build_projection(const titans_projection_desc* desc, ProjectionShape* s) {
+  if (!desc || desc->abi_version != TITANS_MEM_ABI_VERSION) return TM_ERR_INVALID;
+  if (desc->rows < 0 || desc->K <= 0 || desc->O <= 0) return TM_ERR_INVALID;
+  if (desc->io_dtype != TM_IO_F32 && desc->io_dtype != TM_IO_BF16) return TM_ERR_INVALID;
+  if (desc->activation != TM_ACT_SILU && desc->activation != TM_ACT_NONE) return TM_ERR_INVALID;
+  if (desc->flags) return TM_ERR_INVALID;
+  const double rows = (double)desc->rows;
+  if (rows * desc->K > kMostElements || rows * desc->O > kMostElements) return TM_ERR_UNSUPPORTED;
+  *s = {desc->rows, desc->K, desc->O, desc->io_dtype, desc->activation == TM_ACT_SILU};
+  return titans::projection_supported(*s) ? TM_OK : TM_ERR_UNSUPPORTED;
 }
 
 int delta_path(const DeltaShape& s) {
@@ -671,6 +684,54 @@ int titans_mem_attention_step(const titans_attention_step_desc* desc, const void
   if (!disjoint(r, 8)) return TM_ERR_ALIAS;
   return titans::launch_attention_step(s, q, k, v, k_new, v_new, lengths, out, (float*)workspace, (hipStream_t)stream) ==
                  hipSuccess
+             ? TM_OK
+             : TM_ERR_HIP;
+}
+
+int titans_mem_projection(const titans_projection_desc* desc, const void* x, const void* weight, const float* bias,
+                          const void* residual, void* out, void* pre_out, void* stream) {
+  ProjectionShape s;
+  int rc = build_projection(desc, &s);
+  if (rc) return rc;
+  const int64_t esz = s.io == TM_IO_BF16 ? 2 : 4, in = s.M * s.K * esz, all = s.M * s.O * esz;
+  const int64_t w = (int64_t)s.O * s.K * esz;
+  if (!needed(x, in) || !needed(weight, w) || !needed(out, all) || !aligned16(bias) || !aligned16(residual) ||
+      !aligned16(pre_out))
+    return TM_ERR_INVALID;
+  const Range r[] = {{(const char*)x, in, false},          {(const char*)weight, w, false},
+                     {(const char*)bias, (int64_t)s.O * 4, false}, {(const char*)residual, all, false},
+                     {(const char*)out, all, true},        {(const char*)pre_out, all, true}};
+  if (!disjoint(r, 6, 3, 4)) return TM_ERR_ALIAS;
+  return titans::launch_projection(s, x, weight, bias, residual, out, pre_out, (hipStream_t)stream) == hipSuccess
+             ? TM_OK
+             : TM_ERR_HIP;
+}
+
+int64_t titans_mem_projection_backward_workspace_bytes(const titans_projection_desc* desc) {
+  ProjectionShape s;
+  int rc = build_projection(desc, &s);
+  return rc ? rc : titans::projection_backward_ws_bytes(s);
+}
+
+int titans_mem_projection_backward(const titans_projection_desc* desc, const void* x, const void* weight,
+                                   const void* pre, const void* dout, void* dx, float* dweight, float* dbias,
+                                   void* workspace, int64_t workspace_bytes, void* stream) {
+  ProjectionShape s;
+  int rc = build_projection(desc, &s);
+  if (rc) return rc;
+  const int64_t esz = s.io == TM_IO_BF16 ? 2 : 4, in = s.M * s.K * esz, all = s.M * s.O * esz;
+  const int64_t w = (int64_t)s.O * s.K * esz, dw = (int64_t)s.O * s.K * 4, db = (int64_t)s.O * 4;
+  if (!needed(x, in) || !needed(weight, w) || !needed(dout, all) || !needed(dx, in) || !needed(dweight, dw) ||
+      !needed(dbias, db) || !aligned16(pre) || !aligned16(workspace) || (s.silu ? !needed(pre, all) : pre != nullptr))
+    return TM_ERR_INVALID;
+  const int64_t need = titans::projection_backward_ws_bytes(s);
+  if (!workspace || workspace_bytes < need) return TM_ERR_WORKSPACE;
+  const Range r[] = {{(const char*)x, in, false},    {(const char*)weight, w, false},  {(const char*)pre, all, false},
+                     {(const char*)dout, all, false}, {(const char*)dx, in, true},     {(const char*)dweight, dw, true},
+                     {(const char*)dbias, db, true}, {(const char*)workspace, need, true}};
+  if (!disjoint(r, 8)) return TM_ERR_ALIAS;
+  return titans::launch_projection_backward(s, x, weight, pre, dout, dx, dweight, dbias, workspace,
+                                            (hipStream_t)stream) == hipSuccess
              ? TM_OK
              : TM_ERR_HIP;
 }

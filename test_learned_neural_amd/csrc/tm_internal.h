@@ -196,4 +196,18 @@ int64_t attention_step_ws_bytes(const AttentionStepShape& s);
 hipError_t launch_attention_step(const AttentionStepShape& s, const void* q, void* k, void* v, const void* k_new,
                                  const void* v_new, const int32_t* lengths, void* out, float* ws, hipStream_t stream);
 
+// A matrix product with bias, activation and residual, M rows from K to O
+// channels, and its gradient.  bias, residual and pre may be null.
+struct ProjectionShape {
+  int64_t M;
+  int K, O, io, silu;
+};
+bool projection_supported(const ProjectionShape& s);
+hipError_t launch_projection(const ProjectionShape& s, const void* x, const void* weight, const float* bias,
+                             const void* residual, void* out, void* pre, hipStream_t stream);
+int64_t projection_backward_ws_bytes(const ProjectionShape& s);
+hipError_t launch_projection_backward(const ProjectionShape& s, const void* x, const void* weight, const void* pre,
+                                      const void* dout, void* dx, float* dweight, float* dbias, void* ws,
+                                      hipStream_t stream);
+
 }  // namespace titans

@@ -36,7 +36,8 @@ EXPORTS = ("titans_mem_abi_version", "titans_mem_param_count", "titans_mem_selec
            "titans_mem_group_norm", "titans_mem_group_norm_backward",
            "titans_mem_group_norm_backward_workspace_bytes", "titans_mem_attention",
            "titans_mem_attention_backward", "titans_mem_attention_backward_workspace_bytes", "titans_mem_attention_step",
-           "titans_mem_attention_step_workspace_bytes", "titans_mem_status_string")
+           "titans_mem_attention_step_workspace_bytes", "titans_mem_projection", "titans_mem_projection_backward",
+           "titans_mem_projection_backward_workspace_bytes", "titans_mem_status_string")
 
 
 class Desc(ctypes.Structure):
@@ -83,6 +84,17 @@ def make_attention_step_desc(B: int, H: int, Hk: int, N: int, C: int, d: int, io
                              prefix: int = 0, scale: Optional[float] = None, flags: int = 0) -> AttentionStepDesc:
     return AttentionStepDesc(ABI_VERSION, B, H, Hk, N, C, d, IO_BF16 if io == "bf16" else IO_F32, window, prefix,
                              max(d, 1) ** -0.5 if scale is None else scale, flags)
+
+
+class ProjectionDesc(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("K", ctypes.c_int32), ("O", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("rows", ctypes.c_int64), ("activation", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
+def make_projection_desc(rows: int, K: int, O: int, io: str = "bf16", activation: int = ACT_NONE,
+                         flags: int = 0) -> ProjectionDesc:
+    return ProjectionDesc(ABI_VERSION, K, O, IO_BF16 if io == "bf16" else IO_F32, rows, activation, flags)
 
 
 def make_attention_desc(B: int, H: int, Hk: int, N: int, d: int, io: str = "bf16", window: int = 0, prefix: int = 0,
@@ -187,6 +199,13 @@ def load():
     lib.titans_mem_attention_step_workspace_bytes.argtypes = [sq]
     lib.titans_mem_attention_step.restype = ctypes.c_int
     lib.titans_mem_attention_step.argtypes = [sq, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+    pq = ctypes.POINTER(ProjectionDesc)
+    lib.titans_mem_projection.restype = ctypes.c_int
+    lib.titans_mem_projection.argtypes = [pq, vp, vp, fp, vp, vp, vp, vp]
+    lib.titans_mem_projection_backward_workspace_bytes.restype = i64
+    lib.titans_mem_projection_backward_workspace_bytes.argtypes = [pq]
+    lib.titans_mem_projection_backward.restype = ctypes.c_int
+    lib.titans_mem_projection_backward.argtypes = [pq, vp, vp, vp, vp, vp, fp, fp, vp, i64, vp]
     lib.titans_mem_group_norm_backward.restype = ctypes.c_int
     lib.titans_mem_group_norm_backward.argtypes = [nq, vp, vp, fp, fp, vp, vp, vp, vp, fp, fp, vp, i64, vp]
     lib.titans_mem_status_string.restype = ctypes.c_char_p
@@ -305,6 +324,22 @@ def raw_attention_step(desc: AttentionStepDesc, q, k, v, k_new, v_new, lengths, 
     """Direct call of titans_mem_attention_step with integer device addresses; returns the status."""
     return load().titans_mem_attention_step(ctypes.byref(desc), q, k, v, k_new, v_new, lengths, out, workspace,
                                             int(workspace_bytes_), stream)
+
+
+def raw_projection(desc: ProjectionDesc, x, weight, bias, residual, out, pre_out, stream) -> int:
+    """Direct call of titans_mem_projection with integer device addresses; returns the status."""
+    return load().titans_mem_projection(ctypes.byref(desc), x, weight, bias, residual, out, pre_out, stream)
+
+
+def projection_backward_workspace_bytes(desc: ProjectionDesc) -> int:
+    return int(load().titans_mem_projection_backward_workspace_bytes(ctypes.byref(desc)))
+
+
+def raw_projection_backward(desc: ProjectionDesc, x, weight, pre, dout, dx, dweight, dbias, workspace, workspace_bytes_,
+                            stream) -> int:
+    """Direct call of titans_mem_projection_backward with integer device addresses; returns the status."""
+    return load().titans_mem_projection_backward(ctypes.byref(desc), x, weight, pre, dout, dx, dweight, dbias, workspace,
+                                                 int(workspace_bytes_), stream)
 
 
 def raw_group_norm(desc: NormDesc, x, gate, weight, bias, lengths, out, stream) -> int:
@@ -525,7 +560,7 @@ def _io_of(dtype) -> str:
     raise ValueError(f"float32 or bfloat16 expected, got {dtype}")
 
 
-_OPTIONAL = frozenset(("lengths", "dW_out", "weight", "bias", "gate", "offsets", "k_new", "v_new"))
+_OPTIONAL = frozenset(("lengths", "dW_out", "weight", "bias", "gate", "offsets", "k_new", "v_new", "residual"))
 
 
 def _missing(name):
@@ -867,3 +902,77 @@ def attention_step(q, k, v, lengths, *, k_new=None, v_new=None, window: int = 0,
     _on_device(index, "titans_mem_attention_step", load().titans_mem_attention_step, plan.ref, q.data_ptr(), k.data_ptr(),
                v.data_ptr(), _ptr(k_new), _ptr(v_new), lengths.data_ptr(), out.data_ptr(), _ptr(ws), ws_bytes)
     return out
+
+
+class _ProjectionPlan:
+    """What a call's shapes, type and options fix."""
+
+    def __init__(self, rows, weight, dtype, activation):
+        if not rows or len(weight) != 2:
+            raise ValueError("x must be [..., K], weight [O, K]")
+        O, K = weight
+        _fits(K, O)
+        self.rows, self.out, self.weight, self.channels = rows[:-1] + (K,), rows[:-1] + (O,), (O, K), (O,)
+        n = 1
+        for r in rows[:-1]:
+            n *= r
+        self.desc = make_projection_desc(n, K, O, _io_of(dtype), activation)
+        self.ref = ctypes.byref(self.desc)
+        self.back = projection_backward_workspace_bytes(self.desc)
+
+
+_projection_plan = functools.lru_cache(maxsize=256)(_ProjectionPlan)
+
+
+def _check_projection(x, weight, activation):
+    for name, t in (("x", x), ("weight", weight)):
+        if t is None:
+            _missing(name)
+    io, index = x.dtype, x.get_device()
+    plan = _projection_plan(tuple(x.shape), tuple(weight.shape), io, activation)
+    _want(x.device, index, ("x", x, plan.rows, io), ("weight", weight, plan.weight, io))
+    return plan, index
+
+
+def projection(x, weight, bias=None, *, residual=None, activation: int = ACT_NONE, out=None, pre_out=None):
+    """act(x W^T + bias) + residual (titans_mem_projection).
+
+    x: [..., K]; weight: [O, K] (float32 or bfloat16); bias: [O] float32 or
+    None; residual: [..., O] or None.  pre_out: [..., O], written with what goes
+    into the activation (projection_backward() needs it with ACT_SILU), or None.
+    Returns out [..., O]; it may be the residual.
+    """
+    torch = _torch()
+    plan, index = _check_projection(x, weight, activation)
+    io = x.dtype
+    if out is None:
+        out = torch.empty(plan.out, dtype=io, device=x.device)
+    _want(x.device, index, ("out", out, plan.out, io), ("bias", bias, plan.channels, torch.float32),
+          ("residual", residual, plan.out, io))
+    if pre_out is not None:
+        _want(x.device, index, ("pre_out", pre_out, plan.out, io))
+    _on_device(index, "titans_mem_projection", load().titans_mem_projection, plan.ref, x.data_ptr(), weight.data_ptr(),
+               _ptr(bias), _ptr(residual), out.data_ptr(), _ptr(pre_out))
+    return out
+
+
+def projection_backward(x, weight, dout, *, pre=None, activation: int = ACT_NONE, workspace=None):
+    """Gradients through projection() (titans_mem_projection_backward).
+
+    x and weight as in projection(); dout: [..., O] in x's type; pre: what the
+    forward call wrote to pre_out, with ACT_SILU.  Returns a dict: x (x's shape
+    and type), weight [O, K] and bias [O] float32.  The residual's gradient is
+    dout.
+    """
+    torch = _torch()
+    plan, index = _check_projection(x, weight, activation)
+    _want(x.device, index, ("dout", dout, plan.out, x.dtype))
+    if activation == ACT_SILU or pre is not None:
+        _want(x.device, index, ("pre", pre, plan.out, x.dtype))
+    g = {"x": torch.empty_like(x), "weight": torch.empty(plan.weight, dtype=torch.float32, device=x.device),
+         "bias": torch.empty(plan.channels, dtype=torch.float32, device=x.device)}
+    ws, ws_bytes = _workspace(workspace, plan.back, x.device, "titans_mem_projection_backward_workspace_bytes")
+    _on_device(index, "titans_mem_projection_backward", load().titans_mem_projection_backward, plan.ref, x.data_ptr(),
+               weight.data_ptr(), _ptr(pre), dout.data_ptr(), g["x"].data_ptr(), g["weight"].data_ptr(),
+               g["bias"].data_ptr(), _ptr(ws), ws_bytes)
+    return g
