@@ -94,10 +94,20 @@ __device__ __forceinline__ float other_half(float x) {
   return __builtin_bit_cast(float, (threadIdx.x & 32) ? r[0] : r[1]);
 }
 
+// LDS has 64 banks of 4 bytes.  Reads of 16 bytes a lane go 16 lanes at a time,
+// transposing ones of 8 bytes 32 lanes at a time: 16 rows of one chunk, or 4
+// rows of 4 neighbouring chunks, have to fall on 16 different places of 16
+// bytes in 256.  Rows of NC chunks fill those 256 bytes by 16 / NC; chunk c of
+// row r lies at c ^ swizzle(r).
+template <int NC>
+__device__ __forceinline__ int swizzle(int r) {
+  if (NC == 4) return (r >> 2) & 3;
+  if (NC == 8) return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
+  return (r & 3) << 2 | ((r >> 2) & 3);
+}
+
 // A tile's rows in LDS: LS elements each (the padded width up to the next
-// power of two), 16-byte chunk c of row r at c ^ swz(r).  A row's own chunks
-// are then read by 8 or 16 rows at once from different banks, and so are the
-// 4 rows x 4 chunks of a transposing read.
+// power of two), 16-byte chunk c of row r at c ^ swz(r).
 template <bool BF16, int DP>
 struct Tile {
   typedef typename Types<BF16>::elem elem;
@@ -109,9 +119,7 @@ struct Tile {
   static constexpr int PC = 16 / kSize;       // elements of a chunk
 
   static __device__ __forceinline__ int swz(int r) {
-    if (NC == 4) return (r >> 1) & 3;
-    if (NC == 8) return (r & 1) << 2 | ((r >> 1) & 3);
-    return (r & 3) << 2 | ((r >> 2) & 3);
+    return swizzle<NC>(r);
   }
 
   // step s of row r, contraction along the row
@@ -148,40 +156,51 @@ struct Tile {
     }
   }
 
-  // Rows j0 .. j0 + ROWS - 1 of a tensor (its rows `tok` elements apart, rows
-  // past `last` as row `last`) into LDS by THREADS threads: wide pieces
-  // straight to LDS, or element by element where rows are not made of 16-byte
-  // pieces.  Columns from d on are zero: cleared once (clear()) where pieces
-  // go straight to LDS, which then leaves them alone.
+  // Rows j0 .. j0 + ROWS - 1 of a tensor (rows `tok` elements apart, rows past
+  // `last` as row `last`) into LDS by THREADS threads: wide pieces straight to
+  // LDS, or element by element where rows are not made of 16-byte pieces.
+  // Columns from d on are zero: cleared once (clear()) where pieces go straight
+  // to LDS, which then leaves them alone.  A thread's places within a tile are
+  // the same in every whole tile, so it keeps their distances from the tile's
+  // first row (32 bits: 64 rows of 2^22 elements), which is the wave's.
   template <int ROWS, int THREADS, int VEC>
-  static __device__ __forceinline__ void load(unsigned char* t, const elem* src, int64_t tok, int j0, int last, int d,
-                                              int tid) {
-    constexpr int kChunks = ROWS * NC;
-    if constexpr (VEC != kOdd) {
-      static_assert(kChunks % THREADS == 0, "");
-      const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  struct Loads {
+    static constexpr int kCount = ROWS * NC / THREADS;
+    uint32_t off[kCount];
+
+    __device__ __forceinline__ Loads(int64_t tok, int tid) {
+      static_assert(ROWS * NC % THREADS == 0, "");
 #pragma unroll
-      for (int i = 0; i < kChunks / THREADS; ++i) {
-        const int base = i * THREADS + wave * 64, at = base + lane;
-        const int r = at / NC, c = (at % NC) ^ swz(r);
-        const int j = j0 + r < last ? j0 + r : last;
-        if (VEC == kFull && DP == LS ? true : c * PC < d)
-          __builtin_amdgcn_global_load_lds((const void*)(src + (int64_t)j * tok + c * PC), (lds_void_ptr)(t + base * 16), 16, 0,
-                                           0);
-      }
-    } else {
-      for (int at = tid; at < kChunks; at += THREADS) {
-        const int r = at / NC, c = (at % NC) ^ swz(r);
-        const int j = j0 + r < last ? j0 + r : last;
-        const elem* s = src + (int64_t)j * tok + c * PC;
-        elem x[PC];
-#pragma unroll
-        for (int e = 0; e < PC; ++e) x[e] = c * PC + e < d ? s[e] : (elem)0.f;
-#pragma unroll
-        for (int e = 0; e < PC; ++e) ((elem*)(t + at * 16))[e] = x[e];
+      for (int i = 0; i < kCount; ++i) {
+        const int at = i * THREADS + tid, r = at / NC, c = (at % NC) ^ swz(r);
+        off[i] = (uint32_t)(r * (int)tok + c * PC) * kSize;
       }
     }
-  }
+
+    __device__ __forceinline__ void operator()(unsigned char* t, const elem* src, int64_t tok, int j0, int last, int d,
+                                               int tid) const {
+      const elem* row0 = src + (int64_t)j0 * tok;
+      const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+#pragma unroll
+      for (int i = 0; i < kCount; ++i) {
+        const int base = i * THREADS + wave * 64, at = i * THREADS + tid;
+        const int r = at / NC, c = (at % NC) ^ swz(r);
+        if constexpr (VEC != kOdd) {
+          uint32_t o = off[i];
+          if (j0 + ROWS - 1 > last) o = (uint32_t)(min(r, last - j0) * (int)tok + c * PC) * kSize;
+          if (VEC == kFull && DP == LS ? true : c * PC < d)
+            __builtin_amdgcn_global_load_lds((const void*)((const char*)row0 + o), (lds_void_ptr)(t + base * 16), 16, 0, 0);
+        } else {
+          const elem* s = row0 + (int64_t)min(r, last - j0) * tok + c * PC;
+          elem x[PC];
+#pragma unroll
+          for (int e = 0; e < PC; ++e) x[e] = c * PC + e < d ? s[e] : (elem)0.f;
+#pragma unroll
+          for (int e = 0; e < PC; ++e) ((elem*)(t + at * 16))[e] = x[e];
+        }
+      }
+    }
+  };
 
   // row j (clamped) of a tensor as an operand's DP / 16 steps, straight from memory
   template <int VEC>

@@ -36,7 +36,7 @@ template <bool BF16>
 constexpr int keys_of() { return BF16 ? 64 : 32; }
 
 template <bool BF16, int DP, int VEC>
-__global__ void __launch_bounds__(kThreads, 2) attention_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, BF16 && DP <= 64 ? 4 : 2) attention_kernel(Params p) {
   typedef Tile<BF16, DP> T;
   typedef typename T::elem elem;
   typedef typename T::frag frag;
@@ -65,8 +65,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(Params p) {
     clear(smem, 4 * kBytes, tid, kThreads);
     __syncthreads();
   }
-  T::template load<KT, kThreads, VEC>(smem, kp, p.k_tok, t * KT, last, p.d, tid);
-  T::template load<KT, kThreads, VEC>(smem + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
+  const typename T::template Loads<KT, kThreads, VEC> load(p.k_tok, tid);
+  load(smem, kp, p.k_tok, t * KT, last, p.d, tid);
+  load(smem + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
   frag q[DP / 16];
   T::template row<VEC>(q, qp, p.d, half);
 
@@ -77,11 +78,11 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(Params p) {
   // The tile in kb, while tile t goes to nb.  That the two are apart is said to
   // the compiler (restrict): its transposing reads would wait for the loads
   // under way otherwise.
-  auto step = [&](const unsigned char* __restrict__ kb, unsigned char* __restrict__ nb, int t, int k0) {
+  auto step = [&](const unsigned char* __restrict__ kb, unsigned char* __restrict__ nb, int t, int k0) __attribute__((always_inline)) {
     const unsigned char* vb = kb + kBytes;
     if (t <= top) {
-      T::template load<KT, kThreads, VEC>(nb, kp, p.k_tok, t * KT, last, p.d, tid);
-      T::template load<KT, kThreads, VEC>(nb + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
+      load(nb, kp, p.k_tok, t * KT, last, p.d, tid);
+      load(nb + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
     }
     // nothing of the tile is seen by this wave's queries
     if (w0 > last || k0 > w0 + 31 || (p.window && w0 - (k0 + KT - 1) >= p.window && k0 >= p.prefix)) return;
@@ -126,11 +127,15 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(Params p) {
       for (int e = 0; e < DP / 32; ++e) mma(o[e], T::across(vb, 0, s, 32 * e, lane), w);
     }
     };
-  for (int buf = 0; t <= top; buf ^= 1) {
+  auto turn = [&](int buf) __attribute__((always_inline)) {
     const int k0 = t * KT;
     t = t + 1 == pre ? lo : t + 1;
     landed();   // this tile is there, and nobody reads the other any more
     step(smem + buf * 2 * kBytes, smem + (buf ^ 1) * 2 * kBytes, t, k0);
+  };
+  while (t <= top) {   // (both buffers in turn, their places in LDS constant)
+    turn(0);
+    if (t <= top) turn(1);
   }
   if (qi > last) return;
   l += other_half(l);
@@ -167,7 +172,9 @@ int64_t attention_blocks(const AttentionShape& s, int rows, int heads) {
   return (streams * units + 7) / 8 * 8 * heads;
 }
 
-bool attention_supported(const AttentionShape& s) { return attention_blocks(s, 64, s.H / s.Hk) < kMostBlocks; }
+bool attention_supported(const AttentionShape& s) {
+  return attention_blocks(s, 32, s.H / s.Hk) < kMostBlocks && (int64_t)s.H * s.d <= 1 << 22;   // (Loads' distances)
+}
 
 hipError_t launch_attention(const AttentionShape& s, const void* q, const void* k, const void* v,
                             const int32_t* offsets, const int32_t* lengths, void* out, float* lse,

@@ -96,8 +96,9 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
     clear(smem, 4 * kBytes, tid, kThreads);
     __syncthreads();
   }
-  T::template load<KT, kThreads, VEC>(smem, kp, p.k_tok, t * KT, last, p.d, tid);
-  T::template load<KT, kThreads, VEC>(smem + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
+  const typename T::template Loads<KT, kThreads, VEC> load(p.k_tok, tid);
+  load(smem, kp, p.k_tok, t * KT, last, p.d, tid);
+  load(smem + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
 
   frag q[DP / 16], go[DP / 16];
   T::template row<VEC>(q, (const elem*)p.q + at.seq * p.q_seq + h * p.q_head + qt * p.q_tok, p.d, half);
@@ -123,11 +124,11 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
   const float c = p.scale * kLog2e;
   f32x16 acc[DP / 32] = {};
   // (restrict: the transposing reads do not wait for the loads under way)
-  auto step = [&](const unsigned char* __restrict__ kb, unsigned char* __restrict__ nb, int t, int k0) {
+  auto step = [&](const unsigned char* __restrict__ kb, unsigned char* __restrict__ nb, int t, int k0) __attribute__((always_inline)) {
     const unsigned char* vb = kb + kBytes;
     if (t <= top) {
-      T::template load<KT, kThreads, VEC>(nb, kp, p.k_tok, t * KT, last, p.d, tid);
-      T::template load<KT, kThreads, VEC>(nb + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
+      load(nb, kp, p.k_tok, t * KT, last, p.d, tid);
+      load(nb + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
     }
 #pragma unroll
     for (int g = 0; g < KT / 32; ++g) {
@@ -151,11 +152,15 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
       }
     }
     };
-  for (int buf = 0; t <= top; buf ^= 1) {
+  auto turn = [&](int buf) __attribute__((always_inline)) {
     const int k0 = t * KT;
     t = t + 1 == pre ? lo : t + 1;
     landed();
     step(smem + buf * 2 * kBytes, smem + (buf ^ 1) * 2 * kBytes, t, k0);
+  };
+  while (t <= top) {
+    turn(0);
+    if (t <= top) turn(1);
   }
   if (qi > last) return;
   dq += (int64_t)qi * p.q_tok;
@@ -200,12 +205,13 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
   }
   // tile number n of all: head n / per, query tile lo + n % per
   int lh = 0, lt = lo;
+  const typename T::template Loads<QT, kThreads, VEC> load_q(p.q_tok, tid), load_o(p.o_tok, tid);
   auto issue = [&](unsigned char* b) {
     const int h = at.head0 + lh;
     const elem* qp = (const elem*)p.q + at.seq * p.q_seq + h * p.q_head + (int64_t)at.t0 * p.q_tok;
     const elem* op = (const elem*)p.dout + at.seq * p.o_seq + (int64_t)at.t0 * p.o_tok + h * p.d;
-    T::template load<QT, kThreads, VEC>(b, qp, p.q_tok, lt * QT, last, p.d, tid);
-    T::template load<QT, kThreads, VEC>(b + kBytes, op, p.o_tok, lt * QT, last, p.d, tid);
+    load_q(b, qp, p.q_tok, lt * QT, last, p.d, tid);
+    load_o(b + kBytes, op, p.o_tok, lt * QT, last, p.d, tid);
     if (wave < 2) {   // 64 rows of lse, of D (QT of them are used)
       const float* st = p.stats + (wave ? p.stat_rows : 0) + ((int64_t)at.seq * p.H + h) * p.N + at.t0;
       __builtin_amdgcn_global_load_lds((const void*)(st + min(lt * QT + lane, last)),
@@ -220,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
 
   const float c = p.scale * kLog2e;
   f32x16 ak[DP / 32] = {}, av[DP / 32] = {};
-  auto step = [&](const unsigned char* __restrict__ qb, unsigned char* __restrict__ nb, int n, int q0) {
+  auto step = [&](const unsigned char* __restrict__ qb, unsigned char* __restrict__ nb, int n, int q0) __attribute__((always_inline)) {
     const unsigned char* ob = qb + kBytes;
     const float* ls = (const float*)(qb + 2 * kBytes);
     if (n + 1 < all) issue(nb);
@@ -265,11 +271,15 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
     }
     };
   int qt = lo;
-  for (int n = 0; n < all; ++n) {
+  auto turn = [&](int n, int buf) __attribute__((always_inline)) {
     const int q0 = qt * QT;
     if (++qt == lo + per) qt = lo;
     landed();
-    step(smem + (n & 1) * kStage, smem + (~n & 1) * kStage, n, q0);
+    step(smem + buf * kStage, smem + (buf ^ 1) * kStage, n, q0);
+  };
+  for (int n = 0; n < all; n += 2) {
+    turn(n, 0);
+    if (n + 1 < all) turn(n + 1, 1);
   }
   if (kj > last) return;
   dk += (int64_t)kj * p.k_tok;

@@ -43,11 +43,16 @@ constexpr int wave_lds() { return 4 * kKeys * Tile<BF16, DP>::RB; }
 
 // Keys j0 .. j0 + 31 of the cache, those from `fresh` on from the new ones.
 template <bool BF16, int DP, int VEC, typename T = Tile<BF16, DP>>
-__device__ __forceinline__ void load_keys(unsigned char* t, const typename T::elem* cache, const typename T::elem* added,
-                                          int fresh, int j0, int last, int d, int lane) {
+__device__ __forceinline__ void load_keys(const typename T::template Loads<kKeys, 64, VEC>& load, unsigned char* t,
+                                          const typename T::elem* cache, const typename T::elem* added, int fresh, int j0,
+                                          int last, int d, int lane) {
   typedef typename T::elem elem;
-#pragma unroll 8
-  for (int i = 0; i < kKeys * T::NC / 64; ++i) {
+  if (j0 + kKeys <= fresh) {
+    load(t, cache, d, j0, last, d, lane);
+    return;
+  }
+#pragma unroll 4
+  for (int i = 0; i < load.kCount; ++i) {
     const int at = i * 64 + lane, r = at / T::NC, c = (at % T::NC) ^ T::swz(r), j = min(j0 + r, last);
     const elem* row = j >= fresh ? added + (int64_t)(j - fresh) * d : cache + (int64_t)j * d;
     if constexpr (VEC != kOdd) {
@@ -95,9 +100,10 @@ __global__ void __launch_bounds__((64 * waves_of<BF16, DP>())) attention_step_ke
   int x = part * per + wave;
   if (VEC == kPieces && p.d < DP) clear(mine, 4 * kBytes, lane, 64);
   auto tile = [&](int i) { return i < pre ? i : lo + i - pre; };
+  const typename T::template Loads<kKeys, 64, VEC> load(p.d, lane);
   auto issue = [&](unsigned char* t, int i) {
-    load_keys<BF16, DP, VEC>(t, kc, kn, fresh, tile(i) * kKeys, last, p.d, lane);
-    load_keys<BF16, DP, VEC>(t + kBytes, vc, vn, fresh, tile(i) * kKeys, last, p.d, lane);
+    load_keys<BF16, DP, VEC>(load, t, kc, kn, fresh, tile(i) * kKeys, last, p.d, lane);
+    load_keys<BF16, DP, VEC>(load, t + kBytes, vc, vn, fresh, tile(i) * kKeys, last, p.d, lane);
   };
   // (what was cleared is there before a load may write beside it)
   landed_in_wave();
@@ -108,7 +114,7 @@ __global__ void __launch_bounds__((64 * waves_of<BF16, DP>())) attention_step_ke
   const float c = p.scale * kLog2e;
   float m = kLowest, l = 0.f;
   f32x16 o[DP / 32] = {};
-  auto step = [&](const unsigned char* __restrict__ kb, unsigned char* __restrict__ nb) {
+  auto step = [&](const unsigned char* __restrict__ kb, unsigned char* __restrict__ nb) __attribute__((always_inline)) {
     const unsigned char* vb = kb + kBytes;
     const int k0 = tile(x) * kKeys;
     if (x + W < end) issue(nb, x + W);
@@ -148,9 +154,13 @@ __global__ void __launch_bounds__((64 * waves_of<BF16, DP>())) attention_step_ke
           vc[(int64_t)j * p.d + e] = vn[(int64_t)(j - fresh) * p.d + e];
         }
   };
-  for (int buf = 0; x < end; buf ^= 1, x += W) {
+  for (; x < end; x += W) {
     landed_in_wave();   // its tile is there
-    step(mine + buf * 2 * kBytes, mine + (buf ^ 1) * 2 * kBytes);
+    step(mine, mine + 2 * kBytes);
+    x += W;
+    if (x >= end) break;
+    landed_in_wave();
+    step(mine + 2 * kBytes, mine);
   }
 
   // join the waves: each leaves its rows' outputs in LDS, [row][DP + 4]
@@ -192,18 +202,30 @@ __global__ void __launch_bounds__((64 * waves_of<BF16, DP>())) attention_step_ke
   }
 }
 
-// Parts of a row, a wave each row.
+// Parts of a row, a workgroup each row: its waves share the parts, then a
+// column's sums are joined in their order.
 template <bool BF16>
 __global__ void __launch_bounds__(256) step_join_kernel(StepParams p) {
   typedef typename Types<BF16>::elem elem;
-  const int lane = threadIdx.x & 63, G = p.H / p.Hk, rows = G * p.n;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (at >= (int64_t)p.B * p.Hk * rows) return;
+  __shared__ float acc[4][128];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, G = p.H / p.Hk, rows = G * p.n;
+  const int64_t at = blockIdx.x;
+  const float* o = p.po + at * p.parts * p.d;
   float m = kLowest, l = 0.f;
   if (lane < p.parts) {
     const f32x2 x = *(const f32x2*)(p.pml + 2 * (at * p.parts + lane));
     m = x[0], l = x[1];
   }
+  // columns lane and 64 + lane of parts wave, wave + 4 ..: loads before the weights are known
+  constexpr int kEach = kMostParts / 4;
+  float x[kEach][2];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int s = wave + 4 * i, c = lane + 64 * e;
+      x[i][e] = s < p.parts && c < p.d ? o[(int64_t)s * p.d + c] : 0.f;
+    }
   float top = m;
 #pragma unroll
   for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
@@ -211,17 +233,21 @@ __global__ void __launch_bounds__(256) step_join_kernel(StepParams p) {
   float sum = l * f;
 #pragma unroll
   for (int i = 1; i < 64; i *= 2) sum += __shfl_xor(sum, i);
+  float a[2] = {};
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const float w = __shfl(f, wave + 4 * i);
+    a[0] = fmaf(x[i][0], w, a[0]);
+    a[1] = fmaf(x[i][1], w, a[1]);
+  }
+  acc[wave][lane] = a[0], acc[wave][64 + lane] = a[1];
+  __syncthreads();
+  if (tid >= p.d) return;
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
   const int row = (int)(at % rows);
   const int64_t stream = at / rows, b = stream / p.Hk, hk = stream % p.Hk;
   elem* out = (elem*)p.out + ((b * p.n + row % p.n) * p.H + hk * G + row / p.n) * p.d;
-  const float* o = p.po + at * p.parts * p.d;
-  for (int c = lane; c < p.d; c += 64) {
-    float acc = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < p.parts; ++s) acc = fmaf(o[(int64_t)s * p.d + c], __shfl(f, s), acc);
-    out[c] = (elem)(acc * inv);
-  }
+  out[tid] = (elem)((acc[0][tid] + acc[1][tid] + acc[2][tid] + acc[3][tid]) * inv);
 }
 
 int64_t row_tiles_of(const AttentionStepShape& s) { return ((int64_t)s.H / s.Hk * s.n + 31) / 32; }
@@ -241,7 +267,7 @@ int parts_of(const AttentionStepShape& s) {
 
 bool attention_step_supported(const AttentionStepShape& s) {
   return (double)s.B * s.Hk * row_tiles_of(s) * parts_of(s) < (double)kMostBlocks &&
-         (double)s.B * s.H * s.n < 4.0 * kMostBlocks;
+         (double)s.B * s.H * s.n < (double)kMostBlocks;
 }
 
 int64_t attention_step_ws_bytes(const AttentionStepShape& s) {
@@ -270,9 +296,9 @@ hipError_t launch_attention_step(const AttentionStepShape& s, const void* q, voi
   });
   if (err != hipSuccess || p.parts == 1) return err;
   if (s.io == TM_IO_BF16)
-    step_join_kernel<true><<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(p);
+    step_join_kernel<true><<<(unsigned)rows, 256, 0, stream>>>(p);
   else
-    step_join_kernel<false><<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(p);
+    step_join_kernel<false><<<(unsigned)rows, 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 
