@@ -3,8 +3,8 @@
 // from them.
 //
 // Matrix products are 32x32 tiles with a contraction in steps of 16, bf16 in
-// one instruction (v_mfma_f32_32x32x16_bf16) and fp32 in eight
-// (v_mfma_f32_32x32x2_f32).  Either way a lane holds 8 elements of its row (or
+// one instruction (v_mfma_f32_32x32x16_bf16) and fp32 in six of them (Planes).
+// Either way a lane holds 8 elements of its row (or
 // column) lane % 32 a step, the lower half of the wave the first 8 of a step's
 // 16 and the upper half the others; any order will do that both operands keep.
 // An accumulator has its column in lane % 32 and its rows 8 (r / 4) + 4 (lane /
@@ -13,6 +13,8 @@
 // keys: registers 8 s .. 8 s + 7 are step s, whose keys are 16 s + 4 (lane /
 // 32) + {0..3, 8..11}, and no lane hands anything to another.
 #pragma once
+
+#include <limits.h>
 
 #include <type_traits>
 
@@ -39,6 +41,9 @@ constexpr float kLowest = -1e30f;   // a running maximum before its first score
 struct Params {
   const void *q, *k, *v, *dout;
   void *out, *dq, *dk, *dv;
+  float *parts_k, *parts_v;   // the gradient's parts of dk and dv, where there are several
+  int64_t part_size;
+  int parts, ahead;
   float *lse, *stats;       // stats: the gradient's two fp32 values a query and head, stat_rows apart
   int64_t stat_rows;
   const int32_t *offsets, *lengths;
@@ -53,38 +58,77 @@ struct Params {
 // DP, as whole pieces, or as anything.
 constexpr int kOdd = 0, kPieces = 1, kFull = 2;
 
+// An fp32 factor as three bf16 numbers that add up to it (8 bits each, cut
+// off, the rest exact).  Six of the nine products are kept: what is left out
+// is below 2^-23 of a product, as one rounding of fp32, and six bf16
+// instructions take 192 cycles for a step where the fp32 ones take 512.  An
+// infinity becomes NaN on the way.
+struct Planes {
+  bf16x8 h, m, l;
+};
+
 template <bool BF16>
 struct Types;
 template <>
 struct Types<true> {
   typedef __bf16 elem;
-  typedef bf16x8 frag;
+  typedef bf16x8 frag;   // 8 elements
+  typedef bf16x8 op;     // the same as a factor
 };
 template <>
 struct Types<false> {
   typedef float elem;
   typedef f32x8 frag;
+  typedef Planes op;
 };
 
-__device__ __forceinline__ void mma(f32x16& acc, bf16x8 a, bf16x8 b) {
-  acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
-}
-__device__ __forceinline__ void mma(f32x16& acc, f32x8 a, f32x8 b) {
+__device__ __forceinline__ bf16x8 factor(bf16x8 f) { return f; }
+__device__ __forceinline__ Planes factor(f32x8 f) {
+  typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
+  u32x4 a, b, c;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], acc, 0, 0, 0);
+  for (int i = 0; i < 4; ++i) {
+    unsigned u[2], v[2], w[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float y = f[2 * i + e];
+      u[e] = __builtin_bit_cast(unsigned, y);
+      const float r = y - __builtin_bit_cast(float, u[e] & 0xffff0000u);
+      v[e] = __builtin_bit_cast(unsigned, r);
+      w[e] = __builtin_bit_cast(unsigned, r - __builtin_bit_cast(float, v[e] & 0xffff0000u));
+    }
+    a[i] = __builtin_amdgcn_perm(u[1], u[0], 0x07060302u);   // the upper halves of both
+    b[i] = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
+    c[i] = __builtin_amdgcn_perm(w[1], w[0], 0x07060302u);
+  }
+  return {__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, c)};
 }
 
-// registers 8 s .. 8 s + 7 of an accumulator as an operand, rounded to bf16
-// for bf16 tensors: a weight keeps 8 bits, as the values that it multiplies
-__device__ __forceinline__ void operand(const f32x16& x, int s, bf16x8& f) {
+// f(x, y) for the products that a b is made of, the small ones first
+template <typename F>
+__device__ __forceinline__ void products(const bf16x8& a, const bf16x8& b, F f) {
+  f(a, b);
+}
+template <typename F>
+__device__ __forceinline__ void products(const Planes& a, const Planes& b, F f) {
+  f(a.l, b.h), f(a.h, b.l), f(a.m, b.m), f(a.m, b.h), f(a.h, b.m), f(a.h, b.h);
+}
+template <typename Op>
+__device__ __forceinline__ void mma(f32x16& acc, const Op& a, const Op& b) {
+  products(a, b, [&](bf16x8 x, bf16x8 y) { acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, acc, 0, 0, 0); });
+}
+
+// registers 8 s .. 8 s + 7 of an accumulator as a factor, rounded to bf16 for
+// bf16 tensors: a weight keeps 8 bits, as the values that it multiplies
+template <typename Op>
+__device__ __forceinline__ Op operand(const f32x16& x, int s) {
   f32x8 t;
 #pragma unroll
   for (int j = 0; j < 8; ++j) t[j] = x[8 * s + j];
-  f = __builtin_convertvector(t, bf16x8);
-}
-__device__ __forceinline__ void operand(const f32x16& x, int s, f32x8& f) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = x[8 * s + j];
+  if constexpr (sizeof(Op) == sizeof(bf16x8))
+    return __builtin_convertvector(t, bf16x8);
+  else
+    return factor(t);
 }
 
 // the other half wave's value
@@ -112,6 +156,7 @@ template <bool BF16, int DP>
 struct Tile {
   typedef typename Types<BF16>::elem elem;
   typedef typename Types<BF16>::frag frag;
+  typedef typename Types<BF16>::op op;
   static constexpr int kSize = BF16 ? 2 : 4;
   static constexpr int LS = DP == 96 ? 128 : DP;
   static constexpr int RB = LS * kSize;       // bytes of a row
@@ -123,18 +168,18 @@ struct Tile {
   }
 
   // step s of row r, contraction along the row
-  static __device__ __forceinline__ frag along(const unsigned char* t, int r, int s, int half) {
+  static __device__ __forceinline__ op along(const unsigned char* t, int r, int s, int half) {
     if constexpr (BF16) {
       return *(const frag*)(t + r * RB + ((2 * s + half) ^ swz(r)) * 16);
     } else {
       const f32x4 a = *(const f32x4*)(t + r * RB + ((4 * s + 2 * half) ^ swz(r)) * 16);
       const f32x4 b = *(const f32x4*)(t + r * RB + ((4 * s + 2 * half + 1) ^ swz(r)) * 16);
-      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+      return factor(__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
 
   // step s of column c0 + lane % 32, contraction over rows r0 + 16 s + .. in an accumulator's order
-  static __device__ __forceinline__ frag across(const unsigned char* t, int r0, int s, int c0, int lane) {
+  static __device__ __forceinline__ op across(const unsigned char* t, int r0, int s, int c0, int lane) {
     const int half = lane >> 5;
     if constexpr (BF16) {
       const int l = lane & 15, col = c0 + (lane & 16) + 4 * (l & 3);
@@ -152,7 +197,7 @@ struct Tile {
         const int r = r0 + 16 * s + 4 * half + (j & 3) + 8 * (j >> 2);
         f[j] = *(const float*)(t + r * RB + ((col / 4) ^ swz(r)) * 16 + (col & 3) * 4);
       }
-      return f;
+      return factor(f);
     }
   }
 
@@ -308,14 +353,21 @@ __device__ __forceinline__ bool find(const Params& p, int stream, int unit, Plac
 // Block -> (stream, unit, head of the group).  Blocks go round the 8 XCDs.
 // With streams in eights every XCD takes whole streams, one after the other,
 // so that their keys stay in its L2; otherwise units go round the XCDs.  The
-// heads that share keys are neighbours on one XCD in both.
+// heads that share keys are neighbours on one XCD in both.  The first `ahead`
+// units of every stream (much longer ones) come before all others.
 __device__ __forceinline__ bool place_of(const Params& p, int heads, int& stream, int& unit, int& head) {
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
   head = slot % heads;
   const int u = slot / heads;
   if (p.streams % 8 == 0) {
-    stream = xcd + 8 * (u / p.units);
-    unit = u % p.units;
+    const int each = p.streams / 8, v = u - each * p.ahead;
+    if (v < 0) {
+      stream = xcd + 8 * (u % each);
+      unit = u / each;
+    } else {
+      stream = xcd + 8 * (v / (p.units - p.ahead));
+      unit = p.ahead + v % (p.units - p.ahead);
+    }
     return true;
   }
   const int64_t v = (int64_t)u * 8 + xcd;
@@ -324,16 +376,26 @@ __device__ __forceinline__ bool place_of(const Params& p, int heads, int& stream
   return unit < p.units;
 }
 
-// Scores that the mask takes away, registers of one 32 x 32 tile.  j0: the
-// key of register 0 in this lane; i: the query (KEYS_IN_ROWS; otherwise j0 and i change places).
+// Scores that the mask takes away, registers of one 32 x 32 tile: keys in rows
+// and queries in columns, or the other way round.  row0: the row of register 0
+// in this lane; col: the lane's column; some keys are below the prefix or none.
+// Behind the prefix j <= i and i - j < window are one unsigned comparison.
 template <bool KEYS_IN_ROWS>
-__device__ __forceinline__ void mask_tile(f32x16& x, int row0, int col, int window, int prefix) {
+__device__ __forceinline__ void mask_tile(f32x16& x, int row0, int col, int window, int prefix, bool some_below) {
+  const int far = KEYS_IN_ROWS ? col - row0 : row0 - col;
+  if (!some_below) {
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int row = row0 + 8 * (r >> 2) + (r & 3);
-    const int i = KEYS_IN_ROWS ? col : row, j = KEYS_IN_ROWS ? row : col;
-    const bool seen = (j <= i) & ((i - j < window) | (j < prefix));
-    x[r] = seen ? x[r] : -__builtin_inff();
+    for (int r = 0; r < 16; ++r) {
+      const int c = 8 * (r >> 2) + (r & 3);
+      x[r] = (unsigned)(KEYS_IN_ROWS ? far - c : far + c) < (unsigned)window ? x[r] : -__builtin_inff();
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int c = 8 * (r >> 2) + (r & 3), apart = KEYS_IN_ROWS ? far - c : far + c, j = KEYS_IN_ROWS ? row0 + c : col;
+      const int reach = j < prefix ? INT_MAX : window;
+      x[r] = (unsigned)apart < (unsigned)reach ? x[r] : -__builtin_inff();
+    }
   }
 }
 

@@ -18,8 +18,6 @@
 // and the scores' registers are an operand of the second product as they lie.
 // Keys and values go through LDS in tiles, loaded straight to it one tile
 // ahead.
-#include <limits.h>
-
 #include "tm_attention.h"
 
 namespace titans {
@@ -36,10 +34,10 @@ template <bool BF16>
 constexpr int keys_of() { return BF16 ? 64 : 32; }
 
 template <bool BF16, int DP, int VEC>
-__global__ void __launch_bounds__(kThreads, BF16 && DP <= 64 ? 4 : 2) attention_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, BF16 && DP <= 64 ? 3 : 2) attention_kernel(Params p) {
   typedef Tile<BF16, DP> T;
   typedef typename T::elem elem;
-  typedef typename T::frag frag;
+  typedef typename T::op op;
   constexpr int KT = keys_of<BF16>(), kBytes = KT * T::RB;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2][K, V]
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -68,8 +66,13 @@ __global__ void __launch_bounds__(kThreads, BF16 && DP <= 64 ? 4 : 2) attention_
   const typename T::template Loads<KT, kThreads, VEC> load(p.k_tok, tid);
   load(smem, kp, p.k_tok, t * KT, last, p.d, tid);
   load(smem + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
-  frag q[DP / 16];
-  T::template row<VEC>(q, qp, p.d, half);
+  op q[DP / 16];
+  {
+    typename T::frag f[DP / 16];
+    T::template row<VEC>(f, qp, p.d, half);
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) q[s] = factor(f[s]);
+  }
 
   const int window = p.window ? p.window : INT_MAX;
   const float c = p.scale * kLog2e;
@@ -87,13 +90,15 @@ __global__ void __launch_bounds__(kThreads, BF16 && DP <= 64 ? 4 : 2) attention_
     // nothing of the tile is seen by this wave's queries
     if (w0 > last || k0 > w0 + 31 || (p.window && w0 - (k0 + KT - 1) >= p.window && k0 >= p.prefix)) return;
     f32x16 x[KT / 32] = {};
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < DP / 16; ++s)
 #pragma unroll
       for (int g = 0; g < KT / 32; ++g) mma(x[g], T::along(kb, 32 * g + (lane & 31), s, half), q[s]);
+    __builtin_amdgcn_s_setprio(0);
     if (k0 + KT - 1 > w0 || (p.window && w0 + 31 - k0 >= p.window)) {
 #pragma unroll
-      for (int g = 0; g < KT / 32; ++g) mask_tile<true>(x[g], k0 + 32 * g + 4 * half, qi, window, p.prefix);
+      for (int g = 0; g < KT / 32; ++g) mask_tile<true>(x[g], k0 + 32 * g + 4 * half, qi, window, p.prefix, k0 < p.prefix);
     }
     float mx = x[0][0];
 #pragma unroll
@@ -119,13 +124,14 @@ __global__ void __launch_bounds__(kThreads, BF16 && DP <= 64 ? 4 : 2) attention_
         sum += x[g][r];
       }
     l += sum;
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < KT / 16; ++s) {
-      frag w;
-      operand(x[s / 2], s % 2, w);
+      const op w = operand<op>(x[s / 2], s % 2);
 #pragma unroll
       for (int e = 0; e < DP / 32; ++e) mma(o[e], T::across(vb, 0, s, 32 * e, lane), w);
     }
+    __builtin_amdgcn_s_setprio(0);
     };
   auto turn = [&](int buf) __attribute__((always_inline)) {
     const int k0 = t * KT;
@@ -140,12 +146,12 @@ __global__ void __launch_bounds__(kThreads, BF16 && DP <= 64 ? 4 : 2) attention_
   if (qi > last) return;
   l += other_half(l);
   const float inv = 1.f / l;
-  elem* op = (elem*)p.out + at.seq * p.o_seq + (int64_t)(at.t0 + qi) * p.o_tok + h * p.d;
+  elem* to = (elem*)p.out + at.seq * p.o_seq + (int64_t)(at.t0 + qi) * p.o_tok + h * p.d;
 #pragma unroll
   for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
     for (int g = 0; g < 4; ++g)
-      T::template store4<VEC>(op, 32 * e + 8 * g + 4 * half, p.d,
+      T::template store4<VEC>(to, 32 * e + 8 * g + 4 * half, p.d,
                               f32x4{o[e][4 * g] * inv, o[e][4 * g + 1] * inv, o[e][4 * g + 2] * inv, o[e][4 * g + 3] * inv});
   if (p.lse && half == 0)
     p.lse[((int64_t)at.seq * p.H + h) * p.N + at.t0 + qi] = kLn2 * (m + __builtin_amdgcn_logf(l));

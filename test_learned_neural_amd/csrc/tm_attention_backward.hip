@@ -16,8 +16,6 @@
 // Either kernel forms its scores so that what it owns lies in the lanes, and
 // what it sums over in the registers, where P and dS are operands as they lie
 // (tm_attention.h).  P and dS are rounded to bf16 there for bf16 tensors.
-#include <limits.h>
-
 #include "tm_attention.h"
 
 namespace titans {
@@ -64,10 +62,11 @@ __device__ __forceinline__ void zero_past(const Params& p, int row0, int n, elem
 
 // dq, and per query lse log2 e and D for the other kernel.
 template <bool BF16, int DP, int VEC>
-__global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_dq_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, (BF16 ? (DP <= 64 ? 3 : 2) : DP < 96 ? 2 : 1)) attention_dq_kernel(Params p) {
   typedef Tile<BF16, DP> T;
   typedef typename T::elem elem;
   typedef typename T::frag frag;
+  typedef typename T::op op;
   constexpr int KT = tile_of<BF16, DP>(), kBytes = KT * T::RB;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2][K, V]
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -100,18 +99,22 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
   load(smem, kp, p.k_tok, t * KT, last, p.d, tid);
   load(smem + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
 
-  frag q[DP / 16], go[DP / 16];
-  T::template row<VEC>(q, (const elem*)p.q + at.seq * p.q_seq + h * p.q_head + qt * p.q_tok, p.d, half);
+  op q[DP / 16], go[DP / 16];
   const int64_t ot = at.seq * p.o_seq + qt * p.o_tok + h * p.d, stat = ((int64_t)at.seq * p.H + h) * p.N + qt;
-  T::template row<VEC>(go, (const elem*)p.dout + ot, p.d, half);
   float D = 0.f;
   {
-    frag o[DP / 16];
-    T::template row<VEC>(o, (const elem*)p.out + ot, p.d, half);
+    frag x[DP / 16], y[DP / 16];
+    T::template row<VEC>(x, (const elem*)p.dout + ot, p.d, half);
+    T::template row<VEC>(y, (const elem*)p.out + ot, p.d, half);
 #pragma unroll
-    for (int s = 0; s < DP / 16; ++s)
+    for (int s = 0; s < DP / 16; ++s) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) D = fmaf((float)go[s][e], (float)o[s][e], D);
+      for (int e = 0; e < 8; ++e) D = fmaf((float)x[s][e], (float)y[s][e], D);
+      go[s] = factor(x[s]);
+    }
+    T::template row<VEC>(x, (const elem*)p.q + at.seq * p.q_seq + h * p.q_head + qt * p.q_tok, p.d, half);
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) q[s] = factor(x[s]);
   }
   D += other_half(D);
   const float lse = p.lse[stat] * kLog2e;
@@ -140,13 +143,12 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
         mma(x, T::along(kb, 32 * g + (lane & 31), s, half), q[s]);
         mma(y, T::along(vb, 32 * g + (lane & 31), s, half), go[s]);
       }
-      if (g0 + 31 > w0 || w0 + 31 - g0 >= window) mask_tile<true>(x, g0 + 4 * half, qi, window, p.prefix);
+      if (g0 + 31 > w0 || w0 + 31 - g0 >= window) mask_tile<true>(x, g0 + 4 * half, qi, window, p.prefix, g0 < p.prefix);
 #pragma unroll
       for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse)) * (y[r] - D);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        frag w;
-        operand(x, s, w);
+        const op w = operand<op>(x, s);
 #pragma unroll
         for (int e = 0; e < DP / 32; ++e) mma(acc[e], T::across(kb, 32 * g, s, 32 * e, lane), w);
       }
@@ -174,10 +176,11 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
 
 // dk and dv of one key head.
 template <bool BF16, int DP, int VEC>
-__global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_dkv_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, (BF16 ? (DP <= 64 ? 3 : 2) : DP < 64 ? 2 : 1)) attention_dkv_kernel(Params p) {
   typedef Tile<BF16, DP> T;
   typedef typename T::elem elem;
   typedef typename T::frag frag;
+  typedef typename T::op op;
   constexpr int QT = tile_of<BF16, DP>(), kBytes = QT * T::RB, kStage = 2 * kBytes + 2 * 64 * 4;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2][Q, dout, lse[64], D[64]]
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -186,11 +189,24 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
   if (!place_of(p, 1, stream, unit, head)) return;
   Place at;
   const bool found = find<kRows>(p, stream, unit, at);
-  if (p.offsets) zero_rows(p, unit, (elem*)p.dk + at.key_head * p.k_head, (elem*)p.dv + at.key_head * p.k_head, p.k_tok);
+  const int part = blockIdx.y;
   const int64_t kv = at.seq * p.k_seq + at.key_head * p.k_head + (int64_t)at.t0 * p.k_tok;
+  // where there are several parts, each leaves its sums in fp32
+  float *pk = p.parts_k + part * p.part_size, *pv = p.parts_v + part * p.part_size;
   elem* dk = (elem*)p.dk + kv;
   elem* dv = (elem*)p.dv + kv;
-  if (p.lengths) zero_past(p, at.tile * kRows, at.n, dk, dv, p.k_tok);
+  if (p.offsets) {
+    if (p.parts == 1)
+      zero_rows(p, unit, (elem*)p.dk + at.key_head * p.k_head, (elem*)p.dv + at.key_head * p.k_head, p.k_tok);
+    else
+      zero_rows(p, unit, pk + at.key_head * p.k_head, pv + at.key_head * p.k_head, p.k_tok);
+  }
+  if (p.lengths) {
+    if (p.parts == 1)
+      zero_past(p, at.tile * kRows, at.n, dk, dv, p.k_tok);
+    else
+      zero_past(p, at.tile * kRows, at.n, pk + kv, pv + kv, p.k_tok);
+  }
   if (!found) return;
   const int j0 = at.tile * kRows, w0 = j0 + 32 * wave, kj = w0 + (lane & 31), last = at.n - 1, G = p.H / p.Hk;
   const int window = p.window ? p.window : INT_MAX;
@@ -198,20 +214,22 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
   // tiles of queries: from the workgroup's first key to the last query in reach of its last one
   const int lo = j0 / QT;
   const int end = p.window && j0 >= p.prefix ? (int)min((int64_t)last, (int64_t)j0 + kRows - 1 + p.window - 1) : last;
-  const int per = end / QT - lo + 1, all = per * G;
+  const int per = end / QT - lo + 1, share = (per * G + p.parts - 1) / p.parts;
+  const int from = part * share, all = min(per * G, from + share);   // this part's
   if (VEC == kPieces && p.d < DP) {
     clear(smem, 2 * kStage, tid, kThreads);
     __syncthreads();
   }
   // tile number n of all: head n / per, query tile lo + n % per
-  int lh = 0, lt = lo;
+  const int lt0 = lo + from % per;
+  int lh = from / per, lt = lt0;
   const typename T::template Loads<QT, kThreads, VEC> load_q(p.q_tok, tid), load_o(p.o_tok, tid);
   auto issue = [&](unsigned char* b) {
     const int h = at.head0 + lh;
     const elem* qp = (const elem*)p.q + at.seq * p.q_seq + h * p.q_head + (int64_t)at.t0 * p.q_tok;
-    const elem* op = (const elem*)p.dout + at.seq * p.o_seq + (int64_t)at.t0 * p.o_tok + h * p.d;
+    const elem* go = (const elem*)p.dout + at.seq * p.o_seq + (int64_t)at.t0 * p.o_tok + h * p.d;
     load_q(b, qp, p.q_tok, lt * QT, last, p.d, tid);
-    load_o(b + kBytes, op, p.o_tok, lt * QT, last, p.d, tid);
+    load_o(b + kBytes, go, p.o_tok, lt * QT, last, p.d, tid);
     if (wave < 2) {   // 64 rows of lse, of D (QT of them are used)
       const float* st = p.stats + (wave ? p.stat_rows : 0) + ((int64_t)at.seq * p.H + h) * p.N + at.t0;
       __builtin_amdgcn_global_load_lds((const void*)(st + min(lt * QT + lane, last)),
@@ -219,10 +237,17 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
     }
     if (++lt == lo + per) lt = lo, ++lh;
   };
-  issue(smem);
-  frag k[DP / 16], v[DP / 16];
-  T::template row<VEC>(k, (const elem*)p.k + kv + (int64_t)min(kj, last) * p.k_tok, p.d, half);
-  T::template row<VEC>(v, (const elem*)p.v + kv + (int64_t)min(kj, last) * p.k_tok, p.d, half);
+  if (from < all) issue(smem);
+  op k[DP / 16], v[DP / 16];
+  {
+    frag x[DP / 16];
+    T::template row<VEC>(x, (const elem*)p.k + kv + (int64_t)min(kj, last) * p.k_tok, p.d, half);
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) k[s] = factor(x[s]);
+    T::template row<VEC>(x, (const elem*)p.v + kv + (int64_t)min(kj, last) * p.k_tok, p.d, half);
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) v[s] = factor(x[s]);
+  }
 
   const float c = p.scale * kLog2e;
   f32x16 ak[DP / 32] = {}, av[DP / 32] = {};
@@ -241,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
         mma(y, T::along(ob, 32 * g + (lane & 31), s, half), v[s]);
       }
       if (g0 < w0 + 31 || g0 + 31 > last || g0 + 31 - w0 >= window) {
-        mask_tile<false>(x, g0 + 4 * half, kj, window, p.prefix);
+        mask_tile<false>(x, g0 + 4 * half, kj, window, p.prefix, w0 < p.prefix);
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           x[r] = g0 + 4 * half + 8 * (r >> 2) + (r & 3) <= last ? x[r] : -__builtin_inff();
@@ -259,9 +284,7 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        frag w, z;
-        operand(x, s, w);
-        operand(ds, s, z);
+        const op w = operand<op>(x, s), z = operand<op>(ds, s);
 #pragma unroll
         for (int e = 0; e < DP / 32; ++e) {
           mma(av[e], T::across(ob, 32 * g, s, 32 * e, lane), w);
@@ -270,34 +293,66 @@ __global__ void __launch_bounds__(kThreads, BF16 || DP < 96 ? 2 : 1) attention_d
       }
     }
     };
-  int qt = lo;
+  int qt = lt0;
   auto turn = [&](int n, int buf) __attribute__((always_inline)) {
     const int q0 = qt * QT;
     if (++qt == lo + per) qt = lo;
     landed();
     step(smem + buf * kStage, smem + (buf ^ 1) * kStage, n, q0);
   };
-  for (int n = 0; n < all; n += 2) {
+  for (int n = from; n < all; n += 2) {
     turn(n, 0);
     if (n + 1 < all) turn(n + 1, 1);
   }
   if (kj > last) return;
-  dk += (int64_t)kj * p.k_tok;
-  dv += (int64_t)kj * p.k_tok;
 #pragma unroll
   for (int e = 0; e < DP / 32; ++e)
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int ch = 32 * e + 8 * g + 4 * half;
-      T::template store4<VEC>(dk, ch, p.d, f32x4{ak[e][4 * g], ak[e][4 * g + 1], ak[e][4 * g + 2], ak[e][4 * g + 3]} * p.scale);
-      T::template store4<VEC>(dv, ch, p.d, f32x4{av[e][4 * g], av[e][4 * g + 1], av[e][4 * g + 2], av[e][4 * g + 3]});
+      const f32x4 x = f32x4{ak[e][4 * g], ak[e][4 * g + 1], ak[e][4 * g + 2], ak[e][4 * g + 3]} * p.scale;
+      const f32x4 y = {av[e][4 * g], av[e][4 * g + 1], av[e][4 * g + 2], av[e][4 * g + 3]};
+      const int64_t row = (int64_t)kj * p.k_tok;
+      if (p.parts == 1) {
+        T::template store4<VEC>(dk + row, ch, p.d, x);
+        T::template store4<VEC>(dv + row, ch, p.d, y);
+      } else {
+        Tile<false, DP>::template store4<VEC>(pk + kv + row, ch, p.d, x);
+        Tile<false, DP>::template store4<VEC>(pv + kv + row, ch, p.d, y);
+      }
     }
 }
+
+// dk and dv from their parts, in the parts' order
+template <bool BF16>
+__global__ void __launch_bounds__(256) attention_join_kernel(Params p) {
+  typedef typename Types<BF16>::elem elem;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= p.part_size) return;
+  const float* from = blockIdx.y ? p.parts_v : p.parts_k;
+  float sum = from[i];
+#pragma unroll 4
+  for (int n = 1; n < p.parts; ++n) sum += from[n * p.part_size + i];
+  ((elem*)(blockIdx.y ? p.dv : p.dk))[i] = (elem)sum;
+}
+
+// Workgroups that share a tile of keys' queries: so many that the device is
+// full where tiles are few, with 4 tiles of queries each where there are.
+int parts_of(const AttentionShape& s) {
+  const int64_t blocks = attention_blocks(s, kRows, 1), tiles = ((int64_t)s.N + 31) / 32 * (s.H / s.Hk);
+  int64_t parts = 768 / blocks;
+  if (parts > tiles / 4) parts = tiles / 4;
+  return parts < 1 ? 1 : parts > 8 ? 8 : (int)parts;
+}
+
+int64_t key_elements(const AttentionShape& s) { return (s.packed ? 1 : (int64_t)s.B) * s.N * s.Hk * s.d; }
+int64_t stat_bytes(const AttentionShape& s) { return ((s.packed ? 1 : (int64_t)s.B) * s.H * s.N * 8 + 15) / 16 * 16; }
 
 }  // namespace
 
 int64_t attention_backward_ws_bytes(const AttentionShape& s) {
-  return 2 * (s.packed ? 1 : (int64_t)s.B) * s.H * s.N * 4;
+  const int parts = parts_of(s);
+  return stat_bytes(s) + (parts > 1 ? key_elements(s) * parts * 8 : 0);
 }
 
 hipError_t launch_attention_backward(const AttentionShape& s, const void* q, const void* k, const void* v,
@@ -306,20 +361,33 @@ hipError_t launch_attention_backward(const AttentionShape& s, const void* q, con
   if (s.N == 0) return hipSuccess;
   Params p = attention_params(s);
   p.q = q, p.k = k, p.v = v, p.out = (void*)out, p.lse = (float*)lse, p.dout = dout, p.offsets = offsets, p.lengths = lengths;
-  p.dq = dq, p.dk = dk, p.dv = dv, p.stats = ws, p.stat_rows = attention_backward_ws_bytes(s) / 8;
+  p.dq = dq, p.dk = dk, p.dv = dv, p.stats = ws, p.stat_rows = (s.packed ? 1 : (int64_t)s.B) * s.H * s.N;
   p.streams = s.packed ? s.Hk : s.B * s.Hk, p.units = (int)attention_units(s, kRows);
-  return by_type(s.io, s.d, [&](auto bf16, auto dp, auto vec) {
+  p.parts = parts_of(s), p.part_size = key_elements(s);
+  p.parts_k = ws + stat_bytes(s) / 4, p.parts_v = p.parts_k + p.parts * p.part_size;
+  hipError_t err = by_type(s.io, s.d, [&](auto bf16, auto dp, auto vec) {
     constexpr bool BF16 = decltype(bf16)::value;
     constexpr int DP = decltype(dp)::value, VEC = decltype(vec)::value;
-    constexpr int lds = 4 * tile_of<BF16, DP>() * Tile<BF16, DP>::RB;
+    constexpr int lds = 4 * tile_of<BF16, DP>() * Tile<BF16, DP>::RB, stats = 4 * 64 * 4;
     attention_dq_kernel<BF16, DP, VEC>
         <<<(unsigned)attention_blocks(s, kRows, s.H / s.Hk), kThreads, lds, stream>>>(p);
-    hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-    attention_dkv_kernel<BF16, DP, VEC>
-        <<<(unsigned)attention_blocks(s, kRows, 1), kThreads, lds + 4 * 64 * 4, stream>>>(p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    auto kernel = attention_dkv_kernel<BF16, DP, VEC>;
+    e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds + stats);
+    if (e != hipSuccess) return e;
+    // the keys of the prefix are seen by all queries, those behind it only in the window
+    if (s.window && !s.packed) p.ahead = (int)(((int64_t)s.prefix + kRows - 1) / kRows);
+    kernel<<<dim3((unsigned)attention_blocks(s, kRows, 1), p.parts), kThreads, lds + stats, stream>>>(p);
     return hipGetLastError();
   });
+  if (err != hipSuccess || p.parts == 1) return err;
+  const dim3 grid((unsigned)((p.part_size + 255) / 256), 2);
+  if (s.io == TM_IO_BF16)
+    attention_join_kernel<true><<<grid, 256, 0, stream>>>(p);
+  else
+    attention_join_kernel<false><<<grid, 256, 0, stream>>>(p);
+  return hipGetLastError();
 }
 
 }  // namespace titans

@@ -13,8 +13,6 @@
 //
 // New keys and values come in with the call and are stored to the cache by the
 // wave whose tile they belong to; nobody reads those rows of the cache.
-#include <limits.h>
-
 #include "tm_attention.h"
 
 namespace titans {
@@ -72,7 +70,7 @@ template <bool BF16, int DP, int VEC>
 __global__ void __launch_bounds__((64 * waves_of<BF16, DP>())) attention_step_kernel(StepParams p) {
   typedef Tile<BF16, DP> T;
   typedef typename T::elem elem;
-  typedef typename T::frag frag;
+  typedef typename T::op op;
   constexpr int W = waves_of<BF16, DP>(), kBytes = kKeys * T::RB;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   __shared__ float ml[W][2][32];
@@ -108,8 +106,13 @@ __global__ void __launch_bounds__((64 * waves_of<BF16, DP>())) attention_step_ke
   // (what was cleared is there before a load may write beside it)
   landed_in_wave();
   if (x < end) issue(mine, x);
-  frag q[DP / 16];
-  T::template row<VEC>(q, (const elem*)p.q + ((int64_t)stream * rows + min(r, rows - 1)) * p.d, p.d, half);
+  op q[DP / 16];
+  {
+    typename T::frag f[DP / 16];
+    T::template row<VEC>(f, (const elem*)p.q + ((int64_t)stream * rows + min(r, rows - 1)) * p.d, p.d, half);
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) q[i] = factor(f[i]);
+  }
 
   const float c = p.scale * kLog2e;
   float m = kLowest, l = 0.f;
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__((64 * waves_of<BF16, DP>())) attention_step_ke
     f32x16 s = {};
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) mma(s, T::along(kb, lane & 31, i, half), q[i]);
-    if (k0 + kKeys > first || last - k0 >= window) mask_tile<true>(s, k0 + 4 * half, pos, window, p.prefix);
+    if (k0 + kKeys > first || last - k0 >= window) mask_tile<true>(s, k0 + 4 * half, pos, window, p.prefix, k0 < p.prefix);
     float mx = s[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
@@ -141,8 +144,7 @@ __global__ void __launch_bounds__((64 * waves_of<BF16, DP>())) attention_step_ke
       for (int i = 0; i < 16; ++i) o[e][i] *= f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      frag w;
-      operand(s, i, w);
+      const op w = operand<op>(s, i);
 #pragma unroll
       for (int e = 0; e < DP / 32; ++e) mma(o[e], T::across(vb, 0, i, 32 * e, lane), w);
     }
@@ -192,8 +194,8 @@ __global__ void __launch_bounds__((64 * waves_of<BF16, DP>())) attention_step_ke
     const int row = 32 * rt + i;
     if (p.parts == 1) {
       const float inv = sum != 0.f ? 1.f / sum : 0.f;   // a row that sees nothing: zeros
-      elem* op = (elem*)p.out + (((int64_t)b * p.n + row % p.n) * p.H + hk * G + row / p.n) * p.d;
-      T::template store4<VEC>(op, ch, p.d, acc * inv);
+      elem* to = (elem*)p.out + (((int64_t)b * p.n + row % p.n) * p.H + hk * G + row / p.n) * p.d;
+      T::template store4<VEC>(to, ch, p.d, acc * inv);
     } else {
       const int64_t at = ((int64_t)stream * rows + row) * p.parts + part;
       Tile<false, DP>::template store4<VEC>(p.po + at * p.d, ch, p.d, acc);

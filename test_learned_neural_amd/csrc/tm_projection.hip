@@ -14,10 +14,8 @@
 // registers and r in lanes; they go through LDS once more, so that bias,
 // residual and out are met in whole rows.
 //
-// fp32 factors are taken apart into three bf16 numbers that add up to them
-// (8 bits each, by cutting off), of whose products the six largest are kept:
-// what is left out is below 2^-23 of a product, as one rounding of fp32, and
-// six bf16 instructions take 3/8 of the time of the fp32 ones.
+// fp32 factors go through the bf16 matrix cores as three planes each
+// (tm_attention.h).
 #include "tm_attention.h"
 
 namespace titans {
@@ -26,6 +24,7 @@ namespace {
 using att::bf16x4;
 using att::bf16x8;
 using att::f32x2;
+using att::factor;
 using att::f32x4;
 using att::f32x8;
 using att::f32x16;
@@ -55,47 +54,6 @@ struct Gemm {
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 // ---------------------------------------------------------------- operands
-template <bool BF16>
-struct Factor;
-template <>
-struct Factor<true> {
-  bf16x8 x;
-  __device__ __forceinline__ void set(bf16x8 f) { x = f; }
-};
-template <>
-struct Factor<false> {
-  bf16x8 h, m, l;
-  __device__ __forceinline__ void set(f32x8 f) {
-    typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
-    u32x4 a, b, c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      unsigned u[2], v[2], w[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float y = f[2 * i + e];
-        u[e] = __builtin_bit_cast(unsigned, y);
-        const float r = y - __builtin_bit_cast(float, u[e] & 0xffff0000u);
-        v[e] = __builtin_bit_cast(unsigned, r);
-        w[e] = __builtin_bit_cast(unsigned, r - __builtin_bit_cast(float, v[e] & 0xffff0000u));
-      }
-      a[i] = __builtin_amdgcn_perm(u[1], u[0], 0x07060302u);
-      b[i] = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
-      c[i] = __builtin_amdgcn_perm(w[1], w[0], 0x07060302u);
-    }
-    h = __builtin_bit_cast(bf16x8, a), m = __builtin_bit_cast(bf16x8, b), l = __builtin_bit_cast(bf16x8, c);
-  }
-};
-
-template <typename F>
-__device__ __forceinline__ void products(const Factor<true>& a, const Factor<true>& b, F f) {
-  f(a.x, b.x);
-}
-template <typename F>
-__device__ __forceinline__ void products(const Factor<false>& a, const Factor<false>& b, F f) {
-  f(a.l, b.h), f(a.h, b.l), f(a.m, b.m), f(a.m, b.h), f(a.h, b.m), f(a.h, b.h);   // the small ones first
-}
-
 // One operand's slice in LDS, and its fragments: EXTENT values of c (or r) by
 // kT of t; ALONG: rows are values, else rows are steps of t.
 template <bool BF16, bool ALONG, int EXTENT, int THREADS>
@@ -195,6 +153,7 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   typedef Slice<BF16, P_ALONG, S::TC, S::kThreads> SP;
   typedef Slice<BF16, Q_ALONG, S::TR, S::kThreads> SQ;
   typedef typename SP::elem elem;
+  typedef typename att::Types<BF16>::op Op;
   constexpr int kStage = SP::kBytes + SQ::kBytes, kLoads = SP::kLoads + SQ::kLoads;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -224,18 +183,14 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
     if (i < slices) issue(next, i);
 #pragma unroll
     for (int k = 0; k < kT / 16; ++k) {
-      Factor<BF16> q[NR];
+      Op q[NR];
 #pragma unroll
-      for (int a = 0; a < NR; ++a) q[a].set(SQ::get(cur + SP::kBytes, 32 * (NR * wr + a), k, lane));
+      for (int a = 0; a < NR; ++a) q[a] = factor(SQ::get(cur + SP::kBytes, 32 * (NR * wr + a), k, lane));
 #pragma unroll
       for (int b = 0; b < NCOL; ++b) {
-        Factor<BF16> p;
-        p.set(SP::get(cur, 32 * (NCOL * wc + b), k, lane));
+        const Op p = factor(SP::get(cur, 32 * (NCOL * wc + b), k, lane));
 #pragma unroll
-        for (int a = 0; a < NR; ++a)
-          products(p, q[a], [&](bf16x8 x, bf16x8 y) {
-            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, acc[a][b], 0, 0, 0);
-          });
+        for (int a = 0; a < NR; ++a) att::mma(acc[a][b], p, q[a]);
       }
     }
   };
@@ -337,6 +292,7 @@ template <bool BF16, int BLOCKS, bool VEC>
 __global__ void __launch_bounds__(512) narrow_kernel(Gemm g) {
   typedef typename att::Types<BF16>::elem elem;
   typedef typename att::Types<BF16>::frag frag;
+  typedef typename att::Types<BF16>::op Op;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c0 = blockIdx.x * 16, v = lane & 15;
   const elem* p = (const elem*)g.P + (int64_t)min(c0 + v, g.C - 1) * g.p_row;
@@ -363,14 +319,12 @@ __global__ void __launch_bounds__(512) narrow_kernel(Gemm g) {
 #pragma unroll 4
   for (int t0 = wave * 32; t0 < g.T; t0 += 256) {
     const int t = t0 + 8 * (lane >> 4);
-    Factor<BF16> a;
-    a.set(get(p, t));
+    const Op a = factor(get(p, t));
 #pragma unroll
     for (int b = 0; b < BLOCKS; ++b) {
-      Factor<BF16> x;
       const int64_t r = 16 * b + v < g.R ? 16 * b + v : g.R - 1;
-      x.set(get((const elem*)g.Q + r * g.q_row, t));
-      products(a, x, [&](bf16x8 y, bf16x8 z) {
+      const Op x = factor(get((const elem*)g.Q + r * g.q_row, t));
+      att::products(a, x, [&](bf16x8 y, bf16x8 z) {
         acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y, z, acc[b], 0, 0, 0);
       });
     }
