@@ -39,7 +39,7 @@ constexpr int kNarrowRows = 64;  // rows up to which the narrow kernel runs
 __device__ const float4 kZeros[1] = {};
 
 struct Gemm {
-  const void *P, *Q;
+  const void *P, *Q, *Q2;    // Q2: what Q was rounded by, for the parts behind the first half (or null)
   int64_t p_row, q_row;      // elements from one row to the next
   int64_t R, T;              // rows of out, length of the sum
   int C;                     // columns of out
@@ -68,43 +68,69 @@ struct Slice {
   static constexpr int kLoads = kBytes / 16 / THREADS;   // of a thread
   static_assert(kBytes % (16 * THREADS) == 0, "");
 
-  static __device__ __forceinline__ int swz(int r) {
-    if (NC == 4) return (r >> 1) & 3;
-    if (NC == 8) return ALONG ? r & 7 : (r & 1) << 2 | ((r >> 1) & 3);
-    return (r & 3) << 2 | ((r >> 2) & 3);
-  }
+  static __device__ __forceinline__ int swz(int r) { return att::swizzle<NC>(r); }
 
-  // values v0.. and steps t0..; `values` and `end` bound both.  Values past the
-  // end are some other value (their results are not stored), steps are zero.
-  template <bool VEC>
-  static __device__ __forceinline__ void load(unsigned char* s, const elem* src, int64_t row, int64_t v0, int64_t values,
-                                              int64_t t0, int64_t end, int tid) {
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // A thread's pieces of a slice: their distances from the slice's start (32
+  // bits: 256 rows of 2^22 elements), which is the wave's.  Values past the
+  // end are some other value (their results are not stored).
+  struct Loads {
+    uint32_t off[kLoads];
+
+    // values v0 .. `values` - 1 of rows `row` elements apart
+    __device__ __forceinline__ Loads(int64_t row, int64_t v0, int64_t values, int tid) {
+      const int most = (int)(values - v0 < EXTENT ? values - v0 : EXTENT);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int base = i * THREADS + wave * 64, at = base + (tid & 63);
-      const int r = at / NC, c = ((at % NC) ^ swz(r)) * PC;
-      const int64_t t = t0 + (ALONG ? c : r);
-      if constexpr (VEC) {
-        int64_t v = v0 + (ALONG ? r : c);
-        if (v >= values) v = ALONG ? values - 1 : values - PC;
-        const elem* p = src + (ALONG ? v * row + t : t * row + v);
-        if (t >= end) p = (const elem*)kZeros;
-        __builtin_amdgcn_global_load_lds((const void*)p, (lds_void_ptr)(s + base * 16), 16, 0, 0);
-      } else {
-        elem x[PC];
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = i * THREADS + tid, r = at / NC, c = ((at % NC) ^ swz(r)) * PC;
+        const int v = ALONG ? min(r, most - 1) : min(c, max(most - PC, 0));
+        off[i] = (uint32_t)((ALONG ? v : r) * (uint32_t)row + (ALONG ? c : v)) * kSize;
+      }
+    }
+    // the slice at step t of the sum straight to LDS; steps from `end` on are zero
+    __device__ __forceinline__ void wide(unsigned char* s, const elem* src, int64_t row, int64_t v0, int64_t t, int64_t end,
+                                         int tid) const {
+      const elem* start = src + (ALONG ? v0 * row + t : t * row + v0);
+      const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+      const bool all = t + kT <= end;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = i * THREADS + tid, r = at / NC, c = ((at % NC) ^ swz(r)) * PC;
+        if (all) {
+          __builtin_amdgcn_global_load_lds((const void*)((const char*)start + off[i]),
+                                           (lds_void_ptr)(s + (i * THREADS + wave * 64) * 16), 16, 0, 0);
+        } else {
+          const void* p = t + (ALONG ? c : r) < end ? (const void*)((const char*)start + off[i]) : (const void*)kZeros;
+          __builtin_amdgcn_global_load_lds(p, (lds_void_ptr)(s + (i * THREADS + wave * 64) * 16), 16, 0, 0);
+        }
+      }
+    }
+    // the same element by element, where rows are not made of 16-byte pieces: into registers, then to LDS
+    typedef elem Held[kLoads][PC];
+    static __device__ __forceinline__ void fetch(Held& x, const elem* src, int64_t row, int64_t v0, int64_t values,
+                                                 int64_t t0, int64_t end, int tid) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = i * THREADS + tid, r = at / NC, c = ((at % NC) ^ swz(r)) * PC;
 #pragma unroll
         for (int e = 0; e < PC; ++e) {
           int64_t v = v0 + (ALONG ? r : c + e);
           v = v < values ? v : values - 1;
-          const int64_t te = t + (ALONG ? e : 0);
-          x[e] = te < end ? src[ALONG ? v * row + te : te * row + v] : (elem)0.f;
+          const int64_t t = t0 + (ALONG ? c + e : r);
+          x[i][e] = t < end ? src[ALONG ? v * row + t : t * row + v] : (elem)0.f;
         }
-#pragma unroll
-        for (int e = 0; e < PC; ++e) ((elem*)(s + at * 16))[e] = x[e];
       }
     }
-  }
+    static __device__ __forceinline__ void put(unsigned char* s, const Held& x, int tid) {
+      typedef __attribute__((ext_vector_type(PC))) elem piece;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        piece v;
+#pragma unroll
+        for (int e = 0; e < PC; ++e) v[e] = x[i][e];
+        *(piece*)(s + (i * THREADS + tid) * 16) = v;
+      }
+    }
+  };
 
   // value v0 + lane % 32, steps 16 k + 8 (lane / 32) + 0..7
   static __device__ __forceinline__ frag get(const unsigned char* s, int v0, int k, int lane) {
@@ -136,6 +162,48 @@ struct Slice {
     }
   }
 };
+
+// 8 neighbouring elements of a row, n of which are there; whole: as pieces of 16 bytes
+__device__ __forceinline__ f32x8 load8(const __bf16* p, int n, bool whole) {
+  if (whole) return __builtin_convertvector(*(const bf16x8*)p, f32x8);
+  f32x8 x = {};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < n) x[e] = (float)p[e];
+  return x;
+}
+__device__ __forceinline__ f32x8 load8(const float* p, int n, bool whole) {
+  f32x8 x = {};
+  if (whole) {
+    const f32x4 a = *(const f32x4*)p;
+    f32x4 b = {};
+    if (n > 4) b = *(const f32x4*)(p + 4);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < n) x[e] = p[e];
+  return x;
+}
+__device__ __forceinline__ void store8(__bf16* p, f32x8 x, int n, bool whole) {
+  if (whole) {
+    *(bf16x8*)p = __builtin_convertvector(x, bf16x8);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < n) p[e] = (__bf16)x[e];
+}
+__device__ __forceinline__ void store8(float* p, f32x8 x, int n, bool whole) {
+  if (whole) {
+    *(f32x4*)p = __builtin_shufflevector(x, x, 0, 1, 2, 3);
+    if (n > 4) *(f32x4*)(p + 4) = __builtin_shufflevector(x, x, 4, 5, 6, 7);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < n) p[e] = x[e];
+}
 
 // ---------------------------------------------------------------- the tile kernel
 // TR x TC of out by WR x WC waves.
@@ -172,15 +240,37 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   const int64_t r0 = (int64_t)(8 * group + id % rows_here) * S::TR;
   const int c0 = id / rows_here * S::TC;
 
-  const int64_t t0 = part * g.per, t1 = t0 + g.per < g.T ? t0 + g.per : g.T;
+  const bool second = g.Q2 && part >= g.parts / 2;
+  const elem *P = (const elem*)g.P, *Q = (const elem*)(second ? g.Q2 : g.Q);
+  const int64_t t0 = (second ? part - g.parts / 2 : part) * g.per, t1 = t0 + g.per < g.T ? t0 + g.per : g.T;
   const int slices = t1 > t0 ? (int)((t1 - t0 + kT - 1) / kT) : 0;
-  auto issue = [&](unsigned char* s, int i) {
-    SP::template load<VEC>(s, (const elem*)g.P, g.p_row, c0, g.C, t0 + (int64_t)i * kT, t1, tid);
-    SQ::template load<VEC>(s + SP::kBytes, (const elem*)g.Q, g.q_row, r0, g.R, t0 + (int64_t)i * kT, t1, tid);
+  const typename SP::Loads load_p(g.p_row, c0, g.C, tid);
+  const typename SQ::Loads load_q(g.q_row, r0, g.R, tid);
+  typename SP::Loads::Held hp;
+  typename SQ::Loads::Held hq;
+  auto issue = [&](unsigned char* s, int i) __attribute__((always_inline)) {
+    const int64_t t = t0 + (int64_t)i * kT;
+    if constexpr (VEC) {
+      load_p.wide(s, P, g.p_row, c0, t, t1, tid);
+      load_q.wide(s + SP::kBytes, Q, g.q_row, r0, t, t1, tid);
+    } else {
+      SP::Loads::fetch(hp, P, g.p_row, c0, g.C, t, t1, tid);
+      SQ::Loads::fetch(hq, Q, g.q_row, r0, g.R, t, t1, tid);
+    }
+  };
+  auto put = [&](unsigned char* s) __attribute__((always_inline)) {
+    if constexpr (!VEC) {
+      SP::Loads::put(s, hp, tid);
+      SQ::Loads::put(s + SP::kBytes, hq, tid);
+    }
   };
   f32x16 acc[NR][NCOL] = {};
-  auto step = [&](const unsigned char* __restrict__ cur, unsigned char* __restrict__ next, int i) {
-    if (i < slices) issue(next, i);
+  // slice i + STAGES - 1 goes to `next` (restrict: the transposing reads of
+  // this one do not wait for it)
+  auto step = [&](const unsigned char* __restrict__ cur, unsigned char* __restrict__ next, int i)
+                  __attribute__((always_inline)) {
+    const bool more = i + S::STAGES - 1 < slices;
+    if (more) issue(next, i + S::STAGES - 1);
 #pragma unroll
     for (int k = 0; k < kT / 16; ++k) {
       Op q[NR];
@@ -193,20 +283,25 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
         for (int a = 0; a < NR; ++a) att::mma(acc[a][b], p, q[a]);
       }
     }
+    if (more) put(next);
   };
 #pragma unroll
   for (int i = 0; i < S::STAGES - 1; ++i)
-    if (i < slices) issue(smem + i * kStage, i);
-  int cur = 0, next = S::STAGES - 1;
-  for (int i = 0; i < slices; ++i) {
-    // this slice has landed; those issued after it may still be under way
-    if (!VEC || S::STAGES == 2 || i + S::STAGES - 2 >= slices)
-      att::landed();
-    else
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::STAGES - 2) * kLoads) : "memory");
-    step(smem + cur * kStage, smem + next * kStage, i + S::STAGES - 1);
-    cur = cur + 1 == S::STAGES ? 0 : cur + 1;
-    next = next + 1 == S::STAGES ? 0 : next + 1;
+    if (i < slices) {
+      issue(smem + i * kStage, i);
+      put(smem + i * kStage);
+    }
+  for (int i = 0; i < slices;) {
+#pragma unroll
+    for (int st = 0; st < S::STAGES; ++st) {   // (places in LDS that are constant)
+      // this slice has landed; those issued after it may still be under way
+      if (!VEC || S::STAGES == 2 || i + S::STAGES - 2 >= slices)
+        att::landed();
+      else
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::STAGES - 2) * kLoads) : "memory");
+      step(smem + st * kStage, smem + (st + S::STAGES - 1) % S::STAGES * kStage, i);
+      if (++i >= slices) break;
+    }
   }
 
   // through LDS, 32 rows of the wave's columns at a time
@@ -215,7 +310,7 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   __syncthreads();
   float* mine = (float*)(smem + wave * 32 * LD * 4);
   const int ch = lane % kLanes * 8, c = c0 + wc * CW + ch;
-  const bool whole = F32_OUT ? g.C % 4 == 0 : g.C % 8 == 0;   // rows of 16-byte pieces
+  const bool whole = g.C % (F32_OUT || !BF16 ? 4 : 8) == 0;   // rows of 16-byte pieces
   float bias[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) bias[e] = g.bias && c + e < g.C ? g.bias[c + e] : 0.f;
@@ -238,47 +333,17 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
       f32x8 x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
       const int64_t o = r * g.C + c;
       if constexpr (F32_OUT) {
-        float* out = (float*)g.out + (int64_t)part * g.R * g.C + o;
-        if (whole) {
-          *(f32x4*)out = x0;
-          if (c + 4 < g.C) *(f32x4*)(out + 4) = x1;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e < g.C) out[e] = x[e];
-        }
+        store8((float*)g.out + (int64_t)part * g.R * g.C + o, x, g.C - c < 8 ? g.C - c : 8, whole);
       } else {
-        typedef __attribute__((ext_vector_type(8))) elem elem8;
-        elem* out = (elem*)g.out + o;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += bias[e];
-        if (g.pre) {
-          elem* pre = (elem*)g.pre + o;
-          if (whole)
-            *(elem8*)pre = __builtin_convertvector(x, elem8);
-          else
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (c + e < g.C) pre[e] = (elem)x[e];
-        }
+        const int n = g.C - c < 8 ? g.C - c : 8;
+        if (g.pre) store8((elem*)g.pre + o, x, n, whole);
         if (g.silu)
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] *= sigmoid(x[e]);
-        if (g.residual) {
-          const elem* res = (const elem*)g.residual + o;
-          if (whole)
-            x += __builtin_convertvector(*(const elem8*)res, f32x8);
-          else
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (c + e < g.C) x[e] += (float)res[e];
-        }
-        if (whole)
-          *(elem8*)out = __builtin_convertvector(x, elem8);
-        else
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e < g.C) out[e] = (elem)x[e];
+        if (g.residual) x += load8((const elem*)g.residual + o, n, whole);
+        store8((elem*)g.out + o, x, n, whole);
       }
     }
   }
@@ -351,17 +416,19 @@ __global__ void __launch_bounds__(512) narrow_kernel(Gemm g) {
 }
 
 // ---------------------------------------------------------------- dz and dbias
-// dz = dout act'(pre), rounded to the io type that the two products read, and
-// its column sums: a workgroup has 64 lanes x PC columns and `per` rows, which
-// its 4 waves share.
+// dz = dout act'(pre) and its column sums.  The products read it in the io
+// type; dx is of that type too, but dweight is fp32, for which a bf16 dz comes
+// with what it was rounded by (dz2: together 16 bits, 2^-18 off), the second
+// half of a sum twice as long.  A workgroup has 64 lanes x PC columns and `per`
+// rows, which its 4 waves share.
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(256) slope_kernel(const void* dout_, const void* pre_, void* dz_, float* sums, int64_t R,
-                                                    int C, int64_t per) {
+__global__ void __launch_bounds__(256) slope_kernel(const void* dout_, const void* pre_, void* dz_, void* dz2_, float* sums,
+                                                    int64_t R, int C, int64_t per) {
   typedef typename att::Types<BF16>::elem elem;
   constexpr int PC = VEC ? (BF16 ? 8 : 4) : 1;
   typedef __attribute__((ext_vector_type(PC))) elem piece;
   const elem *dout = (const elem*)dout_, *pre = (const elem*)pre_;
-  elem* dz = (elem*)dz_;
+  elem *dz = (elem*)dz_, *dz2 = (elem*)dz2_;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = ((int)blockIdx.x * 64 + lane) * PC;
   const int64_t r0 = blockIdx.y * per, r1 = r0 + per < R ? r0 + per : R;
@@ -370,18 +437,25 @@ __global__ void __launch_bounds__(256) slope_kernel(const void* dout_, const voi
 #pragma unroll 4
     for (int64_t r = r0 + wave; r < r1; r += 4) {
       const int64_t o = r * C + c;
-      piece x = *(const piece*)(dout + o);
+      const piece x = *(const piece*)(dout + o);
+      float y[PC];
+#pragma unroll
+      for (int e = 0; e < PC; ++e) y[e] = (float)x[e];
       if (pre) {
         const piece z = *(const piece*)(pre + o);
+        piece hi, lo;
 #pragma unroll
         for (int e = 0; e < PC; ++e) {
           const float a = (float)z[e], sg = sigmoid(a);
-          x[e] = (elem)((float)x[e] * sg * fmaf(a, 1.f - sg, 1.f));
+          y[e] *= sg * fmaf(a, 1.f - sg, 1.f);
+          hi[e] = (elem)y[e];
+          lo[e] = (elem)(y[e] - (float)hi[e]);
         }
-        *(piece*)(dz + o) = x;
+        *(piece*)(dz + o) = hi;
+        if (BF16) *(piece*)(dz2 + o) = lo;
       }
 #pragma unroll
-      for (int e = 0; e < PC; ++e) sum[e] += (float)x[e];
+      for (int e = 0; e < PC; ++e) sum[e] += y[e];
     }
   __shared__ float red[4][64 * PC];
 #pragma unroll
@@ -481,14 +555,22 @@ hipError_t launch_narrow(const Gemm& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// the weight's gradient: parts of the rows that together fill the device
+// The weight's gradient: parts of the rows that together fill the device, a
+// part with 128 rows at least; large tiles where there are enough of them.
+// With two planes of dz half of the parts belong to each.
 int weight_parts(const ProjectionShape& s, bool* big) {
-  *big = large(s.O, s.K, s.io) || (s.O >= 128 && s.K >= 128);
-  const int64_t tr = *big ? (s.io == TM_IO_BF16 ? 256 : 128) : 64, tc = *big ? 128 : 64;
-  const int64_t tiles = (s.O + tr - 1) / tr * ((s.K + tc - 1) / tc);
-  int64_t parts = (512 + tiles - 1) / tiles, most = s.M / 256;   // a part has 256 rows at least
-  if (parts > most) parts = most;
-  return parts < 1 ? 1 : parts > 64 ? 64 : (int)parts;
+  const int planes = s.silu && s.io == TM_IO_BF16 ? 2 : 1;
+  int64_t parts = 1;
+  for (int pass = 0; pass < 2; ++pass) {
+    *big = pass == 0;
+    const int64_t tr = *big ? (s.io == TM_IO_BF16 ? 256 : 128) : 64, tc = *big ? 128 : 64;
+    const int64_t tiles = (s.O + tr - 1) / tr * ((s.K + tc - 1) / tc), most = s.M / 128 > 1 ? s.M / 128 : 1;
+    parts = (512 / planes + tiles - 1) / tiles;
+    if (parts > most) parts = most;
+    if (parts > 64) parts = 64;
+    if (tiles * parts * planes >= 192) break;
+  }
+  return (int)parts * planes;
 }
 
 int slope_parts(const ProjectionShape& s) {
@@ -506,7 +588,8 @@ int64_t round_t(int64_t x) { return (x + kT - 1) / kT * kT; }
 
 bool projection_supported(const ProjectionShape& s) {
   const double m = (double)(s.M / 64 + 1), k = (double)(s.K / 64 + 1), o = (double)(s.O / 64 + 1);
-  return m * o < (double)kMostBlocks && m * k < (double)kMostBlocks && o * k * 64 < (double)kMostBlocks;
+  return m * o < (double)kMostBlocks && m * k < (double)kMostBlocks && o * k * 128 < (double)kMostBlocks &&
+         s.K <= 1 << 22 && s.O <= 1 << 22;   // (Loads' distances)
 }
 
 hipError_t launch_projection(const ProjectionShape& s, const void* x, const void* weight, const float* bias,
@@ -523,11 +606,11 @@ hipError_t launch_projection(const ProjectionShape& s, const void* x, const void
   return launch_gemm<true, true, false>(g, s.io, large(s.M, s.O, s.io), stream);
 }
 
-// dz (where there is an activation), the weight's parts, the bias's sums
+// dz and its second plane (where there is an activation), the weight's parts, the bias's sums
 int64_t projection_backward_ws_bytes(const ProjectionShape& s) {
   bool big;
   const int parts = weight_parts(s, &big);
-  return (s.silu ? round16(s.M * s.O * (s.io == TM_IO_BF16 ? 2 : 4)) : 0) +
+  return (s.silu ? 2 * round16(s.M * s.O * (s.io == TM_IO_BF16 ? 2 : 4)) : 0) +
          (parts > 1 ? round16((int64_t)parts * s.O * s.K * 4) : 0) + round16((int64_t)slope_parts(s) * s.O * 4);
 }
 
@@ -538,8 +621,11 @@ hipError_t launch_projection_backward(const ProjectionShape& s, const void* x, c
   bool big;
   const int parts = weight_parts(s, &big), sparts = slope_parts(s);
   char* at = (char*)ws;
-  void* dz = s.silu ? at : nullptr;
-  if (s.silu) at += round16(s.M * s.O * esz);
+  void *dz = nullptr, *dz2 = nullptr;
+  if (s.silu) {
+    dz = at, at += round16(s.M * s.O * esz);
+    dz2 = at, at += round16(s.M * s.O * esz);
+  }
   float* wparts = parts > 1 ? (float*)at : nullptr;
   if (wparts) at += round16((int64_t)parts * s.O * s.K * 4);
   float* bparts = (float*)at;
@@ -549,7 +635,7 @@ hipError_t launch_projection_backward(const ProjectionShape& s, const void* x, c
   const int64_t per = (s.M + sparts - 1) / sparts;
   auto slope = s.io == TM_IO_BF16 ? (whole ? slope_kernel<true, true> : slope_kernel<true, false>)
                                   : (whole ? slope_kernel<false, true> : slope_kernel<false, false>);
-  slope<<<grid, 256, 0, stream>>>(dout, s.silu ? pre : nullptr, dz, sparts > 1 ? bparts : dbias, s.M, s.O, per);
+  slope<<<grid, 256, 0, stream>>>(dout, s.silu ? pre : nullptr, dz, dz2, sparts > 1 ? bparts : dbias, s.M, s.O, per);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const void* z = s.silu ? dz : dout;
@@ -562,7 +648,10 @@ hipError_t launch_projection_backward(const ProjectionShape& s, const void* x, c
   }
   g = Gemm();
   g.P = x, g.Q = z, g.p_row = s.K, g.q_row = s.O, g.R = s.O, g.C = s.K, g.T = s.M;
-  g.parts = parts, g.per = round_t((s.M + parts - 1) / parts), g.out = parts > 1 ? wparts : dweight;
+  const bool two = s.silu && s.io == TM_IO_BF16;
+  const int64_t each = two ? parts / 2 : parts;
+  if (two) g.Q2 = dz2;
+  g.parts = parts, g.per = round_t((s.M + each - 1) / each), g.out = parts > 1 ? wparts : dweight;
   err = launch_gemm<false, false, true>(g, s.io, big, stream);
   if (err != hipSuccess || (parts == 1 && sparts == 1)) return err;
   const int64_t n = (int64_t)s.O * s.K;
