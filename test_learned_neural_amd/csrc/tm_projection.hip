@@ -54,6 +54,9 @@ struct Gemm {
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 // ---------------------------------------------------------------- operands
+// How rows lie in memory: as whole 16-byte pieces, as fp32 elements, as anything.
+constexpr int kPieces = 0, kWords = 1, kOdd = 2;
+
 // One operand's slice in LDS, and its fragments: EXTENT values of c (or r) by
 // kT of t; ALONG: rows are values, else rows are steps of t.
 template <bool BF16, bool ALONG, int EXTENT, int THREADS>
@@ -91,32 +94,54 @@ struct Slice {
                                          int tid) const {
       const elem* start = src + (ALONG ? v0 * row + t : t * row + v0);
       const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-      const bool all = t + kT <= end;
+      if (t + kT <= end) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int at = i * THREADS + tid, r = at / NC, c = ((at % NC) ^ swz(r)) * PC;
-        if (all) {
+        for (int i = 0; i < kLoads; ++i)
           __builtin_amdgcn_global_load_lds((const void*)((const char*)start + off[i]),
                                            (lds_void_ptr)(s + (i * THREADS + wave * 64) * 16), 16, 0, 0);
-        } else {
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int at = i * THREADS + tid, r = at / NC, c = ((at % NC) ^ swz(r)) * PC;
           const void* p = t + (ALONG ? c : r) < end ? (const void*)((const char*)start + off[i]) : (const void*)kZeros;
           __builtin_amdgcn_global_load_lds(p, (lds_void_ptr)(s + (i * THREADS + wave * 64) * 16), 16, 0, 0);
         }
+        asm volatile("; the last slice");   // (or the compiler joins the two, and the whole one pays for it)
       }
     }
-    // the same element by element, where rows are not made of 16-byte pieces: into registers, then to LDS
+    // the same by elements of 4 bytes, for fp32 rows that are not made of 16-byte pieces
+    static __device__ __forceinline__ void words(unsigned char* s, const elem* src, int64_t row, int64_t v0, int64_t values,
+                                                 int64_t t, int64_t end, int tid) {
+      const elem* start = src + (ALONG ? v0 * row + t : t * row + v0);
+      const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), most = (int)(values - v0 < EXTENT ? values - v0 : EXTENT) - 1;
+#pragma unroll
+      for (int i = 0; i < kBytes / 4 / THREADS; ++i) {
+        const int at = i * THREADS + tid, r = at / 4 / NC, c = ((at / 4 % NC) ^ swz(r)) * 4 + at % 4;
+        const int v = min(ALONG ? r : c, most), dt = ALONG ? c : r;
+        const void* p = (const char*)start + (uint32_t)((ALONG ? v : dt) * (uint32_t)row + (ALONG ? dt : v)) * 4u;
+        if (t + dt >= end) p = (const void*)kZeros;
+        __builtin_amdgcn_global_load_lds(p, (lds_void_ptr)(s + (i * THREADS + wave * 64) * 4), 4, 0, 0);
+      }
+    }
+    // the same into registers, then to LDS, where rows are not made of whole pieces: 16 bytes from any address
     typedef elem Held[kLoads][PC];
     static __device__ __forceinline__ void fetch(Held& x, const elem* src, int64_t row, int64_t v0, int64_t values,
                                                  int64_t t0, int64_t end, int tid) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int at = i * THREADS + tid, r = at / NC, c = ((at % NC) ^ swz(r)) * PC;
+        const int64_t t = t0 + (ALONG ? c : r);
+        int64_t v = v0 + (ALONG ? r : c);
+        const bool whole = ALONG ? t + PC <= end : t < end && v + PC <= values;
+        if (ALONG && v >= values) v = values - 1;
+        if (whole) {
+          __builtin_memcpy(x[i], src + (ALONG ? v * row + t : t * row + v), 16);
+        } else {
 #pragma unroll
-        for (int e = 0; e < PC; ++e) {
-          int64_t v = v0 + (ALONG ? r : c + e);
-          v = v < values ? v : values - 1;
-          const int64_t t = t0 + (ALONG ? c + e : r);
-          x[i][e] = t < end ? src[ALONG ? v * row + t : t * row + v] : (elem)0.f;
+          for (int e = 0; e < PC; ++e) {
+            const int64_t te = t + (ALONG ? e : 0), ve = ALONG ? v : v + e < values ? v + e : values - 1;
+            x[i][e] = te < end ? src[ALONG ? ve * row + te : te * row + ve] : (elem)0.f;
+          }
         }
       }
     }
@@ -205,41 +230,117 @@ __device__ __forceinline__ void store8(float* p, f32x8 x, int n, bool whole) {
     if (e < n) p[e] = x[e];
 }
 
+// A wave's accumulators, 32 NR rows from r0 on by 32 NCOL columns from c0 on,
+// to memory: 32 x 32 at a time through 4 KB of LDS, so that bias, residual and
+// out are met in pieces of rows.  (A wave's LDS operations stay in their order:
+// only the compiler has to keep it.)
+constexpr int kPiece = 4096;
+
+template <bool BF16, bool F32_OUT, int NR, int NCOL>
+__device__ __forceinline__ void finish(const Gemm& g, f32x16 (&acc)[NR][NCOL], unsigned char* mine, int64_t r0, int c0,
+                                       int part, int lane) {
+  typedef typename att::Types<BF16>::elem elem;
+  typedef __attribute__((ext_vector_type(8))) elem elem8;
+  const bool whole = g.C % (F32_OUT || !BF16 ? 4 : 8) == 0;   // rows of 16-byte pieces
+  // The residual may be out, so that no piece of it could pass a store: where
+  // pieces are whole, those of 32 rows are sent for ahead of the rows before.
+  const bool ahead = !F32_OUT && g.residual && g.C % 8 == 0;
+  elem8 res[2][F32_OUT ? 1 : NCOL][2];
+  auto send = [&](int a) __attribute__((always_inline)) {
+    if constexpr (!F32_OUT) {
+#pragma unroll
+      for (int b = 0; b < NCOL; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int64_t r = r0 + 32 * a + 16 * i + lane / 4;
+          const int c = c0 + 32 * b + lane % 4 * 8;
+          if (r < g.R && c < g.C) res[a & 1][b][i] = *(const elem8*)((const elem*)g.residual + r * g.C + c);
+        }
+    }
+  };
+  if (ahead) send(0);
+#pragma unroll
+  for (int a = 0; a < NR; ++a) {
+    if (ahead && a + 1 < NR) send(a + 1);
+#pragma unroll
+    for (int b = 0; b < NCOL; ++b) {
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int u = 0; u < 4; ++u)   // 16-byte chunk c of row r at c ^ (r & 7)
+        *(f32x4*)(mine + (lane & 31) * 128 + ((2 * u + (lane >> 5)) ^ (lane & 7)) * 16) =
+            f32x4{acc[a][b][4 * u], acc[a][b][4 * u + 1], acc[a][b][4 * u + 2], acc[a][b][4 * u + 3]};
+      asm volatile("" ::: "memory");
+      const int c = c0 + 32 * b + lane % 4 * 8, n = g.C - c < 8 ? g.C - c : 8;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = 16 * i + lane / 4;
+        const int64_t r = r0 + 32 * a + row;
+        if (r >= g.R || n <= 0) continue;
+        const f32x4 x0 = *(const f32x4*)(mine + row * 128 + ((lane % 4 * 2) ^ (row & 7)) * 16);
+        const f32x4 x1 = *(const f32x4*)(mine + row * 128 + ((lane % 4 * 2 + 1) ^ (row & 7)) * 16);
+        f32x8 x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
+        const int64_t o = r * g.C + c;
+        if constexpr (F32_OUT) {
+          store8((float*)g.out + (int64_t)part * g.R * g.C + o, x, n, whole);
+        } else {
+          if (g.bias) x += load8(g.bias + c, n, false);
+          if (g.pre) store8((elem*)g.pre + o, x, n, whole);
+          if (g.silu)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= sigmoid(x[e]);
+          if (ahead)
+            x += __builtin_convertvector(res[a & 1][b][i], f32x8);
+          else if (g.residual)
+            x += load8((const elem*)g.residual + o, n, whole);
+          store8((elem*)g.out + o, x, n, whole);
+        }
+      }
+    }
+  }
+}
+
+// Tile `id` of all, part by part: an XCD's tiles run one after the other, and
+// walk the columns of 8 row tiles at a time, so that both factors stay in its
+// L2.
+template <int TR, int TC>
+__device__ __forceinline__ void tile_of(const Gemm& g, unsigned id, int& part, int64_t& r0, int& c0) {
+  const unsigned tiles = (unsigned)g.row_tiles * g.col_tiles;
+  part = id / tiles;
+  id -= part * tiles;
+  const int group = id / (8 * g.col_tiles), rows = min(8, g.row_tiles - 8 * group);
+  id -= group * 8 * g.col_tiles;
+  r0 = (int64_t)(8 * group + id % rows) * TR;
+  c0 = id / rows * TC;
+}
+
 // ---------------------------------------------------------------- the tile kernel
 // TR x TC of out by WR x WC waves.
 template <bool BF16_, int TR_, int TC_, int WR_, int WC_, int STAGES_>
-struct Shape2 {
+struct Form {
   static constexpr bool BF16 = BF16_;
   static constexpr int TR = TR_, TC = TC_, WR = WR_, WC = WC_, STAGES = STAGES_;
   static constexpr int kThreads = 64 * WR * WC;
 };
 
-template <typename S, bool P_ALONG, bool Q_ALONG, bool VEC, bool F32_OUT>
+template <typename S, bool P_ALONG, bool Q_ALONG, int KIND, bool F32_OUT>
 __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   constexpr bool BF16 = S::BF16;
-  constexpr int NR = S::TR / S::WR / 32, NCOL = S::TC / S::WC / 32, CW = 32 * NCOL;
+  constexpr int NR = S::TR / S::WR / 32, NCOL = S::TC / S::WC / 32;
   typedef Slice<BF16, P_ALONG, S::TC, S::kThreads> SP;
   typedef Slice<BF16, Q_ALONG, S::TR, S::kThreads> SQ;
   typedef typename SP::elem elem;
   typedef typename att::Types<BF16>::op Op;
-  constexpr int kStage = SP::kBytes + SQ::kBytes, kLoads = SP::kLoads + SQ::kLoads;
+  constexpr int kStage = SP::kBytes + SQ::kBytes, kLoads = (SP::kLoads + SQ::kLoads) * (KIND == kWords ? 4 : 1);
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / S::WC, wc = wave % S::WC;
-
-  // Blocks go round the 8 XCDs; each takes a run of tiles that walks the
-  // columns of 8 row tiles at a time, so that both factors stay in its L2
-  const unsigned tiles = (unsigned)g.row_tiles * g.col_tiles, all = tiles * g.parts;
-  const unsigned share = (all + 7) / 8;
-  unsigned id = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+  // blocks go round the 8 XCDs
+  const unsigned all = (unsigned)g.row_tiles * g.col_tiles * g.parts, share = (all + 7) / 8;
+  const unsigned id = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
   if (id >= all || (blockIdx.x >> 3) >= share) return;
-  const int part = id / tiles;
-  id -= part * tiles;
-  const int group = id / (8 * g.col_tiles), rows_here = min(8, g.row_tiles - 8 * group);
-  id -= group * 8 * g.col_tiles;
-  const int64_t r0 = (int64_t)(8 * group + id % rows_here) * S::TR;
-  const int c0 = id / rows_here * S::TC;
-
+  int part, c0;
+  int64_t r0;
+  tile_of<S::TR, S::TC>(g, id, part, r0, c0);
   const bool second = g.Q2 && part >= g.parts / 2;
   const elem *P = (const elem*)g.P, *Q = (const elem*)(second ? g.Q2 : g.Q);
   const int64_t t0 = (second ? part - g.parts / 2 : part) * g.per, t1 = t0 + g.per < g.T ? t0 + g.per : g.T;
@@ -250,16 +351,19 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   typename SQ::Loads::Held hq;
   auto issue = [&](unsigned char* s, int i) __attribute__((always_inline)) {
     const int64_t t = t0 + (int64_t)i * kT;
-    if constexpr (VEC) {
+    if constexpr (KIND == kPieces) {
       load_p.wide(s, P, g.p_row, c0, t, t1, tid);
       load_q.wide(s + SP::kBytes, Q, g.q_row, r0, t, t1, tid);
+    } else if constexpr (KIND == kWords) {
+      SP::Loads::words(s, P, g.p_row, c0, g.C, t, t1, tid);
+      SQ::Loads::words(s + SP::kBytes, Q, g.q_row, r0, g.R, t, t1, tid);
     } else {
       SP::Loads::fetch(hp, P, g.p_row, c0, g.C, t, t1, tid);
       SQ::Loads::fetch(hq, Q, g.q_row, r0, g.R, t, t1, tid);
     }
   };
   auto put = [&](unsigned char* s) __attribute__((always_inline)) {
-    if constexpr (!VEC) {
+    if constexpr (KIND == kOdd) {
       SP::Loads::put(s, hp, tid);
       SQ::Loads::put(s + SP::kBytes, hq, tid);
     }
@@ -270,19 +374,23 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   auto step = [&](const unsigned char* __restrict__ cur, unsigned char* __restrict__ next, int i)
                   __attribute__((always_inline)) {
     const bool more = i + S::STAGES - 1 < slices;
-    if (more) issue(next, i + S::STAGES - 1);
+    Op q[kT / 16][NR], p[kT / 16][NCOL];
 #pragma unroll
     for (int k = 0; k < kT / 16; ++k) {
-      Op q[NR];
 #pragma unroll
-      for (int a = 0; a < NR; ++a) q[a] = factor(SQ::get(cur + SP::kBytes, 32 * (NR * wr + a), k, lane));
+      for (int a = 0; a < NR; ++a) q[k][a] = factor(SQ::get(cur + SP::kBytes, 32 * (NR * wr + a), k, lane));
 #pragma unroll
-      for (int b = 0; b < NCOL; ++b) {
-        const Op p = factor(SP::get(cur, 32 * (NCOL * wc + b), k, lane));
-#pragma unroll
-        for (int a = 0; a < NR; ++a) att::mma(acc[a][b], p, q[a]);
-      }
+      for (int b = 0; b < NCOL; ++b) p[k][b] = factor(SP::get(cur, 32 * (NCOL * wc + b), k, lane));
     }
+    if (more) issue(next, i + S::STAGES - 1);   // (while the operands come)
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int k = 0; k < kT / 16; ++k)
+#pragma unroll
+      for (int b = 0; b < NCOL; ++b)
+#pragma unroll
+        for (int a = 0; a < NR; ++a) att::mma(acc[a][b], p[k][b], q[k][a]);
+    __builtin_amdgcn_s_setprio(0);
     if (more) put(next);
   };
 #pragma unroll
@@ -295,7 +403,7 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
 #pragma unroll
     for (int st = 0; st < S::STAGES; ++st) {   // (places in LDS that are constant)
       // this slice has landed; those issued after it may still be under way
-      if (!VEC || S::STAGES == 2 || i + S::STAGES - 2 >= slices)
+      if (KIND == kOdd || S::STAGES == 2 || i + S::STAGES - 2 >= slices)
         att::landed();
       else
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::STAGES - 2) * kLoads) : "memory");
@@ -303,49 +411,140 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
       if (++i >= slices) break;
     }
   }
-
-  // through LDS, 32 rows of the wave's columns at a time
-  constexpr int LD = CW + 4, kLanes = CW / 8;
-  static_assert(32 * LD * 4 * S::WR * S::WC <= S::STAGES * kStage, "");
+  static_assert(kPiece * S::WR * S::WC <= S::STAGES * kStage, "");
   __syncthreads();
-  float* mine = (float*)(smem + wave * 32 * LD * 4);
-  const int ch = lane % kLanes * 8, c = c0 + wc * CW + ch;
-  const bool whole = g.C % (F32_OUT || !BF16 ? 4 : 8) == 0;   // rows of 16-byte pieces
-  float bias[8];
+  finish<BF16, F32_OUT>(g, acc, smem + wave * kPiece, r0 + 32 * NR * wr, c0 + 32 * NCOL * wc, part, lane);
+}
+
+// ---------------------------------------------------------------- the wide tile kernel
+// 256 x 256 of out by 8 waves, bf16 in whole pieces: a SIMD has two waves, and
+// while one multiplies, the other fetches its next operands from LDS and sends
+// for the slice three ahead.  Both kinds of phase end in the workgroup's
+// barrier, which the upper four waves reach one phase later, so the matrix
+// cores do not wait for LDS and a slice has six phases to arrive.  A workgroup
+// takes tile after tile; the next one's first slices are sent for before a tile
+// is written, and the residual's lines half way through it, so that memory
+// works while the matrix cores do.
+constexpr int kWide = 256, kWideStages = 4, kWideBlocks = 256;
+
+template <int N>
+__device__ __forceinline__ void phase_end() {   // N: loads that may still be under way, -1: all
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (N < 0)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N < 0 ? 0 : N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <bool P_ALONG, bool Q_ALONG, bool F32_OUT>
+__global__ void __launch_bounds__(512, 2) wide_kernel(Gemm g) {
+  typedef Slice<true, P_ALONG, kWide, 512> SP;
+  typedef Slice<true, Q_ALONG, kWide, 512> SQ;
+  constexpr int NR = 2, NCOL = 4, kStage = SP::kBytes + SQ::kBytes, kLoads = SP::kLoads + SQ::kLoads;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [stages], then a piece for every wave
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave >> 1, wc = wave & 1;
+  const bool late = wave >= 4;
+  // blocks go round the 8 XCDs; a block's tiles are gridDim / 8 apart in its XCD's run
+  const unsigned all = (unsigned)g.row_tiles * g.col_tiles * g.parts, share = (all + 7) / 8, stride = gridDim.x >> 3;
+  const unsigned first = (blockIdx.x & 7) * share, end = min(first + share, all);
+  unsigned id = first + (blockIdx.x >> 3);
+  int part, c0, slices;
+  int64_t r0, t0, t1;
+  const __bf16 *P = (const __bf16*)g.P, *Q;
+  typename SP::Loads load_p(g.p_row, 0, kWide, tid);
+  typename SQ::Loads load_q(g.q_row, 0, kWide, tid);
+  auto issue = [&](unsigned char* s, int i) __attribute__((always_inline)) {
+    const int64_t t = t0 + (int64_t)i * kT;
+    load_p.wide(s, P, g.p_row, c0, t, t1, tid);
+    load_q.wide(s + SP::kBytes, Q, g.q_row, r0, t, t1, tid);
+  };
+  auto begin = [&]() __attribute__((always_inline)) {   // tile `id`, and its first slices
+    tile_of<kWide, kWide>(g, id, part, r0, c0);
+    const bool second = g.Q2 && part >= g.parts / 2;
+    Q = (const __bf16*)(second ? g.Q2 : g.Q);
+    t0 = (second ? part - g.parts / 2 : part) * g.per, t1 = t0 + g.per < g.T ? t0 + g.per : g.T;
+    slices = t1 > t0 ? (int)((t1 - t0 + kT - 1) / kT) : 0;
+    load_p = typename SP::Loads(g.p_row, c0, g.C, tid);
+    load_q = typename SQ::Loads(g.q_row, r0, g.R, tid);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) bias[e] = g.bias && c + e < g.C ? g.bias[c + e] : 0.f;
+    for (int i = 0; i < 3; ++i)
+      if (i < slices) issue(smem + i * kStage, i);
+  };
+  if (id >= end) return;
+  begin();
+  for (;;) {
+    f32x16 acc[NR][NCOL] = {};
+    bf16x8 q[2][NR], p[2][NCOL];
+    // (restrict: the transposing reads do not wait for the loads under way)
+    auto fetch = [&](const unsigned char* __restrict__ cur, unsigned char* __restrict__ next, int i)
+                     __attribute__((always_inline)) {
 #pragma unroll
-  for (int a = 0; a < NR; ++a) {
-    att::landed_in_wave();   // (the rows before have been read)
+      for (int k = 0; k < 2; ++k) {
 #pragma unroll
-    for (int b = 0; b < NCOL; ++b)
+        for (int a = 0; a < NR; ++a) q[k][a] = SQ::get(cur + SP::kBytes, 32 * (NR * wr + a), k, lane);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        *(f32x4*)(mine + (lane & 31) * LD + 32 * b + 8 * u + 4 * (lane >> 5)) =
-            f32x4{acc[a][b][4 * u], acc[a][b][4 * u + 1], acc[a][b][4 * u + 2], acc[a][b][4 * u + 3]};
-    att::landed_in_wave();
+        for (int b = 0; b < NCOL; ++b) p[k][b] = SP::get(cur, 32 * (NCOL * wc + b), k, lane);
+      }
+      if (i + 3 < slices) issue(next, i + 3);
+    };
+    auto multiply = [&]() __attribute__((always_inline)) {
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int i = 0; i < 32 * kLanes / 64; ++i) {
-      const int row = i * (64 / kLanes) + lane / kLanes;
-      const int64_t r = r0 + 32 * (NR * wr + a) + row;
-      if (r >= g.R || c >= g.C) continue;
-      const f32x4 x0 = *(const f32x4*)(mine + row * LD + ch), x1 = *(const f32x4*)(mine + row * LD + ch + 4);
-      f32x8 x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
-      const int64_t o = r * g.C + c;
-      if constexpr (F32_OUT) {
-        store8((float*)g.out + (int64_t)part * g.R * g.C + o, x, g.C - c < 8 ? g.C - c : 8, whole);
-      } else {
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += bias[e];
-        const int n = g.C - c < 8 ? g.C - c : 8;
-        if (g.pre) store8((elem*)g.pre + o, x, n, whole);
-        if (g.silu)
+        for (int b = 0; b < NCOL; ++b)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= sigmoid(x[e]);
-        if (g.residual) x += load8((const elem*)g.residual + o, n, whole);
-        store8((elem*)g.out + o, x, n, whole);
+          for (int a = 0; a < NR; ++a) att::mma(acc[a][b], p[k][b], q[k][a]);
+      __builtin_amdgcn_s_setprio(0);
+    };
+    // ends a phase behind which this wave's group reads the slice after i
+    auto arrived = [&](int i) __attribute__((always_inline)) {
+      if (i + 3 < slices)
+        phase_end<2 * kLoads>();
+      else if (i + 2 < slices)
+        phase_end<kLoads>();
+      else
+        phase_end<0>();
+    };
+    arrived(-1);
+    if (late) phase_end<-1>();
+    uint32_t line[2] = {};
+    for (int i = 0; i < slices;) {
+#pragma unroll
+      for (int st = 0; st < kWideStages; ++st) {   // (places in LDS that are constant)
+        fetch(smem + st * kStage, smem + (st + 3) % kWideStages * kStage, i);
+        if (late)
+          arrived(i);
+        else
+          phase_end<-1>();
+        multiply();
+        if (late)
+          phase_end<-1>();
+        else
+          arrived(i);
+        if (++i >= slices) break;
+      }
+      if (!F32_OUT && g.residual && i * 2 >= slices && i * 2 < slices + 2 * kWideStages) {
+        // a word of each of the wave's 128-byte lines of the residual: into the caches
+        const int64_t r = r0 + 64 * wr + lane;
+        const int c = c0 + 128 * wc;
+        const __bf16* at = (const __bf16*)g.residual + (r < g.R ? r : g.R - 1) * g.C;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) line[e] = *(const uint16_t*)(at + min(c + 64 * e, g.C - 1));
       }
     }
+    if (!late) phase_end<-1>();
+    asm volatile("" ::"v"(line[0]), "v"(line[1]));
+    const int was_part = part, was_c = c0;
+    const int64_t was_r = r0;
+    id += stride;
+    const bool more = id < end;
+    if (more) begin();
+    finish<true, F32_OUT>(g, acc, smem + kWideStages * kStage + wave * kPiece, was_r + 32 * NR * wr, was_c + 32 * NCOL * wc,
+                          was_part, lane);
+    if (!more) return;
   }
 }
 
@@ -502,45 +701,61 @@ __global__ void __launch_bounds__(256) parts_kernel(const float* in, int parts, 
 }
 
 // ---------------------------------------------------------------- launches
-template <typename S, bool P_ALONG, bool Q_ALONG, bool VEC, bool F32_OUT>
+template <typename S, bool P_ALONG, bool Q_ALONG, int KIND, bool F32_OUT>
 hipError_t launch_tiles(Gemm g, hipStream_t stream) {
   constexpr int lds = S::STAGES * (Slice<S::BF16, P_ALONG, S::TC, S::kThreads>::kBytes +
                                    Slice<S::BF16, Q_ALONG, S::TR, S::kThreads>::kBytes);
   g.row_tiles = (int)((g.R + S::TR - 1) / S::TR), g.col_tiles = (g.C + S::TC - 1) / S::TC;
   const int64_t all = (int64_t)g.row_tiles * g.col_tiles * g.parts;
-  auto kernel = gemm_kernel<S, P_ALONG, Q_ALONG, VEC, F32_OUT>;
+  auto kernel = gemm_kernel<S, P_ALONG, Q_ALONG, KIND, F32_OUT>;
   hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   kernel<<<(unsigned)((all + 7) / 8 * 8), S::kThreads, lds, stream>>>(g);
   return hipGetLastError();
 }
 
-template <bool BF16>
-using Large = Shape2<BF16, BF16 ? 256 : 128, 128, BF16 ? 4 : 2, BF16 ? 1 : 2, BF16 ? 3 : 2>;
-template <bool BF16>
-using Small = Shape2<BF16, 64, 64, 2, 2, BF16 ? 3 : 2>;
+template <bool P_ALONG, bool Q_ALONG, bool F32_OUT>
+hipError_t launch_wide(Gemm g, hipStream_t stream) {
+  constexpr int lds = kWideStages * 2 * kWide * kT * 2 + 8 * kPiece;
+  g.row_tiles = (int)((g.R + kWide - 1) / kWide), g.col_tiles = (g.C + kWide - 1) / kWide;
+  const int64_t all = (int64_t)g.row_tiles * g.col_tiles * g.parts;
+  auto kernel = wide_kernel<P_ALONG, Q_ALONG, F32_OUT>;
+  hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  kernel<<<all < kWideBlocks ? (unsigned)((all + 7) / 8 * 8) : kWideBlocks, 512, lds, stream>>>(g);
+  return hipGetLastError();
+}
 
-// Large tiles from one for every CU on, small ones below.
+template <bool BF16>
+using Large = Form<BF16, BF16 ? 256 : 128, 128, BF16 ? 4 : 2, BF16 ? 1 : 2, BF16 ? 3 : 2>;
+template <bool BF16>
+using Small = Form<BF16, 64, 64, 2, 2, BF16 ? 3 : 2>;
+
+// Large tiles from three for every four CUs on, small ones below.
 bool large(int64_t R, int64_t C, int io) {
   const int64_t tr = io == TM_IO_BF16 ? 256 : 128;
   return (R + tr - 1) / tr * ((C + 127) / 128) >= 192;
 }
 
-template <bool P_ALONG, bool Q_ALONG, bool F32_OUT, bool BF16, bool VEC>
+template <bool P_ALONG, bool Q_ALONG, bool F32_OUT, bool BF16, int KIND>
 hipError_t launch_sized(const Gemm& g, bool big, hipStream_t stream) {
-  return big ? launch_tiles<Large<BF16>, P_ALONG, Q_ALONG, VEC, F32_OUT>(g, stream)
-             : launch_tiles<Small<BF16>, P_ALONG, Q_ALONG, VEC, F32_OUT>(g, stream);
+  return big ? launch_tiles<Large<BF16>, P_ALONG, Q_ALONG, KIND, F32_OUT>(g, stream)
+             : launch_tiles<Small<BF16>, P_ALONG, Q_ALONG, KIND, F32_OUT>(g, stream);
 }
 
 template <bool P_ALONG, bool Q_ALONG, bool F32_OUT>
 hipError_t launch_gemm(const Gemm& g, int io, bool big, hipStream_t stream) {
   const int pc = io == TM_IO_BF16 ? 8 : 4;
-  const bool vec = g.p_row % pc == 0 && g.q_row % pc == 0;
-  if (io == TM_IO_BF16)
-    return vec ? launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, true>(g, big, stream)
-               : launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, false>(g, big, stream);
-  return vec ? launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, true>(g, big, stream)
-             : launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, false>(g, big, stream);
+  const bool pieces = g.p_row % pc == 0 && g.q_row % pc == 0;
+  if (io == TM_IO_BF16) {
+    // from two rounds of the device on
+    if (pieces && (g.R + kWide - 1) / kWide * ((g.C + kWide - 1) / kWide) * g.parts >= 2 * kWideBlocks)
+      return launch_wide<P_ALONG, Q_ALONG, F32_OUT>(g, stream);
+    return pieces ? launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, kPieces>(g, big, stream)
+                  : launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, kOdd>(g, big, stream);
+  }
+  return pieces ? launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, kPieces>(g, big, stream)
+                : launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, kWords>(g, big, stream);
 }
 
 template <bool BF16, bool VEC>
