@@ -314,12 +314,13 @@ __device__ __forceinline__ void tile_of(const Gemm& g, unsigned id, int& part, i
 }
 
 // ---------------------------------------------------------------- the tile kernel
-// TR x TC of out by WR x WC waves.
-template <bool BF16_, int TR_, int TC_, int WR_, int WC_, int STAGES_>
+// TR x TC of out by WR x WC waves; by twice as many where HALVES is 2, each of
+// which takes half of a slice's steps, and whose sums are joined in the end.
+template <bool BF16_, int TR_, int TC_, int WR_, int WC_, int STAGES_, int HALVES_ = 1>
 struct Form {
   static constexpr bool BF16 = BF16_;
-  static constexpr int TR = TR_, TC = TC_, WR = WR_, WC = WC_, STAGES = STAGES_;
-  static constexpr int kThreads = 64 * WR * WC;
+  static constexpr int TR = TR_, TC = TC_, WR = WR_, WC = WC_, STAGES = STAGES_, HALVES = HALVES_;
+  static constexpr int kThreads = 64 * WR * WC * HALVES;
 };
 
 template <typename S, bool P_ALONG, bool Q_ALONG, int KIND, bool F32_OUT>
@@ -333,7 +334,8 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   constexpr int kStage = SP::kBytes + SQ::kBytes, kLoads = (SP::kLoads + SQ::kLoads) * (KIND == kWords ? 4 : 1);
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wr = wave / S::WC, wc = wave % S::WC;
+  constexpr int kSteps = kT / 16 / S::HALVES;   // of a wave, in a slice
+  const int wr = wave / S::WC % S::WR, wc = wave % S::WC, k0 = S::HALVES == 1 ? 0 : wave / (S::WC * S::WR) * kSteps;
   // blocks go round the 8 XCDs
   const unsigned all = (unsigned)g.row_tiles * g.col_tiles * g.parts, share = (all + 7) / 8;
   const unsigned id = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
@@ -347,9 +349,13 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   const int slices = t1 > t0 ? (int)((t1 - t0 + kT - 1) / kT) : 0;
   const typename SP::Loads load_p(g.p_row, c0, g.C, tid);
   const typename SQ::Loads load_q(g.q_row, r0, g.R, tid);
-  typename SP::Loads::Held hp;
-  typename SQ::Loads::Held hq;
-  auto issue = [&](unsigned char* s, int i) __attribute__((always_inline)) {
+  // Pieces on their way through registers, of several slices where they are
+  // few.  They are held as long, so that memory has as many steps to answer as
+  // in the other kinds; kept in one set, it has one.
+  constexpr int kSets = KIND == kOdd && kLoads <= 4 ? S::STAGES : 1;
+  typename SP::Loads::Held hp[kSets];
+  typename SQ::Loads::Held hq[kSets];
+  auto issue = [&](unsigned char* s, int i, int set) __attribute__((always_inline)) {
     const int64_t t = t0 + (int64_t)i * kT;
     if constexpr (KIND == kPieces) {
       load_p.wide(s, P, g.p_row, c0, t, t1, tid);
@@ -358,61 +364,80 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
       SP::Loads::words(s, P, g.p_row, c0, g.C, t, t1, tid);
       SQ::Loads::words(s + SP::kBytes, Q, g.q_row, r0, g.R, t, t1, tid);
     } else {
-      SP::Loads::fetch(hp, P, g.p_row, c0, g.C, t, t1, tid);
-      SQ::Loads::fetch(hq, Q, g.q_row, r0, g.R, t, t1, tid);
+      SP::Loads::fetch(hp[set % kSets], P, g.p_row, c0, g.C, t, t1, tid);
+      SQ::Loads::fetch(hq[set % kSets], Q, g.q_row, r0, g.R, t, t1, tid);
     }
   };
-  auto put = [&](unsigned char* s) __attribute__((always_inline)) {
+  auto put = [&](unsigned char* s, int set) __attribute__((always_inline)) {
     if constexpr (KIND == kOdd) {
-      SP::Loads::put(s, hp, tid);
-      SQ::Loads::put(s + SP::kBytes, hq, tid);
+      SP::Loads::put(s, hp[set % kSets], tid);
+      SQ::Loads::put(s + SP::kBytes, hq[set % kSets], tid);
     }
   };
   f32x16 acc[NR][NCOL] = {};
   // slice i + STAGES - 1 goes to `next` (restrict: the transposing reads of
   // this one do not wait for it)
-  auto step = [&](const unsigned char* __restrict__ cur, unsigned char* __restrict__ next, int i)
+  auto step = [&](const unsigned char* __restrict__ cur, unsigned char* __restrict__ next, int i, int st)
                   __attribute__((always_inline)) {
     const bool more = i + S::STAGES - 1 < slices;
-    Op q[kT / 16][NR], p[kT / 16][NCOL];
+    Op q[kSteps][NR], p[kSteps][NCOL];
 #pragma unroll
-    for (int k = 0; k < kT / 16; ++k) {
+    for (int k = 0; k < kSteps; ++k) {
 #pragma unroll
-      for (int a = 0; a < NR; ++a) q[k][a] = factor(SQ::get(cur + SP::kBytes, 32 * (NR * wr + a), k, lane));
+      for (int a = 0; a < NR; ++a) q[k][a] = factor(SQ::get(cur + SP::kBytes, 32 * (NR * wr + a), k0 + k, lane));
 #pragma unroll
-      for (int b = 0; b < NCOL; ++b) p[k][b] = factor(SP::get(cur, 32 * (NCOL * wc + b), k, lane));
+      for (int b = 0; b < NCOL; ++b) p[k][b] = factor(SP::get(cur, 32 * (NCOL * wc + b), k0 + k, lane));
     }
-    if (more) issue(next, i + S::STAGES - 1);   // (while the operands come)
+    if (more) issue(next, i + S::STAGES - 1, st + S::STAGES - 1);   // (while the operands come)
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int k = 0; k < kT / 16; ++k)
+    for (int k = 0; k < kSteps; ++k)
 #pragma unroll
       for (int b = 0; b < NCOL; ++b)
 #pragma unroll
         for (int a = 0; a < NR; ++a) att::mma(acc[a][b], p[k][b], q[k][a]);
     __builtin_amdgcn_s_setprio(0);
-    if (more) put(next);
+    if (kSets == 1 && more) put(next, 0);
   };
 #pragma unroll
   for (int i = 0; i < S::STAGES - 1; ++i)
     if (i < slices) {
-      issue(smem + i * kStage, i);
-      put(smem + i * kStage);
+      issue(smem + i * kStage, i, i);
+      if (kSets == 1 || i == 0) put(smem + i * kStage, i);
     }
   for (int i = 0; i < slices;) {
 #pragma unroll
     for (int st = 0; st < S::STAGES; ++st) {   // (places in LDS that are constant)
       // this slice has landed; those issued after it may still be under way
-      if (KIND == kOdd || S::STAGES == 2 || i + S::STAGES - 2 >= slices)
+      if (KIND == kOdd)   // (only LDS is waited for)
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      else if (S::STAGES == 2 || i + S::STAGES - 2 >= slices)
         att::landed();
       else
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::STAGES - 2) * kLoads) : "memory");
-      step(smem + st * kStage, smem + (st + S::STAGES - 1) % S::STAGES * kStage, i);
+      step(smem + st * kStage, smem + (st + S::STAGES - 1) % S::STAGES * kStage, i, st);
       if (++i >= slices) break;
+      if (kSets > 1) put(smem + (st + 1) % S::STAGES * kStage, st + 1);
     }
   }
   static_assert(kPiece * S::WR * S::WC <= S::STAGES * kStage, "");
   __syncthreads();
+  if constexpr (S::HALVES == 2) {
+    static_assert(NR == 1 && NCOL == 1, "");
+    f32x4* sums = (f32x4*)(smem + wave % (S::WR * S::WC) * kPiece) + lane;
+    if (k0)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        sums[64 * u] = f32x4{acc[0][0][4 * u], acc[0][0][4 * u + 1], acc[0][0][4 * u + 2], acc[0][0][4 * u + 3]};
+    __syncthreads();
+    if (k0) return;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const f32x4 x = sums[64 * u];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[0][0][4 * u + e] += x[e];
+    }
+  }
   finish<BF16, F32_OUT>(g, acc, smem + wave * kPiece, r0 + 32 * NR * wr, c0 + 32 * NCOL * wc, part, lane);
 }
 
@@ -729,7 +754,7 @@ hipError_t launch_wide(Gemm g, hipStream_t stream) {
 template <bool BF16>
 using Large = Form<BF16, BF16 ? 256 : 128, 128, BF16 ? 4 : 2, BF16 ? 1 : 2, BF16 ? 3 : 2>;
 template <bool BF16>
-using Small = Form<BF16, 64, 64, 2, 2, BF16 ? 3 : 2>;
+using Small = Form<BF16, 64, 64, 2, 2, BF16 ? 6 : 4, BF16 ? 1 : 2>;   // (a slice is short: more of them on their way)
 
 // Large tiles from three for every four CUs on, small ones below.
 bool large(int64_t R, int64_t C, int io) {
@@ -747,6 +772,9 @@ template <bool P_ALONG, bool Q_ALONG, bool F32_OUT>
 hipError_t launch_gemm(const Gemm& g, int io, bool big, hipStream_t stream) {
   const int pc = io == TM_IO_BF16 ? 8 : 4;
   const bool pieces = g.p_row % pc == 0 && g.q_row % pc == 0;
+  // Rows of fp32 elements take four times the loads, whose distances do not
+  // fit large tiles' registers (1001 rows, 777 to 500: 43 us, small ones ..).
+  if (io == TM_IO_F32 && !pieces) big = false;
   if (io == TM_IO_BF16) {
     // from two rounds of the device on
     if (pieces && (g.R + kWide - 1) / kWide * ((g.C + kWide - 1) / kWide) * g.parts >= 2 * kWideBlocks)
@@ -774,9 +802,10 @@ hipError_t launch_narrow(const Gemm& g, hipStream_t stream) {
 // part with 128 rows at least; large tiles where there are enough of them.
 // With two planes of dz half of the parts belong to each.
 int weight_parts(const ProjectionShape& s, bool* big) {
+  const bool words = s.io == TM_IO_F32 && (s.O % 4 || s.K % 4);   // small tiles only
   const int planes = s.silu && s.io == TM_IO_BF16 ? 2 : 1;
   int64_t parts = 1;
-  for (int pass = 0; pass < 2; ++pass) {
+  for (int pass = words; pass < 2; ++pass) {
     *big = pass == 0;
     const int64_t tr = *big ? (s.io == TM_IO_BF16 ? 256 : 128) : 64, tc = *big ? 128 : 64;
     const int64_t tiles = (s.O + tr - 1) / tr * ((s.K + tc - 1) / tc), most = s.M / 128 > 1 ? s.M / 128 : 1;
