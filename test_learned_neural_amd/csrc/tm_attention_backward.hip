@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(Params p) {
 // full where tiles are few, with 4 tiles of queries each where there are.
 int parts_of(const AttentionShape& s) {
   const int64_t blocks = attention_blocks(s, kRows, 1), tiles = ((int64_t)s.N + 31) / 32 * (s.H / s.Hk);
-  int64_t parts = 768 / blocks;
+  int64_t parts = 768 / (blocks > 0 ? blocks : 1);
   if (parts > tiles / 4) parts = tiles / 4;
   return parts < 1 ? 1 : parts > 8 ? 8 : (int)parts;
 }

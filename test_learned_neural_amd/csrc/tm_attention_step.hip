@@ -257,6 +257,7 @@ int64_t row_tiles_of(const AttentionStepShape& s) { return ((int64_t)s.H / s.Hk 
 // Workgroups of a row: enough for four a CU, with at least 8 tiles each.
 int parts_of(const AttentionStepShape& s) {
   const int64_t rows = (int64_t)s.B * s.Hk * row_tiles_of(s);
+  if (rows == 0) return 1;
   int64_t keys = s.C;
   if (s.window && (int64_t)s.window + s.n + s.prefix < keys) keys = (int64_t)s.window + s.n + s.prefix;
   int64_t parts = (1024 + rows - 1) / rows, most = keys / kKeys / 8;
