@@ -58,14 +58,14 @@ __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf
 constexpr int kPieces = 0, kWords = 1, kOdd = 2;
 
 // One operand's slice in LDS, and its fragments: EXTENT values of c (or r) by
-// kT of t; ALONG: rows are values, else rows are steps of t.
-template <bool BF16, bool ALONG, int EXTENT, int THREADS>
+// KT of t; ALONG: rows are values, else rows are steps of t.
+template <bool BF16, bool ALONG, int EXTENT, int THREADS, int KT = kT>
 struct Slice {
   typedef typename att::Types<BF16>::elem elem;
   typedef typename att::Types<BF16>::frag frag;
   static constexpr int kSize = BF16 ? 2 : 4;
   static constexpr int PC = 16 / kSize;
-  static constexpr int ROWS = ALONG ? EXTENT : kT, COLS = ALONG ? kT : EXTENT;
+  static constexpr int ROWS = ALONG ? EXTENT : KT, COLS = ALONG ? KT : EXTENT;
   static constexpr int RB = COLS * kSize, NC = RB / 16;
   static constexpr int kBytes = ROWS * RB;
   static constexpr int kLoads = kBytes / 16 / THREADS;   // of a thread
@@ -94,7 +94,7 @@ struct Slice {
                                          int tid) const {
       const elem* start = src + (ALONG ? v0 * row + t : t * row + v0);
       const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-      if (t + kT <= end) {
+      if (t + KT <= end) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
           __builtin_amdgcn_global_load_lds((const void*)((const char*)start + off[i]),
@@ -108,6 +108,16 @@ struct Slice {
         }
         asm volatile("; the last slice");   // (or the compiler joins the two, and the whole one pays for it)
       }
+    }
+    // piece i of them alone, without a branch: `left` steps are there
+    __device__ __forceinline__ void one(unsigned char* s, const elem* start, int left, int i, int tid) const {
+      const int at = i * THREADS + tid, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+      const int t = ALONG ? ((at % NC) ^ swz(at / NC)) * PC : at / NC;
+      const void* p = t < left ? (const void*)((const char*)start + off[i]) : (const void*)kZeros;
+      __builtin_amdgcn_global_load_lds(p, (lds_void_ptr)(s + (i * THREADS + wave * 64) * 16), 16, 0, 0);
+    }
+    static __device__ __forceinline__ const elem* start(const elem* src, int64_t row, int64_t v0, int64_t t) {
+      return src + (ALONG ? v0 * row + t : t * row + v0);
     }
     // the same by elements of 4 bytes, for fp32 rows that are not made of 16-byte pieces
     static __device__ __forceinline__ void words(unsigned char* s, const elem* src, int64_t row, int64_t v0, int64_t values,
@@ -231,29 +241,32 @@ __device__ __forceinline__ void store8(float* p, f32x8 x, int n, bool whole) {
 }
 
 // A wave's accumulators, 32 NR rows from r0 on by 32 NCOL columns from c0 on,
-// to memory: 32 x 32 at a time through 4 KB of LDS, so that bias, residual and
-// out are met in pieces of rows.  (A wave's LDS operations stay in their order:
-// only the compiler has to keep it.)
-constexpr int kPiece = 4096;
+// to memory: 32 rows by W columns at a time through LDS, so that bias, residual
+// and out are met in pieces of rows, lines of 128 bytes where NCOL is even.  (A
+// wave's LDS operations stay in their order: only the compiler has to keep it.)
+template <int NCOL>
+constexpr int piece_of() { return NCOL % 2 ? 4096 : 8192; }   // of LDS, a wave's
 
 template <bool BF16, bool F32_OUT, int NR, int NCOL>
 __device__ __forceinline__ void finish(const Gemm& g, f32x16 (&acc)[NR][NCOL], unsigned char* mine, int64_t r0, int c0,
                                        int part, int lane) {
   typedef typename att::Types<BF16>::elem elem;
   typedef __attribute__((ext_vector_type(8))) elem elem8;
+  constexpr int E = NCOL % 2 ? 1 : 2, W = 32 * E, L = W / 8, TURNS = 32 * L / 64;   // lanes of a row, rows' turns
   const bool whole = g.C % (F32_OUT || !BF16 ? 4 : 8) == 0;   // rows of 16-byte pieces
   // The residual may be out, so that no piece of it could pass a store: where
   // pieces are whole, those of 32 rows are sent for ahead of the rows before.
   const bool ahead = !F32_OUT && g.residual && g.C % 8 == 0;
-  elem8 res[2][F32_OUT ? 1 : NCOL][2];
+  constexpr int NB = NCOL / E;
+  elem8 res[2][F32_OUT ? 1 : NB][TURNS];
   auto send = [&](int a) __attribute__((always_inline)) {
     if constexpr (!F32_OUT) {
 #pragma unroll
-      for (int b = 0; b < NCOL; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t r = r0 + 32 * a + 16 * i + lane / 4;
-          const int c = c0 + 32 * b + lane % 4 * 8;
+        for (int i = 0; i < TURNS; ++i) {
+          const int64_t r = r0 + 32 * a + 64 / L * i + lane / L;
+          const int c = c0 + W * b + lane % L * 8;
           if (r < g.R && c < g.C) res[a & 1][b][i] = *(const elem8*)((const elem*)g.residual + r * g.C + c);
         }
     }
@@ -263,21 +276,24 @@ __device__ __forceinline__ void finish(const Gemm& g, f32x16 (&acc)[NR][NCOL], u
   for (int a = 0; a < NR; ++a) {
     if (ahead && a + 1 < NR) send(a + 1);
 #pragma unroll
-    for (int b = 0; b < NCOL; ++b) {
+    for (int b = 0; b < NB; ++b) {
       asm volatile("" ::: "memory");
 #pragma unroll
-      for (int u = 0; u < 4; ++u)   // 16-byte chunk c of row r at c ^ (r & 7)
-        *(f32x4*)(mine + (lane & 31) * 128 + ((2 * u + (lane >> 5)) ^ (lane & 7)) * 16) =
-            f32x4{acc[a][b][4 * u], acc[a][b][4 * u + 1], acc[a][b][4 * u + 2], acc[a][b][4 * u + 3]};
+      for (int u = 0; u < 4 * E; ++u) {   // 16-byte chunk c of row r at c ^ (r % chunks)
+        const f32x16& x = acc[a][E * b + u / 4];
+        const int v = u % 4;
+        *(f32x4*)(mine + (lane & 31) * W * 4 + ((2 * u + (lane >> 5)) ^ (lane & (8 * E - 1))) * 16) =
+            f32x4{x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]};
+      }
       asm volatile("" ::: "memory");
-      const int c = c0 + 32 * b + lane % 4 * 8, n = g.C - c < 8 ? g.C - c : 8;
+      const int l = lane % L * 2, c = c0 + W * b + 4 * l, n = g.C - c < 8 ? g.C - c : 8;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = 16 * i + lane / 4;
+      for (int i = 0; i < TURNS; ++i) {
+        const int row = 64 / L * i + lane / L;
         const int64_t r = r0 + 32 * a + row;
         if (r >= g.R || n <= 0) continue;
-        const f32x4 x0 = *(const f32x4*)(mine + row * 128 + ((lane % 4 * 2) ^ (row & 7)) * 16);
-        const f32x4 x1 = *(const f32x4*)(mine + row * 128 + ((lane % 4 * 2 + 1) ^ (row & 7)) * 16);
+        const f32x4 x0 = *(const f32x4*)(mine + row * W * 4 + (l ^ (row & (8 * E - 1))) * 16);
+        const f32x4 x1 = *(const f32x4*)(mine + row * W * 4 + ((l + 1) ^ (row & (8 * E - 1))) * 16);
         f32x8 x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
         const int64_t o = r * g.C + c;
         if constexpr (F32_OUT) {
@@ -420,6 +436,7 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
       if (kSets > 1) put(smem + (st + 1) % S::STAGES * kStage, st + 1);
     }
   }
+  constexpr int kPiece = piece_of<NCOL>();
   static_assert(kPiece * S::WR * S::WC <= S::STAGES * kStage, "");
   __syncthreads();
   if constexpr (S::HALVES == 2) {
@@ -442,35 +459,24 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
 }
 
 // ---------------------------------------------------------------- the wide tile kernel
-// 256 x 256 of out by 8 waves, bf16 in whole pieces: a SIMD has two waves, and
-// while one multiplies, the other fetches its next operands from LDS and sends
-// for the slice three ahead.  Both kinds of phase end in the workgroup's
-// barrier, which the upper four waves reach one phase later, so the matrix
-// cores do not wait for LDS and a slice has six phases to arrive.  A workgroup
-// takes tile after tile; the next one's first slices are sent for before a tile
-// is written, and the residual's lines half way through it, so that memory
-// works while the matrix cores do.
-constexpr int kWide = 256, kWideStages = 4, kWideBlocks = 256;
-
-template <int N>
-__device__ __forceinline__ void phase_end() {   // N: loads that may still be under way, -1: all
-  __builtin_amdgcn_sched_barrier(0);
-  if constexpr (N < 0)
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  else
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N < 0 ? 0 : N) : "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
+// 256 x 256 of out by 4 waves of 128 x 128, bf16 in whole pieces.  A slice's
+// operands are read from LDS by 16 KB a wave for 2^20 products: three quarters
+// of the matrix cores' time (waves of 64 x 128, eight of them: all of it).  With
+// one wave a SIMD, a step's operands are fetched while the step before it is
+// multiplied, and the next slice is on its way.  A slice has 64 steps, so that a
+// row's piece is a whole line of the caches (with 32, every line passed from L2
+// twice: 0.95 us for 32 steps instead of ..).  A workgroup takes tile after
+// tile; the next one's first slice is sent for before a tile is written.
+constexpr int kWide = 256, kWideT = 64, kWideBlocks = 256;
 
 template <bool P_ALONG, bool Q_ALONG, bool F32_OUT>
-__global__ void __launch_bounds__(512, 2) wide_kernel(Gemm g) {
-  typedef Slice<true, P_ALONG, kWide, 512> SP;
-  typedef Slice<true, Q_ALONG, kWide, 512> SQ;
-  constexpr int NR = 2, NCOL = 4, kStage = SP::kBytes + SQ::kBytes, kLoads = SP::kLoads + SQ::kLoads;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [stages], then a piece for every wave
+__global__ void __launch_bounds__(256, 1) wide_kernel(Gemm g) {
+  typedef Slice<true, P_ALONG, kWide, 256, kWideT> SP;
+  typedef Slice<true, Q_ALONG, kWide, 256, kWideT> SQ;
+  constexpr int NR = 4, NCOL = 4, kStage = SP::kBytes + SQ::kBytes;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2 slices], then a piece for every wave
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave >> 1, wc = wave & 1;
-  const bool late = wave >= 4;
   // blocks go round the 8 XCDs; a block's tiles are gridDim / 8 apart in its XCD's run
   const unsigned all = (unsigned)g.row_tiles * g.col_tiles * g.parts, share = (all + 7) / 8, stride = gridDim.x >> 3;
   const unsigned first = (blockIdx.x & 7) * share, end = min(first + share, all);
@@ -480,96 +486,96 @@ __global__ void __launch_bounds__(512, 2) wide_kernel(Gemm g) {
   const __bf16 *P = (const __bf16*)g.P, *Q;
   typename SP::Loads load_p(g.p_row, 0, kWide, tid);
   typename SQ::Loads load_q(g.q_row, 0, kWide, tid);
-  auto issue = [&](unsigned char* s, int i) __attribute__((always_inline)) {
-    const int64_t t = t0 + (int64_t)i * kT;
-    load_p.wide(s, P, g.p_row, c0, t, t1, tid);
-    load_q.wide(s + SP::kBytes, Q, g.q_row, r0, t, t1, tid);
+  constexpr int kLoads = SP::kLoads + SQ::kLoads;
+  // pieces from .. to - 1 of the slice at step t
+  auto issue = [&](unsigned char* s, int64_t t, int from, int to) __attribute__((always_inline)) {
+    const int left = (int)(t1 - t < kWideT ? t1 - t : kWideT);   // (zero or less behind the last slice)
+    const __bf16 *sp = SP::Loads::start(P, g.p_row, c0, t), *sq = SQ::Loads::start(Q, g.q_row, r0, t);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      if (i >= from && i < to) {
+        if (i < SP::kLoads)
+          load_p.one(s, sp, left, i, tid);
+        else
+          load_q.one(s + SP::kBytes, sq, left, i - SP::kLoads, tid);
+      }
   };
-  auto begin = [&]() __attribute__((always_inline)) {   // tile `id`, and its first slices
+  auto begin = [&]() __attribute__((always_inline)) {   // tile `id`, and its first slice
     tile_of<kWide, kWide>(g, id, part, r0, c0);
     const bool second = g.Q2 && part >= g.parts / 2;
     Q = (const __bf16*)(second ? g.Q2 : g.Q);
     t0 = (second ? part - g.parts / 2 : part) * g.per, t1 = t0 + g.per < g.T ? t0 + g.per : g.T;
-    slices = t1 > t0 ? (int)((t1 - t0 + kT - 1) / kT) : 0;
+    slices = t1 > t0 ? (int)((t1 - t0 + kWideT - 1) / kWideT) : 0;
     load_p = typename SP::Loads(g.p_row, c0, g.C, tid);
     load_q = typename SQ::Loads(g.q_row, r0, g.R, tid);
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (i < slices) issue(smem + i * kStage, i);
+    issue(smem, t0, 0, kLoads);
   };
   if (id >= end) return;
   begin();
+  bool stores = false;   // 32 of them, at least, were issued behind the slice that is waited for
   for (;;) {
     f32x16 acc[NR][NCOL] = {};
     bf16x8 q[2][NR], p[2][NCOL];
-    // (restrict: the transposing reads do not wait for the loads under way)
-    auto fetch = [&](const unsigned char* __restrict__ cur, unsigned char* __restrict__ next, int i)
-                     __attribute__((always_inline)) {
+    auto fetch = [&](const unsigned char* cur, int k) __attribute__((always_inline)) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int a = 0; a < NR; ++a) q[k % 2][a] = SQ::get(cur + SP::kBytes, 32 * (NR * wr + a), k, lane);
 #pragma unroll
-        for (int a = 0; a < NR; ++a) q[k][a] = SQ::get(cur + SP::kBytes, 32 * (NR * wr + a), k, lane);
+      for (int b = 0; b < NCOL; ++b) p[k % 2][b] = SP::get(cur, 32 * (NCOL * wc + b), k, lane);
+    };
+    auto multiply = [&](int k) __attribute__((always_inline)) {
 #pragma unroll
-        for (int b = 0; b < NCOL; ++b) p[k][b] = SP::get(cur, 32 * (NCOL * wc + b), k, lane);
+      for (int b = 0; b < NCOL; ++b)
+#pragma unroll
+        for (int a = 0; a < NR; ++a) att::mma(acc[a][b], p[k % 2][b], q[k % 2][a]);
+    };
+    // The next step's operands come while one is multiplied, and the next
+    // slice's pieces are sent for one by one between the products: together
+    // they would hold the wave up for as long as 16 products take.  (restrict:
+    // the transposing reads do not wait for the loads under way)
+    auto step = [&](const unsigned char* __restrict__ cur, unsigned char* __restrict__ next, int64_t t)
+                    __attribute__((always_inline)) {
+#pragma unroll
+      for (int k = 0; k + 1 < kWideT / 16; ++k) {
+        constexpr int each = kLoads / 2;   // (in the first two steps: they have the third to arrive in)
+        fetch(cur, k + 1);
+        issue(next, t, each * k, each * (k + 1));
+        multiply(k);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);              // a read of LDS,
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);              // a product,
+          if (k < 2) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // a load,
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);              // a product
+        }
       }
-      if (i + 3 < slices) issue(next, i + 3);
     };
-    auto multiply = [&]() __attribute__((always_inline)) {
-      __builtin_amdgcn_s_setprio(1);
+    if (stores)
+      asm volatile("s_waitcnt vmcnt(32) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else
+      att::landed();
+    fetch(smem, 0);
+#pragma unroll 1
+    for (int i = 0; i < slices; ++i) {
+      unsigned char* next = smem + (i + 1) % 2 * kStage;
+      step(smem + i % 2 * kStage, next, t0 + (int64_t)(i + 1) * kWideT);
+      att::landed();     // the next slice is there for everyone, and nobody reads this one any more
+      fetch(next, 0);    // (behind the last slice: not used)
+      multiply(kWideT / 16 - 1);
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int b = 0; b < NCOL; ++b)
-#pragma unroll
-          for (int a = 0; a < NR; ++a) att::mma(acc[a][b], p[k][b], q[k][a]);
-      __builtin_amdgcn_s_setprio(0);
-    };
-    // ends a phase behind which this wave's group reads the slice after i
-    auto arrived = [&](int i) __attribute__((always_inline)) {
-      if (i + 3 < slices)
-        phase_end<2 * kLoads>();
-      else if (i + 2 < slices)
-        phase_end<kLoads>();
-      else
-        phase_end<0>();
-    };
-    arrived(-1);
-    if (late) phase_end<-1>();
-    uint32_t line[2] = {};
-    for (int i = 0; i < slices;) {
-#pragma unroll
-      for (int st = 0; st < kWideStages; ++st) {   // (places in LDS that are constant)
-        fetch(smem + st * kStage, smem + (st + 3) % kWideStages * kStage, i);
-        if (late)
-          arrived(i);
-        else
-          phase_end<-1>();
-        multiply();
-        if (late)
-          phase_end<-1>();
-        else
-          arrived(i);
-        if (++i >= slices) break;
-      }
-      if (!F32_OUT && g.residual && i * 2 >= slices && i * 2 < slices + 2 * kWideStages) {
-        // a word of each of the wave's 128-byte lines of the residual: into the caches
-        const int64_t r = r0 + 64 * wr + lane;
-        const int c = c0 + 128 * wc;
-        const __bf16* at = (const __bf16*)g.residual + (r < g.R ? r : g.R - 1) * g.C;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) line[e] = *(const uint16_t*)(at + min(c + 64 * e, g.C - 1));
+      for (int n = 0; n < 8; ++n) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       }
     }
-    if (!late) phase_end<-1>();
-    asm volatile("" ::"v"(line[0]), "v"(line[1]));
     const int was_part = part, was_c = c0;
     const int64_t was_r = r0;
     id += stride;
     const bool more = id < end;
+    // (the last slice was read before the last barrier; what was fetched behind it is not used)
     if (more) begin();
-    finish<true, F32_OUT>(g, acc, smem + kWideStages * kStage + wave * kPiece, was_r + 32 * NR * wr, was_c + 32 * NCOL * wc,
-                          was_part, lane);
+    finish<true, F32_OUT>(g, acc, smem + 2 * kStage + wave * piece_of<NCOL>(), was_r + 32 * NR * wr, was_c + 32 * NCOL * wc, was_part, lane);
     if (!more) return;
+    stores = was_r + kWide <= g.R && was_c + kWide <= g.C && g.C % 8 == 0;
   }
 }
 
@@ -741,13 +747,13 @@ hipError_t launch_tiles(Gemm g, hipStream_t stream) {
 
 template <bool P_ALONG, bool Q_ALONG, bool F32_OUT>
 hipError_t launch_wide(Gemm g, hipStream_t stream) {
-  constexpr int lds = kWideStages * 2 * kWide * kT * 2 + 8 * kPiece;
+  constexpr int lds = 2 * 2 * kWide * kWideT * 2 + 4 * piece_of<4>();
   g.row_tiles = (int)((g.R + kWide - 1) / kWide), g.col_tiles = (g.C + kWide - 1) / kWide;
   const int64_t all = (int64_t)g.row_tiles * g.col_tiles * g.parts;
   auto kernel = wide_kernel<P_ALONG, Q_ALONG, F32_OUT>;
   hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
-  kernel<<<all < kWideBlocks ? (unsigned)((all + 7) / 8 * 8) : kWideBlocks, 512, lds, stream>>>(g);
+  kernel<<<all < kWideBlocks ? (unsigned)((all + 7) / 8 * 8) : kWideBlocks, 256, lds, stream>>>(g);
   return hipGetLastError();
 }
 
@@ -826,7 +832,7 @@ int slope_parts(const ProjectionShape& s) {
 }
 
 int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
-int64_t round_t(int64_t x) { return (x + kT - 1) / kT * kT; }
+int64_t round_t(int64_t x) { return (x + 63) / 64 * 64; }   // (slices of either length)
 
 }  // namespace
 
