@@ -54,8 +54,8 @@ struct Gemm {
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 // ---------------------------------------------------------------- operands
-// How rows lie in memory: as whole 16-byte pieces, as fp32 elements, as anything.
-constexpr int kPieces = 0, kWords = 1, kOdd = 2;
+// How rows lie in memory: as whole 16-byte pieces, or as anything.
+constexpr int kPieces = 0, kOdd = 1;
 
 // One operand's slice in LDS, and its fragments: EXTENT values of c (or r) by
 // KT of t; ALONG: rows are values, else rows are steps of t.
@@ -119,44 +119,43 @@ struct Slice {
     static __device__ __forceinline__ const elem* start(const elem* src, int64_t row, int64_t v0, int64_t t) {
       return src + (ALONG ? v0 * row + t : t * row + v0);
     }
-    // the same by elements of 4 bytes, for fp32 rows that are not made of 16-byte pieces
-    static __device__ __forceinline__ void words(unsigned char* s, const elem* src, int64_t row, int64_t v0, int64_t values,
-                                                 int64_t t, int64_t end, int tid) {
-      const elem* start = src + (ALONG ? v0 * row + t : t * row + v0);
-      const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), most = (int)(values - v0 < EXTENT ? values - v0 : EXTENT) - 1;
-#pragma unroll
-      for (int i = 0; i < kBytes / 4 / THREADS; ++i) {
-        const int at = i * THREADS + tid, r = at / 4 / NC, c = ((at / 4 % NC) ^ swz(r)) * 4 + at % 4;
-        const int v = min(ALONG ? r : c, most), dt = ALONG ? c : r;
-        const void* p = (const char*)start + (uint32_t)((ALONG ? v : dt) * (uint32_t)row + (ALONG ? dt : v)) * 4u;
-        if (t + dt >= end) p = (const void*)kZeros;
-        __builtin_amdgcn_global_load_lds(p, (lds_void_ptr)(s + (i * THREADS + wave * 64) * 4), 4, 0, 0);
-      }
-    }
-    // the same into registers, then to LDS, where rows are not made of whole pieces: 16 bytes from any address
+    // The same into registers, then to LDS, where rows are not made of whole
+    // pieces: 16 bytes from any address.  Across, the last piece of a row ends
+    // with it, and is shifted into its place on the way to LDS.
     typedef elem Held[kLoads][PC];
-    static __device__ __forceinline__ void fetch(Held& x, const elem* src, int64_t row, int64_t v0, int64_t values,
-                                                 int64_t t0, int64_t end, int tid) {
+    __device__ __forceinline__ void fetch(Held& x, const elem* src, int64_t row, int64_t v0, int64_t values, int64_t t,
+                                          int64_t end, int tid) const {
+      const elem* from = start(src, row, v0, t);
+      const int left = end - t < KT ? (int)(end - t) : KT;
+      if (ALONG ? left == KT : values - v0 >= PC) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int at = i * THREADS + tid, r = at / NC, c = ((at % NC) ^ swz(r)) * PC;
-        const int64_t t = t0 + (ALONG ? c : r);
-        int64_t v = v0 + (ALONG ? r : c);
-        const bool whole = ALONG ? t + PC <= end : t < end && v + PC <= values;
-        if (ALONG && v >= values) v = values - 1;
-        if (whole) {
-          __builtin_memcpy(x[i], src + (ALONG ? v * row + t : t * row + v), 16);
-        } else {
+        for (int i = 0; i < kLoads; ++i) {
+          const void* p = ALONG || (i * THREADS + tid) / NC < left ? (const void*)((const char*)from + off[i]) : (const void*)kZeros;
+          __builtin_memcpy(x[i], p, 16);
+        }
+      } else {
 #pragma unroll
-          for (int e = 0; e < PC; ++e) {
-            const int64_t te = t + (ALONG ? e : 0), ve = ALONG ? v : v + e < values ? v + e : values - 1;
-            x[i][e] = te < end ? src[ALONG ? ve * row + te : te * row + ve] : (elem)0.f;
+        for (int i = 0; i < kLoads; ++i) {
+          const int at = i * THREADS + tid, r = at / NC, c = ((at % NC) ^ swz(r)) * PC;
+#pragma unroll
+          for (int e = 0; e < PC; ++e) {   // (across: fewer than PC values)
+            const bool there = ALONG ? c + e < left : r < left && c + e < values - v0;
+            x[i][e] = there ? *(const elem*)((const char*)from + off[i] + (ALONG || c == 0 ? e * kSize : 0)) : (elem)0.f;
           }
         }
       }
     }
-    static __device__ __forceinline__ void put(unsigned char* s, const Held& x, int tid) {
+    static __device__ __forceinline__ void put(unsigned char* s, Held& x, int64_t v0, int64_t values, int tid) {
       typedef __attribute__((ext_vector_type(PC))) elem piece;
+      if (!ALONG && values - v0 < EXTENT && values - v0 >= PC)
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int at = i * THREADS + tid, by = ((at % NC) ^ swz(at / NC)) * PC + PC - (int)(values - v0);
+#pragma unroll
+          for (int n = 1; n < PC; n *= 2)
+#pragma unroll
+            for (int e = 0; e + n < PC; ++e) x[i][e] = by > 0 && (by & n) ? x[i][e + n] : x[i][e];
+        }
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         piece v;
@@ -330,12 +329,15 @@ __device__ __forceinline__ void tile_of(const Gemm& g, unsigned id, int& part, i
 }
 
 // ---------------------------------------------------------------- the tile kernel
-// TR x TC of out by WR x WC waves; by twice as many where HALVES is 2, each of
-// which takes half of a slice's steps, and whose sums are joined in the end.
-template <bool BF16_, int TR_, int TC_, int WR_, int WC_, int STAGES_, int HALVES_ = 1>
+// TR x TC of out by WR x WC waves; by HALVES times as many, each set of which
+// takes its share of a slice's steps, and whose sums are joined in the end.
+// fp32 factors are split where they are used, which takes a SIMD as long as their
+// products: with four sets a wave's splitting runs beside others' products
+// (two sets and slices of 32 steps: 22 us for 1001 x 777 to 500, now 16).
+template <bool BF16_, int TR_, int TC_, int WR_, int WC_, int STAGES_, int HALVES_ = 1, int KT_ = kT>
 struct Form {
   static constexpr bool BF16 = BF16_;
-  static constexpr int TR = TR_, TC = TC_, WR = WR_, WC = WC_, STAGES = STAGES_, HALVES = HALVES_;
+  static constexpr int TR = TR_, TC = TC_, WR = WR_, WC = WC_, STAGES = STAGES_, HALVES = HALVES_, KT = KT_;
   static constexpr int kThreads = 64 * WR * WC * HALVES;
 };
 
@@ -343,14 +345,14 @@ template <typename S, bool P_ALONG, bool Q_ALONG, int KIND, bool F32_OUT>
 __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   constexpr bool BF16 = S::BF16;
   constexpr int NR = S::TR / S::WR / 32, NCOL = S::TC / S::WC / 32;
-  typedef Slice<BF16, P_ALONG, S::TC, S::kThreads> SP;
-  typedef Slice<BF16, Q_ALONG, S::TR, S::kThreads> SQ;
+  typedef Slice<BF16, P_ALONG, S::TC, S::kThreads, S::KT> SP;
+  typedef Slice<BF16, Q_ALONG, S::TR, S::kThreads, S::KT> SQ;
   typedef typename SP::elem elem;
   typedef typename att::Types<BF16>::op Op;
-  constexpr int kStage = SP::kBytes + SQ::kBytes, kLoads = (SP::kLoads + SQ::kLoads) * (KIND == kWords ? 4 : 1);
+  constexpr int kStage = SP::kBytes + SQ::kBytes, kLoads = (SP::kLoads + SQ::kLoads);
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  constexpr int kSteps = kT / 16 / S::HALVES;   // of a wave, in a slice
+  constexpr int kSteps = S::KT / 16 / S::HALVES;   // of a wave, in a slice
   const int wr = wave / S::WC % S::WR, wc = wave % S::WC, k0 = S::HALVES == 1 ? 0 : wave / (S::WC * S::WR) * kSteps;
   // blocks go round the 8 XCDs
   const unsigned all = (unsigned)g.row_tiles * g.col_tiles * g.parts, share = (all + 7) / 8;
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   const bool second = g.Q2 && part >= g.parts / 2;
   const elem *P = (const elem*)g.P, *Q = (const elem*)(second ? g.Q2 : g.Q);
   const int64_t t0 = (second ? part - g.parts / 2 : part) * g.per, t1 = t0 + g.per < g.T ? t0 + g.per : g.T;
-  const int slices = t1 > t0 ? (int)((t1 - t0 + kT - 1) / kT) : 0;
+  const int slices = t1 > t0 ? (int)((t1 - t0 + S::KT - 1) / S::KT) : 0;
   const typename SP::Loads load_p(g.p_row, c0, g.C, tid);
   const typename SQ::Loads load_q(g.q_row, r0, g.R, tid);
   // Pieces on their way through registers, of several slices where they are
@@ -372,22 +374,19 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   typename SP::Loads::Held hp[kSets];
   typename SQ::Loads::Held hq[kSets];
   auto issue = [&](unsigned char* s, int i, int set) __attribute__((always_inline)) {
-    const int64_t t = t0 + (int64_t)i * kT;
+    const int64_t t = t0 + (int64_t)i * S::KT;
     if constexpr (KIND == kPieces) {
       load_p.wide(s, P, g.p_row, c0, t, t1, tid);
       load_q.wide(s + SP::kBytes, Q, g.q_row, r0, t, t1, tid);
-    } else if constexpr (KIND == kWords) {
-      SP::Loads::words(s, P, g.p_row, c0, g.C, t, t1, tid);
-      SQ::Loads::words(s + SP::kBytes, Q, g.q_row, r0, g.R, t, t1, tid);
     } else {
-      SP::Loads::fetch(hp[set % kSets], P, g.p_row, c0, g.C, t, t1, tid);
-      SQ::Loads::fetch(hq[set % kSets], Q, g.q_row, r0, g.R, t, t1, tid);
+      load_p.fetch(hp[set % kSets], P, g.p_row, c0, g.C, t, t1, tid);
+      load_q.fetch(hq[set % kSets], Q, g.q_row, r0, g.R, t, t1, tid);
     }
   };
   auto put = [&](unsigned char* s, int set) __attribute__((always_inline)) {
     if constexpr (KIND == kOdd) {
-      SP::Loads::put(s, hp[set % kSets], tid);
-      SQ::Loads::put(s + SP::kBytes, hq[set % kSets], tid);
+      SP::Loads::put(s, hp[set % kSets], c0, g.C, tid);
+      SQ::Loads::put(s + SP::kBytes, hq[set % kSets], r0, g.R, tid);
     }
   };
   f32x16 acc[NR][NCOL] = {};
@@ -439,21 +438,25 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   constexpr int kPiece = piece_of<NCOL>();
   static_assert(kPiece * S::WR * S::WC <= S::STAGES * kStage, "");
   __syncthreads();
-  if constexpr (S::HALVES == 2) {
-    static_assert(NR == 1 && NCOL == 1, "");
-    f32x4* sums = (f32x4*)(smem + wave % (S::WR * S::WC) * kPiece) + lane;
-    if (k0)
+  if constexpr (S::HALVES > 1) {
+    static_assert(NR == 1 && NCOL == 1 && kPiece * S::WR * S::WC * (S::HALVES - 1) <= S::STAGES * kStage, "");
+    constexpr int kWaves = S::WR * S::WC;
+    f32x4* sums = (f32x4*)(smem + wave % kWaves * kPiece) + lane;
+    if (wave >= kWaves)
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        sums[64 * u] = f32x4{acc[0][0][4 * u], acc[0][0][4 * u + 1], acc[0][0][4 * u + 2], acc[0][0][4 * u + 3]};
+        sums[(wave / kWaves - 1) * kWaves * kPiece / 16 + 64 * u] =
+            f32x4{acc[0][0][4 * u], acc[0][0][4 * u + 1], acc[0][0][4 * u + 2], acc[0][0][4 * u + 3]};
     __syncthreads();
-    if (k0) return;
+    if (wave >= kWaves) return;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const f32x4 x = sums[64 * u];
+    for (int h = 0; h < S::HALVES - 1; ++h)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[0][0][4 * u + e] += x[e];
-    }
+      for (int u = 0; u < 4; ++u) {
+        const f32x4 x = sums[h * kWaves * kPiece / 16 + 64 * u];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0][0][4 * u + e] += x[e];
+      }
   }
   finish<BF16, F32_OUT>(g, acc, smem + wave * kPiece, r0 + 32 * NR * wr, c0 + 32 * NCOL * wc, part, lane);
 }
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
 // one wave a SIMD, a step's operands are fetched while the step before it is
 // multiplied, and the next slice is on its way.  A slice has 64 steps, so that a
 // row's piece is a whole line of the caches (with 32, every line passed from L2
-// twice: 0.95 us for 32 steps instead of ..).  A workgroup takes tile after
+// twice: 0.95 us for 32 steps instead of 0.88).  A workgroup takes tile after
 // tile; the next one's first slice is sent for before a tile is written.
 constexpr int kWide = 256, kWideT = 64, kWideBlocks = 256;
 
@@ -734,8 +737,8 @@ __global__ void __launch_bounds__(256) parts_kernel(const float* in, int parts, 
 // ---------------------------------------------------------------- launches
 template <typename S, bool P_ALONG, bool Q_ALONG, int KIND, bool F32_OUT>
 hipError_t launch_tiles(Gemm g, hipStream_t stream) {
-  constexpr int lds = S::STAGES * (Slice<S::BF16, P_ALONG, S::TC, S::kThreads>::kBytes +
-                                   Slice<S::BF16, Q_ALONG, S::TR, S::kThreads>::kBytes);
+  constexpr int lds = S::STAGES * (Slice<S::BF16, P_ALONG, S::TC, S::kThreads, S::KT>::kBytes +
+                                   Slice<S::BF16, Q_ALONG, S::TR, S::kThreads, S::KT>::kBytes);
   g.row_tiles = (int)((g.R + S::TR - 1) / S::TR), g.col_tiles = (g.C + S::TC - 1) / S::TC;
   const int64_t all = (int64_t)g.row_tiles * g.col_tiles * g.parts;
   auto kernel = gemm_kernel<S, P_ALONG, Q_ALONG, KIND, F32_OUT>;
@@ -760,7 +763,7 @@ hipError_t launch_wide(Gemm g, hipStream_t stream) {
 template <bool BF16>
 using Large = Form<BF16, BF16 ? 256 : 128, 128, BF16 ? 4 : 2, BF16 ? 1 : 2, BF16 ? 3 : 2>;
 template <bool BF16>
-using Small = Form<BF16, 64, 64, 2, 2, BF16 ? 6 : 4, BF16 ? 1 : 2>;   // (a slice is short: more of them on their way)
+using Small = Form<BF16, 64, 64, 2, 2, BF16 ? 6 : 2, BF16 ? 1 : 4, BF16 ? 32 : 64>;   // (a slice is short: more of them on their way)
 
 // Large tiles from three for every four CUs on, small ones below.
 bool large(int64_t R, int64_t C, int io) {
@@ -778,18 +781,23 @@ template <bool P_ALONG, bool Q_ALONG, bool F32_OUT>
 hipError_t launch_gemm(const Gemm& g, int io, bool big, hipStream_t stream) {
   const int pc = io == TM_IO_BF16 ? 8 : 4;
   const bool pieces = g.p_row % pc == 0 && g.q_row % pc == 0;
-  // Rows of fp32 elements take four times the loads, whose distances do not
-  // fit large tiles' registers (1001 rows, 777 to 500: 43 us, small ones ..).
-  if (io == TM_IO_F32 && !pieces) big = false;
   if (io == TM_IO_BF16) {
     // from two rounds of the device on
     if (pieces && (g.R + kWide - 1) / kWide * ((g.C + kWide - 1) / kWide) * g.parts >= 2 * kWideBlocks)
       return launch_wide<P_ALONG, Q_ALONG, F32_OUT>(g, stream);
-    return pieces ? launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, kPieces>(g, big, stream)
-                  : launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, kOdd>(g, big, stream);
+    if (pieces) return launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, kPieces>(g, big, stream);
+  } else if (pieces) {
+    return launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, kPieces>(g, big, stream);
   }
-  return pieces ? launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, kPieces>(g, big, stream)
-                : launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, kWords>(g, big, stream);
+  // Rows on their way through registers leave none to large tiles of operands
+  // across: 5387 fp32 rows, 640 to 1165, the gradient 220 us, by small tiles
+  // 208 (along, 20000 rows, 643 to 1160: 242, by small tiles 264).
+  if constexpr (P_ALONG)
+    return io == TM_IO_BF16 ? launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, kOdd>(g, big, stream)
+                            : launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, kOdd>(g, big, stream);
+  else
+    return io == TM_IO_BF16 ? launch_tiles<Small<true>, P_ALONG, Q_ALONG, kOdd, F32_OUT>(g, stream)
+                            : launch_tiles<Small<false>, P_ALONG, Q_ALONG, kOdd, F32_OUT>(g, stream);
 }
 
 template <bool BF16, bool VEC>
@@ -806,16 +814,18 @@ hipError_t launch_narrow(const Gemm& g, hipStream_t stream) {
 
 // The weight's gradient: parts of the rows that together fill the device, a
 // part with 128 rows at least; large tiles where there are enough of them.
-// With two planes of dz half of the parts belong to each.
+// With two planes of dz half of the parts belong to each.  Small fp32 tiles
+// have a CU each: a part more than fits at once costs a round of the device
+// (1001 rows, 500 to 777, 104 tiles: 2 parts 42 us for the whole gradient, 5 parts 49).
 int weight_parts(const ProjectionShape& s, bool* big) {
-  const bool words = s.io == TM_IO_F32 && (s.O % 4 || s.K % 4);   // small tiles only
+  const int pc = s.io == TM_IO_BF16 ? 8 : 4;
   const int planes = s.silu && s.io == TM_IO_BF16 ? 2 : 1;
   int64_t parts = 1;
-  for (int pass = words; pass < 2; ++pass) {
+  for (int pass = s.O % pc || s.K % pc; pass < 2; ++pass) {   // (odd rows: small tiles only)
     *big = pass == 0;
     const int64_t tr = *big ? (s.io == TM_IO_BF16 ? 256 : 128) : 64, tc = *big ? 128 : 64;
     const int64_t tiles = (s.O + tr - 1) / tr * ((s.K + tc - 1) / tc), most = s.M / 128 > 1 ? s.M / 128 : 1;
-    parts = (512 / planes + tiles - 1) / tiles;
+    parts = *big || s.io == TM_IO_BF16 ? (512 / planes + tiles - 1) / tiles : tiles < 256 ? 256 / tiles : 1;
     if (parts > most) parts = most;
     if (parts > 64) parts = 64;
     if (tiles * parts * planes >= 192) break;
