@@ -314,6 +314,83 @@ __device__ __forceinline__ void finish(const Gemm& g, f32x16 (&acc)[NR][NCOL], u
   }
 }
 
+// The same of 32 x 32 fp32 sums that SETS waves hold a share of each: every
+// wave writes its share to LDS, and stores 32 / SETS rows of the total.  Bias
+// and residual are sent for ahead of the product (an element's place in out is
+// written by the lane that read its residual).
+template <int SETS>
+struct Shared {
+  static constexpr int ROWS = 32 / SETS, kBytes = 4096;   // of LDS, a wave's
+  static_assert(ROWS == 8, "");
+  f32x4 bias = {}, res = {};
+  int64_t o[4];    // places in out (or -1)
+  int at[4];       // in a wave's 32 x 32 sums
+
+  // 4 neighbours a lane where rows are whole pieces, else one each of 4 pairs of rows
+  __device__ __forceinline__ Shared(const Gemm& g, int64_t r0, int c0, int set, int lane) {
+    const bool whole = g.C % 4 == 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = set * ROWS + (whole ? lane >> 3 : 2 * e + (lane >> 5)), c = whole ? 4 * (lane & 7) + e : lane & 31;
+      at[e] = row * 32 + ((c >> 2) ^ (row & 7)) * 4 + (c & 3);
+      o[e] = r0 + row < g.R && c0 + c < g.C ? (r0 + row) * g.C + c0 + c : -1;
+      if (g.bias && o[e] >= 0) bias[e] = g.bias[c0 + c];
+    }
+    if (g.residual) {
+      if (whole) {
+        if (o[0] >= 0) res = *(const f32x4*)((const float*)g.residual + o[0]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (o[e] >= 0) res[e] = ((const float*)g.residual)[o[e]];
+      }
+    }
+  }
+  __device__ __forceinline__ void put(unsigned char* mine, const f32x16& x, int lane) const {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      *(f32x4*)(mine + (lane & 31) * 128 + ((2 * u + (lane >> 5)) ^ (lane & 7)) * 16) =
+          f32x4{x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]};
+  }
+  // shares of the tile lie `apart` bytes from each other
+  __device__ __forceinline__ void store(const Gemm& g, const unsigned char* shares, int apart, int part) const {
+    f32x4 x = {};
+    const bool whole = g.C % 4 == 0;
+#pragma unroll
+    for (int h = 0; h < SETS; ++h) {
+      const float* s = (const float*)(shares + h * apart);
+      if (whole)
+        x += *(const f32x4*)(s + at[0]);
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += s[at[e]];
+    }
+    x += bias;
+    f32x4 y = x;
+    if (g.silu)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] *= sigmoid(y[e]);
+    y += res;
+    float* out = (float*)g.out + (int64_t)part * g.R * g.C;
+    if (whole) {
+      if (o[0] < 0) return;
+      if (g.pre) *(f32x4*)((float*)g.pre + o[0]) = x;
+      *(f32x4*)(out + o[0]) = y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (o[e] >= 0) {
+          if (g.pre) ((float*)g.pre)[o[e]] = x[e];
+          out[o[e]] = y[e];
+        }
+    }
+  }
+};
+
+struct Nothing {
+  __device__ __forceinline__ Nothing(const Gemm&, int64_t, int, int, int) {}
+};
+
 // Tile `id` of all, part by part: an XCD's tiles run one after the other, and
 // walk the columns of 8 row tiles at a time, so that both factors stay in its
 // L2.
@@ -329,16 +406,16 @@ __device__ __forceinline__ void tile_of(const Gemm& g, unsigned id, int& part, i
 }
 
 // ---------------------------------------------------------------- the tile kernel
-// TR x TC of out by WR x WC waves; by HALVES times as many, each set of which
+// TR x TC of out by WR x WC waves; by SETS times as many, each set of which
 // takes its share of a slice's steps, and whose sums are joined in the end.
 // fp32 factors are split where they are used, which takes a SIMD as long as their
 // products: with four sets a wave's splitting runs beside others' products
 // (two sets and slices of 32 steps: 22 us for 1001 x 777 to 500, now 16).
-template <bool BF16_, int TR_, int TC_, int WR_, int WC_, int STAGES_, int HALVES_ = 1, int KT_ = kT>
+template <bool BF16_, int TR_, int TC_, int WR_, int WC_, int STAGES_, int SETS_ = 1, int KT_ = kT>
 struct Form {
   static constexpr bool BF16 = BF16_;
-  static constexpr int TR = TR_, TC = TC_, WR = WR_, WC = WC_, STAGES = STAGES_, HALVES = HALVES_, KT = KT_;
-  static constexpr int kThreads = 64 * WR * WC * HALVES;
+  static constexpr int TR = TR_, TC = TC_, WR = WR_, WC = WC_, STAGES = STAGES_, SETS = SETS_, KT = KT_;
+  static constexpr int kThreads = 64 * WR * WC * SETS;
 };
 
 template <typename S, bool P_ALONG, bool Q_ALONG, int KIND, bool F32_OUT>
@@ -352,8 +429,8 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   constexpr int kStage = SP::kBytes + SQ::kBytes, kLoads = (SP::kLoads + SQ::kLoads);
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  constexpr int kSteps = S::KT / 16 / S::HALVES;   // of a wave, in a slice
-  const int wr = wave / S::WC % S::WR, wc = wave % S::WC, k0 = S::HALVES == 1 ? 0 : wave / (S::WC * S::WR) * kSteps;
+  constexpr int kSteps = S::KT / 16 / S::SETS;   // of a wave, in a slice
+  const int wr = wave / S::WC % S::WR, wc = wave % S::WC, k0 = S::SETS == 1 ? 0 : wave / (S::WC * S::WR) * kSteps;
   // blocks go round the 8 XCDs
   const unsigned all = (unsigned)g.row_tiles * g.col_tiles * g.parts, share = (all + 7) / 8;
   const unsigned id = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
@@ -367,6 +444,7 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
   const int slices = t1 > t0 ? (int)((t1 - t0 + S::KT - 1) / S::KT) : 0;
   const typename SP::Loads load_p(g.p_row, c0, g.C, tid);
   const typename SQ::Loads load_q(g.q_row, r0, g.R, tid);
+  typename std::conditional<(S::SETS > 1), Shared<4>, Nothing>::type shared(g, r0 + 32 * wr, c0 + 32 * wc, wave / (S::WR * S::WC), lane);
   // Pieces on their way through registers, of several slices where they are
   // few.  They are held as long, so that memory has as many steps to answer as
   // in the other kinds; kept in one set, it has one.
@@ -435,30 +513,19 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
       if (kSets > 1) put(smem + (st + 1) % S::STAGES * kStage, st + 1);
     }
   }
-  constexpr int kPiece = piece_of<NCOL>();
-  static_assert(kPiece * S::WR * S::WC <= S::STAGES * kStage, "");
   __syncthreads();
-  if constexpr (S::HALVES > 1) {
-    static_assert(NR == 1 && NCOL == 1 && kPiece * S::WR * S::WC * (S::HALVES - 1) <= S::STAGES * kStage, "");
-    constexpr int kWaves = S::WR * S::WC;
-    f32x4* sums = (f32x4*)(smem + wave % kWaves * kPiece) + lane;
-    if (wave >= kWaves)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        sums[(wave / kWaves - 1) * kWaves * kPiece / 16 + 64 * u] =
-            f32x4{acc[0][0][4 * u], acc[0][0][4 * u + 1], acc[0][0][4 * u + 2], acc[0][0][4 * u + 3]};
+  if constexpr (S::SETS > 1) {
+    static_assert(NR == 1 && NCOL == 1 && !BF16, "");
+    constexpr int kPiece = decltype(shared)::kBytes, kWaves = S::WR * S::WC;
+    static_assert(kPiece * kWaves * S::SETS <= S::STAGES * kStage, "");
+    shared.put(smem + wave * kPiece, acc[0][0], lane);
     __syncthreads();
-    if (wave >= kWaves) return;
-#pragma unroll
-    for (int h = 0; h < S::HALVES - 1; ++h)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const f32x4 x = sums[h * kWaves * kPiece / 16 + 64 * u];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[0][0][4 * u + e] += x[e];
-      }
+    shared.store(g, smem + wave % kWaves * kPiece, kWaves * kPiece, part);
+  } else {
+    constexpr int kPiece = piece_of<NCOL>();
+    static_assert(kPiece * S::WR * S::WC <= S::STAGES * kStage, "");
+    finish<BF16, F32_OUT>(g, acc, smem + wave * kPiece, r0 + 32 * NR * wr, c0 + 32 * NCOL * wc, part, lane);
   }
-  finish<BF16, F32_OUT>(g, acc, smem + wave * kPiece, r0 + 32 * NR * wr, c0 + 32 * NCOL * wc, part, lane);
 }
 
 // ---------------------------------------------------------------- the wide tile kernel
