@@ -34,7 +34,7 @@ template <bool BF16>
 constexpr int keys_of() { return BF16 ? 64 : 32; }
 
 template <bool BF16, int DP, int VEC>
-__global__ void __launch_bounds__(kThreads, BF16 && DP <= 64 ? 3 : 2) attention_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, BF16 && DP <= 64 ? 3 : BF16 || DP <= 96 ? 2 : 1) attention_kernel(Params p) {
   typedef Tile<BF16, DP> T;
   typedef typename T::elem elem;
   typedef typename T::op op;

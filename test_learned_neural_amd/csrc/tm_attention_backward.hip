@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, (BF16 ? (DP <= 64 ? 3 : 2) : DP < 96
 
 // dk and dv of one key head.
 template <bool BF16, int DP, int VEC>
-__global__ void __launch_bounds__(kThreads, (BF16 ? (DP <= 64 ? 3 : 2) : DP < 64 ? 2 : 1)) attention_dkv_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, (BF16 ? (DP <= 64 ? 2 : 1) : DP < 64 ? 2 : 1)) attention_dkv_kernel(Params p) {
   typedef Tile<BF16, DP> T;
   typedef typename T::elem elem;
   typedef typename T::frag frag;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, (BF16 ? (DP <= 64 ? 3 : 2) : DP < 64
   const int lt0 = lo + from % per;
   int lh = from / per, lt = lt0;
   const typename T::template Loads<QT, kThreads, VEC> load_q(p.q_tok, tid), load_o(p.o_tok, tid);
-  auto issue = [&](unsigned char* b) {
+  auto issue = [&](unsigned char* b) __attribute__((always_inline)) {
     const int h = at.head0 + lh;
     const elem* qp = (const elem*)p.q + at.seq * p.q_seq + h * p.q_head + (int64_t)at.t0 * p.q_tok;
     const elem* go = (const elem*)p.dout + at.seq * p.o_seq + (int64_t)at.t0 * p.o_tok + h * p.d;
@@ -338,6 +338,9 @@ __global__ void __launch_bounds__(256) attention_join_kernel(Params p) {
 
 // Workgroups that share a tile of keys' queries: so many that the device is
 // full where tiles are few, with 4 tiles of queries each where there are.
+// 3001 packed tokens, 2 key heads, d 80, fp32: 258 us, one workgroup a tile
+// 1078; 2048 tokens, 4 key heads, d 64, bf16: 99, 281.  With twice as many both
+// take as long, and 4096 tokens, 16 heads, d 128 2% longer.
 int parts_of(const AttentionShape& s) {
   const int64_t blocks = attention_blocks(s, kRows, 1), tiles = ((int64_t)s.N + 31) / 32 * (s.H / s.Hk);
   int64_t parts = 768 / (blocks > 0 ? blocks : 1);

@@ -97,9 +97,9 @@ __global__ void __launch_bounds__((64 * waves_of<BF16, DP>())) attention_step_ke
   unsigned char* mine = smem + wave * wave_lds<BF16, DP>();
   int x = part * per + wave;
   if (VEC == kPieces && p.d < DP) clear(mine, 4 * kBytes, lane, 64);
-  auto tile = [&](int i) { return i < pre ? i : lo + i - pre; };
+  auto tile = [&](int i) __attribute__((always_inline)) { return i < pre ? i : lo + i - pre; };
   const typename T::template Loads<kKeys, 64, VEC> load(p.d, lane);
-  auto issue = [&](unsigned char* t, int i) {
+  auto issue = [&](unsigned char* t, int i) __attribute__((always_inline)) {
     load_keys<BF16, DP, VEC>(load, t, kc, kn, fresh, tile(i) * kKeys, last, p.d, lane);
     load_keys<BF16, DP, VEC>(load, t + kBytes, vc, vn, fresh, tile(i) * kKeys, last, p.d, lane);
   };
@@ -254,13 +254,18 @@ __global__ void __launch_bounds__(256) step_join_kernel(StepParams p) {
 
 int64_t row_tiles_of(const AttentionStepShape& s) { return ((int64_t)s.H / s.Hk * s.n + 31) / 32; }
 
-// Workgroups of a row: enough for four a CU, with at least 8 tiles each.
+// Workgroups of a row: so many that every CU has one, with 8 tiles each at
+// least.  Each has four waves that load ahead on their own, so more of them
+// only add to what is joined.  In us, by one, two and four a CU (bf16, one query a
+// key head unless said): 192 sequences of 2048 keys, 4 queries, d 128: 81, 82,
+// 93; 64 of them 44, 50, 52; one of 16384, d 64: 18.5, 18.5, 20; 8 of 1024, fp32,
+// d 64: 16.8, 16.8, 18.
 int parts_of(const AttentionStepShape& s) {
   const int64_t rows = (int64_t)s.B * s.Hk * row_tiles_of(s);
   if (rows == 0) return 1;
   int64_t keys = s.C;
   if (s.window && (int64_t)s.window + s.n + s.prefix < keys) keys = (int64_t)s.window + s.n + s.prefix;
-  int64_t parts = (1024 + rows - 1) / rows, most = keys / kKeys / 8;
+  int64_t parts = (256 + rows - 1) / rows, most = keys / kKeys / 8;
   if (parts > most) parts = most;
   if (parts > kMostParts) parts = kMostParts;
   return parts < 1 ? 1 : (int)parts;

@@ -33,7 +33,9 @@ using att::lds_void_ptr;
 using att::u32x2;
 
 constexpr int kT = 32;           // steps of t in a slice
-constexpr int kNarrowRows = 64;  // rows up to which the narrow kernel runs
+// Rows up to which the narrow kernel runs.  bf16, 1024 to 1024, in us, 64 x 64
+// tiles second: 16 rows 11.6, 20.9; 64 rows 11.5, 22.7 (4096 to 4096: 27.6, 70.1).
+constexpr int kNarrowRows = 64;
 
 // what a slice's end past t is made of
 __device__ const float4 kZeros[1] = {};
@@ -539,27 +541,26 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_kernel(Gemm g) {
 // tile; the next one's first slice is sent for before a tile is written.
 constexpr int kWide = 256, kWideT = 64, kWideBlocks = 256;
 
-template <bool P_ALONG, bool Q_ALONG, bool F32_OUT>
 __global__ void __launch_bounds__(256, 1) wide_kernel(Gemm g) {
-  typedef Slice<true, P_ALONG, kWide, 256, kWideT> SP;
-  typedef Slice<true, Q_ALONG, kWide, 256, kWideT> SQ;
+  typedef Slice<true, true, kWide, 256, kWideT> SP, SQ;
   constexpr int NR = 4, NCOL = 4, kStage = SP::kBytes + SQ::kBytes;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2 slices], then a piece for every wave
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave >> 1, wc = wave & 1;
   // blocks go round the 8 XCDs; a block's tiles are gridDim / 8 apart in its XCD's run
-  const unsigned all = (unsigned)g.row_tiles * g.col_tiles * g.parts, share = (all + 7) / 8, stride = gridDim.x >> 3;
+  const unsigned all = (unsigned)g.row_tiles * g.col_tiles, share = (all + 7) / 8, stride = gridDim.x >> 3;
   const unsigned first = (blockIdx.x & 7) * share, end = min(first + share, all);
   unsigned id = first + (blockIdx.x >> 3);
-  int part, c0, slices;
-  int64_t r0, t0, t1;
-  const __bf16 *P = (const __bf16*)g.P, *Q;
+  int part, c0;   // (one part)
+  int64_t r0;
+  const int slices = (int)((g.T + kWideT - 1) / kWideT);
+  const __bf16 *P = (const __bf16*)g.P, *Q = (const __bf16*)g.Q;
   typename SP::Loads load_p(g.p_row, 0, kWide, tid);
   typename SQ::Loads load_q(g.q_row, 0, kWide, tid);
   constexpr int kLoads = SP::kLoads + SQ::kLoads;
   // pieces from .. to - 1 of the slice at step t
   auto issue = [&](unsigned char* s, int64_t t, int from, int to) __attribute__((always_inline)) {
-    const int left = (int)(t1 - t < kWideT ? t1 - t : kWideT);   // (zero or less behind the last slice)
+    const int left = (int)(g.T - t < kWideT ? g.T - t : kWideT);   // (zero or less behind the last slice)
     const __bf16 *sp = SP::Loads::start(P, g.p_row, c0, t), *sq = SQ::Loads::start(Q, g.q_row, r0, t);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
@@ -572,13 +573,9 @@ __global__ void __launch_bounds__(256, 1) wide_kernel(Gemm g) {
   };
   auto begin = [&]() __attribute__((always_inline)) {   // tile `id`, and its first slice
     tile_of<kWide, kWide>(g, id, part, r0, c0);
-    const bool second = g.Q2 && part >= g.parts / 2;
-    Q = (const __bf16*)(second ? g.Q2 : g.Q);
-    t0 = (second ? part - g.parts / 2 : part) * g.per, t1 = t0 + g.per < g.T ? t0 + g.per : g.T;
-    slices = t1 > t0 ? (int)((t1 - t0 + kWideT - 1) / kWideT) : 0;
     load_p = typename SP::Loads(g.p_row, c0, g.C, tid);
     load_q = typename SQ::Loads(g.q_row, r0, g.R, tid);
-    issue(smem, t0, 0, kLoads);
+    issue(smem, 0, 0, kLoads);
   };
   if (id >= end) return;
   begin();
@@ -627,7 +624,7 @@ __global__ void __launch_bounds__(256, 1) wide_kernel(Gemm g) {
 #pragma unroll 1
     for (int i = 0; i < slices; ++i) {
       unsigned char* next = smem + (i + 1) % 2 * kStage;
-      step(smem + i % 2 * kStage, next, t0 + (int64_t)(i + 1) * kWideT);
+      step(smem + i % 2 * kStage, next, (int64_t)(i + 1) * kWideT);
       att::landed();     // the next slice is there for everyone, and nobody reads this one any more
       fetch(next, 0);    // (behind the last slice: not used)
       multiply(kWideT / 16 - 1);
@@ -637,13 +634,13 @@ __global__ void __launch_bounds__(256, 1) wide_kernel(Gemm g) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       }
     }
-    const int was_part = part, was_c = c0;
+    const int was_c = c0;
     const int64_t was_r = r0;
     id += stride;
     const bool more = id < end;
     // (the last slice was read before the last barrier; what was fetched behind it is not used)
     if (more) begin();
-    finish<true, F32_OUT>(g, acc, smem + 2 * kStage + wave * piece_of<NCOL>(), was_r + 32 * NR * wr, was_c + 32 * NCOL * wc, was_part, lane);
+    finish<true, false>(g, acc, smem + 2 * kStage + wave * piece_of<NCOL>(), was_r + 32 * NR * wr, was_c + 32 * NCOL * wc, 0, lane);
     if (!more) return;
     stores = was_r + kWide <= g.R && was_c + kWide <= g.C && g.C % 8 == 0;
   }
@@ -662,7 +659,7 @@ __global__ void __launch_bounds__(512) narrow_kernel(Gemm g) {
   const int c0 = blockIdx.x * 16, v = lane & 15;
   const elem* p = (const elem*)g.P + (int64_t)min(c0 + v, g.C - 1) * g.p_row;
   f32x4 acc[BLOCKS] = {};
-  auto get = [&](const elem* row, int t) {
+  auto get = [&](const elem* row, int t) __attribute__((always_inline)) {
     frag f = {};
     if (VEC) {
       if (t < g.T) {
@@ -815,15 +812,13 @@ hipError_t launch_tiles(Gemm g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool P_ALONG, bool Q_ALONG, bool F32_OUT>
 hipError_t launch_wide(Gemm g, hipStream_t stream) {
   constexpr int lds = 2 * 2 * kWide * kWideT * 2 + 4 * piece_of<4>();
   g.row_tiles = (int)((g.R + kWide - 1) / kWide), g.col_tiles = (g.C + kWide - 1) / kWide;
-  const int64_t all = (int64_t)g.row_tiles * g.col_tiles * g.parts;
-  auto kernel = wide_kernel<P_ALONG, Q_ALONG, F32_OUT>;
-  hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  const int64_t all = (int64_t)g.row_tiles * g.col_tiles;
+  hipError_t e = hipFuncSetAttribute((const void*)wide_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
-  kernel<<<all < kWideBlocks ? (unsigned)((all + 7) / 8 * 8) : kWideBlocks, 256, lds, stream>>>(g);
+  wide_kernel<<<all < kWideBlocks ? (unsigned)((all + 7) / 8 * 8) : kWideBlocks, 256, lds, stream>>>(g);
   return hipGetLastError();
 }
 
@@ -832,7 +827,10 @@ using Large = Form<BF16, BF16 ? 256 : 128, 128, BF16 ? 4 : 2, BF16 ? 1 : 2, BF16
 template <bool BF16>
 using Small = Form<BF16, 64, 64, 2, 2, BF16 ? 6 : 2, BF16 ? 1 : 4, BF16 ? 32 : 64>;   // (a slice is short: more of them on their way)
 
-// Large tiles from three for every four CUs on, small ones below.
+// Large tiles from three for every four CUs on, small ones below.  1024 to 1024,
+// in us, large tiles first: bf16 4096 rows (128 tiles) 25.1, 24.2; 6144 rows 25.9,
+// 31.2; 8192 rows 26.9, 38.9; fp32 1536 rows (96 tiles) 56, 39; 3000 rows (192)
+// 58, 58; 4096 rows 60, 75.
 bool large(int64_t R, int64_t C, int io) {
   const int64_t tr = io == TM_IO_BF16 ? 256 : 128;
   return (R + tr - 1) / tr * ((C + 127) / 128) >= 192;
@@ -849,9 +847,13 @@ hipError_t launch_gemm(const Gemm& g, int io, bool big, hipStream_t stream) {
   const int pc = io == TM_IO_BF16 ? 8 : 4;
   const bool pieces = g.p_row % pc == 0 && g.q_row % pc == 0;
   if (io == TM_IO_BF16) {
-    // from two rounds of the device on
-    if (pieces && (g.R + kWide - 1) / kWide * ((g.C + kWide - 1) / kWide) * g.parts >= 2 * kWideBlocks)
-      return launch_wide<P_ALONG, Q_ALONG, F32_OUT>(g, stream);
+    // Wide tiles from two rounds of the device on, and along only.  1024 to
+    // 1024, in us, large tiles first: 20480 rows 60, 68; 24576 rows 63, 70; 65536
+    // rows 146, 144; 131072 rows with a residual 380, 347.  Across, the
+    // transposing reads' addresses do not fit beside the tile: dx and dweight
+    // of 60000 rows 302, wide 350.
+    if constexpr (P_ALONG && Q_ALONG)
+      if (pieces && (g.R + kWide - 1) / kWide * ((g.C + kWide - 1) / kWide) >= 2 * kWideBlocks) return launch_wide(g, stream);
     if (pieces) return launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, kPieces>(g, big, stream);
   } else if (pieces) {
     return launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, kPieces>(g, big, stream);
