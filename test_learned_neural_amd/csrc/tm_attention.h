@@ -201,9 +201,34 @@ struct Tile {
     }
   }
 
+  // The elements from c on of a row of d, a chunk of them, from any address, zero
+  // behind the row's end: 16 bytes that end with the row where the chunk
+  // passes it, shifted into place.
+  typedef __attribute__((ext_vector_type(PC))) elem piece;
+  static __device__ __forceinline__ piece odd(const elem* row, int c, int d) {
+    piece x = {};
+    if (d >= PC) {
+      const int from = min(c, d - PC), by = c - from;
+      __builtin_memcpy(&x, row + from, 16);
+      if (by) {
+#pragma unroll
+        for (int n = 1; n < PC; n *= 2)
+#pragma unroll
+          for (int e = 0; e + n < PC; ++e) x[e] = by & n ? x[e + n] : x[e];
+#pragma unroll
+        for (int e = 0; e < PC; ++e) x[e] = c + e < d ? x[e] : (elem)0.f;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < PC; ++e)
+        if (c + e < d) x[e] = row[c + e];
+    }
+    return x;
+  }
+
   // Rows j0 .. j0 + ROWS - 1 of a tensor (rows `tok` elements apart, rows past
   // `last` as row `last`) into LDS by THREADS threads: wide pieces straight to
-  // LDS, or element by element where rows are not made of 16-byte pieces.
+  // LDS, or through registers where rows are not made of 16-byte pieces.
   // Columns from d on are zero: cleared once (clear()) where pieces go straight
   // to LDS, which then leaves them alone.  A thread's places within a tile are
   // the same in every whole tile, so it keeps their distances from the tile's
@@ -236,12 +261,7 @@ struct Tile {
           if (VEC == kFull && DP == LS ? true : c * PC < d)
             __builtin_amdgcn_global_load_lds((const void*)((const char*)row0 + o), (lds_void_ptr)(t + base * 16), 16, 0, 0);
         } else {
-          const elem* s = row0 + (int64_t)min(r, last - j0) * tok + c * PC;
-          elem x[PC];
-#pragma unroll
-          for (int e = 0; e < PC; ++e) x[e] = c * PC + e < d ? s[e] : (elem)0.f;
-#pragma unroll
-          for (int e = 0; e < PC; ++e) ((elem*)(t + at * 16))[e] = x[e];
+          *(piece*)(t + at * 16) = odd(row0 + (int64_t)min(r, last - j0) * tok, c * PC, d);
         }
       }
     }

@@ -57,11 +57,7 @@ __device__ __forceinline__ void load_keys(const typename T::template Loads<kKeys
       if (VEC == kFull && DP == T::LS ? true : c * T::PC < d)
         __builtin_amdgcn_global_load_lds((const void*)(row + c * T::PC), (lds_void_ptr)(t + i * 1024), 16, 0, 0);
     } else {
-      elem x[T::PC];
-#pragma unroll
-      for (int e = 0; e < T::PC; ++e) x[e] = c * T::PC + e < d ? row[c * T::PC + e] : (elem)0.f;
-#pragma unroll
-      for (int e = 0; e < T::PC; ++e) ((elem*)(t + at * 16))[e] = x[e];
+      *(typename T::piece*)(t + at * 16) = T::odd(row, c * T::PC, d);
     }
   }
 }
