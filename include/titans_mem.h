@@ -522,7 +522,8 @@ int titans_mem_group_norm_backward(const titans_norm_desc* desc, const void* x,
  * as they were.  Sums and the softmax are fp32; for bf16 tensors the weights
  * are rounded to bf16 before they meet v, and out is rounded once.  A NaN or
  * infinity in v may reach other queries too that come up to 127 tokens
- * before it, or that it is out of the window of by up to 127.
+ * before it, or that it is out of the window of by up to 127.  Scores may be
+ * up to 2^29 either way; behind that NaN may come out.
  * d <= 128, scale > 0 (TM_ERR_UNSUPPORTED, TM_ERR_INVALID otherwise).
  */
 typedef struct {
@@ -652,8 +653,9 @@ int titans_mem_projection(const titans_projection_desc* desc, const void* x,
  *   dx         [rows,K]    io dtype, device, written
  *   dweight    [O,K]       fp32, device, written
  *   dbias      [O]         fp32, device, written
- * (dL/dresidual is dout.)  dz = dout act'(z) is rounded to the io dtype once,
- * before the products; sums are fp32, in a fixed order.  rows == 0 writes
+ * (dL/dresidual is dout.)  dz = dout act'(z) is rounded to the io dtype before
+ * the product for dx; dweight takes a bf16 one's remainder along (16 bits), and
+ * dbias what it was.  Sums are fp32, in a fixed order.  rows == 0 writes
  * zeros.  Any overlap of a written buffer is TM_ERR_ALIAS.
  */
 int64_t titans_mem_projection_backward_workspace_bytes(const titans_projection_desc* desc);

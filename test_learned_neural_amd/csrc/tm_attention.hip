@@ -18,6 +18,15 @@
 // and the scores' registers are an operand of the second product as they lie.
 // Keys and values go through LDS in tiles, loaded straight to it one tile
 // ahead.
+//
+// Measured: 8 x 16 sequences of 16384, d 64, bf16, a window of 1024: 785 us, 690
+// TFLOP/s of scores seen (a product of 8192^3 by the library: 1137).  Its
+// exponentials, maxima, sums and roundings bound it: 5 vector instructions a
+// score are as long as its two products.  32768 packed tokens in 12 sequences, 16
+// query heads, 4 key heads, d 128: 1689 us, 1037 TFLOP/s, matrix cores 53% busy
+// at the clock that they leave.  LDS is read without bank conflicts.  fp32, d 128:
+// 120 TFLOP/s with a wave a SIMD, whose registers hold all planes; two waves of
+// half the registers spill and take 1.9 times as long.
 #include "tm_attention.h"
 
 namespace titans {

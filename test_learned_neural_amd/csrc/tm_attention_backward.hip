@@ -15,7 +15,14 @@
 //
 // Either kernel forms its scores so that what it owns lies in the lanes, and
 // what it sums over in the registers, where P and dS are operands as they lie
-// (tm_attention.h).  P and dS are rounded to bf16 there for bf16 tensors.
+// (tm_attention.h).  P and dS are rounded to bf16 there for bf16 tensors: each
+// meets factors that have 8 bits themselves.
+//
+// Measured, 8 x 16 sequences of 1024, d 64, bf16: 54 us and 82 us, 129 for the call;
+// matrix cores 30% busy, the rest is the exponentials' and masks' vector work and
+// tiles of the diagonal, half of which the mask takes.  Registers decide the other
+// kernel's waves a SIMD: d 128, one 374 us for 2 x 8 x 4096, two (which spill) 602;
+// d 64, two 201 us for 4 x 16 x 2048, three 210.
 #include "tm_attention.h"
 
 namespace titans {
