@@ -73,6 +73,20 @@ def test_forward_and_gradient(shape, silu):
         t["x"], t["weight"], t["dout"], pre=pre if silu else None, activation=act).items())
 
 
+# rows that are not made of 16-byte pieces: fewer elements than a piece has, pieces
+# that pass a row's end by each number of elements, large tiles and small ones
+ODD = [(65, 3, 2, "f32"), (70, 5, 3, "f32"), (90, 2, 3, "bf16"), (90, 9, 7, "bf16"), (66, 66, 67, "f32"), (130, 129, 63, "f32"),
+       (200, 63, 131, "f32"), (100, 17, 130, "bf16"), (100, 18, 131, "bf16"), (100, 19, 132, "bf16"), (100, 20, 133, "bf16"),
+       (100, 21, 134, "bf16"), (100, 22, 135, "bf16"), (100, 23, 129, "bf16"), (5000, 43, 1001, "f32"), (9000, 43, 1001, "bf16"),
+       (4100, 321, 333, "f32")]
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("shape", ODD, ids=str)
+def test_rows_of_any_size(shape, silu):
+    test_forward_and_gradient(shape, silu)
+
+
 def test_rows_shapes_and_nothing_to_do():
     import torch
     from test_learned_neural_amd import titans_mem as tmm
