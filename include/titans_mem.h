@@ -626,8 +626,9 @@ int titans_mem_attention_step(const titans_attention_step_desc* desc,
  *   pre_out    [rows,O]    io dtype, device, written, or NULL: z, which the
  *              gradient of an activation needs
  * Products of bf16 inputs are exact, sums, bias and activation fp32, out is
- * rounded once.  fp32 products keep 24 bits; a row or column of fp32 with an
- * infinity in it comes out as NaN.
+ * rounded once.  fp32 products go through three bf16 numbers a factor, by
+ * which each is off by 2^-22 of itself at most, of either sign; a row or column
+ * of fp32 with an infinity in it comes out as NaN.
  * TM_ERR_UNSUPPORTED where a launch would have 2^24 tiles of 64 x 64.
  */
 typedef struct {
