@@ -427,7 +427,7 @@ int build_step(const titans_attention_step_desc* desc, AttentionStepShape* s) {
   return titans::attention_step_supported(*s) ? TM_OK : TM_ERR_UNSUPPORTED;
 }
 
-int build_projection(const titans_projection_desc* desc, ProjectionShape* s) {
+int build_projection(const titans_projection_desc* desc, bool backward, ProjectionShape* s) {
   if (!desc || desc->abi_version != TITANS_MEM_ABI_VERSION) return TM_ERR_INVALID;
   if (desc->rows < 0 || desc->K <= 0 || desc->O <= 0) return TM_ERR_INVALID;
   if (desc->io_dtype != TM_IO_F32 && desc->io_dtype != TM_IO_BF16) return TM_ERR_INVALID;
@@ -436,7 +436,7 @@ int build_projection(const titans_projection_desc* desc, ProjectionShape* s) {
   const double rows = (double)desc->rows;
   if (rows * desc->K > kMostElements || rows * desc->O > kMostElements) return TM_ERR_UNSUPPORTED;
   *s = {desc->rows, desc->K, desc->O, desc->io_dtype, desc->activation == TM_ACT_SILU};
-  return titans::projection_supported(*s) ? TM_OK : TM_ERR_UNSUPPORTED;
+  return titans::projection_supported(*s, backward) ? TM_OK : TM_ERR_UNSUPPORTED;
 }
 
 int delta_path(const DeltaShape& s) {
@@ -691,7 +691,7 @@ int titans_mem_attention_step(const titans_attention_step_desc* desc, const void
 int titans_mem_projection(const titans_projection_desc* desc, const void* x, const void* weight, const float* bias,
                           const void* residual, void* out, void* pre_out, void* stream) {
   ProjectionShape s;
-  int rc = build_projection(desc, &s);
+  int rc = build_projection(desc, false, &s);
   if (rc) return rc;
   const int64_t esz = s.io == TM_IO_BF16 ? 2 : 4, in = s.M * s.K * esz, all = s.M * s.O * esz;
   const int64_t w = (int64_t)s.O * s.K * esz;
@@ -709,7 +709,7 @@ int titans_mem_projection(const titans_projection_desc* desc, const void* x, con
 
 int64_t titans_mem_projection_backward_workspace_bytes(const titans_projection_desc* desc) {
   ProjectionShape s;
-  int rc = build_projection(desc, &s);
+  int rc = build_projection(desc, true, &s);
   return rc ? rc : titans::projection_backward_ws_bytes(s);
 }
 
@@ -717,7 +717,7 @@ int titans_mem_projection_backward(const titans_projection_desc* desc, const voi
                                    const void* pre, const void* dout, void* dx, float* dweight, float* dbias,
                                    void* workspace, int64_t workspace_bytes, void* stream) {
   ProjectionShape s;
-  int rc = build_projection(desc, &s);
+  int rc = build_projection(desc, true, &s);
   if (rc) return rc;
   const int64_t esz = s.io == TM_IO_BF16 ? 2 : 4, in = s.M * s.K * esz, all = s.M * s.O * esz;
   const int64_t w = (int64_t)s.O * s.K * esz, dw = (int64_t)s.O * s.K * 4, db = (int64_t)s.O * 4;

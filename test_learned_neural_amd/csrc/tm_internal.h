@@ -202,7 +202,7 @@ struct ProjectionShape {
   int64_t M;
   int K, O, io, silu;
 };
-bool projection_supported(const ProjectionShape& s);
+bool projection_supported(const ProjectionShape& s, bool backward);
 hipError_t launch_projection(const ProjectionShape& s, const void* x, const void* weight, const float* bias,
                              const void* residual, void* out, void* pre, hipStream_t stream);
 int64_t projection_backward_ws_bytes(const ProjectionShape& s);

@@ -849,28 +849,54 @@ hipError_t launch_sized(const Gemm& g, bool big, hipStream_t stream) {
              : launch_tiles<Small<BF16>, P_ALONG, Q_ALONG, KIND, F32_OUT>(g, stream);
 }
 
+// Rows made of whole 16-byte pieces, in both factors.
+bool whole_pieces(const Gemm& g, int io) {
+  const int pc = io == TM_IO_BF16 ? 8 : 4;
+  return g.p_row % pc == 0 && g.q_row % pc == 0;
+}
+
+// The tiles that a product is made by.
+// Wide tiles from two rounds of the device on, bf16 along in whole pieces only.  1024 to
+// 1024, in us, large tiles first: 20480 rows 60, 68; 24576 rows 63, 70; 65536
+// rows 146, 144; 131072 rows with a residual 380, 347.  Across, the
+// transposing reads' addresses do not fit beside the tile: dx and dweight
+// of 60000 rows 302, wide 350.
+// Rows on their way through registers leave none to large tiles of operands
+// across: 5387 fp32 rows, 640 to 1165, the gradient 220 us, by small tiles
+// 208 (along, 20000 rows, 643 to 1160: 242, by small tiles 264).
+enum Tiles { kSmallTiles, kLargeTiles, kWideTiles };
+Tiles tiles_by(const Gemm& g, int io, bool big, bool p_along, bool q_along) {
+  const bool whole = whole_pieces(g, io);
+  if (io == TM_IO_BF16 && whole && p_along && q_along &&
+      (g.R + kWide - 1) / kWide * ((g.C + kWide - 1) / kWide) >= 2 * kWideBlocks)
+    return kWideTiles;
+  return big && (whole || p_along) ? kLargeTiles : kSmallTiles;
+}
+
+template <typename S>
+int64_t count(const Gemm& g) {
+  return (g.R + S::TR - 1) / S::TR * ((g.C + S::TC - 1) / S::TC) * g.parts;
+}
+// how many of them
+int64_t tiles_of(const Gemm& g, int io, bool big, bool p_along, bool q_along) {
+  const Tiles by = tiles_by(g, io, big, p_along, q_along);
+  if (by == kWideTiles) return (g.R + kWide - 1) / kWide * ((g.C + kWide - 1) / kWide);
+  if (io == TM_IO_BF16) return by == kLargeTiles ? count<Large<true>>(g) : count<Small<true>>(g);
+  return by == kLargeTiles ? count<Large<false>>(g) : count<Small<false>>(g);
+}
+
 template <bool P_ALONG, bool Q_ALONG, bool F32_OUT>
 hipError_t launch_gemm(const Gemm& g, int io, bool big, hipStream_t stream) {
-  const int pc = io == TM_IO_BF16 ? 8 : 4;
-  const bool pieces = g.p_row % pc == 0 && g.q_row % pc == 0;
-  if (io == TM_IO_BF16) {
-    // Wide tiles from two rounds of the device on, and along only.  1024 to
-    // 1024, in us, large tiles first: 20480 rows 60, 68; 24576 rows 63, 70; 65536
-    // rows 146, 144; 131072 rows with a residual 380, 347.  Across, the
-    // transposing reads' addresses do not fit beside the tile: dx and dweight
-    // of 60000 rows 302, wide 350.
-    if constexpr (P_ALONG && Q_ALONG)
-      if (pieces && (g.R + kWide - 1) / kWide * ((g.C + kWide - 1) / kWide) >= 2 * kWideBlocks) return launch_wide(g, stream);
-    if (pieces) return launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, kPieces>(g, big, stream);
-  } else if (pieces) {
-    return launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, kPieces>(g, big, stream);
-  }
-  // Rows on their way through registers leave none to large tiles of operands
-  // across: 5387 fp32 rows, 640 to 1165, the gradient 220 us, by small tiles
-  // 208 (along, 20000 rows, 643 to 1160: 242, by small tiles 264).
+  const Tiles by = tiles_by(g, io, big, P_ALONG, Q_ALONG);
+  const bool large = by == kLargeTiles;
+  if constexpr (P_ALONG && Q_ALONG)
+    if (by == kWideTiles) return launch_wide(g, stream);
+  if (whole_pieces(g, io))
+    return io == TM_IO_BF16 ? launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, kPieces>(g, large, stream)
+                            : launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, kPieces>(g, large, stream);
   if constexpr (P_ALONG)
-    return io == TM_IO_BF16 ? launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, kOdd>(g, big, stream)
-                            : launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, kOdd>(g, big, stream);
+    return io == TM_IO_BF16 ? launch_sized<P_ALONG, Q_ALONG, F32_OUT, true, kOdd>(g, large, stream)
+                            : launch_sized<P_ALONG, Q_ALONG, F32_OUT, false, kOdd>(g, large, stream);
   else
     return io == TM_IO_BF16 ? launch_tiles<Small<true>, P_ALONG, Q_ALONG, kOdd, F32_OUT>(g, stream)
                             : launch_tiles<Small<false>, P_ALONG, Q_ALONG, kOdd, F32_OUT>(g, stream);
@@ -922,18 +948,44 @@ int64_t round_t(int64_t x) { return (x + 63) / 64 * 64; }   // (slices of either
 
 }  // namespace
 
-bool projection_supported(const ProjectionShape& s) {
-  const double m = (double)(s.M / 64 + 1), k = (double)(s.K / 64 + 1), o = (double)(s.O / 64 + 1);
-  return m * o < (double)kMostBlocks && m * k < (double)kMostBlocks && o * k * 128 < (double)kMostBlocks &&
-         s.K <= 1 << 22 && s.O <= 1 << 22;   // (Loads' distances)
+namespace {
+
+// The three products, without their pointers.
+Gemm forward_product(const ProjectionShape& s) {
+  Gemm g = {};
+  g.p_row = g.q_row = s.K, g.R = s.M, g.C = s.O, g.T = s.K, g.per = round_t(s.K), g.parts = 1;
+  return g;
+}
+Gemm dx_product(const ProjectionShape& s) {
+  Gemm g = {};
+  g.p_row = s.K, g.q_row = s.O, g.R = s.M, g.C = s.K, g.T = s.O, g.per = round_t(s.O), g.parts = 1;
+  return g;
+}
+Gemm dweight_product(const ProjectionShape& s, int parts) {
+  Gemm g = {};
+  const int64_t each = s.silu && s.io == TM_IO_BF16 ? parts / 2 : parts;
+  g.p_row = s.K, g.q_row = s.O, g.R = s.O, g.C = s.K, g.T = s.M, g.per = round_t((s.M + each - 1) / each), g.parts = parts;
+  return g;
+}
+
+}  // namespace
+
+bool projection_supported(const ProjectionShape& s, bool backward) {
+  if (s.K > 1 << 22 || s.O > 1 << 22) return false;   // (Loads' distances)
+  if (!backward)   // (few rows: a workgroup for 16 columns)
+    return s.M <= kNarrowRows || tiles_of(forward_product(s), s.io, large(s.M, s.O, s.io), true, true) < kMostBlocks;
+  bool big;
+  const int parts = weight_parts(s, &big);
+  return tiles_of(dx_product(s), s.io, large(s.M, s.K, s.io), false, true) < kMostBlocks &&
+         tiles_of(dweight_product(s, parts), s.io, big, false, false) < kMostBlocks &&
+         (int64_t)s.O * s.K / 1024 < kMostBlocks;   // (the parts' sums)
 }
 
 hipError_t launch_projection(const ProjectionShape& s, const void* x, const void* weight, const float* bias,
                              const void* residual, void* out, void* pre, hipStream_t stream) {
   if (s.M == 0) return hipSuccess;
-  Gemm g = {};
-  g.P = weight, g.Q = x, g.p_row = g.q_row = s.K, g.R = s.M, g.C = s.O, g.T = s.K;
-  g.per = round_t(s.K), g.parts = 1, g.bias = bias, g.residual = residual, g.out = out, g.pre = pre, g.silu = s.silu;
+  Gemm g = forward_product(s);
+  g.P = weight, g.Q = x, g.bias = bias, g.residual = residual, g.out = out, g.pre = pre, g.silu = s.silu;
   if (s.M <= kNarrowRows) {
     const bool vec = s.K % (s.io == TM_IO_BF16 ? 8 : 4) == 0;
     if (s.io == TM_IO_BF16) return vec ? launch_narrow<true, true>(g, stream) : launch_narrow<true, false>(g, stream);
@@ -975,19 +1027,16 @@ hipError_t launch_projection_backward(const ProjectionShape& s, const void* x, c
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const void* z = s.silu ? dz : dout;
-  Gemm g = {};
+  Gemm g;
   if (s.M > 0) {
-    g.P = weight, g.Q = z, g.p_row = s.K, g.q_row = s.O, g.R = s.M, g.C = s.K, g.T = s.O, g.per = round_t(s.O);
-    g.parts = 1, g.out = dx;
+    g = dx_product(s);
+    g.P = weight, g.Q = z, g.out = dx;
     err = launch_gemm<false, true, false>(g, s.io, large(s.M, s.K, s.io), stream);
     if (err != hipSuccess) return err;
   }
-  g = Gemm();
-  g.P = x, g.Q = z, g.p_row = s.K, g.q_row = s.O, g.R = s.O, g.C = s.K, g.T = s.M;
-  const bool two = s.silu && s.io == TM_IO_BF16;
-  const int64_t each = two ? parts / 2 : parts;
-  if (two) g.Q2 = dz2;
-  g.parts = parts, g.per = round_t((s.M + each - 1) / each), g.out = parts > 1 ? wparts : dweight;
+  g = dweight_product(s, parts);
+  g.P = x, g.Q = z, g.out = parts > 1 ? wparts : dweight;
+  if (s.silu && s.io == TM_IO_BF16) g.Q2 = dz2;
   err = launch_gemm<false, false, true>(g, s.io, big, stream);
   if (err != hipSuccess || (parts == 1 && sparts == 1)) return err;
   const int64_t n = (int64_t)s.O * s.K;
