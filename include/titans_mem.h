@@ -630,7 +630,7 @@ int titans_mem_attention_step(const titans_attention_step_desc* desc,
  * which each is off by 2^-22 of itself at most, of either sign; a row or column
  * of fp32 with an infinity in it comes out as NaN.
  * TM_ERR_UNSUPPORTED for more than 2^22 channels, or where out (in the gradient's
- * call dx, or dweight) is too large for a launch; fewer than 2^22 tiles of 64 x 64
+ * call dx, or dweight) is too large for a launch; up to 2^22 - 8 tiles of 64 x 64
  * of it never are.
  */
 typedef struct {

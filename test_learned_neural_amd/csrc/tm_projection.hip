@@ -874,15 +874,17 @@ Tiles tiles_by(const Gemm& g, int io, bool big, bool p_along, bool q_along) {
 }
 
 template <typename S>
-int64_t count(const Gemm& g) {
-  return (g.R + S::TR - 1) / S::TR * ((g.C + S::TC - 1) / S::TC) * g.parts;
+bool fits(const Gemm& g) {   // fewer than 2^32 threads, tiles in eights
+  const int64_t all = (g.R + S::TR - 1) / S::TR * ((g.C + S::TC - 1) / S::TC) * g.parts;
+  return (all + 7) / 8 * 8 < ((int64_t)1 << 32) / S::kThreads;
 }
-// how many of them
-int64_t tiles_of(const Gemm& g, int io, bool big, bool p_along, bool q_along) {
+// whether one launch can hold them
+bool one_launch(const Gemm& g, int io, bool big, bool p_along, bool q_along) {
   const Tiles by = tiles_by(g, io, big, p_along, q_along);
-  if (by == kWideTiles) return (g.R + kWide - 1) / kWide * ((g.C + kWide - 1) / kWide);
-  if (io == TM_IO_BF16) return by == kLargeTiles ? count<Large<true>>(g) : count<Small<true>>(g);
-  return by == kLargeTiles ? count<Large<false>>(g) : count<Small<false>>(g);
+  if (by == kWideTiles)   // (always 256 workgroups: counted in 32 bits)
+    return (g.R + kWide - 1) / kWide * ((g.C + kWide - 1) / kWide) < ((int64_t)1 << 31);
+  if (io == TM_IO_BF16) return by == kLargeTiles ? fits<Large<true>>(g) : fits<Small<true>>(g);
+  return by == kLargeTiles ? fits<Large<false>>(g) : fits<Small<false>>(g);
 }
 
 template <bool P_ALONG, bool Q_ALONG, bool F32_OUT>
@@ -973,11 +975,11 @@ Gemm dweight_product(const ProjectionShape& s, int parts) {
 bool projection_supported(const ProjectionShape& s, bool backward) {
   if (s.K > 1 << 22 || s.O > 1 << 22) return false;   // (Loads' distances)
   if (!backward)   // (few rows: a workgroup for 16 columns)
-    return s.M <= kNarrowRows || tiles_of(forward_product(s), s.io, large(s.M, s.O, s.io), true, true) < kMostBlocks;
+    return s.M <= kNarrowRows || one_launch(forward_product(s), s.io, large(s.M, s.O, s.io), true, true);
   bool big;
   const int parts = weight_parts(s, &big);
-  return tiles_of(dx_product(s), s.io, large(s.M, s.K, s.io), false, true) < kMostBlocks &&
-         tiles_of(dweight_product(s, parts), s.io, big, false, false) < kMostBlocks &&
+  return one_launch(dx_product(s), s.io, large(s.M, s.K, s.io), false, true) &&
+         one_launch(dweight_product(s, parts), s.io, big, false, false) &&
          (int64_t)s.O * s.K / 1024 < kMostBlocks;   // (the parts' sums)
 }
 

@@ -38,3 +38,25 @@ def test_too_many_channels_or_tiles():
     for K, O in (((1 << 22) + 1, 8), (8, (1 << 22) + 1)):
         assert forward(1, K, O) == tmm.ERR_UNSUPPORTED and backward(1, K, O) == tmm.ERR_UNSUPPORTED
     assert forward(1 << 40, 8, 8) == tmm.ERR_UNSUPPORTED and backward(1 << 40, 8, 8) == tmm.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("act", [tmm.ACT_NONE, tmm.ACT_SILU])
+def test_small_fp32_tiles_have_1024_threads(act):
+    """dx of fp32 rows that are not whole pieces goes by tiles of 64 x 64 and 1024 threads, 2^22 of which are
+    2^32 threads, too many for a launch.  The forward call goes by 128 x 128 and 256 threads.  (Launches are
+    rounded up to eight workgroups.)"""
+    most = 64 * ((1 << 22) - 8)
+    for K, O in ((3, 3), (64, 3), (3, 64), (1, 4)):
+        assert backward(most, K, O, "f32", act) > 0
+        assert backward(most + 1, K, O, "f32", act) == tmm.ERR_UNSUPPORTED
+        assert backward(300_000_000, K, O, "f32", act) == tmm.ERR_UNSUPPORTED
+        assert forward(300_000_000, K, O, "f32", act) == tmm.ERR_ALIAS
+    # whole pieces: 128 x 128 by 256 threads
+    assert backward(300_000_000, 4, 4, "f32", act) > 0 and backward(128 * ((1 << 24) - 8), 4, 4, "f32", act) > 0
+    assert backward(128 * ((1 << 24) - 8) + 1, 4, 4, "f32", act) == tmm.ERR_UNSUPPORTED
+    # bf16: small tiles of 256 threads
+    assert backward(64 * ((1 << 24) - 8), 3, 3, "bf16", act) > 0
+    assert backward(64 * ((1 << 24) - 8) + 1, 3, 3, "bf16", act) == tmm.ERR_UNSUPPORTED
+    # large odd tiles forward
+    assert forward(128 * ((1 << 24) - 8), 3, 3, "f32", act) == tmm.ERR_ALIAS
+    assert forward(128 * ((1 << 24) - 8) + 1, 3, 3, "f32", act) == tmm.ERR_UNSUPPORTED
