@@ -33,7 +33,7 @@ struct StepParams {
   const void *q, *k_new, *v_new;
   void *k, *v, *out;
   const int32_t* lengths;
-  float *po, *pml;   // parts: outputs [row][part][d], (m, l) [row][part][2]
+  float *po, *pml;   // parts: outputs [row][part][d], (m, l) [row][part][2], each from 16 bytes on
   int B, H, Hk, n, C, d, window, prefix, row_tiles, parts;
   float scale;
 };
@@ -273,6 +273,11 @@ int parts_of(const AttentionStepShape& s) {
   return parts < 1 ? 1 : (int)parts;
 }
 
+// Bytes of the parts' outputs, up to where their maxima and sums (read in pairs) may lie.
+int64_t outputs_bytes(const AttentionStepShape& s, int parts) {
+  return ((int64_t)s.B * s.H * s.n * parts * s.d * 4 + 15) / 16 * 16;
+}
+
 }  // namespace
 
 bool attention_step_supported(const AttentionStepShape& s) {
@@ -282,7 +287,7 @@ bool attention_step_supported(const AttentionStepShape& s) {
 
 int64_t attention_step_ws_bytes(const AttentionStepShape& s) {
   const int parts = parts_of(s);
-  return parts == 1 ? 0 : (int64_t)s.B * s.H * s.n * parts * (s.d + 2) * 4;
+  return parts == 1 ? 0 : outputs_bytes(s, parts) + (int64_t)s.B * s.H * s.n * parts * 8;
 }
 
 hipError_t launch_attention_step(const AttentionStepShape& s, const void* q, void* k, void* v, const void* k_new,
@@ -293,7 +298,7 @@ hipError_t launch_attention_step(const AttentionStepShape& s, const void* q, voi
   p.B = s.B, p.H = s.H, p.Hk = s.Hk, p.n = s.n, p.C = s.C, p.d = s.d, p.window = s.window, p.prefix = s.prefix;
   p.scale = s.scale, p.row_tiles = (int)row_tiles_of(s), p.parts = parts_of(s);
   const int64_t rows = (int64_t)s.B * s.H * s.n;
-  p.po = ws, p.pml = ws + rows * p.parts * s.d;
+  p.po = ws, p.pml = ws + outputs_bytes(s, p.parts) / 4;
   const unsigned grid = (unsigned)(s.B * s.Hk * p.row_tiles * p.parts);
   hipError_t err = by_type(s.io, s.d, [&](auto bf16, auto dp, auto vec) {
     constexpr bool BF16 = decltype(bf16)::value;
