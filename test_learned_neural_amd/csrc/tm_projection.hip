@@ -258,7 +258,7 @@ template <bool BF16, bool F32_OUT, int NR, int NCOL>
 __device__ __forceinline__ void finish(const Gemm& g, f32x16 (&acc)[NR][NCOL], unsigned char* mine, int64_t r0, int c0,
                                        int part, int lane) {
   typedef typename att::Types<BF16>::elem elem;
-  typedef __attribute__((ext_vector_type(8))) elem elem8;
+  typedef __attribute__((ext_vector_type(8), aligned(16))) elem elem8;   // (8 floats, too: rows begin at 16 bytes, not 32)
   constexpr int E = NCOL % 2 ? 1 : 2, W = 32 * E, L = W / 8, TURNS = 32 * L / 64;   // lanes of a row, rows' turns
   const bool whole = g.C % (F32_OUT || !BF16 ? 4 : 8) == 0;   // rows of 16-byte pieces
   // The residual may be out, so that no piece of it could pass a store: where
