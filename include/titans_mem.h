@@ -586,7 +586,8 @@ int titans_mem_attention_backward(const titans_attention_desc* desc,
  * Nothing else of the cache is written, and nothing past a length is read.
  * Arithmetic and limits as in titans_mem_attention.  A call reads the cache
  * once for every 32 of the H/Hk * N queries of a key head.  Any overlap of a
- * written buffer is TM_ERR_ALIAS (the cache is one if k_new is there).
+ * written buffer is TM_ERR_ALIAS (the cache is one if k_new is there).  C <=
+ * 2^31 - 32 (TM_ERR_UNSUPPORTED otherwise).
  */
 typedef struct {
     int32_t abi_version;  /* must equal TITANS_MEM_ABI_VERSION */

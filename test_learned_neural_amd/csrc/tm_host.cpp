@@ -419,7 +419,7 @@ int build_step(const titans_attention_step_desc* desc, AttentionStepShape* s) {
   if (desc->io_dtype != TM_IO_F32 && desc->io_dtype != TM_IO_BF16) return TM_ERR_INVALID;
   if (desc->window < 0 || desc->prefix < 0 || !(desc->scale > 0.f) || desc->scale > 3.0e38f) return TM_ERR_INVALID;
   if (desc->flags) return TM_ERR_INVALID;
-  if (desc->d > titans::kMaxWidthAttention) return TM_ERR_UNSUPPORTED;
+  if (desc->d > titans::kMaxWidthAttention || desc->C > titans::kMostRoom) return TM_ERR_UNSUPPORTED;
   if ((double)desc->B * desc->Hk * desc->C * desc->d > kMostElements) return TM_ERR_UNSUPPORTED;
   if ((double)desc->H / desc->Hk * desc->N > (double)(1 << 30)) return TM_ERR_UNSUPPORTED;
   *s = {desc->B, desc->H, desc->Hk, desc->N, desc->C, desc->d, desc->io_dtype,

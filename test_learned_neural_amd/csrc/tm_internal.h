@@ -187,6 +187,7 @@ hipError_t launch_attention_backward(const AttentionShape& s, const void* q, con
                                      const void* dout, void* dq, void* dk, void* dv, float* ws, hipStream_t stream);
 // n new tokens a sequence over a cache of C; k_new and v_new are both null or
 // both there.  window is 0 or less than C, prefix at most C.
+constexpr int kMostRoom = 0x7fffffff - 31;   // the end of the last tile of 32 keys is an int, too
 struct AttentionStepShape {
   int B, H, Hk, n, C, d, io, window, prefix;
   float scale;

@@ -1,0 +1,15 @@
+"""Host-only: the rooms of a cache that the step takes."""
+import pytest
+
+from test_learned_neural_amd import titans_mem as tmm
+
+
+@pytest.mark.parametrize("window", [0, 80])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_room(io, window):
+    """Places are 32-bit: with more room the end of the last tile of 32 keys would not be one."""
+    ok = lambda C: tmm.attention_step_workspace_bytes(  # noqa: E731
+        tmm.make_attention_step_desc(1, 1, 1, 1, C, 1, io, window=window))
+    assert ok((1 << 31) - 32) >= 0
+    for C in ((1 << 31) - 31, (1 << 31) - 1):
+        assert ok(C) == tmm.ERR_UNSUPPORTED, C
