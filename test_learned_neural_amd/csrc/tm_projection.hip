@@ -996,11 +996,11 @@ hipError_t launch_projection(const ProjectionShape& s, const void* x, const void
   return launch_gemm<true, true, false>(g, s.io, large(s.M, s.O, s.io), stream);
 }
 
-// dz and its second plane (where there is an activation), the weight's parts, the bias's sums
+// dz (where there is an activation) and what a bf16 one was rounded by, the weight's parts, the bias's sums
 int64_t projection_backward_ws_bytes(const ProjectionShape& s) {
   bool big;
   const int parts = weight_parts(s, &big);
-  return (s.silu ? 2 * round16(s.M * s.O * (s.io == TM_IO_BF16 ? 2 : 4)) : 0) +
+  return (s.silu ? (s.io == TM_IO_BF16 ? 2 * round16(s.M * s.O * 2) : round16(s.M * s.O * 4)) : 0) +
          (parts > 1 ? round16((int64_t)parts * s.O * s.K * 4) : 0) + round16((int64_t)slope_parts(s) * s.O * 4);
 }
 
@@ -1014,7 +1014,7 @@ hipError_t launch_projection_backward(const ProjectionShape& s, const void* x, c
   void *dz = nullptr, *dz2 = nullptr;
   if (s.silu) {
     dz = at, at += round16(s.M * s.O * esz);
-    dz2 = at, at += round16(s.M * s.O * esz);
+    if (s.io == TM_IO_BF16) dz2 = at, at += round16(s.M * s.O * esz);
   }
   float* wparts = parts > 1 ? (float*)at : nullptr;
   if (wparts) at += round16((int64_t)parts * s.O * s.K * 4);
