@@ -770,21 +770,24 @@ def group_norm_backward(x, weight, bias, dout, *, H: Optional[int] = None, gate=
 class _AttentionPlan:
     """What a call's shapes, type and options fix."""
 
-    def __init__(self, queries, keys, dtype, sequences, window, prefix, scale):
+    def __init__(self, queries, keys, dtype, sequences, window, prefix, scale, last=None):
+        last = sequences is not None if last is None else bool(last)
         if sequences is not None:
             if len(queries) != 3 or len(keys) != 3:
-                raise ValueError("with offsets q must be [N, H, d], k and v [N, Hk, d]")
-            (N, H, d), Hk, B, flags = queries, keys[1], sequences, FLAG_CHANNELS_LAST
-            self.keys, self.out, self.lse = (N, Hk, d), (N, H * d), (H, N)
+                raise ValueError("with offsets q must be [N, H, d], k and v [N, Hk, d] ([H, N, d] and [Hk, N, d] heads first)")
+            (N, H, d), Hk, B = (queries, keys[1], sequences) if last else ((queries[1], queries[0], queries[2]), keys[0], sequences)
+            self.keys, self.out, self.lse = (N, Hk, d) if last else (Hk, N, d), (N, H * d), (H, N)
         else:
             if len(queries) != 4 or len(keys) != 4:
-                raise ValueError("q must be [B, H, N, d], k and v [B, Hk, N, d] (or three dimensions, and offsets)")
-            (B, H, N, d), Hk, flags = queries, keys[1], 0
-            self.keys, self.out, self.lse = (B, Hk, N, d), (B, N, H * d), (B, H, N)
+                raise ValueError("q must be [B, H, N, d], k and v [B, Hk, N, d] ([B, N, H, d] and [B, N, Hk, d] channels last; "
+                                 "or three dimensions, and offsets)")
+            B, d = queries[0], queries[3]
+            (N, H), Hk = (queries[1:3], keys[2]) if last else (queries[2:0:-1], keys[1])
+            self.keys, self.out, self.lse = (B, N, Hk, d) if last else (B, Hk, N, d), (B, N, H * d), (B, H, N)
         window, prefix = min(window, (1 << 31) - 1), min(prefix, (1 << 31) - 1)
         _fits(B + 1, H, Hk, N, d)
         self.batch, self.cuts = (B,), (B + 1,)
-        self.desc = make_attention_desc(B, H, Hk, N, d, _io_of(dtype), window, prefix, scale, flags)
+        self.desc = make_attention_desc(B, H, Hk, N, d, _io_of(dtype), window, prefix, scale, FLAG_CHANNELS_LAST if last else 0)
         self.ref = ctypes.byref(self.desc)
         self.back = attention_backward_workspace_bytes(self.desc, sequences is not None)
 
@@ -792,7 +795,7 @@ class _AttentionPlan:
 _attention_plan = functools.lru_cache(maxsize=256)(_AttentionPlan)
 
 
-def _check_attention(q, k, v, offsets, lengths, window, prefix, scale):
+def _check_attention(q, k, v, offsets, lengths, window, prefix, scale, last):
     torch = _torch()
     for name, t in (("q", q), ("k", k)):
         if t is None:
@@ -800,20 +803,22 @@ def _check_attention(q, k, v, offsets, lengths, window, prefix, scale):
     if offsets is not None and (lengths is not None or offsets.dim() != 1 or offsets.shape[0] < 2):
         raise ValueError("offsets must be [sequences + 1], and come without lengths")
     io, index = q.dtype, q.get_device()
-    plan = _attention_plan(q.shape, k.shape, io, None if offsets is None else offsets.shape[0] - 1, window, prefix, scale)
+    plan = _attention_plan(q.shape, k.shape, io, None if offsets is None else offsets.shape[0] - 1, window, prefix, scale, last)
     _want(q.device, index, ("q", q, q.shape, io), ("k", k, plan.keys, io), ("v", v, plan.keys, io),
           ("offsets", offsets, plan.cuts, torch.int32), ("lengths", lengths, plan.batch, torch.int32))
     return plan, index
 
 
 def attention(q, k, v, *, offsets=None, lengths=None, window: int = 0, prefix: int = 0, scale: Optional[float] = None,
-              out=None, lse_out=None) -> Tuple:
+              channels_last: Optional[bool] = None, out=None, lse_out=None) -> Tuple:
     """Causal attention over whole prompts (titans_mem_attention).
 
     q: [B, H, N, d], k, v: [B, Hk, N, d] (float32 or bfloat16, Hk divides H:
     query head h reads key head h // (H // Hk)) with lengths [B] int32 or None;
     or sequences one behind the other, q: [N, H, d], k, v: [N, Hk, d] with
-    offsets [sequences + 1] int32.  Token i sees token j <= i of its sequence
+    offsets [sequences + 1] int32.  channels_last says otherwise: True with q
+    [B, N, H, d] and k, v [B, N, Hk, d], False with offsets, q [H, N, d] and k, v
+    [Hk, N, d].  Token i sees token j <= i of its sequence
     where window is 0, i - j < window or j < prefix.  scale is 1/sqrt(d) by
     default.  Returns (out, lse): [B, N, H*d] in q's type and [B, H, N]
     float32, or [N, H*d] and [H, N].  New ones hold zeros for tokens of no
@@ -821,7 +826,7 @@ def attention(q, k, v, *, offsets=None, lengths=None, window: int = 0, prefix: i
     were.
     """
     torch = _torch()
-    plan, index = _check_attention(q, k, v, offsets, lengths, window, prefix, scale)
+    plan, index = _check_attention(q, k, v, offsets, lengths, window, prefix, scale, channels_last)
     new = torch.empty if offsets is None and lengths is None else torch.zeros
     if out is None:
         out = new(plan.out, dtype=q.dtype, device=q.device)
@@ -837,7 +842,7 @@ def attention(q, k, v, *, offsets=None, lengths=None, window: int = 0, prefix: i
 
 
 def attention_backward(q, k, v, out, lse, dout, *, offsets=None, lengths=None, window: int = 0, prefix: int = 0,
-                       scale: Optional[float] = None, workspace=None):
+                       scale: Optional[float] = None, channels_last: Optional[bool] = None, workspace=None):
     """Gradients through attention() (titans_mem_attention_backward).
 
     Same inputs as attention(), what it returned, and dout in out's shape and
@@ -845,7 +850,7 @@ def attention_backward(q, k, v, out, lse, dout, *, offsets=None, lengths=None, w
     the query heads of a key head; zero for tokens of no sequence).
     """
     torch = _torch()
-    plan, index = _check_attention(q, k, v, offsets, lengths, window, prefix, scale)
+    plan, index = _check_attention(q, k, v, offsets, lengths, window, prefix, scale, channels_last)
     _want(q.device, index, ("out", out, plan.out, q.dtype), ("lse", lse, plan.lse, torch.float32),
           ("dout", dout, plan.out, q.dtype))
     g = {n: torch.empty_like(t) for n, t in (("q", q), ("k", k), ("v", v))}
