@@ -524,7 +524,7 @@ int titans_mem_group_norm_backward(const titans_norm_desc* desc, const void* x,
  * infinity in v may reach other queries too that come up to 127 tokens
  * before it, or that it is out of the window of by up to 127.  Scores may be
  * up to 2^29 either way; behind that NaN may come out.
- * d <= 128, scale > 0 (TM_ERR_UNSUPPORTED, TM_ERR_INVALID otherwise).
+ * d <= 128, 0 < scale <= 2e38 (TM_ERR_UNSUPPORTED, TM_ERR_INVALID otherwise).
  */
 typedef struct {
     int32_t abi_version;  /* must equal TITANS_MEM_ABI_VERSION */

@@ -389,6 +389,9 @@ int build_norm(const titans_norm_desc* desc, NormShape* s) {
   return TM_OK;
 }
 
+// positive, and finite in base 2 (scale log2 e), too
+bool good_scale(float scale) { return scale > 0.f && scale <= 2.0e38f; }
+
 struct AttentionBytes {
   int64_t q, k, lse;   // of q and out, of k and v, of lse
 };
@@ -398,7 +401,7 @@ int build_attention(const titans_attention_desc* desc, bool packed, AttentionSha
   if (desc->B <= 0 || desc->H <= 0 || desc->Hk <= 0 || desc->H % desc->Hk || desc->N < 0 || desc->d <= 0)
     return TM_ERR_INVALID;
   if (desc->io_dtype != TM_IO_F32 && desc->io_dtype != TM_IO_BF16) return TM_ERR_INVALID;
-  if (desc->window < 0 || desc->prefix < 0 || !(desc->scale > 0.f) || desc->scale > 3.0e38f) return TM_ERR_INVALID;
+  if (desc->window < 0 || desc->prefix < 0 || !good_scale(desc->scale)) return TM_ERR_INVALID;
   if (desc->flags & ~TM_FLAG_CHANNELS_LAST) return TM_ERR_INVALID;
   if (desc->d > titans::kMaxWidthAttention) return TM_ERR_UNSUPPORTED;
   const int64_t rows = (packed ? 1 : (int64_t)desc->B) * desc->N;
@@ -417,7 +420,7 @@ int build_step(const titans_attention_step_desc* desc, AttentionStepShape* s) {
   if (desc->B <= 0 || desc->H <= 0 || desc->Hk <= 0 || desc->H % desc->Hk || desc->N < 0 || desc->C <= 0 || desc->d <= 0)
     return TM_ERR_INVALID;
   if (desc->io_dtype != TM_IO_F32 && desc->io_dtype != TM_IO_BF16) return TM_ERR_INVALID;
-  if (desc->window < 0 || desc->prefix < 0 || !(desc->scale > 0.f) || desc->scale > 3.0e38f) return TM_ERR_INVALID;
+  if (desc->window < 0 || desc->prefix < 0 || !good_scale(desc->scale)) return TM_ERR_INVALID;
   if (desc->flags) return TM_ERR_INVALID;
   if (desc->d > titans::kMaxWidthAttention || desc->C > titans::kMostRoom) return TM_ERR_UNSUPPORTED;
   if ((double)desc->B * desc->Hk * desc->C * desc->d > kMostElements) return TM_ERR_UNSUPPORTED;
