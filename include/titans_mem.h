@@ -584,7 +584,8 @@ int titans_mem_attention_backward(const titans_attention_desc* desc,
  *   out        [B,N,H*d]   io dtype, device, written; zeros for a token whose
  *              place would be before the first (an idle row has length 0)
  * Nothing else of the cache is written, and nothing past a length is read.
- * Arithmetic and limits as in titans_mem_attention.  A call reads the cache
+ * Arithmetic and limits as in titans_mem_attention, but that weights keep 16
+ * bits before they meet v for bf16 tensors.  A call reads the cache
  * once for every 32 of the H/Hk * N queries of a key head.  Any overlap of a
  * written buffer is TM_ERR_ALIAS (the cache is one if k_new is there).  C <=
  * 2^31 - 32 (TM_ERR_UNSUPPORTED otherwise).

@@ -134,6 +134,14 @@ __device__ __forceinline__ Op operand(const f32x16& x, int s) {
     return factor(t);
 }
 
+// what operand() has rounded them by, rounded itself: with it a weight keeps 16 bits
+__device__ __forceinline__ bf16x8 remainder(const f32x16& x, int s, const bf16x8& rounded) {
+  f32x8 t;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) t[j] = x[8 * s + j] - (float)rounded[j];
+  return __builtin_convertvector(t, bf16x8);
+}
+
 // the other half wave's value
 __device__ __forceinline__ float other_half(float x) {
   const unsigned u = __builtin_bit_cast(unsigned, x);
