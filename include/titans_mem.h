@@ -522,8 +522,9 @@ int titans_mem_group_norm_backward(const titans_norm_desc* desc, const void* x,
  * as they were.  Sums and the softmax are fp32; for bf16 tensors the weights
  * are rounded to bf16 before they meet v, and out is rounded once.  A NaN or
  * infinity in v may reach other queries too that come up to 127 tokens
- * before it, or that it is out of the window of by up to 127.  Scores may be
- * up to 2^29 either way; behind that NaN may come out.
+ * before it, or that it is out of the window of by up to 190.  An infinity in
+ * an fp32 q or k is a NaN in the scores that it is part of.  Scores may be up to
+ * 2^29 either way; behind that NaN may come out.
  * d <= 128, 0 < scale <= 2e38 (TM_ERR_UNSUPPORTED, TM_ERR_INVALID otherwise).
  */
 typedef struct {
@@ -553,9 +554,11 @@ int titans_mem_attention(const titans_attention_desc* desc, const void* q,
  * Same inputs as the forward call.  Tokens of no sequence get zero gradients.
  * Sums are fp32 and in a fixed order; for bf16 tensors the weights and their
  * derivatives are rounded to bf16 before they meet q, k and dout, and results
- * once.  A NaN or infinity in q, k, v or dout may reach the gradients of the
- * 255 tokens before it and behind it too.  Any overlap of a written buffer is
- * TM_ERR_ALIAS.
+ * once.  Weights are formed from lse, whose rounding they carry (2^-22 of its
+ * size, relative to them).  A NaN or infinity in q, k, v or dout may reach the
+ * gradients of the 255 tokens before it and behind it too, and in q or dout,
+ * where there is a window, those of the 31 tokens behind the persistent ones.
+ * Any overlap of a written buffer is TM_ERR_ALIAS.
  * packed: whether the call has offsets.
  */
 int64_t titans_mem_attention_backward_workspace_bytes(const titans_attention_desc* desc, int32_t packed);
@@ -585,7 +588,8 @@ int titans_mem_attention_backward(const titans_attention_desc* desc,
  *              place would be before the first (an idle row has length 0)
  * Nothing else of the cache is written, and nothing past a length is read.
  * Arithmetic and limits as in titans_mem_attention, but that weights keep 16
- * bits before they meet v for bf16 tensors.  A call reads the cache
+ * bits before they meet v for bf16 tensors, and that a NaN or infinity in v may
+ * reach all new tokens of its row.  A call reads the cache
  * once for every 32 of the H/Hk * N queries of a key head.  Any overlap of a
  * written buffer is TM_ERR_ALIAS (the cache is one if k_new is there).  C <=
  * 2^31 - 32 (TM_ERR_UNSUPPORTED otherwise).

@@ -98,13 +98,15 @@ __global__ void __launch_bounds__(kThreads, (BF16 ? (DP <= 64 ? 3 : 2) : DP < 96
   const int lo = p.window ? max(0, i0 - p.window + 1) / KT : 0;
   const int pre = min((p.prefix + KT - 1) / KT, lo);
   int t = pre > 0 ? 0 : lo;
+  // (of the prefix's tiles only the persistent tokens are read: a NaN behind them is not met by a weight of 0)
+  auto end_of = [&](int t) __attribute__((always_inline)) { return t < pre ? min(last, p.prefix - 1) : last; };
   if (VEC == kPieces && p.d < DP) {
     clear(smem, 4 * kBytes, tid, kThreads);
     __syncthreads();
   }
   const typename T::template Loads<KT, kThreads, VEC> load(p.k_tok, tid);
-  load(smem, kp, p.k_tok, t * KT, last, p.d, tid);
-  load(smem + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
+  load(smem, kp, p.k_tok, t * KT, end_of(t), p.d, tid);
+  load(smem + kBytes, vp, p.k_tok, t * KT, end_of(t), p.d, tid);
 
   op q[DP / 16], go[DP / 16];
   const int64_t ot = at.seq * p.o_seq + qt * p.o_tok + h * p.d, stat = ((int64_t)at.seq * p.H + h) * p.N + qt;
@@ -137,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, (BF16 ? (DP <= 64 ? 3 : 2) : DP < 96
   auto step = [&](const unsigned char* __restrict__ kb, unsigned char* __restrict__ nb, int t, int k0) __attribute__((always_inline)) {
     const unsigned char* vb = kb + kBytes;
     if (t <= top) {
-      load(nb, kp, p.k_tok, t * KT, last, p.d, tid);
-      load(nb + kBytes, vp, p.k_tok, t * KT, last, p.d, tid);
+      load(nb, kp, p.k_tok, t * KT, end_of(t), p.d, tid);
+      load(nb + kBytes, vp, p.k_tok, t * KT, end_of(t), p.d, tid);
     }
 #pragma unroll
     for (int g = 0; g < KT / 32; ++g) {

@@ -107,8 +107,10 @@ __global__ void __launch_bounds__((64 * waves_of<BF16, DP>())) attention_step_ke
   auto tile = [&](int i) __attribute__((always_inline)) { return i < pre ? i : lo + i - pre; };
   const typename T::template Loads<kKeys, 64, VEC> load(p.d, lane);
   auto issue = [&](unsigned char* t, int i) __attribute__((always_inline)) {
-    load_keys<BF16, DP, VEC>(load, t, kc, kn, fresh, tile(i) * kKeys, last, p.d, lane);
-    load_keys<BF16, DP, VEC>(load, t + kBytes, vc, vn, fresh, tile(i) * kKeys, last, p.d, lane);
+    // (of the prefix's tiles only the persistent tokens are read: a NaN behind them is not met by a weight of 0)
+    const int to = i < pre ? min(last, p.prefix - 1) : last;
+    load_keys<BF16, DP, VEC>(load, t, kc, kn, fresh, tile(i) * kKeys, to, p.d, lane);
+    load_keys<BF16, DP, VEC>(load, t + kBytes, vc, vn, fresh, tile(i) * kKeys, to, p.d, lane);
   };
   // (what was cleared is there before a load may write beside it)
   landed_in_wave();
