@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const void* dout_, const voi
           const float a = (float)z[e], sg = sigmoid(a);
           y[e] *= sg * fmaf(a, 1.f - sg, 1.f);
           hi[e] = (elem)y[e];
-          lo[e] = (elem)(y[e] - (float)hi[e]);
+          lo[e] = (elem)(__builtin_isinf((float)hi[e]) ? 0.f : y[e] - (float)hi[e]);   // (an infinity leaves nothing)
         }
         *(piece*)(dz + o) = hi;
         if (BF16) *(piece*)(dz2 + o) = lo;
