@@ -19,14 +19,20 @@
 // Keys and values go through LDS in tiles, loaded straight to it one tile
 // ahead.
 //
-// Measured: 8 x 16 sequences of 16384, d 64, bf16, a window of 1024: 785 us, 690
+// Weights are rounded to bf16 before they meet v for bf16 tensors, which puts out
+// 2.0e-3 off where its own rounding is 1.6e-3.  As two bf16 numbers (what the
+// step's kernel does, where memory is waited for) they would take a third more: the
+// two cases below 1061 us instead of 804, and 2338 instead of 1720.
+//
+// Measured: 8 x 16 sequences of 16384, d 64, bf16, a window of 1024: 777 us, 697
 // TFLOP/s of scores seen (a product of 8192^3 by the library: 1137).  Its
 // exponentials, maxima, sums and roundings bound it: 5 vector instructions a
 // score are as long as its two products.  32768 packed tokens in 12 sequences, 16
-// query heads, 4 key heads, d 128: 1689 us, 1037 TFLOP/s, matrix cores 53% busy
-// at the clock that they leave.  LDS is read without bank conflicts.  fp32, d 128:
-// 120 TFLOP/s with a wave a SIMD, whose registers hold all planes; two waves of
-// half the registers spill and take 1.9 times as long.
+// query heads, 4 key heads, d 128: 1745 us, 1004 TFLOP/s, matrix cores 52% busy
+// at the clock that they leave.  LDS is read without bank conflicts.  fp32, 2 x 8
+// sequences of 4096, d 128: 550 us, 125 TFLOP/s with a wave a SIMD, whose registers
+// hold all planes; two waves of half the registers spill and took 1.9 times as
+// long.  d 64: 365 us, 94 TFLOP/s.
 #include "tm_attention.h"
 
 namespace titans {

@@ -16,12 +16,14 @@
 // Either kernel forms its scores so that what it owns lies in the lanes, and
 // what it sums over in the registers, where P and dS are operands as they lie
 // (tm_attention.h).  P and dS are rounded to bf16 there for bf16 tensors: each
-// meets factors that have 8 bits themselves.
+// meets factors that have 8 bits themselves.  Gradients are 2.4e-3 off by that; as
+// two bf16 numbers each they would be 1.8e-3 off, for 161 us instead of 127 (the
+// case below), and 445 instead of 373 at d 128, 2 x 8 x 4096.
 //
-// Measured, 8 x 16 sequences of 1024, d 64, bf16: 54 us and 82 us, 129 for the call;
+// Measured, 8 x 16 sequences of 1024, d 64, bf16: 54 us and 82 us, 130 for the call;
 // matrix cores 30% busy, the rest is the exponentials' and masks' vector work and
 // tiles of the diagonal, half of which the mask takes.  Registers decide the other
-// kernel's waves a SIMD: d 128, one 374 us for 2 x 8 x 4096, two (which spill) 602;
+// kernel's waves a SIMD: d 128, one 373 us for 2 x 8 x 4096, two (which spill) 602;
 // d 64, two 201 us for 4 x 16 x 2048, three 210.
 #include "tm_attention.h"
 
@@ -347,9 +349,12 @@ __global__ void __launch_bounds__(256) attention_join_kernel(Params p) {
 
 // Workgroups that share a tile of keys' queries: so many that the device is
 // full where tiles are few, with 4 tiles of queries each where there are.
-// 3001 packed tokens, 2 key heads, d 80, fp32: 258 us, one workgroup a tile
+// 3001 packed tokens, 2 key heads, d 80, fp32: 257 us, one workgroup a tile
 // 1078; 2048 tokens, 4 key heads, d 64, bf16: 99, 281.  With twice as many both
-// take as long, and 4096 tokens, 16 heads, d 128 2% longer.
+// take as long, and 4096 tokens, 16 heads, d 128 2% longer.  Tiles are counted
+// for the call, empty ones of short sequences too: 16 sequences, 4 key heads, d 64,
+// one of 8192 tokens and the others of 256 have one workgroup a tile, 897 us for dk
+// and dv, where that sequence alone has several, 419.
 int parts_of(const AttentionShape& s) {
   const int64_t blocks = attention_blocks(s, kRows, 1), tiles = ((int64_t)s.N + 31) / 32 * (s.H / s.Hk);
   int64_t parts = 768 / (blocks > 0 ? blocks : 1);

@@ -12,10 +12,10 @@
 // workgroups are joined by a second kernel, in the parts' order.
 //
 // Measured: 192 sequences of up to 2048 keys, 16 query heads, 4 key heads, d 128, bf16:
-// 81 us, 5.0 TB/s, what a copy reaches.  One sequence of 16384, 16 heads, d 64: 14 us,
+// 82 us, 4.9 TB/s, what a copy reaches.  One sequence of 16384, 16 heads, d 64: 14 us,
 // 4.7 TB/s, and 4 us for the second kernel.  fp32 at d 96 and more has two waves a
 // workgroup and one workgroup a CU (a wave's stages are 64 KB): 24 x 16 x 4096 x 128
-// 555 us, 2.9 TB/s, bound by the splitting into planes; at d 64 166 us, 4.9 TB/s.
+// 541 us, 3.0 TB/s, bound by the splitting into planes; at d 64 168 us, 4.8 TB/s.
 //
 // bf16 weights meet the values as two bf16 numbers, what they are rounded to and
 // what that left: out is then off by its own rounding alone, and beside the
@@ -274,7 +274,10 @@ int64_t row_tiles_of(const AttentionStepShape& s) { return ((int64_t)s.H / s.Hk 
 // only add to what is joined.  In us, by one, two and four a CU (bf16, one query a
 // key head unless said): 192 sequences of 2048 keys, 4 queries, d 128: 81, 82,
 // 93; 64 of them 44, 50, 52; one of 16384, d 64: 18.5, 18.5, 20; 8 of 1024, fp32,
-// d 64: 16.8, 16.8, 18.
+// d 64: 16.8, 16.8, 18.  Lengths, which the host does not know, have no say: among
+// 256 rows of one workgroup each a long context is read by its own alone (64
+// sequences, 4 key heads, d 128, room for 65536: one full and the others of 512
+// tokens 590 us, all of 1528 41).
 int parts_of(const AttentionStepShape& s) {
   const int64_t rows = (int64_t)s.B * s.Hk * row_tiles_of(s);
   if (rows == 0) return 1;

@@ -19,9 +19,10 @@
 //
 // Measured, bf16, 1024 to 1024: 131072 rows with a residual 347 us (a copy of what
 // is read and written: 157; the product by the library alone: 213 to 263); the
-// gradient of 16384 rows with SiLU 161: slope 25 (at a copy's rate), dx 42, dweight 75
-// (twice the work: two planes), its parts 20.  8192^3: 903 us, 1218 TFLOP/s.  fp32,
-// 1001 rows of 500 to 777: 13 to 15 us, the gradient 41: slope 3, dx 20, dweight 17, parts 4.
+// gradient of 16384 rows with SiLU 160: slope 26 (at a copy's rate), dx 43, dweight 75
+// (twice the work: two planes), its parts 20.  8192^3: 903 to 925 us, 1190 TFLOP/s.  fp32,
+// 1001 rows of 500 to 777: 14 to 15 us, the gradient 41: slope 4, dx 21, dweight 18, parts 4;
+// 4096 rows, 1024 to 1024, 59 us, 145 TFLOP/s.
 #include "tm_attention.h"
 
 namespace titans {
@@ -418,7 +419,7 @@ __device__ __forceinline__ void tile_of(const Gemm& g, unsigned id, int& part, i
 // takes its share of a slice's steps, and whose sums are joined in the end.
 // fp32 factors are split where they are used, which takes a SIMD as long as their
 // products: with four sets a wave's splitting runs beside others' products
-// (two sets and slices of 32 steps: 22 us for 1001 x 777 to 500, now 16).
+// (two sets and slices of 32 steps: 22 us for 1001 x 777 to 500; this 16 to 17).
 template <bool BF16_, int TR_, int TC_, int WR_, int WC_, int STAGES_, int SETS_ = 1, int KT_ = kT>
 struct Form {
   static constexpr bool BF16 = BF16_;
@@ -722,9 +723,11 @@ __global__ void __launch_bounds__(512) narrow_kernel(Gemm g) {
 // ---------------------------------------------------------------- dz and dbias
 // dz = dout act'(pre) and its column sums.  The products read it in the io
 // type; dx is of that type too, but dweight is fp32, for which a bf16 dz comes
-// with what it was rounded by (dz2: together 16 bits, 2^-18 off), the second
-// half of a sum twice as long (by one plane dweight would be 1.7e-3 off).  A workgroup has 64 lanes x PC columns and `per`
-// rows, which its 4 waves share.
+// with what it was rounded by (dz2: together 16 bits, 2^-16 off at most), the
+// second half of a sum twice as long (dweight is 2.5e-6 off; by one plane it would
+// be 1.7e-3).  dx, 2.3e-3 off where its own rounding is 1.7e-3, takes one plane: two
+// would be its product twice, 43 us of 160 for 16384 rows.  A workgroup has 64
+// lanes x PC columns and `per` rows, which its 4 waves share.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) slope_kernel(const void* dout_, const void* pre_, void* dz_, void* dz2_, float* sums,
                                                     int64_t R, int C, int64_t per) {
@@ -836,8 +839,8 @@ using Small = Form<BF16, 64, 64, 2, 2, BF16 ? 6 : 2, BF16 ? 1 : 4, BF16 ? 32 : 6
 
 // Large tiles from three for every four CUs on, small ones below.  1024 to 1024,
 // in us, large tiles first: bf16 4096 rows (128 tiles) 25.1, 24.2; 6144 rows 25.9,
-// 31.2; 8192 rows 26.9, 38.9; fp32 1536 rows (96 tiles) 56, 39; 3000 rows (192)
-// 58, 58; 4096 rows 60, 75.
+// 31.2; 8192 rows 26.9, 38.9; fp32 1536 rows (96 tiles) 55, 43; 3000 rows (192)
+// 57, 63; 4096 rows 59, 82.
 bool large(int64_t R, int64_t C, int io) {
   const int64_t tr = io == TM_IO_BF16 ? 256 : 128;
   return (R + tr - 1) / tr * ((C + 127) / 128) >= 192;
@@ -861,9 +864,11 @@ bool whole_pieces(const Gemm& g, int io) {
 // rows 146, 144; 131072 rows with a residual 380, 347.  Across, the
 // transposing reads' addresses do not fit beside the tile: dx and dweight
 // of 60000 rows 302, wide 350.
-// Rows on their way through registers leave none to large tiles of operands
-// across: 5387 fp32 rows, 640 to 1165, the gradient 220 us, by small tiles
-// 208 (along, 20000 rows, 643 to 1160: 242, by small tiles 264).
+// Rows on their way through registers leave few to large tiles of operands
+// across, and neither is always faster (fp32, the gradient in us, large tiles
+// first: 5387 rows, 641 to 1165 254, 222; 4100 rows, 1023 to 1025 302, 294; 20000
+// rows, 643 to 1160 715, 765; 30001 rows, 255 to 257 120, 144): small ones are
+// taken.  Along, 20000 rows, 643 to 1160: 237, by small tiles 330.
 enum Tiles { kSmallTiles, kLargeTiles, kWideTiles };
 Tiles tiles_by(const Gemm& g, int io, bool big, bool p_along, bool q_along) {
   const bool whole = whole_pieces(g, io);
@@ -920,7 +925,7 @@ hipError_t launch_narrow(const Gemm& g, hipStream_t stream) {
 // part with 128 rows at least; large tiles where there are enough of them.
 // With two planes of dz half of the parts belong to each.  Small fp32 tiles
 // have a CU each: a part more than fits at once costs a round of the device
-// (1001 rows, 500 to 777, 104 tiles: 2 parts 42 us for the whole gradient, 5 parts 49).
+// (1001 rows, 500 to 777, 104 tiles: 2 parts 41 us for the whole gradient, 5 parts 54).
 int weight_parts(const ProjectionShape& s, bool* big) {
   const int pc = s.io == TM_IO_BF16 ? 8 : 4;
   const int planes = s.silu && s.io == TM_IO_BF16 ? 2 : 1;
