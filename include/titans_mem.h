@@ -525,7 +525,9 @@ int titans_mem_group_norm_backward(const titans_norm_desc* desc, const void* x,
  * before it, or that it is out of the window of by up to 190.  An infinity in
  * an fp32 q or k is a NaN in the scores that it is part of.  Scores may be up to
  * 2^29 either way; behind that NaN may come out.
- * d <= 128, 0 < scale <= 2e38 (TM_ERR_UNSUPPORTED, TM_ERR_INVALID otherwise).
+ * d <= 128, 0 < scale <= 2e38 (TM_ERR_UNSUPPORTED, TM_ERR_INVALID otherwise);
+ * H d <= 2^22, and fewer than 2^24 tiles of 32 tokens of a query head: B H
+ * ceil(N / 32), or H (N / 32 + B) with offsets (TM_ERR_UNSUPPORTED).
  */
 typedef struct {
     int32_t abi_version;  /* must equal TITANS_MEM_ABI_VERSION */
@@ -592,7 +594,8 @@ int titans_mem_attention_backward(const titans_attention_desc* desc,
  * reach all new tokens of its row.  A call reads the cache
  * once for every 32 of the H/Hk * N queries of a key head.  Any overlap of a
  * written buffer is TM_ERR_ALIAS (the cache is one if k_new is there).  C <=
- * 2^31 - 32 (TM_ERR_UNSUPPORTED otherwise).
+ * 2^31 - 32, fewer than 2^24 queries (B H N) and, for every part of the cache (64
+ * at most), 2^24 tiles of 32 of them (TM_ERR_UNSUPPORTED otherwise).
  */
 typedef struct {
     int32_t abi_version;  /* must equal TITANS_MEM_ABI_VERSION */
@@ -633,8 +636,9 @@ int titans_mem_attention_step(const titans_attention_step_desc* desc,
  *              gradient of an activation needs
  * Products of bf16 inputs are exact, sums, bias and activation fp32, out is
  * rounded once.  fp32 products go through three bf16 numbers a factor, by
- * which each is off by 2^-22 of itself at most, of either sign; a row or column
- * of fp32 with an infinity in it comes out as NaN.
+ * which each is off by 2^-22 of itself at most, of either sign (where a factor is
+ * below 2^-110, as if it were off by 2^-133); a row or column of fp32 with an
+ * infinity in it comes out as NaN.
  * TM_ERR_UNSUPPORTED for more than 2^22 channels, or where out (in the gradient's
  * call dx, or dweight) is too large for a launch; up to 2^22 - 8 tiles of 64 x 64
  * of it never are.

@@ -86,3 +86,18 @@ def test_the_largest_and_the_infinite():
         want = (x[:2].double() @ w.double().t())
         assert ((got[:2].double() - want).abs() <= 6.2 * U * want.abs()).all()
         assert torch.isnan(got[2:4]).all() and torch.equal(got[4:], w.t().expand(rows - 4, 3))
+
+
+@pytest.mark.parametrize("rows", [8, 100, 1800])
+@pytest.mark.parametrize("low", [110, 113, 120, 126])
+def test_small_factors(rows, low):
+    """Factors down to 2^-126: planes end at bf16's last step, 2^-133, where the third is cut off; from 2^-110 on nothing
+    is lost by that, below a product is off by that times the other factor more."""
+    import torch
+    from test_learned_neural_amd import titans_mem as tmm
+    x, y = _factors(3, rows), _factors(4, 1800)
+    a = torch.from_numpy(x * np.float32(2.0 ** -low))[:, None].cuda()
+    b = torch.from_numpy(y * np.float32(2.0 ** 100))[:, None].cuda()
+    exact = x.astype(np.float64)[:, None] * y.astype(np.float64)[None]
+    off = np.abs(tmm.projection(a, b).double().cpu().numpy() * 2.0 ** (low - 100) - exact)
+    assert (off <= 6.2 * U * exact + 2.0 ** (low - 133) * y[None].astype(np.float64)).all()
