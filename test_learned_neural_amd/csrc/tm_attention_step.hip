@@ -297,8 +297,9 @@ int64_t outputs_bytes(const AttentionStepShape& s, int parts) {
 }  // namespace
 
 bool attention_step_supported(const AttentionStepShape& s) {
-  return (double)s.B * s.Hk * row_tiles_of(s) * parts_of(s) < (double)kMostBlocks &&
-         (double)s.B * s.H * s.n < (double)kMostBlocks;
+  // (the queries first: parts_of() multiplies what they bound)
+  return (double)s.B * s.H * s.n < (double)kMostBlocks &&
+         (double)s.B * s.Hk * row_tiles_of(s) * parts_of(s) < (double)kMostBlocks;
 }
 
 int64_t attention_step_ws_bytes(const AttentionStepShape& s) {
